@@ -37,6 +37,7 @@ EXPORTED = [
     "domino_verify_sampled_workspace_bytes", "domino_verify_sampled",
     "domino_draft_chain_stats_supported", "domino_draft_chain_stats",
     "domino_verify_sampled_head_workspace_bytes", "domino_verify_sampled_head",
+    "domino_qk_norm_rope", "domino_block_attention_workspace_bytes", "domino_block_attention", "domino_sample",
 ]
 
 
@@ -53,6 +54,20 @@ class domino_head(ctypes.Structure):
                 ("w_hh", ctypes.c_void_p), ("b_ih", ctypes.c_void_p), ("b_hh", ctypes.c_void_p),
                 ("w1", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("gate_table", ctypes.c_void_p)]
 
+
+class domino_kv_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("capacity", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("request_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64)]
+
+
+class domino_block(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_ctx", ctypes.c_int32),
+                ("q_start", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
+MASK_CAUSAL, MASK_FULL, MASK_TREE = 0, 1, 2
 
 _vp, _i32, _i64, _sz, _f32, _u64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t,
                                     ctypes.c_float, ctypes.c_uint64)
@@ -98,6 +113,12 @@ _sig("domino_headoff_workspace_bytes", _sz, [_i32, _i32, _i32, _i32, _i32])
 _sig("domino_draft_chain_headoff", _i32, [_vp, _i32, _i32, _i32, _f32, _vp, _i64, _vp, _vp, _sz, _vp])
 _sig("dominotree_build_marginal", _i32, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp,
                                          _sz, _vp])
+_CP, _BP = ctypes.POINTER(domino_kv_cache), ctypes.POINTER(domino_block)
+_sig("domino_qk_norm_rope", _i32, [_CP, _BP, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _i32, _i32,
+                                   _i32, _vp, _vp, _sz, _vp])
+_sig("domino_block_attention_workspace_bytes", _sz, [_CP, _BP, _i32])
+_sig("domino_block_attention", _i32, [_CP, _BP, _i32, _vp, _f32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp])
+_sig("domino_sample", _i32, [_i32, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp])
 
 
 def _ptr(t):
@@ -298,3 +319,49 @@ def domino_verify_sampled_head(head: Head, draft, L_base, u, lse, target_logits,
                                           float(temperature), _ptr(accept_len), _ptr(advanced), _ptr(next_token),
                                           _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
            "domino_verify_sampled_head")
+
+
+def kv_cache(k, v) -> domino_kv_cache:
+    """The struct of a layer's cache from tensors k and v [batch, n_kv_heads, capacity, head_dim] of the same
+    strides (any order of the first three axes in memory; the last one contiguous)."""
+    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or k.stride(3) != 1:
+        raise ValueError("k and v: [batch, n_kv_heads, capacity, head_dim] of one type and the same strides, the last 1")
+    dt = {torch.bfloat16: BF16, torch.float32: F32}.get(k.dtype)
+    if dt is None:
+        raise ValueError(f"cache type {k.dtype}: bfloat16 or float32")
+    b, h, s, d = k.shape
+    return domino_kv_cache(dt, b, h, d, s, _ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2))
+
+
+def block(tokens: int, max_q: int, max_ctx: int, ctx_len, q_start=None, positions=None) -> domino_block:
+    return domino_block(tokens, max_q, max_ctx, _ptr(q_start), _ptr(ctx_len), _ptr(positions))
+
+
+def domino_qk_norm_rope(cache: domino_kv_cache, rows: domino_block, n_q_heads: int, q, q_stride: int, k, k_stride: int,
+                        v, v_stride: int, q_weight, k_weight, eps: float, rope, max_pos: int, rot_dim: int,
+                        interleaved: bool, q_out, ws, stream=None):
+    _check(lib.domino_qk_norm_rope(ctypes.byref(cache), ctypes.byref(rows), n_q_heads, _ptr(q), q_stride, _ptr(k),
+                                   k_stride, _ptr(v), v_stride, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope),
+                                   max_pos, rot_dim, int(interleaved), _ptr(q_out), _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream(stream)), "domino_qk_norm_rope")
+
+
+def domino_block_attention_workspace_bytes(cache: domino_kv_cache, rows: domino_block, n_q_heads: int) -> int:
+    return lib.domino_block_attention_workspace_bytes(ctypes.byref(cache), ctypes.byref(rows), n_q_heads)
+
+
+def domino_block_attention(cache: domino_kv_cache, rows: domino_block, n_q_heads: int, q, scale: float, mask_mode: int,
+                           mask, window: int, sinks: int, out, lse, ws, stream=None):
+    _check(lib.domino_block_attention(ctypes.byref(cache), ctypes.byref(rows), n_q_heads, _ptr(q), float(scale),
+                                      mask_mode, _ptr(mask), window, sinks, _ptr(out), _ptr(lse), _ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream(stream)), "domino_block_attention")
+
+
+def domino_sample(logits, rows: int, V: int, temperature, top_k, top_p, min_p, gumbel, tokens, logprob, ws, stream=None,
+                  logits_stride=None, gumbel_stride=None):
+    """logits: bfloat16 or float32; row strides default to V."""
+    dt = BF16 if logits.dtype == torch.bfloat16 else F32
+    _check(lib.domino_sample(dt, _ptr(logits), V if logits_stride is None else logits_stride, rows, V,
+                             _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(gumbel),
+                             V if gumbel_stride is None else gumbel_stride, _ptr(tokens), _ptr(logprob), _ptr(ws),
+                             ws.numel() * ws.element_size(), _stream(stream)), "domino_sample")

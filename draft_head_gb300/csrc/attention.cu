@@ -1,0 +1,261 @@
+// Attention of a block's rows over the cache (domino_block_attention; the
+// definition is in domino.h): the kernel on CUDA cores, for fp32 and for every
+// head size.
+//
+// One pass over the keys with the running maximum m and sum l of the softmax:
+// per key tile s = scale q.k, m' = max(m, s), o = o 2^(m - m') + 2^(s - m') v
+// (scores in units of log2(e), so that one exp2 is the exponential). A CTA holds
+// 32 packed rows (row and query head of one kv head) and takes key tiles of 32
+// slots. A thread has 4 rows x 2 keys of the scores and 4 rows x D / 16 columns of o.
+// Few tiles and a long cache: the key tiles are split over CTAs, each writes its
+// (o, m, l), and the last one of a tile to arrive joins them in split order, so the
+// result does not depend on the arrival order.
+#include <math.h>
+
+#include "attention.cuh"
+
+namespace domino {
+
+namespace {
+
+constexpr int kBM = 32, kBN = 32, kThr = 128;
+constexpr int kLeast = 2;  // key tiles per split at least
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct SimtP {
+  AttnArgs a;
+  Partials part;
+  int splits, row_tiles;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__ SimtP p) {
+  extern __shared__ float sm[];
+  __shared__ int s_last;
+  const AttnArgs& a = p.a;
+  const int D = a.D, ldq = D + 4;
+  float* sq = sm;                 // [kBM][D + 4]
+  float* sk = sq + kBM * ldq;     // [kBN][D + 4]
+  float* sv = sk + kBN * ldq;     // [kBN][D]
+  float* sp = sv + kBN * D;       // [kBM][kBN + 1]
+  int* s_i = (int*)(sp + kBM * (kBN + 1));  // place, window begin of each row
+  int* s_low = s_i + kBM;
+  const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+  const int h = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
+  const int G = a.hq / a.hkv;
+  int q0, n, ctx;
+  if (!request_rows(a.rows, b, q0, n, ctx, t == 0, a.ctl)) return;
+  const int r0 = tile * kBM, rows = min(kBM, n * G - r0);
+  if (rows <= 0) return;
+
+  if (t < kBM) {
+    const int i = min(r0 + t, n * G - 1) / G;
+    const int pos = a.rows.positions ? a.rows.positions[q0 + i] : ctx + i;
+    s_i[t] = i;
+    s_low[t] = window_low(pos, a.window);
+  }
+  const T* q = (const T*)a.q;
+  for (int x = t; x < kBM * D; x += kThr) {
+    const int r = x / D, e = x - r * D, pr = r0 + r;
+    sq[r * ldq + e] = r < rows ? to_f<T>(q[((int64_t)(q0 + pr / G) * a.hq + h * G + pr % G) * D + e]) * (a.scale * kLog2e) : 0.0f;
+  }
+  __syncthreads();
+  int low = 0x7fffffff;
+  for (int r = 0; r < rows; ++r) low = min(low, s_low[r]);
+  const KeyTiles kt = key_tiles(a.mode, a.sinks, low, ctx, n, s_i[rows - 1], kBN);
+  const int used = splits_used(p.splits, kt.count, kLeast);
+  if (split >= used) return;
+  const int k_begin = (int)((int64_t)kt.count * split / used), k_end = (int)((int64_t)kt.count * (split + 1) / used);
+
+  const int tr = t >> 4, tc = t & 15;
+  float m[4], l[4], o[4][16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) o[i][c] = 0.0f;
+  }
+  const T* kb = (const T*)a.k + (int64_t)b * a.rs + (int64_t)h * a.hs;
+  const T* vb = (const T*)a.v + (int64_t)b * a.rs + (int64_t)h * a.hs;
+  const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.rows.max_q * a.rows.max_q : nullptr;
+  for (int k = k_begin; k < k_end; ++k) {
+    const int s0 = kt.slot(k, kBN);
+    __syncthreads();
+    for (int x = t; x < kBN * D; x += kThr) {
+      const int r = x / D, e = x - r * D, s = s0 + r;
+      // Slots past the request's rows are not read.
+      sk[r * ldq + e] = s < ctx + n ? to_f<T>(kb[(int64_t)s * a.ss + e]) : 0.0f;
+      sv[r * D + e] = s < ctx + n ? to_f<T>(vb[(int64_t)s * a.ss + e]) : 0.0f;
+    }
+    __syncthreads();
+    float s[4][2] = {};
+    for (int e = 0; e < D; e += 4) {
+      float4 kq[2], qq[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) kq[j] = *(const float4*)(sk + (tc + 16 * j) * ldq + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qq[i] = *(const float4*)(sq + (tr * 4 + i) * ldq + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          s[i][j] = fmaf(qq[i].x, kq[j].x, fmaf(qq[i].y, kq[j].y, fmaf(qq[i].z, kq[j].z, fmaf(qq[i].w, kq[j].w, s[i][j]))));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = tr * 4 + i;
+      bool in[2];
+      float mx = m[i];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int slot = s0 + tc + 16 * j;
+        in[j] = r < rows && slot < ctx + n &&
+                sees(a.mode, a.sinks, s_low[r], ctx, n, s_i[r], mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, slot);
+        if (in[j]) mx = fmaxf(mx, s[i][j]);
+      }
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      // A row that has seen nothing keeps m = -inf and l = 0.
+      const float keep = mx == -INFINITY || m[i] == mx ? 1.0f : exp2f(m[i] - mx);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float w = in[j] ? exp2f(s[i][j] - mx) : 0.0f;
+        sp[r * (kBN + 1) + tc + 16 * j] = w;
+        sum += w;
+      }
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      l[i] = l[i] * keep + sum;
+      m[i] = mx;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) o[i][c] *= keep;
+    }
+    __syncwarp();  // a row's weights are written and read by one warp
+    for (int j = 0; j < kBN; ++j) {
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = sp[(tr * 4 + i) * (kBN + 1) + j];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int e = c * 64 + tc * 4;
+        if (e < D) {
+          const float4 v = *(const float4*)(sv + j * D + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // A slot that no row of the tile's row sees has weight 0 and is not
+            // multiplied: its v may hold anything.
+            if (w[i] != 0.0f) {
+              o[i][4 * c] = fmaf(w[i], v.x, o[i][4 * c]);
+              o[i][4 * c + 1] = fmaf(w[i], v.y, o[i][4 * c + 1]);
+              o[i][4 * c + 2] = fmaf(w[i], v.z, o[i][4 * c + 2]);
+              o[i][4 * c + 3] = fmaf(w[i], v.w, o[i][4 * c + 3]);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  T* out = (T*)a.out;
+  if (used > 1) {
+    const int64_t tl = ((int64_t)b * a.hkv + h) * p.row_tiles + tile;
+    const int64_t base = (tl * p.splits + split) * kBM;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = tr * 4 + i;
+      if (r >= rows) continue;
+      if (tc == 0) p.part.ml[base + r] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c * 64 + tc * 4 < D)
+          *(float4*)(p.part.o + (base + r) * D + c * 64 + tc * 4) =
+              make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
+    }
+    __threadfence();
+    __syncthreads();
+    if (t == 0) {
+      const unsigned int was = atomicAdd(p.part.arrived + tl, 1u);
+      s_last = was == (unsigned)used - 1u;
+      if (s_last) p.part.arrived[tl] = 0u;  // ready for the next call
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = tr * 4 + i;
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) o[i][c] = 0.0f;
+      if (r >= rows) continue;
+      const int64_t first = tl * p.splits * kBM + r;
+      for (int sp2 = 0; sp2 < used; ++sp2) m[i] = fmaxf(m[i], __ldcg(&p.part.ml[first + (int64_t)sp2 * kBM]).x);
+      if (m[i] == -INFINITY) continue;
+      for (int sp2 = 0; sp2 < used; ++sp2) {
+        const int64_t at = first + (int64_t)sp2 * kBM;
+        const float2 ml = __ldcg(&p.part.ml[at]);
+        if (ml.x == -INFINITY) continue;
+        const float w = ml.x == m[i] ? 1.0f : exp2f(ml.x - m[i]);
+        l[i] += ml.y * w;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c * 64 + tc * 4 < D) {
+            const float4 v = __ldcg((const float4*)(p.part.o + at * D + c * 64 + tc * 4));
+            o[i][4 * c] += v.x * w;
+            o[i][4 * c + 1] += v.y * w;
+            o[i][4 * c + 2] += v.z * w;
+            o[i][4 * c + 3] += v.w * w;
+          }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = tr * 4 + i, pr = r0 + r;
+    if (r >= rows) continue;
+    const int64_t row = (int64_t)(q0 + pr / G) * a.hq + h * G + pr % G;
+    const float inv = l[i] > 0.0f ? 1.0f / l[i] : (l[i] == 0.0f ? 0.0f : NAN);
+    if (a.lse && tc == 0) a.lse[row] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const int e = (c >> 2) * 64 + tc * 4 + (c & 3);
+      if (e < D) out[row * D + e] = (T)(o[i][c] * inv);
+    }
+  }
+}
+
+// Two CTAs per SM.
+int64_t simt_want() { return 2 * (int64_t)num_sms(); }
+
+int simt_row_tiles(const AttnArgs& a) {
+  return (int)(((int64_t)a.rows.max_q * (a.hq / a.hkv) + kBM - 1) / kBM);
+}
+
+}  // namespace
+
+size_t attn_ws_bytes(const AttnArgs& a) { return partial_bytes(simt_want(), kBM, a.D); }
+
+cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
+  SimtP p;
+  p.a = a;
+  p.row_tiles = simt_row_tiles(a);
+  p.splits = splits_for((int64_t)p.row_tiles * a.hkv * a.rows.batch, simt_want(),
+                        ((int64_t)a.rows.max_ctx + a.rows.max_q) / kBN / kLeast);
+  p.part = partials_at(a.scratch, simt_want(), kBM);
+  const size_t smem = sizeof(float) * (kBM * (a.D + 4) + kBN * (a.D + 4) + kBN * a.D + kBM * (kBN + 1)) + 8 * kBM;
+  const dim3 grid((unsigned)(p.row_tiles * p.splits), (unsigned)a.hkv, (unsigned)a.rows.batch);
+  const void* fn = a.dtype == DOMINO_BF16 ? (const void*)attn_simt_kernel<__nv_bfloat16> : (const void*)attn_simt_kernel<float>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 120 * 1024);
+  if (e != cudaSuccess) return e;
+  if (a.dtype == DOMINO_BF16)
+    attn_simt_kernel<__nv_bfloat16><<<grid, kThr, smem, stream>>>(p);
+  else
+    attn_simt_kernel<float><<<grid, kThr, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace domino

@@ -170,4 +170,56 @@ cudaError_t launch_tree_marginal(const float* cand_val, const int32_t* cand_id, 
                                  int32_t* node_parent, int32_t* node_depth, float* node_score, Ctl* ctl,
                                  cudaStream_t stream);
 
+// The target's side of a cycle (declarations and meaning: domino.h).
+struct RowsArgs {
+  int batch, tokens, max_q, max_ctx, capacity;
+  const int32_t* q_start;
+  const int32_t* ctx_len;
+  const int32_t* positions;
+};
+struct NormRopeArgs {
+  RowsArgs rows;
+  int dtype, hq, hkv, D, rot, interleaved, max_pos;
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const void *q_weight, *k_weight;
+  float eps;
+  const float* rope;
+  void *q_out, *k_cache, *v_cache;
+  int64_t rs, hs, ss;  // cache strides: request, head, slot
+  Ctl* ctl;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+
+struct AttnArgs {
+  RowsArgs rows;
+  int dtype, hq, hkv, D;
+  const void *q, *k, *v;
+  int64_t rs, hs, ss;
+  float scale;
+  int mode, window, sinks;
+  const uint8_t* mask;
+  void* out;
+  float* lse;
+  Ctl* ctl;
+  void* scratch;  // behind the control block
+};
+size_t attn_ws_bytes(const AttnArgs& a);
+cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
+
+struct SampleArgs {
+  int dtype, rows, V;
+  const void* logits;
+  int64_t ls;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+  const float* gumbel;
+  int64_t gs;
+  int32_t* tokens;
+  float* logprob;
+  Ctl* ctl;
+};
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
+
 }  // namespace domino

@@ -1,0 +1,58 @@
+// The packed rows of a block (domino_block in domino.h) on the device: which
+// request a row belongs to, and a request's checked lengths.
+#pragma once
+
+#include "common.cuh"
+
+namespace domino {
+
+// Request b's first row, rows and past. False (with DEV_ERR_DATA recorded by
+// the calling threads for which `report` is set) when a length is outside its
+// bound: nothing of the request may then be touched.
+__device__ __forceinline__ bool request_rows(const RowsArgs& r, int b, int& q0, int& n, int& ctx, bool report, Ctl* ctl) {
+  int64_t first, rows;
+  if (r.q_start) {
+    first = r.q_start[b];
+    rows = (int64_t)r.q_start[b + 1] - first;
+  } else {
+    first = (int64_t)b * r.max_q;
+    rows = r.max_q;
+  }
+  const int64_t c = r.ctx_len[b];
+  q0 = (int)first;
+  n = (int)rows;
+  ctx = (int)c;
+  if (first < 0 || rows < 0 || rows > r.max_q || first + rows > r.tokens || c < 0 || c > r.max_ctx ||
+      c + rows > r.capacity) {
+    if (report) dev_error(ctl, DEV_ERR_DATA);
+    return false;
+  }
+  return true;
+}
+
+// The request b and place i of packed row t, and the request's past. Called by
+// whole warps; every lane gets the result. A 32-way search: each round, the
+// lanes look at 32 requests spread over what is left.
+__device__ __forceinline__ bool find_row(const RowsArgs& r, int t, int& b, int& i, int& ctx, Ctl* ctl) {
+  const int lane = threadIdx.x & 31;
+  if (r.q_start) {
+    int lo = 0, n = r.batch;  // the last b in [lo, lo + n) with q_start[b] <= t
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const int at = lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, at < n && r.q_start[lo + at] <= t);
+      const int k = m ? 31 - __clz(m) : 0;
+      lo += k * step;
+      n = min(step, n - k * step);
+    }
+    b = lo;
+  } else {
+    b = t / r.max_q;
+  }
+  int q0, rows;
+  if (!request_rows(r, b, q0, rows, ctx, lane == 0, ctl)) return false;
+  i = t - q0;
+  return i >= 0 && i < rows;  // a row of no request
+}
+
+}  // namespace domino

@@ -387,6 +387,146 @@ domino_status domino_draft_chain_noalloc(const domino_head* head, const float* L
                                          void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The target's side of a cycle: the attention layers' cache and the draw from
+ * the target's logits. The pages leave the target pass to its framework (tree
+ * attention with an ancestor-only mask: "DominoTree…", section 验证; a block
+ * whose rows see each other both ways: "…Speculative Decoding Review" section
+ * 3-2); these calls are the parts of it that depend on the drafted block.
+ *
+ * Rows are packed: request b's rows are rows q_start[b] .. q_start[b + 1] - 1
+ * of every array with a `tokens` axis; row i of request b is written to cache
+ * slot ctx_len[b] + i. A device-side length outside its bound (ctx_len outside
+ * [0, max_ctx], rows outside [0, max_q], more rows than `tokens`, a slot past
+ * the capacity) records DOMINO_ERR_DEVICE_DATA and leaves that request's
+ * outputs unwritten.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Keys and values of one attention layer. Element x of the vector of request
+ * b, kv head h, slot s is k[b * request_stride + h * head_stride + s *
+ * slot_stride + x], and the same for v (strides in elements, multiples of 8 for
+ * bf16 and of 4 for fp32, not negative; pointers 16-byte aligned, head_dim a
+ * multiple of 8 and at most 256). Slots [0, ctx_len) hold the request's past.
+ */
+typedef struct {
+  int32_t dtype;
+  int32_t batch, n_kv_heads, head_dim, capacity;
+  void* k;
+  void* v;
+  int64_t request_stride, head_stride, slot_stride;
+} domino_kv_cache;
+
+/*
+ * The rows of one call.
+ *   tokens     packed rows of all requests
+ *   max_q      no request has more rows
+ *   max_ctx    no request has a longer past (sizes the split of long caches)
+ *   q_start    [batch + 1] device int32, not decreasing, or NULL: every request
+ *              has max_q rows (tokens == batch * max_q)
+ *   ctx_len    [batch] device int32: slots already in the cache
+ *   positions  [tokens] device int32, or NULL: row i is at position ctx_len + i
+ *              (a tree's node is at ctx_len + its depth)
+ */
+typedef struct {
+  int32_t tokens, max_q, max_ctx;
+  const int32_t* q_start;
+  const int32_t* ctx_len;
+  const int32_t* positions;
+} domino_block;
+
+/*
+ * Norm and rotation of queries and keys, and the keys' and values' place in
+ * the cache, in one pass. For every row and head, with x the head's vector:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight        (q and k; fp32)
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the rot_dim / 2 pairs of y;
+ *   pair j is (y[j], y[j + rot_dim / 2]), or with interleaved != 0
+ *   (y[2j], y[2j + 1]); elements from rot_dim on are not rotated.
+ * q goes to q_out [tokens, n_q_heads, head_dim] (contiguous; may be q itself
+ * when q's rows are), k and v (unchanged) to the cache.
+ *   q, k, v      device, cache->dtype: row t's heads start at t * stride, head
+ *                h at + h * head_dim (three parts of a fused projection, say);
+ *                q may be NULL when n_q_heads is 0
+ *   q_weight, k_weight [head_dim] device, cache->dtype, or NULL for ones
+ *   rope         [max_pos, rot_dim] device fp32: a position's rot_dim / 2
+ *                cosines, then its sines; NULL when rot_dim is 0. A position
+ *                outside [0, max_pos) records DOMINO_ERR_DEVICE_DATA and leaves
+ *                the row unwritten.
+ * eps >= 0 and finite; rot_dim even, in [0, head_dim]. Pointers 16-byte
+ * aligned, strides as the cache's. ws: any workspace of at least 256 bytes.
+ */
+domino_status domino_qk_norm_rope(const domino_kv_cache* cache, const domino_block* block, int n_q_heads,
+                                  const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, const void* q_weight,
+                                  const void* k_weight, float eps, const float* rope, int max_pos, int rot_dim,
+                                  int interleaved, void* q_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Which rows of the block a row of the block sees. */
+typedef enum {
+  DOMINO_MASK_CAUSAL = 0, /* itself and the rows before it, within the window */
+  DOMINO_MASK_FULL = 1,   /* all rows of its request (a draft backbone's block) */
+  DOMINO_MASK_TREE = 2    /* rows j with mask[b, i, j] != 0 (dominotree_verify's mask) */
+} domino_mask_mode;
+
+/*
+ * Attention of a block's rows over the cache, which already holds the block's
+ * own keys and values (domino_qk_norm_rope). Query head h reads kv head
+ * h / (n_q_heads / n_kv_heads). With c = ctx_len[b], row i at position p:
+ *   slot s < c is seen iff s < sinks or s > p - window (window 0: always);
+ *   slot c + j is seen iff DOMINO_MASK_CAUSAL: j <= i and (c + j < sinks or
+ *   c + j > p - window or window 0); DOMINO_MASK_FULL: j < the request's rows;
+ *   DOMINO_MASK_TREE: mask[b, i, j] != 0;
+ *   out = sum_s softmax_s(scale q.k_s) v_s over the seen slots, 0 if none is;
+ *   lse = log sum_s exp(scale q.k_s), -inf if none is.
+ *   q, out  [tokens, n_q_heads, head_dim] device, cache->dtype, contiguous
+ *   mask    [batch, max_q, max_q] device uint8 (DOMINO_MASK_TREE only)
+ *   lse     [tokens, n_q_heads] device fp32 out, or NULL
+ * Slots that no row sees are not used, whatever they hold; a seen slot's NaN
+ * or infinity reaches the rows that see it, as the formula says.
+ * Scores, softmax and sums are fp32; in bf16 the softmax weights are rounded to
+ * bf16 for the product with v. scale is finite and not negative.
+ * Workspace: domino_block_attention_workspace_bytes(cache, block, n_q_heads)
+ * (0 if the arguments are invalid; block's device pointers are not read),
+ * zeroed before its first use; each call leaves it ready for the next.
+ */
+size_t domino_block_attention_workspace_bytes(const domino_kv_cache* cache, const domino_block* block,
+                                              int n_q_heads);
+domino_status domino_block_attention(const domino_kv_cache* cache, const domino_block* block, int n_q_heads,
+                                     const void* q, float scale, int mask_mode, const uint8_t* mask, int window,
+                                     int sinks, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The draw from logits [rows, V] under each row's own settings. With T the
+ * row's temperature, tokens ordered by (logit descending, id ascending):
+ *   top_k  the first top_k tokens stay (0: all);
+ *   top_p  of those, a token stays iff the probability (softmax of logit / T
+ *          over the top_k set) before it in the order is below top_p (1: all);
+ *   min_p  of those, a token stays iff exp((logit - max logit) / T) >= min_p;
+ *   tokens[r] = argmax over what stayed of logit / T + gumbel[r, v], ties to
+ *   the lowest id: a draw from softmax(logit / T) over what stayed;
+ *   logprob[r] = the log-probability of tokens[r] in that distribution.
+ * T = 0: tokens[r] = argmax of the logits, logprob 0, noise not read. A row
+ * with no logit above -inf: token -1, logprob -inf. A NaN logit counts as -inf;
+ * +inf logits share the whole probability.
+ *   logits      device, dtype (DOMINO_F32 or DOMINO_BF16), row r at r *
+ *               logits_stride elements
+ *   temperature, top_p, min_p [rows] device fp32, top_k [rows] device int32;
+ *               NULL: 1, 1, 0, 0 (off)
+ *   gumbel      device fp32, row r at r * gumbel_stride, finite: standard
+ *               Gumbel noise; may be NULL only when temperature is given and
+ *               every row's is 0 (a row above 0 then is an invalid setting)
+ *   tokens      [rows] device int32 out; logprob [rows] device fp32 out or NULL
+ * A setting outside its range (T < 0 or not finite, top_k < 0, top_p outside
+ * (0, 1], min_p outside [0, 1]) records DOMINO_ERR_DEVICE_DATA and gives that
+ * row token -1, logprob NaN. ws: any workspace of at least 256 bytes.
+ */
+domino_status domino_sample(int dtype, const void* logits, int64_t logits_stride, int rows, int V,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, const float* gumbel, int64_t gumbel_stride, int32_t* tokens,
+                            float* logprob, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Synchronise `stream`, return the sticky device status recorded in `ws` by
  * earlier calls (DOMINO_OK if none) and clear it.
  */
