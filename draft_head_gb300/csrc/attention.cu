@@ -237,9 +237,12 @@ int simt_row_tiles(const AttnArgs& a) {
 
 }  // namespace
 
-size_t attn_ws_bytes(const AttnArgs& a) { return partial_bytes(simt_want(), kBM, a.D); }
+size_t attn_ws_bytes(const AttnArgs& a) {
+  return attn_tc_applies(a) ? attn_tc_ws_bytes(a) : partial_bytes(simt_want(), kBM, a.D);
+}
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
+  if (attn_tc_applies(a)) return launch_attention_tc(a, stream);
   SimtP p;
   p.a = a;
   p.row_tiles = simt_row_tiles(a);

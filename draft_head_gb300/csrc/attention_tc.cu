@@ -1,0 +1,845 @@
+// Attention of a block's rows over the cache on the tensor cores
+// (domino_block_attention; the definition is in domino.h): bf16, head_dim <= 128.
+//
+// One pass over the keys with the running maximum and sum of the softmax. Per key
+// tile of 128 slots and query tile of 128 packed rows (row and query head of one kv
+// head): S = Q K^T (tcgen05.mma, fp32 in TMEM), a thread per row takes its 128
+// scores to registers, P = 2^(S c - m) goes back over S in TMEM as bf16, and
+// O += P V with P as the TMEM operand and V as it lies in the cache (slots x head_dim,
+// head_dim contiguous: the MN-major operand). O stays in TMEM; it is rescaled only
+// when a row's maximum has grown by more than 2^8 since the last time (P then stays
+// below 2^8, and l and O carry the same factor), which after the first tiles is rare.
+//
+//   warp 0       TMA: key and value tiles into one ring of 32 KB buffers
+//   warp 1       TMEM, and one thread issues the MMAs
+//   warps 2, 3   clear non-finite values of tiles that some row does not see
+//   warps 4 ..   softmax and epilogue, four warps per query tile
+//
+// NQ = 1 (few rows: one token, a draft block, a tree): bound by the cache's bytes;
+// two S buffers, so the next tile's scores are computed under this tile's softmax.
+// NQ = 2 (prompts): bound by the MMAs and the exponentials; the two query tiles share
+// the key and value loads and take turns: one's MMAs run under the other's softmax.
+//
+// The work is the list of all (request, row tile, kv head, key tile), cut into equal
+// pieces, one per CTA of a grid of one CTA per SM; lengths live on the device, so every
+// CTA counts the list itself. A row tile cut over CTAs is joined by the last of them to
+// finish, in piece order, from fp32 sums in the workspace: the result does not depend on
+// the order of arrival.
+#include <cuda.h>
+#include <math.h>
+#include <string.h>
+#include <mutex>
+
+#include "attention.cuh"
+
+namespace domino {
+
+namespace {
+
+constexpr int kBN = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;  // growth of the maximum (log2) that forces a rescale of O
+constexpr int kLeast = 1;      // key tiles per CTA, at least
+constexpr int kBadRing = 8;    // items the roles may be apart, at most (the ring holds fewer tiles)
+
+struct TcAttnP {
+  CUtensorMap tmK, tmV;
+  AttnArgs a;
+  int row_tiles;  // per request, of 128 NQ packed rows
+  int slots;      // ring buffers
+  uint64_t timeout_ns;
+  float c;        // scale log2(e)
+  unsigned int* arrived;  // per CTA: pieces in, of the row tile that begins in it and goes on
+  float2* ml;             // [2 grid][128 NQ]
+  float* o;               // [2 grid][128 NQ][DP]
+};
+
+// A row tile of one request: its rows and the slots they see. `cnt` is 0 when there
+// is nothing to do.
+struct Unit {
+  int q0, n, ctx, r0, rows, i_first, i_last, low_min, low_max, cnt;
+  KeyTiles kt;
+};
+
+template <int BMT>
+__device__ __forceinline__ Unit load_unit(const AttnArgs& a, int row_tiles, int u, bool report) {
+  Unit w;
+  w.cnt = 0;
+  const int b = u / row_tiles, tile = u - b * row_tiles, G = a.hq / a.hkv;
+  if (!request_rows(a.rows, b, w.q0, w.n, w.ctx, report, a.ctl)) return w;
+  w.r0 = tile * BMT;
+  w.rows = min(BMT, w.n * G - w.r0);
+  if (w.rows <= 0) return w;
+  w.i_first = w.r0 / G;
+  w.i_last = (w.r0 + w.rows - 1) / G;
+  if (a.window == 0) {
+    w.low_min = w.low_max = 0;
+  } else if (a.rows.positions) {
+    w.low_min = 0x7fffffff;
+    w.low_max = 0;
+    for (int i = w.i_first; i <= w.i_last; ++i) {
+      const int low = window_low(__ldg(a.rows.positions + w.q0 + i), a.window);
+      w.low_min = min(w.low_min, low);
+      w.low_max = max(w.low_max, low);
+    }
+  } else {
+    w.low_min = window_low(w.ctx + w.i_first, a.window);
+    w.low_max = window_low(w.ctx + w.i_last, a.window);
+  }
+  w.kt = key_tiles(a.mode, a.sinks, w.low_min, w.ctx, w.n, w.i_last, kBN);
+  w.cnt = w.kt.count;
+  return w;
+}
+
+// Whether every row of the tile sees every slot of the key tile at s0.
+__device__ __forceinline__ bool all_seen(const AttnArgs& a, const Unit& w, int s0) {
+  const int hi = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_first + 1 : a.mode == DOMINO_MASK_FULL ? w.ctx + w.n : w.ctx;
+  const int low = a.mode == DOMINO_MASK_CAUSAL ? w.low_max : min(w.low_max, w.ctx);
+  return s0 + kBN <= hi && (s0 >= low || s0 + kBN <= a.sinks);
+}
+
+// A bounded wait that all lanes of a warp leave together, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* s_abort, Ctl* ctl, uint64_t timeout_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, ctl, timeout_ns));
+}
+// Barrier of 128 threads that tells all of them whether every one was `ok`.
+__device__ __forceinline__ bool group_all(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.and.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+// The CTA's part of the work list, walked by every role alike.
+struct Walk {
+  int u, h, k, len;
+  int64_t x;  // place of the next key tile in the list
+  __device__ __forceinline__ void next(int cnt, int piece, int hkv) {
+    len -= piece;
+    x += piece;
+    k += piece;
+    if (k == cnt) {
+      k = 0;
+      if (++h == hkv) {
+        h = 0;
+        ++u;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int s, int h, int b, uint64_t* bar,
+                                            uint64_t policy, bool hint) {
+  if (hint)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+        "l"((uint64_t)tmap), "r"(x), "r"(s), "r"(h), "r"(b), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"((uint64_t)tmap), "r"(x), "r"(s), "r"(h), "r"(b), "r"(smem_u32(bar))
+        : "memory");
+}
+// Shared-memory descriptor of an MN-major operand with 128-byte swizzle: rows of 64
+// elements of N, 8 rows (of K) per 1024-byte atom; the next 8 rows follow at the
+// stride offset, the next 64 elements of N at the leading offset (a whole 128-row block).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBN * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ bool bad16(uint32_t x) {  // a bf16 pair with an infinity or a NaN in it
+  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
+
+// Visibility of the 128 slots from s0 for one row, as bits.
+__device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int i, int low, const uint8_t* mask_row, int s0,
+                                          uint32_t (&bits)[4]) {
+  const int end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + i + 1 : a.mode == DOMINO_MASK_FULL ? w.ctx + w.n : w.ctx;
+  const int from = a.mode == DOMINO_MASK_CAUSAL ? low : min(low, w.ctx);
+  auto below = [&](int x, int word) -> uint32_t {  // slots of the word below slot x
+    const int d = x - (s0 + word * 32);
+    return d <= 0 ? 0u : d >= 32 ? 0xffffffffu : (1u << d) - 1u;
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j) bits[j] = (~below(from, j) | below(a.sinks, j)) & below(end, j);
+  if (a.mode == DOMINO_MASK_TREE) {
+    const int j0 = max(0, s0 - w.ctx), j1 = min(w.n, s0 + kBN - w.ctx);
+    for (int j = j0; j < j1; ++j) {
+      const int at = w.ctx + j - s0;
+      const uint32_t bit = __ldg(mask_row + j) ? 1u << (at & 31) : 0u;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) bits[q] |= (at >> 5) == q ? bit : 0u;
+    }
+  }
+}
+
+// Adds the non-finite values that the row sees in the piece's partly seen tiles to
+// columns [e0, e0 + 32) of its sums: the tiles had them cleared, because the product
+// with V would have spread them to the rows that do not see them.
+__device__ __noinline__ void add_non_finite(const AttnArgs& a, const Unit& w, int b, int h, int k0, int k1, int i, int low,
+                                            const uint8_t* mask_row, int e0, float* o) {
+  const uint16_t* v = (const uint16_t*)a.v + (int64_t)b * a.rs + (int64_t)h * a.hs;
+  for (int k = k0; k < k1; ++k) {
+    const int s0 = w.kt.slot(k, kBN);
+    if (all_seen(a, w, s0)) continue;
+    uint32_t bits[4];
+    seen_bits(a, w, i, low, mask_row, s0, bits);
+    for (int j = 0; j < kBN; ++j) {
+      if (!((bits[j >> 5] >> (j & 31)) & 1u)) continue;
+      const uint16_t* row = v + (int64_t)(s0 + j) * a.ss;
+      for (int e = 0; e < 32 && e0 + e < a.D; ++e) {
+        const uint32_t x = row[e0 + e];
+        if ((x & 0x7f80u) == 0x7f80u) o[e] += __uint_as_float(x << 16);
+      }
+    }
+  }
+}
+
+template <int NQ, int KB>
+struct Cfg {
+  static constexpr int DP = 64 * KB;
+  static constexpr int BMT = 128 * NQ;
+  static constexpr int kThreads = 128 + 128 * NQ;
+  static constexpr uint32_t kTile = (uint32_t)KB * kBN * 128;      // bytes of a key or value tile
+  static constexpr uint32_t kQBytes = (uint32_t)KB * 128 * 128;    // bytes of a query tile
+  static constexpr uint32_t kOCol = 256;                           // S: 128 columns each, then O
+};
+
+template <int NQ, int KB>
+__global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnP p) {
+  using C = Cfg<NQ, KB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = smem;
+  uint8_t* ring = sQ + NQ * C::kQBytes;
+  const int slots = p.slots;
+  uint64_t* full = (uint64_t*)(ring + (size_t)slots * C::kTile);
+  uint64_t* empty = full + slots;
+  uint64_t* s_ready = empty + slots;  // [2]: per query tile (NQ = 2) or per S buffer (NQ = 1)
+  uint64_t* p_ready = s_ready + 2;    // [2] likewise
+  uint64_t* o_done = p_ready + 2;     // [NQ]
+  uint64_t* q_ready = o_done + 2;     // [NQ]
+  uint64_t* v_clean = q_ready + 2;    // [slots]
+  uint64_t* drain = v_clean + slots;
+  int64_t* s_total = (int64_t*)(drain + 1);
+  int64_t* s_prefix = s_total + 1;
+  int* s_unit = (int*)(s_prefix + 1);
+  int* s_last = s_unit + 1;           // [NQ]
+  volatile int* s_bad = s_last + 2;   // [2][kBadRing]
+  uint32_t* tmem_slot = (uint32_t*)(s_last + 2 + 2 * kBadRing);
+  volatile int* s_abort = (volatile int*)(tmem_slot + 1);
+  int64_t* s_scan = (int64_t*)(((uintptr_t)(tmem_slot + 2) + 7) & ~(uintptr_t)7);  // [kThreads / 32]
+
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hkv = a.hkv, G = a.hq / a.hkv;
+  Ctl* ctl = a.ctl;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&v_clean[s], 2);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_ready[s], 1);
+      mbar_init(&p_ready[s], 4);
+      mbar_init(&o_done[s], 1);
+      mbar_init(&q_ready[s], 4);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    for (int i = 0; i < 2 * kBadRing; ++i) s_bad[i] = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&p.tmK);
+    tma_prefetch_desc(&p.tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+
+  // Count the work list (key tiles of one kv head) and find this CTA's part of it.
+  const int units = a.rows.batch * p.row_tiles;
+  const int chunk = (units + C::kThreads - 1) / C::kThreads;
+  const int u_begin = min(units, (int)threadIdx.x * chunk), u_end = min(units, u_begin + chunk);
+  int64_t mine = 0;
+  for (int u = u_begin; u < u_end; ++u)
+    mine += load_unit<C::BMT>(a, p.row_tiles, u, blockIdx.x == 0 && u % p.row_tiles == 0).cnt;
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    const int64_t s = s_scan[w];
+    before += w < warp ? s : 0;
+    total += s;
+  }
+  before += incl - mine;
+  const int64_t list = total * hkv;
+  // CTAs with work: no more than key tiles, so that none of them is empty.
+  const int ctas = (int)min((int64_t)gridDim.x, list / kLeast > 0 ? list / kLeast : 1);
+  const bool idle = (int)blockIdx.x >= ctas || list == 0;
+  const int64_t x0 = idle ? 0 : list * blockIdx.x / ctas, x1 = idle ? 0 : list * (blockIdx.x + 1) / ctas;
+  if (!idle && mine > 0 && before <= x0 / hkv && x0 / hkv < before + mine) {
+    int64_t at = before;
+    for (int u = u_begin; u < u_end; ++u) {
+      const int c = load_unit<C::BMT>(a, p.row_tiles, u, false).cnt;
+      if (x0 < (at + c) * hkv) {
+        *s_unit = u;
+        *s_prefix = at;
+        break;
+      }
+      at += c;
+    }
+  }
+  __syncthreads();
+  Walk walk;
+  walk.len = (int)(x1 - x0);
+  walk.x = x0;
+  walk.u = 0; walk.h = 0; walk.k = 0;
+  if (walk.len > 0) {
+    walk.u = *s_unit;
+    const int cnt = load_unit<C::BMT>(a, p.row_tiles, walk.u, false).cnt;
+    const int64_t in = x0 - *s_prefix * hkv;
+    walk.h = (int)(in / cnt);
+    walk.k = (int)(in - (int64_t)walk.h * cnt);
+  }
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_first();
+      const bool once = p.row_tiles == 1;  // no other row tile reads this cache again
+      int slot = 0;
+      uint32_t phase = 0;
+      long issued = 0;
+      bool ok = true;
+      while (walk.len > 0 && walk.u < units && ok) {
+        const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
+        if (w.cnt == 0) { ++walk.u; continue; }
+        const int b = walk.u / p.row_tiles, piece = min(walk.len, w.cnt - walk.k);
+        for (int k = walk.k; k < walk.k + piece && ok; ++k) {
+          const int s0 = w.kt.slot(k, kBN);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!mbar_wait(&empty[slot], phase ^ 1u, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
+            mbar_expect_tx(&full[slot], C::kTile);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+              tma_load_4d(ring + (size_t)slot * C::kTile + kb * (kBN * 128), kv ? &p.tmV : &p.tmK, kb * 64, s0, walk.h, b,
+                          &full[slot], pol, once);
+            ++issued;
+            if (++slot == slots) { slot = 0; phase ^= 1u; }
+          }
+        }
+        walk.next(w.cnt, piece, hkv);
+      }
+      if (!ok) {
+        // Give up, but first let the copies already in flight land.
+        for (long j = issued - 1; j >= 0 && j >= issued - slots; --j)
+          mbar_wait(&full[j % slots], (uint32_t)((j / slots) & 1), nullptr, ctl, p.timeout_ns);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16_f32(128, kBN);
+      const uint32_t id_o = idesc_bf16_f32(128, C::DP) | (1u << 16);  // B is MN-major
+      int slot = 0;
+      uint32_t phase = 0;
+      uint32_t item = 0, tiles = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, s_abort, ctl, p.timeout_ns)) ok = false;
+        tc_fence_after();
+      };
+      auto advance = [&](int& s, uint32_t& ph) {
+        if (++s == slots) { s = 0; ph ^= 1u; }
+      };
+      auto scores = [&](int qt, uint32_t d, int s) {  // S = Q K^T
+        const uint64_t ad = sdesc_k_sw128(smem_u32(sQ + (size_t)qt * C::kQBytes));
+        const uint64_t bd = sdesc_k_sw128(smem_u32(ring + (size_t)s * C::kTile));
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tmem + d, ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k), bd + (uint64_t)(kb * (kBN * 128 / 16) + 2 * k),
+                      id_s, (kb | k) ? 1u : 0u);
+      };
+      auto values = [&](uint32_t d, uint32_t pcol, int s, bool first) {  // O += P V
+        const uint64_t bd = sdesc_mn_sw128(smem_u32(ring + (size_t)s * C::kTile));
+#pragma unroll
+        for (int k = 0; k < kBN / 16; ++k)
+          umma_bf16_ts(tmem + d, tmem + pcol + (uint32_t)(8 * k), bd + (uint64_t)(k * (16 * 128 / 16)), id_o,
+                       (first && k == 0) ? 0u : 1u);
+      };
+      while (walk.len > 0 && walk.u < units && ok) {
+        const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
+        if (w.cnt == 0) { ++walk.u; continue; }
+        const int piece = min(walk.len, w.cnt - walk.k);
+        // The ring holds K_0, V_0, K_1, V_1, ...; ks / vs are the places of the next of each.
+        int ks = slot, vs = slot;
+        uint32_t kph = phase, vph = phase;
+        advance(vs, vph);
+        auto next2 = [&](int& s, uint32_t& ph) { advance(s, ph); advance(s, ph); };
+        wait(&full[ks], kph);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          wait(&q_ready[q], item & 1u);
+          if (!ok) break;
+          const uint32_t sb = NQ == 1 ? (tiles & 1u) : (uint32_t)q;
+          scores(q, sb * 128, ks);
+          umma_commit(&s_ready[sb]);
+        }
+        if (!ok) break;
+        umma_commit(&empty[ks]);
+        next2(ks, kph);
+        for (int t = 0; t < piece && ok; ++t, ++tiles) {
+          const bool more = t + 1 < piece;
+          if (NQ == 1 && more) {
+            wait(&full[ks], kph);
+            if (!ok) break;
+            scores(0, ((tiles + 1) & 1u) * 128, ks);
+            umma_commit(&s_ready[(tiles + 1) & 1u]);
+            umma_commit(&empty[ks]);
+            next2(ks, kph);
+          }
+          wait(&full[vs], vph);
+          wait(&v_clean[vs], vph);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const uint32_t sb = NQ == 1 ? (tiles & 1u) : (uint32_t)q;
+            wait(&p_ready[sb], NQ == 1 ? ((tiles >> 1) & 1u) : (tiles & 1u));
+            if (!ok) break;
+            values(C::kOCol + (uint32_t)q * C::DP, sb * 128, vs, t == 0);
+            umma_commit(&o_done[q]);
+            if (NQ == 2 && more) {
+              if (q == 0) wait(&full[ks], kph);
+              if (!ok) break;
+              scores(q, sb * 128, ks);
+              umma_commit(&s_ready[sb]);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&empty[vs]);
+          next2(vs, vph);
+          if (NQ == 2 && more) {
+            umma_commit(&empty[ks]);
+            next2(ks, kph);
+          }
+        }
+        slot = ks;
+        phase = kph;
+        ++item;
+        walk.next(w.cnt, piece, hkv);
+      }
+      // Every MMA issued above has finished before TMEM is freed.
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, ctl, p.timeout_ns);
+    }
+  } else if (warp < 4) {
+    // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
+    // or a NaN in the product, so these are cleared here and the row tile is marked.
+    const int t64 = threadIdx.x - 64;
+    int slot = 0;
+    uint32_t phase = 0, item = 0;
+    bool ok = true;
+    while (walk.len > 0 && walk.u < units && ok) {
+      const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
+      if (w.cnt == 0) { ++walk.u; continue; }
+      const int piece = min(walk.len, w.cnt - walk.k);
+      for (int t = 0; t < piece; ++t) {
+        if (++slot == slots) { slot = 0; phase ^= 1u; }  // past the key tile
+        if (!mbar_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
+        if (!all_seen(a, w, w.kt.slot(walk.k + t, kBN))) {
+          uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
+          bool bad = false;
+#pragma unroll 8
+          for (uint32_t x = t64; x < C::kTile / 16; x += 64) {
+            uint4 y = v[x];
+            if (bad16(y.x) | bad16(y.y) | bad16(y.z) | bad16(y.w)) {
+              bad = true;
+              uint16_t* e = (uint16_t*)&v[x];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+            }
+          }
+          if (bad) {
+            s_bad[item & (kBadRing - 1)] = 1;
+            s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
+            __threadfence_block();
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_clean[slot]);
+        if (++slot == slots) { slot = 0; phase ^= 1u; }
+      }
+      ++item;
+      walk.next(w.cnt, piece, hkv);
+    }
+  } else {
+    const int q = (warp - 4) >> 2;  // query tile
+    const int quarter = warp & 3;   // TMEM lanes this warp reaches
+    const int trow = quarter * 32 + lane, r_in = q * 128 + trow;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t o_col = tmem + lanes + C::kOCol + (uint32_t)q * C::DP;
+    uint32_t item = 0, tiles = 0;
+    bool ok = true;
+    const __nv_bfloat16* Q = (const __nv_bfloat16*)a.q;
+    while (walk.len > 0 && walk.u < units && ok) {
+      const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
+      if (w.cnt == 0) { ++walk.u; continue; }
+      const int b = walk.u / p.row_tiles, h = walk.h, piece = min(walk.len, w.cnt - walk.k);
+      const bool live = r_in < w.rows;
+      const int pr = w.r0 + min(r_in, w.rows - 1), i = pr / G;
+      const int64_t row = (int64_t)(w.q0 + i) * a.hq + h * G + (pr - i * G);
+      const int low = a.window == 0 ? 0 : window_low(a.rows.positions ? __ldg(a.rows.positions + w.q0 + i) : w.ctx + i, a.window);
+      const uint8_t* mask_row = a.mask ? a.mask + ((int64_t)b * a.rows.max_q + i) * a.rows.max_q : nullptr;
+      // This row of Q, swizzled as the MMA reads it. The last scores of the item before are
+      // done: their S was waited for below.
+      {
+        const uint4* src = (const uint4*)(Q + row * a.D);
+        uint8_t* dst = sQ + (size_t)q * C::kQBytes + trow * 128;
+#pragma unroll
+        for (int x = 0; x < 8 * KB; ++x) {
+          uint4 y = make_uint4(0, 0, 0, 0);
+          if (live && x * 8 < a.D) y = src[x];
+          *(uint4*)(dst + (x >> 3) * (128 * 128) + (((x & 7) ^ (trow & 7)) << 4)) = y;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_ready[q]);
+      }
+      float m = -INFINITY, l = 0.0f;  // m: log2 units
+      for (int t = 0; t < piece; ++t, ++tiles) {
+        const int s0 = w.kt.slot(walk.k + t, kBN);
+        const uint32_t sb = NQ == 1 ? (tiles & 1u) : (uint32_t)q;
+        const uint32_t s_col = tmem + lanes + sb * 128;
+        ok = warp_wait(&s_ready[sb], NQ == 1 ? ((tiles >> 1) & 1u) : (tiles & 1u), s_abort, ctl, p.timeout_ns);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_col + 32 * c, s + 32 * c);
+        tmem_wait_ld();
+        if (!all_seen(a, w, s0)) {
+          uint32_t bits[4];
+          seen_bits(a, w, i, low, mask_row, s0, bits);
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(s[c]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.c;
+        const bool grow = live && mx > m + kLazy;  // from -inf: any finite maximum
+        bool o_free = t == 0;  // the product before this tile's is done
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = grow ? mx : m;
+          const float f = m == m_new || m == -INFINITY ? 1.0f : ex2(m - m_new);
+          m = m_new;
+          l *= f;
+          if (t > 0) {
+            o_free = true;
+            ok = warp_wait(&o_done[q], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < C::DP; c += 32) {
+              uint32_t o[32];
+              tmem_ld32_nowait(o_col + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_col + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float m_use = m == -INFINITY ? 0.0f : m;
+        const float2 c2 = make_float2(p.c, p.c), n2 = make_float2(-m_use, -m_use);
+        float2 sum2[2] = {make_float2(0, 0), make_float2(0, 0)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int e = half * 64 + 2 * c;
+            float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, n2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            pk[c] = pack_bf16(x.x, x.y);
+            sum2[c & 1] = add2(sum2[c & 1], x);
+          }
+          tmem_st32(s_col + 32 * half, pk);
+        }
+        l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        // Every phase of o_done is waited for: a wait for a later one would take an earlier
+        // one of the same parity for it.
+        if (!o_free) {
+          ok = warp_wait(&o_done[q], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+          if (!ok) break;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[sb]);
+      }
+      ok = ok && warp_wait(&o_done[q], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+      // The group goes on together or not at all: nobody is left at its barriers.
+      ok = group_all(1 + q, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const int bad_at = q * kBadRing + (int)(item & (kBadRing - 1));
+      const bool bad = s_bad[bad_at] != 0;
+
+      // Pieces of this row tile: CTA c holds list places [list c / ctas, list (c + 1) / ctas).
+      const int64_t first_x = walk.x - walk.k, last_x = first_x + w.cnt - 1;
+      const int c_first = (int)(((first_x + 1) * ctas - 1) / list), c_last = (int)(((last_x + 1) * ctas - 1) / list);
+      const int pieces = c_last - c_first + 1;
+      const int64_t mine_at = ((int64_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first ? 1 : 0)) * C::BMT + r_in;
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : NAN);
+#pragma unroll 1
+      for (int c = 0; c < C::DP; c += 32) {
+        uint32_t ou[32];
+        __syncwarp();
+        tmem_ld32_nowait(o_col + c, ou);
+        tmem_wait_ld();
+        if (!live) continue;
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ou[e]);
+        if (bad) add_non_finite(a, w, b, h, walk.k, walk.k + piece, i, low, mask_row, c, o);
+        if (pieces > 1) {
+          float4* dst = (float4*)(p.o + mine_at * C::DP + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else {
+          uint4* dst = (uint4*)((__nv_bfloat16*)a.out + row * a.D + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + 8 * e < a.D)
+              dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                  pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+        }
+      }
+      tc_fence_before();  // these reads of O before the next item's first product
+      if (pieces == 1) {
+        if (live && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        if (live) p.ml[mine_at] = make_float2(m, l);
+        __threadfence();
+      }
+      // The group's threads are done with O, s_bad and (when cut) their partial rows.
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+      if (trow == 0) {
+        s_bad[bad_at] = 0;
+        if (pieces > 1) {
+          // Every query tile of the row tile counts one arrival per piece.
+          const unsigned was = atomicAdd(p.arrived + c_first * NQ + q, 1u);
+          s_last[q] = was == (unsigned)pieces - 1u;
+          if (s_last[q]) p.arrived[c_first * NQ + q] = 0u;  // ready for the next call
+        }
+      }
+      if (pieces > 1) {
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+        if (s_last[q]) {
+          __threadfence();
+          // Columns of a row over neighbouring threads; the pieces in order.
+          const int rows_q = min(128, w.rows - q * 128);
+          for (int x = trow; x < rows_q * (C::DP / 4); x += 128) {
+            const int r = x / (C::DP / 4), e = (x - r * (C::DP / 4)) * 4;
+            auto at = [&](int pc) {
+              return ((int64_t)(c_first + pc) * 2 + (pc == 0 ? 1 : 0)) * C::BMT + q * 128 + r;
+            };
+            float mm = -INFINITY, ll = 0.0f;
+            for (int pc = 0; pc < pieces; ++pc) mm = fmaxf(mm, __ldcg(&p.ml[at(pc)]).x);
+            float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int pc = 0; pc < pieces; ++pc) {
+              const float2 v = __ldcg(&p.ml[at(pc)]);
+              const float4 y = __ldcg((const float4*)(p.o + at(pc) * C::DP + e));
+              if (v.x == -INFINITY) continue;  // saw nothing: its sums are zeros
+              const float f = v.x == mm ? 1.0f : ex2(v.x - mm);
+              ll += v.y * f;
+              acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
+            }
+            const int prr = w.r0 + q * 128 + r, ii = prr / G;
+            const int64_t orow = (int64_t)(w.q0 + ii) * a.hq + h * G + (prr - ii * G);
+            const float iv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN);
+            if (e < a.D)
+              *(uint2*)((__nv_bfloat16*)a.out + orow * a.D + e) =
+                  make_uint2(pack_bf16(acc.x * iv, acc.y * iv), pack_bf16(acc.z * iv, acc.w * iv));
+            if (e == 0 && a.lse) a.lse[orow] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+          }
+        }
+      }
+      ++item;
+      walk.next(w.cnt, piece, hkv);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (EncodeTiledFn)ptr;
+  });
+  return fn;
+}
+
+// The cache as {head_dim, slot, kv head, request}, boxes of 64 x 128 slots. An axis of one
+// entry gets any valid stride. Elements past head_dim read as zero.
+bool make_tmap(CUtensorMap* tm, const void* base, const AttnArgs& a) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.rows.capacity, (cuuint64_t)a.hkv, (cuuint64_t)a.rows.batch};
+  const int64_t st[3] = {a.ss, a.hs, a.rs};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] == 1 ? (cuuint64_t)((a.D * 2 + 15) / 16 * 16) : (cuuint64_t)(st[i] * 2);
+  cuuint32_t box[4] = {64, (cuuint32_t)kBN, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kArrivedBytes = 4096;
+
+template <int NQ, int KB>
+cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
+  using C = Cfg<NQ, KB>;
+  TcAttnP p;
+  memset(&p, 0, sizeof(p));
+  if (!make_tmap(&p.tmK, a.k, a) || !make_tmap(&p.tmV, a.v, a)) return cudaErrorInvalidValue;
+  p.a = a;
+  p.row_tiles = (int)(((int64_t)a.rows.max_q * (a.hq / a.hkv) + C::BMT - 1) / C::BMT);
+  p.timeout_ns = wait_timeout_ns();
+  // A scale of 0 still has to leave a masked score at -inf.
+  p.c = fmaxf(a.scale * kLog2e, 1e-30f);
+  const uint32_t budget = 227 * 1024 - 2048;
+  int slots = (int)((budget - NQ * C::kQBytes) / C::kTile);
+  // Even: a buffer is always a key or always a value buffer, so every phase of a value
+  // buffer is waited for by those who clear it.
+  p.slots = slots > 12 ? 12 : slots & ~1;
+  const size_t smem = 1024 + (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + 1024;
+  const int grid = num_sms();
+  if ((size_t)grid * NQ * 4 > kArrivedBytes || (int64_t)a.rows.batch * p.row_tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
+  uint8_t* w = (uint8_t*)a.scratch;
+  p.arrived = (unsigned int*)w;
+  p.ml = (float2*)(w + kArrivedBytes);
+  p.o = (float*)(w + kArrivedBytes + (size_t)2 * grid * C::BMT * 8);
+  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NQ, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  attn_tc_kernel<NQ, KB><<<grid, C::kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_tc_ws_bytes(const AttnArgs& a) {
+  const size_t dp = a.D > 64 ? 128 : 64;
+  return kArrivedBytes + (size_t)2 * num_sms() * 256 * (8 + dp * 4);
+}
+
+// bf16, head_dim <= 128, and a cache that a tensor map can describe: no axis of more than
+// one entry with a stride of 0 (requests that share a cache), strides below 2^40 bytes.
+bool attn_tc_applies(const AttnArgs& a) {
+  if (a.dtype != DOMINO_BF16 || a.D > 128) return false;
+  const int64_t st[3] = {a.ss, a.hs, a.rs};
+  const int n[3] = {a.rows.capacity, a.hkv, a.rows.batch};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (st[i] == 0 || st[i] * 2 >= ((int64_t)1 << 40))) return false;
+  return true;
+}
+
+cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t stream) {
+  const bool wide = a.D > 64;
+  if ((int64_t)a.rows.max_q * (a.hq / a.hkv) > 128) return wide ? launch_tc<2, 2>(a, stream) : launch_tc<2, 1>(a, stream);
+  return wide ? launch_tc<1, 2>(a, stream) : launch_tc<1, 1>(a, stream);
+}
+
+}  // namespace domino

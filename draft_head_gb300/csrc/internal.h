@@ -206,6 +206,10 @@ struct AttnArgs {
 };
 size_t attn_ws_bytes(const AttnArgs& a);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
+// On the tensor cores: bf16, head_dim <= 128.
+bool attn_tc_applies(const AttnArgs& a);
+size_t attn_tc_ws_bytes(const AttnArgs& a);
+cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t stream);
 
 struct SampleArgs {
   int dtype, rows, V;

@@ -396,6 +396,39 @@ def test_long_cache_offsets_pass_32_bits():
     assert bool((out[:8] == 0).all())
 
 
+@pytest.mark.parametrize("dt,rows,ctx,hq,hkv,D,mode,window,sinks", [
+    (BF, [16] * 48, [1200] * 47 + [40], 16, 4, 128, "full", 1000, 4),      # many requests: several key tiles per CTA
+    (BF, [1] * 200, [300] * 200, 8, 4, 64, "causal", 0, 0),                # several row tiles per CTA
+    (BF, [2500, 1300], [0, 700], 8, 4, 128, "causal", 600, 130),           # prompts, two query tiles
+    (BF, [2500], [100], 8, 4, 64, "causal", 0, 0),
+    (F32, [300, 40], [0, 500], 4, 2, 128, "causal", 200, 3)])
+def test_many_tiles_per_cta(dt, rows, ctx, hq, hkv, D, mode, window, sinks):
+    g = gen(17)
+    st, cap = starts(rows), max(r + c for r, c in zip(rows, ctx))
+    k, v = cache_pair(g, dt, len(rows), hkv, cap, D)
+    q = (2 * randn(g, st[-1], hq, D)).to(dt)
+    p = BlockAttention(k, v, hq, st[-1], max(rows), max(ctx), window=window, sinks=sinks)
+    for _ in range(3):
+        out, lse = p.attend(q, ints(ctx), q_start=ints(st), mask=mode, want_lse=True)
+    assert p.last_status() == 0
+    h = H if dt == BF else 0.0
+    for r, (n, c) in enumerate(zip(rows, ctx)):
+        s, i = torch.arange(c + n, device="cuda")[None], torch.arange(n, device="cuda")[:, None]
+        seen = (s < sinks) | (s > c + i - window) if window else torch.ones(n, c + n, dtype=torch.bool, device="cuda")
+        seen = (seen & (s <= c + i)) if mode == "causal" else seen | (s >= c)
+        kk, vv = k[r, :, :c + n].to(O.F64), v[r, :, :c + n].to(O.F64)
+        for hh in range(hq):
+            x = q[st[r]:st[r + 1], hh].to(O.F64)
+            score = torch.where(seen, (x @ kk[hh * hkv // hq].T) * p.scale, -math.inf)
+            big = float((x.abs() @ kk[hh * hkv // hq].abs().T).max()) * p.scale
+            w = torch.softmax(score, 1)
+            e = (D + 4) * U * big + 2.0 ** -21
+            want = w @ vv[hh * hkv // hq]
+            tol = (2 * e + (c + n) * U + h) * (w @ vv[hh * hkv // hq].abs()) + 1.01 * h * want.abs()
+            assert bool(((out[st[r]:st[r + 1], hh].to(O.F64) - want).abs() <= tol).all()), (r, hh)
+            assert bool(((lse[st[r]:st[r + 1], hh].to(O.F64) - torch.logsumexp(score, 1)).abs() <= 2 * e + (c + n) * U).all())
+
+
 # ---------------------------------------------------------------------------
 # The draw.
 # ---------------------------------------------------------------------------
