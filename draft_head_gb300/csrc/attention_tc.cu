@@ -10,21 +10,23 @@
 // when a row's maximum has grown by more than 2^8 since the last time (P then stays
 // below 2^8, and l and O carry the same factor), which after the first tiles is rare.
 //
-//   warp 0       TMA: key and value tiles into one ring of 32 KB buffers
+//   warp 0       TMA: key and value tiles into one ring of buffers
 //   warp 1       TMEM, and one thread issues the MMAs
 //   warps 2, 3   clear non-finite values of tiles that some row does not see
-//   warps 4 ..   softmax and epilogue, four warps per query tile
+//   warps 4-7, 8-11  two groups of 128 threads: softmax and epilogue
 //
-// NQ = 1 (few rows: one token, a draft block, a tree): bound by the cache's bytes;
-// two S buffers, so the next tile's scores are computed under this tile's softmax.
-// NQ = 2 (prompts): bound by the MMAs and the exponentials; the two query tiles share
-// the key and value loads and take turns: one's MMAs run under the other's softmax.
+// NQ = 2 (prompts): bound by the exponentials and the MMAs. Each group has a query tile of
+// its own; both read the same key and value buffers and take turns: one's MMAs run under the
+// other's softmax.
+// NQ = 1 (few rows: one token, a draft block, a tree): bound by the cache's bytes. The groups
+// take the key tiles of one query tile in turn, each with its own maximum, sum and O, which the
+// epilogue joins.
 //
-// The work is the list of all (request, row tile, kv head, key tile), cut into equal
-// pieces, one per CTA of a grid of one CTA per SM; lengths live on the device, so every
-// CTA counts the list itself. A row tile cut over CTAs is joined by the last of them to
-// finish, in piece order, from fp32 sums in the workspace: the result does not depend on
-// the order of arrival.
+// The work is the list of all (request, row tile, kv head, key tile), cut into equal pieces, one
+// per CTA of a grid of one CTA per SM; lengths live on the device, so every CTA counts the list
+// itself. Every (request, row tile, kv head) counts kItem key tiles more, about what its start and
+// its epilogue cost. A row tile cut over CTAs is joined by the last of them to finish, in piece
+// order, from fp32 sums in the workspace: the result does not depend on the order of arrival.
 #include <cuda.h>
 #include <math.h>
 #include <string.h>
@@ -40,7 +42,7 @@ constexpr int kBN = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // growth of the maximum (log2) that forces a rescale of O
-constexpr int kLeast = 1;      // key tiles per CTA, at least
+constexpr int kItem = 2;       // list places of a row tile beside its key tiles
 constexpr int kBadRing = 8;    // items the roles may be apart, at most (the ring holds fewer tiles)
 
 struct TcAttnP {
@@ -52,7 +54,7 @@ struct TcAttnP {
   float c;        // scale log2(e)
   unsigned int* arrived;  // per CTA: pieces in, of the row tile that begins in it and goes on
   float2* ml;             // [2 grid][128 NQ]
-  float* o;               // [2 grid][128 NQ][DP]
+  float4* o;              // [2 grid][NQ][DP / 4][128]: four columns of a row, rows next to each other
 };
 
 // A row tile of one request: its rows and the slots they see. `cnt` is 0 when there
@@ -103,13 +105,14 @@ __device__ __forceinline__ bool all_seen(const AttnArgs& a, const Unit& w, int s
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* s_abort, Ctl* ctl, uint64_t timeout_ns) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, s_abort, ctl, timeout_ns));
 }
-// Barrier of 128 threads that tells all of them whether every one was `ok`.
+// Barrier of N threads that tells all of them whether every one was `ok`.
+template <int N>
 __device__ __forceinline__ bool group_all(int id, bool ok) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.and.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.and.pred q, %1, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(id), "r"((uint32_t)ok)
+      : "r"(id), "r"((uint32_t)ok), "n"(N)
       : "memory");
   return r != 0;
 }
@@ -117,12 +120,18 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
 // The CTA's part of the work list, walked by every role alike.
 struct Walk {
   int u, h, k, len;
-  int64_t x;  // place of the next key tile in the list
-  __device__ __forceinline__ void next(int cnt, int piece, int hkv) {
+  int64_t x;  // place in the list
+  // Key tiles [k0, k1) of the row tile are the CTA's (may be none).
+  __device__ __forceinline__ void part(int cnt, int& k0, int& k1) const {
+    k0 = max(0, k - kItem);
+    k1 = max(0, k + min(len, cnt + kItem - k) - kItem);
+  }
+  __device__ __forceinline__ void next(int cnt, int hkv) {
+    const int piece = min(len, cnt + kItem - k);
     len -= piece;
     x += piece;
     k += piece;
-    if (k == cnt) {
+    if (k == cnt + kItem) {
       k = 0;
       if (++h == hkv) {
         h = 0;
@@ -160,6 +169,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -256,14 +270,14 @@ template <int NQ, int KB>
 struct Cfg {
   static constexpr int DP = 64 * KB;
   static constexpr int BMT = 128 * NQ;
-  static constexpr int kThreads = 128 + 128 * NQ;
-  static constexpr uint32_t kTile = (uint32_t)KB * kBN * 128;      // bytes of a key or value tile
-  static constexpr uint32_t kQBytes = (uint32_t)KB * 128 * 128;    // bytes of a query tile
-  static constexpr uint32_t kOCol = 256;                           // S: 128 columns each, then O
+  static constexpr uint32_t kTile = (uint32_t)KB * kBN * 128;    // bytes of a key or value tile
+  static constexpr uint32_t kQBytes = (uint32_t)KB * 128 * 128;  // bytes of a query tile
 };
+constexpr int kThreads = 384;
+constexpr uint32_t kOCol = 256;  // TMEM: S of group g at 128 g, O of group g at kOCol + DP g
 
 template <int NQ, int KB>
-__global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnP p) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnP p) {
   using C = Cfg<NQ, KB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -272,20 +286,20 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
   const int slots = p.slots;
   uint64_t* full = (uint64_t*)(ring + (size_t)slots * C::kTile);
   uint64_t* empty = full + slots;
-  uint64_t* s_ready = empty + slots;  // [2]: per query tile (NQ = 2) or per S buffer (NQ = 1)
-  uint64_t* p_ready = s_ready + 2;    // [2] likewise
-  uint64_t* o_done = p_ready + 2;     // [NQ]
-  uint64_t* q_ready = o_done + 2;     // [NQ]
-  uint64_t* v_clean = q_ready + 2;    // [slots]
-  uint64_t* drain = v_clean + slots;
-  int64_t* s_total = (int64_t*)(drain + 1);
-  int64_t* s_prefix = s_total + 1;
-  int* s_unit = (int*)(s_prefix + 1);
-  int* s_last = s_unit + 1;           // [NQ]
-  volatile int* s_bad = s_last + 2;   // [2][kBadRing]
+  uint64_t* v_clean = empty + slots;
+  uint64_t* s_ready = v_clean + slots;  // [2]: per group
+  uint64_t* p_ready = s_ready + 2;      // [2]
+  uint64_t* o_done = p_ready + 2;       // [2]
+  uint64_t* q_ready = o_done + 2;       // [2]: per query tile
+  uint64_t* drain = q_ready + 2;
+  int64_t* s_prefix = (int64_t*)(drain + 1);
+  int64_t* s_scan = s_prefix + 1;       // [kThreads / 32]
+  float2* s_ml = (float2*)(s_scan + kThreads / 32);  // [2][128] NQ = 1: the groups' (m, l)
+  int* s_unit = (int*)(s_ml + 256);
+  int* s_last = s_unit + 1;             // [2]
+  volatile int* s_bad = s_last + 2;     // [2][kBadRing]
   uint32_t* tmem_slot = (uint32_t*)(s_last + 2 + 2 * kBadRing);
   volatile int* s_abort = (volatile int*)(tmem_slot + 1);
-  int64_t* s_scan = (int64_t*)(((uintptr_t)(tmem_slot + 2) + 7) & ~(uintptr_t)7);  // [kThreads / 32]
 
   const AttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -302,7 +316,7 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
       mbar_init(&s_ready[s], 1);
       mbar_init(&p_ready[s], 4);
       mbar_init(&o_done[s], 1);
-      mbar_init(&q_ready[s], 4);
+      mbar_init(&q_ready[s], NQ == 1 ? 8 : 4);
     }
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -316,13 +330,14 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
     tmem_relinquish();
   }
 
-  // Count the work list (key tiles of one kv head) and find this CTA's part of it.
+  // Count the work list (places of one kv head) and find this CTA's part of it.
+  auto places = [](const Unit& w) { return w.cnt > 0 ? w.cnt + kItem : 0; };
   const int units = a.rows.batch * p.row_tiles;
-  const int chunk = (units + C::kThreads - 1) / C::kThreads;
+  const int chunk = (units + kThreads - 1) / kThreads;
   const int u_begin = min(units, (int)threadIdx.x * chunk), u_end = min(units, u_begin + chunk);
   int64_t mine = 0;
   for (int u = u_begin; u < u_end; ++u)
-    mine += load_unit<C::BMT>(a, p.row_tiles, u, blockIdx.x == 0 && u % p.row_tiles == 0).cnt;
+    mine += places(load_unit<C::BMT>(a, p.row_tiles, u, blockIdx.x == 0 && u % p.row_tiles == 0));
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -336,21 +351,21 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
   const uint32_t tmem = *tmem_slot;
   int64_t before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < C::kThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     const int64_t s = s_scan[w];
     before += w < warp ? s : 0;
     total += s;
   }
   before += incl - mine;
   const int64_t list = total * hkv;
-  // CTAs with work: no more than key tiles, so that none of them is empty.
-  const int ctas = (int)min((int64_t)gridDim.x, list / kLeast > 0 ? list / kLeast : 1);
+  // CTAs with work: no more than places, so that none of them is empty.
+  const int ctas = (int)min((int64_t)gridDim.x, max(list, (int64_t)1));
   const bool idle = (int)blockIdx.x >= ctas || list == 0;
   const int64_t x0 = idle ? 0 : list * blockIdx.x / ctas, x1 = idle ? 0 : list * (blockIdx.x + 1) / ctas;
   if (!idle && mine > 0 && before <= x0 / hkv && x0 / hkv < before + mine) {
     int64_t at = before;
     for (int u = u_begin; u < u_end; ++u) {
-      const int c = load_unit<C::BMT>(a, p.row_tiles, u, false).cnt;
+      const int c = places(load_unit<C::BMT>(a, p.row_tiles, u, false));
       if (x0 < (at + c) * hkv) {
         *s_unit = u;
         *s_prefix = at;
@@ -366,14 +381,17 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
   walk.u = 0; walk.h = 0; walk.k = 0;
   if (walk.len > 0) {
     walk.u = *s_unit;
-    const int cnt = load_unit<C::BMT>(a, p.row_tiles, walk.u, false).cnt;
+    const int c = places(load_unit<C::BMT>(a, p.row_tiles, walk.u, false));
     const int64_t in = x0 - *s_prefix * hkv;
-    walk.h = (int)(in / cnt);
-    walk.k = (int)(in - (int64_t)walk.h * cnt);
+    walk.h = (int)(in / c);
+    walk.k = (int)(in - (int64_t)walk.h * c);
   }
 
-  if (warp == 0) {
-    if (lane == 0) {
+  // Registers: launched with 168 a thread; 4 warps keep 88, 8 warps take 208
+  // (128 x 88 + 256 x 208 = 64512 = 384 x 168).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0 && lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
       const bool once = p.row_tiles == 1;  // no other row tile reads this cache again
       int slot = 0;
@@ -383,8 +401,10 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
       while (walk.len > 0 && walk.u < units && ok) {
         const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
         if (w.cnt == 0) { ++walk.u; continue; }
-        const int b = walk.u / p.row_tiles, piece = min(walk.len, w.cnt - walk.k);
-        for (int k = walk.k; k < walk.k + piece && ok; ++k) {
+        const int b = walk.u / p.row_tiles;
+        int k0, k1;
+        walk.part(w.cnt, k0, k1);
+        for (int k = k0; k < k1 && ok; ++k) {
           const int s0 = w.kt.slot(k, kBN);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
@@ -398,125 +418,132 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
             if (++slot == slots) { slot = 0; phase ^= 1u; }
           }
         }
-        walk.next(w.cnt, piece, hkv);
+        walk.next(w.cnt, hkv);
       }
       if (!ok) {
         // Give up, but first let the copies already in flight land.
         for (long j = issued - 1; j >= 0 && j >= issued - slots; --j)
           mbar_wait(&full[j % slots], (uint32_t)((j / slots) & 1), nullptr, ctl, p.timeout_ns);
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       const uint32_t id_s = idesc_bf16_f32(128, kBN);
       const uint32_t id_o = idesc_bf16_f32(128, C::DP) | (1u << 16);  // B is MN-major
-      int slot = 0;
-      uint32_t phase = 0;
-      uint32_t item = 0, tiles = 0;
+      uint32_t item = 0, done[2] = {0, 0};  // key tiles each group has had
       bool ok = true;
+      // The ring holds K_0, V_0, K_1, V_1, ...; two cursors over it.
+      int ks = 0, vs = 1;
+      uint32_t kph = 0, vph = 0;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok && !mbar_wait(bar, parity, s_abort, ctl, p.timeout_ns)) ok = false;
         tc_fence_after();
       };
-      auto advance = [&](int& s, uint32_t& ph) {
-        if (++s == slots) { s = 0; ph ^= 1u; }
+      auto step = [&](int& s, uint32_t& ph) {
+        s += 2;
+        if (s >= slots) { s -= slots; ph ^= 1u; }
       };
-      auto scores = [&](int qt, uint32_t d, int s) {  // S = Q K^T
+      auto scores = [&](int qt, int g) {  // S_g = Q K^T
         const uint64_t ad = sdesc_k_sw128(smem_u32(sQ + (size_t)qt * C::kQBytes));
-        const uint64_t bd = sdesc_k_sw128(smem_u32(ring + (size_t)s * C::kTile));
+        const uint64_t bd = sdesc_k_sw128(smem_u32(ring + (size_t)ks * C::kTile));
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_bf16(tmem + d, ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k), bd + (uint64_t)(kb * (kBN * 128 / 16) + 2 * k),
-                      id_s, (kb | k) ? 1u : 0u);
+            umma_bf16(tmem + (uint32_t)(g * 128), ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k),
+                      bd + (uint64_t)(kb * (kBN * 128 / 16) + 2 * k), id_s, (kb | k) ? 1u : 0u);
+        umma_commit(&s_ready[g]);
       };
-      auto values = [&](uint32_t d, uint32_t pcol, int s, bool first) {  // O += P V
-        const uint64_t bd = sdesc_mn_sw128(smem_u32(ring + (size_t)s * C::kTile));
+      auto values = [&](int g, bool first) {  // O_g += P_g V
+        const uint64_t bd = sdesc_mn_sw128(smem_u32(ring + (size_t)vs * C::kTile));
 #pragma unroll
         for (int k = 0; k < kBN / 16; ++k)
-          umma_bf16_ts(tmem + d, tmem + pcol + (uint32_t)(8 * k), bd + (uint64_t)(k * (16 * 128 / 16)), id_o,
-                       (first && k == 0) ? 0u : 1u);
+          umma_bf16_ts(tmem + kOCol + (uint32_t)(g * C::DP), tmem + (uint32_t)(g * 128 + 8 * k),
+                       bd + (uint64_t)(k * (16 * 128 / 16)), id_o, (first && k == 0) ? 0u : 1u);
+        umma_commit(&o_done[g]);
       };
       while (walk.len > 0 && walk.u < units && ok) {
         const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
         if (w.cnt == 0) { ++walk.u; continue; }
-        const int piece = min(walk.len, w.cnt - walk.k);
-        // The ring holds K_0, V_0, K_1, V_1, ...; ks / vs are the places of the next of each.
-        int ks = slot, vs = slot;
-        uint32_t kph = phase, vph = phase;
-        advance(vs, vph);
-        auto next2 = [&](int& s, uint32_t& ph) { advance(s, ph); advance(s, ph); };
-        wait(&full[ks], kph);
+        int k0, k1;
+        walk.part(w.cnt, k0, k1);
+        walk.next(w.cnt, hkv);
+        const int n = k1 - k0;
+        if (n == 0) continue;
+        if (NQ == 2) {
+          wait(&full[ks], kph);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          wait(&q_ready[q], item & 1u);
-          if (!ok) break;
-          const uint32_t sb = NQ == 1 ? (tiles & 1u) : (uint32_t)q;
-          scores(q, sb * 128, ks);
-          umma_commit(&s_ready[sb]);
-        }
-        if (!ok) break;
-        umma_commit(&empty[ks]);
-        next2(ks, kph);
-        for (int t = 0; t < piece && ok; ++t, ++tiles) {
-          const bool more = t + 1 < piece;
-          if (NQ == 1 && more) {
-            wait(&full[ks], kph);
-            if (!ok) break;
-            scores(0, ((tiles + 1) & 1u) * 128, ks);
-            umma_commit(&s_ready[(tiles + 1) & 1u]);
-            umma_commit(&empty[ks]);
-            next2(ks, kph);
+          for (int g = 0; g < 2; ++g) {
+            wait(&q_ready[g], item & 1u);
+            if (ok) scores(g, g);
           }
-          wait(&full[vs], vph);
-          wait(&v_clean[vs], vph);
+          if (!ok) break;
+          umma_commit(&empty[ks]);
+          step(ks, kph);
+          for (int t = 0; t < n && ok; ++t) {
+            const bool more = t + 1 < n;
+            wait(&v_clean[vs], vph);
+            wait(&full[vs], vph);
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const uint32_t sb = NQ == 1 ? (tiles & 1u) : (uint32_t)q;
-            wait(&p_ready[sb], NQ == 1 ? ((tiles >> 1) & 1u) : (tiles & 1u));
+            for (int g = 0; g < 2; ++g) {
+              wait(&p_ready[g], done[g]++ & 1u);
+              if (ok) values(g, t == 0);
+              if (more) {
+                if (g == 0) wait(&full[ks], kph);
+                if (ok) scores(g, g);
+              }
+            }
             if (!ok) break;
-            values(C::kOCol + (uint32_t)q * C::DP, sb * 128, vs, t == 0);
-            umma_commit(&o_done[q]);
-            if (NQ == 2 && more) {
-              if (q == 0) wait(&full[ks], kph);
-              if (!ok) break;
-              scores(q, sb * 128, ks);
-              umma_commit(&s_ready[sb]);
+            umma_commit(&empty[vs]);
+            step(vs, vph);
+            if (more) {
+              umma_commit(&empty[ks]);
+              step(ks, kph);
             }
           }
-          if (!ok) break;
-          umma_commit(&empty[vs]);
-          next2(vs, vph);
-          if (NQ == 2 && more) {
-            umma_commit(&empty[ks]);
-            next2(ks, kph);
+        } else {
+          wait(&q_ready[0], item & 1u);
+          for (int t = 0; t < n + 2 && ok; ++t) {
+            // Tile t's scores go out once tile t - 2, the one before it in its S, is done.
+            if (t >= 2) {
+              const int g = t & 1;
+              wait(&v_clean[vs], vph);
+              wait(&full[vs], vph);
+              wait(&p_ready[g], done[g]++ & 1u);
+              if (!ok) break;
+              values(g, t < 4);
+              umma_commit(&empty[vs]);
+              step(vs, vph);
+            }
+            if (t < n) {
+              wait(&full[ks], kph);
+              if (!ok) break;
+              scores(0, t & 1);
+              umma_commit(&empty[ks]);
+              step(ks, kph);
+            }
           }
         }
-        slot = ks;
-        phase = kph;
         ++item;
-        walk.next(w.cnt, piece, hkv);
       }
       // Every MMA issued above has finished before TMEM is freed.
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr, ctl, p.timeout_ns);
-    }
-  } else if (warp < 4) {
+    } else if (warp >= 2) {
     // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
     // or a NaN in the product, so these are cleared here and the row tile is marked.
     const int t64 = threadIdx.x - 64;
-    int slot = 0;
+    int slot = 1;
     uint32_t phase = 0, item = 0;
     bool ok = true;
     while (walk.len > 0 && walk.u < units && ok) {
       const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
       if (w.cnt == 0) { ++walk.u; continue; }
-      const int piece = min(walk.len, w.cnt - walk.k);
-      for (int t = 0; t < piece; ++t) {
-        if (++slot == slots) { slot = 0; phase ^= 1u; }  // past the key tile
+      int k0, k1;
+      walk.part(w.cnt, k0, k1);
+      walk.next(w.cnt, hkv);
+      if (k0 == k1) continue;
+      for (int k = k0; k < k1; ++k) {
         if (!mbar_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
-        if (!all_seen(a, w, w.kt.slot(walk.k + t, kBN))) {
+        if (!all_seen(a, w, w.kt.slot(k, kBN))) {
           uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
           bool bad = false;
 #pragma unroll 8
@@ -539,50 +566,66 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_clean[slot]);
-        if (++slot == slots) { slot = 0; phase ^= 1u; }
+        slot += 2;
+        if (slot >= slots) { slot -= slots; phase ^= 1u; }
       }
       ++item;
-      walk.next(w.cnt, piece, hkv);
+    }
     }
   } else {
-    const int q = (warp - 4) >> 2;  // query tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int g = (warp - 4) >> 2;  // group
     const int quarter = warp & 3;   // TMEM lanes this warp reaches
-    const int trow = quarter * 32 + lane, r_in = q * 128 + trow;
+    const int trow = quarter * 32 + lane, r_in = (NQ == 2 ? g * 128 : 0) + trow;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t o_col = tmem + lanes + C::kOCol + (uint32_t)q * C::DP;
+    const uint32_t s_col = tmem + lanes + (uint32_t)(g * 128);
+    const uint32_t o_col = tmem + lanes + kOCol + (uint32_t)(g * C::DP);
+    uint8_t* q_tile = sQ + (NQ == 2 ? (size_t)g * C::kQBytes : 0);
+    // 16-byte chunk x of row r of the query tile, swizzled as the MMA reads it.
+    auto chunk_at = [&](int r, int x) { return q_tile + (x >> 3) * (128 * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4); };
     uint32_t item = 0, tiles = 0;
     bool ok = true;
-    const __nv_bfloat16* Q = (const __nv_bfloat16*)a.q;
     while (walk.len > 0 && walk.u < units && ok) {
       const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
       if (w.cnt == 0) { ++walk.u; continue; }
-      const int b = walk.u / p.row_tiles, h = walk.h, piece = min(walk.len, w.cnt - walk.k);
+      const int b = walk.u / p.row_tiles, h = walk.h;
+      const int64_t first_x = walk.x - walk.k + kItem, last_x = first_x + w.cnt - 1;
+      int k0, k1;
+      walk.part(w.cnt, k0, k1);
+      walk.next(w.cnt, hkv);
+      if (k0 == k1) continue;
       const bool live = r_in < w.rows;
       const int pr = w.r0 + min(r_in, w.rows - 1), i = pr / G;
       const int64_t row = (int64_t)(w.q0 + i) * a.hq + h * G + (pr - i * G);
-      const int low = a.window == 0 ? 0 : window_low(a.rows.positions ? __ldg(a.rows.positions + w.q0 + i) : w.ctx + i, a.window);
-      const uint8_t* mask_row = a.mask ? a.mask + ((int64_t)b * a.rows.max_q + i) * a.rows.max_q : nullptr;
-      // This row of Q, swizzled as the MMA reads it. The last scores of the item before are
-      // done: their S was waited for below.
+      // The query tile, coalesced: neighbouring lanes take the chunks of a row. The last scores
+      // of the item before are done: the products after them were waited for.
       {
-        const uint4* src = (const uint4*)(Q + row * a.D);
-        uint8_t* dst = sQ + (size_t)q * C::kQBytes + trow * 128;
+        constexpr int kPer = 32 / (8 * KB);  // rows per load of the warp
+        constexpr int kRows = NQ == 2 ? 32 : 16;
+        const int x = lane & (8 * KB - 1), rr = lane / (8 * KB);
+        uint4 y[kRows / kPer];
+        const int base = NQ == 2 ? quarter * 32 : quarter * 32 + g * 16;
 #pragma unroll
-        for (int x = 0; x < 8 * KB; ++x) {
-          uint4 y = make_uint4(0, 0, 0, 0);
-          if (live && x * 8 < a.D) y = src[x];
-          *(uint4*)(dst + (x >> 3) * (128 * 128) + (((x & 7) ^ (trow & 7)) << 4)) = y;
+        for (int j = 0; j < kRows / kPer; ++j) {
+          const int r = base + j * kPer + rr;
+          const int64_t row_r = __shfl_sync(0xffffffffu, row, r & 31);
+          y[j] = make_uint4(0, 0, 0, 0);
+          if ((NQ == 2 ? g * 128 : 0) + r < w.rows && x * 8 < a.D)
+            y[j] = *(const uint4*)((const __nv_bfloat16*)a.q + row_r * a.D + x * 8);
         }
+#pragma unroll
+        for (int j = 0; j < kRows / kPer; ++j) *(uint4*)chunk_at(base + j * kPer + rr, x) = y[j];
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_ready[q]);
+        if (lane == 0) mbar_arrive(&q_ready[NQ == 2 ? g : 0]);
       }
+      const int low = a.window == 0 ? 0 : window_low(a.rows.positions ? __ldg(a.rows.positions + w.q0 + i) : w.ctx + i, a.window);
+      const uint8_t* mask_row = a.mask ? a.mask + ((int64_t)b * a.rows.max_q + i) * a.rows.max_q : nullptr;
       float m = -INFINITY, l = 0.0f;  // m: log2 units
-      for (int t = 0; t < piece; ++t, ++tiles) {
-        const int s0 = w.kt.slot(walk.k + t, kBN);
-        const uint32_t sb = NQ == 1 ? (tiles & 1u) : (uint32_t)q;
-        const uint32_t s_col = tmem + lanes + sb * 128;
-        ok = warp_wait(&s_ready[sb], NQ == 1 ? ((tiles >> 1) & 1u) : (tiles & 1u), s_abort, ctl, p.timeout_ns);
+      bool first = true;
+      for (int k = NQ == 2 ? k0 : k0 + g; k < k1; k += NQ == 2 ? 1 : 2, ++tiles, first = false) {
+        const int s0 = w.kt.slot(k, kBN);
+        ok = warp_wait(&s_ready[g], tiles & 1u, s_abort, ctl, p.timeout_ns);
         if (!ok) break;
         tc_fence_after();
         uint32_t s[128];
@@ -596,20 +639,26 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
           for (int c = 0; c < 128; ++c)
             if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
         }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float m4[4];
 #pragma unroll
-        for (int c = 0; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(s[c]));
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.c;
+        for (int c = 0; c < 4; ++c) m4[c] = max3(__uint_as_float(s[c]), __uint_as_float(s[c + 4]), __uint_as_float(s[c + 8]));
+#pragma unroll
+        for (int c = 12; c < 124; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(s[124 + e]));
+        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * p.c;
         const bool grow = live && mx > m + kLazy;  // from -inf: any finite maximum
-        bool o_free = t == 0;  // the product before this tile's is done
+        bool o_free = first;                       // the group's product before this tile's is done
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? mx : m;
           const float f = m == m_new || m == -INFINITY ? 1.0f : ex2(m - m_new);
           m = m_new;
           l *= f;
-          if (t > 0) {
+          if (!first) {
             o_free = true;
-            ok = warp_wait(&o_done[q], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+            ok = warp_wait(&o_done[g], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -647,103 +696,146 @@ __global__ void __launch_bounds__(Cfg<NQ, KB>::kThreads, 1) attn_tc_kernel(const
         // Every phase of o_done is waited for: a wait for a later one would take an earlier
         // one of the same parity for it.
         if (!o_free) {
-          ok = warp_wait(&o_done[q], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+          ok = warp_wait(&o_done[g], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
           if (!ok) break;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[sb]);
+        if (lane == 0) mbar_arrive(&p_ready[g]);
       }
-      ok = ok && warp_wait(&o_done[q], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
-      // The group goes on together or not at all: nobody is left at its barriers.
-      ok = group_all(1 + q, ok);
+      if (ok && !first) ok = warp_wait(&o_done[g], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+      // Whoever shares the epilogue goes on together or not at all: nobody is left at a barrier.
+      if (NQ == 1) s_ml[g * 128 + trow] = make_float2(m, l);
+      ok = NQ == 1 ? group_all<256>(1, ok) : group_all<128>(1 + g, ok);
       if (!ok) break;
       tc_fence_after();
-      const int bad_at = q * kBadRing + (int)(item & (kBadRing - 1));
+      const int bad_at = g * kBadRing + (int)(item & (kBadRing - 1));
       const bool bad = s_bad[bad_at] != 0;
 
-      // Pieces of this row tile: CTA c holds list places [list c / ctas, list (c + 1) / ctas).
-      const int64_t first_x = walk.x - walk.k, last_x = first_x + w.cnt - 1;
+      // NQ = 1: the two groups' results are one; each group takes half of the columns of both O.
+      float f0 = 1.0f, f1 = 0.0f;
+      if (NQ == 1) {
+        const float2 x = s_ml[trow], y = s_ml[128 + trow];
+        m = fmaxf(x.x, y.x);
+        f0 = x.x == m ? 1.0f : ex2(x.x - m);
+        f1 = y.x == -INFINITY ? 0.0f : y.x == m ? 1.0f : ex2(y.x - m);
+        l = x.y * f0 + (f1 != 0.0f ? y.y * f1 : 0.0f);
+      }
+      const bool two = NQ == 1 && k1 - k0 > 1;  // the second O has been written
+      // CTA c holds list places [list c / ctas, list (c + 1) / ctas).
       const int c_first = (int)(((first_x + 1) * ctas - 1) / list), c_last = (int)(((last_x + 1) * ctas - 1) / list);
       const int pieces = c_last - c_first + 1;
-      const int64_t mine_at = ((int64_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first ? 1 : 0)) * C::BMT + r_in;
+      const int64_t mine_at = (int64_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first ? 1 : 0);
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : NAN);
+      constexpr int kCols = NQ == 2 ? C::DP : C::DP / 2;
+      const int col0 = NQ == 2 ? 0 : g * kCols;
+      const uint32_t o_base = tmem + lanes + kOCol + (uint32_t)(NQ == 2 ? g * C::DP : col0);
 #pragma unroll 1
-      for (int c = 0; c < C::DP; c += 32) {
-        uint32_t ou[32];
-        __syncwarp();
-        tmem_ld32_nowait(o_col + c, ou);
+      for (int c = 0; c < kCols; c += 32) {
+        uint32_t o[32];
+        tmem_ld32_nowait(o_base + c, o);
         tmem_wait_ld();
-        if (!live) continue;
-        float o[32];
+        if (NQ == 1) {
+          uint32_t o1[32];
+          if (two) tmem_ld32_nowait(o_base + C::DP + c, o1);
+          tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ou[e]);
-        if (bad) add_non_finite(a, w, b, h, walk.k, walk.k + piece, i, low, mask_row, c, o);
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + (two ? __uint_as_float(o1[e]) * f1 : 0.0f));
+        }
+        if (bad && live) {
+          float y[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]);
+          add_non_finite(a, w, b, h, k0, k1, i, low, mask_row, col0 + c, y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(y[e]);
+        }
+        __syncwarp();
         if (pieces > 1) {
-          float4* dst = (float4*)(p.o + mine_at * C::DP + c);
+          if (live) {
+            float4* dst = p.o + ((mine_at * NQ + (NQ == 2 ? g : 0)) * (C::DP / 4) + (col0 + c) / 4) * 128 + trow;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e)
+              dst[e * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                         __uint_as_float(o[4 * e + 3]));
+          }
         } else {
-          uint4* dst = (uint4*)((__nv_bfloat16*)a.out + row * a.D + c);
+          // Over the query tile, which nothing reads any more, so that the rows leave coalesced.
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + 8 * e < a.D)
-              dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                  pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          for (int e = 0; e < 4; ++e) {
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              y[j] = pack_bf16(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
+            *(uint4*)chunk_at(trow, (col0 + c) / 8 + e) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
       }
       tc_fence_before();  // these reads of O before the next item's first product
       if (pieces == 1) {
-        if (live && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        __syncwarp();
+        constexpr int kCh = kCols / 8;  // chunks of a row
+        constexpr int kPer = 32 / kCh;  // rows per store of the warp
+        const int x = col0 / 8 + (lane & (kCh - 1)), rr = lane / kCh;
+#pragma unroll
+        for (int j = 0; j < 32 / kPer; ++j) {
+          const int r = j * kPer + rr;
+          const int64_t row_r = __shfl_sync(0xffffffffu, row, r);
+          if ((NQ == 2 ? g * 128 : 0) + quarter * 32 + r < w.rows && x * 8 < a.D)
+            *(uint4*)((__nv_bfloat16*)a.out + row_r * a.D + x * 8) = *(const uint4*)chunk_at(quarter * 32 + r, x);
+        }
+        if (live && a.lse && (NQ == 2 || g == 0)) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
-        if (live) p.ml[mine_at] = make_float2(m, l);
+        if (live && (NQ == 2 || g == 0)) p.ml[mine_at * C::BMT + r_in] = make_float2(m, l);
         __threadfence();
       }
-      // The group's threads are done with O, s_bad and (when cut) their partial rows.
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
-      if (trow == 0) {
-        s_bad[bad_at] = 0;
-        if (pieces > 1) {
-          // Every query tile of the row tile counts one arrival per piece.
-          const unsigned was = atomicAdd(p.arrived + c_first * NQ + q, 1u);
-          s_last[q] = was == (unsigned)pieces - 1u;
-          if (s_last[q]) p.arrived[c_first * NQ + q] = 0u;  // ready for the next call
-        }
-      }
+      // Done with O, s_ml, s_bad, the query tile and (when cut) the partial rows.
+      constexpr int kGroup = NQ == 1 ? 256 : 128;
+      const int bar_id = NQ == 1 ? 1 : 1 + g;
+      group_all<kGroup>(bar_id, true);
+      if (trow == 0) s_bad[bad_at] = 0;
       if (pieces > 1) {
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
-        if (s_last[q]) {
+        const int me = NQ == 1 ? g * 128 + trow : trow;
+        if (me == 0) {
+          // Every query tile of the row tile counts one arrival per piece.
+          unsigned* cnt = p.arrived + c_first * NQ + (NQ == 2 ? g : 0);
+          const bool last = atomicAdd(cnt, 1u) == (unsigned)pieces - 1u;
+          if (last) *cnt = 0u;  // ready for the next call
+          s_last[NQ == 2 ? g : 0] = last;
+        }
+        group_all<kGroup>(bar_id, true);
+        if (s_last[NQ == 2 ? g : 0]) {
           __threadfence();
-          // Columns of a row over neighbouring threads; the pieces in order.
-          const int rows_q = min(128, w.rows - q * 128);
-          for (int x = trow; x < rows_q * (C::DP / 4); x += 128) {
-            const int r = x / (C::DP / 4), e = (x - r * (C::DP / 4)) * 4;
-            auto at = [&](int pc) {
-              return ((int64_t)(c_first + pc) * 2 + (pc == 0 ? 1 : 0)) * C::BMT + q * 128 + r;
-            };
+          // The pieces in order; rows over neighbouring threads.
+          const int rows_q = min(128, w.rows - (NQ == 2 ? g * 128 : 0));
+          const int qt = NQ == 2 ? g : 0;
+          for (int x = me; x < rows_q * (C::DP / 4); x += kGroup) {
+            const int e4 = x / rows_q, r = x - e4 * rows_q;
+            auto piece_at = [&](int pc) { return (int64_t)(c_first + pc) * 2 + (pc == 0 ? 1 : 0); };
             float mm = -INFINITY, ll = 0.0f;
-            for (int pc = 0; pc < pieces; ++pc) mm = fmaxf(mm, __ldcg(&p.ml[at(pc)]).x);
+#pragma unroll 8
+            for (int pc = 0; pc < pieces; ++pc) mm = fmaxf(mm, __ldcg(&p.ml[piece_at(pc) * C::BMT + qt * 128 + r]).x);
             float4 acc = make_float4(0, 0, 0, 0);
-#pragma unroll 4
+#pragma unroll 8
             for (int pc = 0; pc < pieces; ++pc) {
-              const float2 v = __ldcg(&p.ml[at(pc)]);
-              const float4 y = __ldcg((const float4*)(p.o + at(pc) * C::DP + e));
-              if (v.x == -INFINITY) continue;  // saw nothing: its sums are zeros
+              const float2 v = __ldcg(&p.ml[piece_at(pc) * C::BMT + qt * 128 + r]);
+              const float4 y = __ldcg(p.o + ((piece_at(pc) * NQ + qt) * (C::DP / 4) + e4) * 128 + r);
+              if (v.x == -INFINITY && v.y == 0.0f) continue;  // saw nothing
               const float f = v.x == mm ? 1.0f : ex2(v.x - mm);
               ll += v.y * f;
               acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
             }
-            const int prr = w.r0 + q * 128 + r, ii = prr / G;
+            const int prr = w.r0 + qt * 128 + r, ii = prr / G;
             const int64_t orow = (int64_t)(w.q0 + ii) * a.hq + h * G + (prr - ii * G);
             const float iv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN);
-            if (e < a.D)
-              *(uint2*)((__nv_bfloat16*)a.out + orow * a.D + e) =
+            if (e4 * 4 < a.D)
+              *(uint2*)((__nv_bfloat16*)a.out + orow * a.D + e4 * 4) =
                   make_uint2(pack_bf16(acc.x * iv, acc.y * iv), pack_bf16(acc.z * iv, acc.w * iv));
-            if (e == 0 && a.lse) a.lse[orow] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            if (e4 == 0 && a.lse) a.lse[orow] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
           }
         }
       }
       ++item;
-      walk.next(w.cnt, piece, hkv);
     }
   }
 
@@ -800,21 +892,21 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   p.timeout_ns = wait_timeout_ns();
   // A scale of 0 still has to leave a masked score at -inf.
   p.c = fmaxf(a.scale * kLog2e, 1e-30f);
-  const uint32_t budget = 227 * 1024 - 2048;
+  const uint32_t budget = 227 * 1024 - 4096;
   int slots = (int)((budget - NQ * C::kQBytes) / C::kTile);
   // Even: a buffer is always a key or always a value buffer, so every phase of a value
   // buffer is waited for by those who clear it.
   p.slots = slots > 12 ? 12 : slots & ~1;
-  const size_t smem = 1024 + (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + 1024;
+  const size_t smem = 1024 + (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + 3072;
   const int grid = num_sms();
   if ((size_t)grid * NQ * 4 > kArrivedBytes || (int64_t)a.rows.batch * p.row_tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
   uint8_t* w = (uint8_t*)a.scratch;
   p.arrived = (unsigned int*)w;
   p.ml = (float2*)(w + kArrivedBytes);
-  p.o = (float*)(w + kArrivedBytes + (size_t)2 * grid * C::BMT * 8);
+  p.o = (float4*)(w + kArrivedBytes + (size_t)2 * grid * C::BMT * 8);
   cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NQ, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
-  attn_tc_kernel<NQ, KB><<<grid, C::kThreads, smem, stream>>>(p);
+  attn_tc_kernel<NQ, KB><<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
