@@ -11,8 +11,11 @@
 // below 2^8, and l and O carry the same factor), which after the first tiles is rare.
 //
 //   warp 0       TMA: key and value tiles into one ring of buffers
-//   warp 1       TMEM, and one thread issues the MMAs
-//   warps 2, 3   clear non-finite values of tiles that some row does not see
+//   warp 1       TMEM and the MMAs. The whole warp runs the loop and one elected thread issues:
+//                under elect.sync an M = 128, N = 128, K = 16 MMA issues every 64 cycles (the
+//                full rate), from a branch on the lane number every 120 to 220 (measured)
+//   warps 2, 3   query tiles, one row tile ahead; clear non-finite values of tiles that some
+//                row does not see
 //   warps 4-7, 8-11  two groups of 128 threads: softmax and epilogue
 //
 // NQ = 2 (prompts): bound by the exponentials and the MMAs. Each group has a query tile of
@@ -115,6 +118,12 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
       : "r"(id), "r"((uint32_t)ok), "n"(N)
       : "memory");
   return r != 0;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
 }
 
 // The CTA's part of the work list, walked by every role alike.
@@ -272,6 +281,7 @@ struct Cfg {
   static constexpr int BMT = 128 * NQ;
   static constexpr uint32_t kTile = (uint32_t)KB * kBN * 128;    // bytes of a key or value tile
   static constexpr uint32_t kQBytes = (uint32_t)KB * 128 * 128;  // bytes of a query tile
+  static constexpr uint32_t kStage = NQ == 2 ? 8 * 2048 : 0;     // output on its way out
 };
 constexpr int kThreads = 384;
 constexpr uint32_t kOCol = 256;  // TMEM: S of group g at 128 g, O of group g at kOCol + DP g
@@ -279,19 +289,20 @@ constexpr uint32_t kOCol = 256;  // TMEM: S of group g at 128 g, O of group g at
 template <int NQ, int KB>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnP p) {
   using C = Cfg<NQ, KB>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* ring = sQ + NQ * C::kQBytes;
   const int slots = p.slots;
-  uint64_t* full = (uint64_t*)(ring + (size_t)slots * C::kTile);
+  uint8_t* stage = ring + (size_t)slots * C::kTile;  // NQ = 2: 2 KB per softmax warp
+  uint64_t* full = (uint64_t*)(stage + C::kStage);
   uint64_t* empty = full + slots;
   uint64_t* v_clean = empty + slots;
   uint64_t* s_ready = v_clean + slots;  // [2]: per group
   uint64_t* p_ready = s_ready + 2;      // [2]
   uint64_t* o_done = p_ready + 2;       // [2]
-  uint64_t* q_ready = o_done + 2;       // [2]: per query tile
-  uint64_t* drain = q_ready + 2;
+  uint64_t* q_ready = o_done + 2;
+  uint64_t* q_free = q_ready + 1;
+  uint64_t* drain = q_free + 1;
   int64_t* s_prefix = (int64_t*)(drain + 1);
   int64_t* s_scan = s_prefix + 1;       // [kThreads / 32]
   float2* s_ml = (float2*)(s_scan + kThreads / 32);  // [2][128] NQ = 1: the groups' (m, l)
@@ -302,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   volatile int* s_abort = (volatile int*)(tmem_slot + 1);
 
   const AttnArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int hkv = a.hkv, G = a.hq / a.hkv;
   Ctl* ctl = a.ctl;
 
@@ -316,8 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mbar_init(&s_ready[s], 1);
       mbar_init(&p_ready[s], 4);
       mbar_init(&o_done[s], 1);
-      mbar_init(&q_ready[s], NQ == 1 ? 8 : 4);
     }
+    mbar_init(q_ready, 2);
+    mbar_init(q_free, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
     for (int i = 0; i < 2 * kBadRing; ++i) s_bad[i] = 0;
@@ -328,6 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
+  }
+  // Columns of the query tiles past head_dim stay zero.
+  if (a.D < C::DP) {
+    for (uint32_t x = threadIdx.x; x < NQ * C::kQBytes / 16; x += kThreads) ((uint4*)sQ)[x] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
 
   // Count the work list (places of one kv head) and find this CTA's part of it.
@@ -348,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   int64_t before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
@@ -398,8 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       uint32_t phase = 0;
       long issued = 0;
       bool ok = true;
+      Unit w;
+      int cur = -1;
       while (walk.len > 0 && walk.u < units && ok) {
-        const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
+        if (walk.u != cur) w = load_unit<C::BMT>(a, p.row_tiles, cur = walk.u, false);
         if (w.cnt == 0) { ++walk.u; continue; }
         const int b = walk.u / p.row_tiles;
         int k0, k1;
@@ -425,58 +444,71 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (long j = issued - 1; j >= 0 && j >= issued - slots; --j)
           mbar_wait(&full[j % slots], (uint32_t)((j / slots) & 1), nullptr, ctl, p.timeout_ns);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       const uint32_t id_s = idesc_bf16_f32(128, kBN);
       const uint32_t id_o = idesc_bf16_f32(128, C::DP) | (1u << 16);  // B is MN-major
+      const bool leader = elect_one();
       uint32_t item = 0, done[2] = {0, 0};  // key tiles each group has had
       bool ok = true;
       // The ring holds K_0, V_0, K_1, V_1, ...; two cursors over it.
       int ks = 0, vs = 1;
       uint32_t kph = 0, vph = 0;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, s_abort, ctl, p.timeout_ns)) ok = false;
+        ok = ok && warp_wait(bar, parity, s_abort, ctl, p.timeout_ns);
         tc_fence_after();
       };
       auto step = [&](int& s, uint32_t& ph) {
         s += 2;
         if (s >= slots) { s -= slots; ph ^= 1u; }
       };
-      auto scores = [&](int qt, int g) {  // S_g = Q K^T
-        const uint64_t ad = sdesc_k_sw128(smem_u32(sQ + (size_t)qt * C::kQBytes));
-        const uint64_t bd = sdesc_k_sw128(smem_u32(ring + (size_t)ks * C::kTile));
+      const uint32_t q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
+      auto scores = [&](int qt, int g, uint64_t* then) {  // S_g = Q K^T
+        const uint64_t ad = sdesc_k_sw128(q_addr + (uint32_t)qt * C::kQBytes);
+        const uint64_t bd = sdesc_k_sw128(ring_addr + (uint32_t)ks * C::kTile);
+        if (leader) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_bf16(tmem + (uint32_t)(g * 128), ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k),
-                      bd + (uint64_t)(kb * (kBN * 128 / 16) + 2 * k), id_s, (kb | k) ? 1u : 0u);
-        umma_commit(&s_ready[g]);
+            for (int k = 0; k < 4; ++k)
+              umma_bf16(tmem + (uint32_t)(g * 128), ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k),
+                        bd + (uint64_t)(kb * (kBN * 128 / 16) + 2 * k), id_s, (kb | k) ? 1u : 0u);
+          umma_commit(&s_ready[g]);
+          if (then) umma_commit(then);
+        }
+        __syncwarp();
       };
       auto values = [&](int g, bool first) {  // O_g += P_g V
-        const uint64_t bd = sdesc_mn_sw128(smem_u32(ring + (size_t)vs * C::kTile));
+        const uint64_t bd = sdesc_mn_sw128(ring_addr + (uint32_t)vs * C::kTile);
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < kBN / 16; ++k)
-          umma_bf16_ts(tmem + kOCol + (uint32_t)(g * C::DP), tmem + (uint32_t)(g * 128 + 8 * k),
-                       bd + (uint64_t)(k * (16 * 128 / 16)), id_o, (first && k == 0) ? 0u : 1u);
-        umma_commit(&o_done[g]);
+          for (int k = 0; k < kBN / 16; ++k)
+            umma_bf16_ts(tmem + kOCol + (uint32_t)(g * C::DP), tmem + (uint32_t)(g * 128 + 8 * k),
+                         bd + (uint64_t)(k * (16 * 128 / 16)), id_o, (first && k == 0) ? 0u : 1u);
+          umma_commit(&o_done[g]);
+        }
+        __syncwarp();
       };
+      auto release = [&](uint64_t* bar) {
+        if (leader) umma_commit(bar);
+        __syncwarp();
+      };
+      Unit w;
+      int cur = -1;
       while (walk.len > 0 && walk.u < units && ok) {
-        const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
+        if (walk.u != cur) w = load_unit<C::BMT>(a, p.row_tiles, cur = walk.u, false);
         if (w.cnt == 0) { ++walk.u; continue; }
         int k0, k1;
         walk.part(w.cnt, k0, k1);
         walk.next(w.cnt, hkv);
         const int n = k1 - k0;
         if (n == 0) continue;
+        wait(q_ready, item & 1u);
         if (NQ == 2) {
           wait(&full[ks], kph);
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            wait(&q_ready[g], item & 1u);
-            if (ok) scores(g, g);
-          }
           if (!ok) break;
-          umma_commit(&empty[ks]);
+          scores(0, 0, nullptr);
+          scores(1, 1, n == 1 ? q_free : nullptr);
+          release(&empty[ks]);
           step(ks, kph);
           for (int t = 0; t < n && ok; ++t) {
             const bool more = t + 1 < n;
@@ -485,39 +517,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               wait(&p_ready[g], done[g]++ & 1u);
-              if (ok) values(g, t == 0);
+              if (!ok) break;
+              values(g, t == 0);
               if (more) {
                 if (g == 0) wait(&full[ks], kph);
-                if (ok) scores(g, g);
+                if (!ok) break;
+                scores(g, g, g == 1 && t + 2 == n ? q_free : nullptr);
               }
             }
             if (!ok) break;
-            umma_commit(&empty[vs]);
+            release(&empty[vs]);
             step(vs, vph);
             if (more) {
-              umma_commit(&empty[ks]);
+              release(&empty[ks]);
               step(ks, kph);
             }
           }
         } else {
-          wait(&q_ready[0], item & 1u);
           for (int t = 0; t < n + 2 && ok; ++t) {
             // Tile t's scores go out once tile t - 2, the one before it in its S, is done.
+            const int g = t & 1;
             if (t >= 2) {
-              const int g = t & 1;
               wait(&v_clean[vs], vph);
               wait(&full[vs], vph);
               wait(&p_ready[g], done[g]++ & 1u);
               if (!ok) break;
               values(g, t < 4);
-              umma_commit(&empty[vs]);
+              release(&empty[vs]);
               step(vs, vph);
             }
             if (t < n) {
               wait(&full[ks], kph);
               if (!ok) break;
-              scores(0, t & 1);
-              umma_commit(&empty[ks]);
+              scores(0, g, t + 1 == n ? q_free : nullptr);
+              release(&empty[ks]);
               step(ks, kph);
             }
           }
@@ -525,22 +558,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         ++item;
       }
       // Every MMA issued above has finished before TMEM is freed.
-      umma_commit(drain);
+      release(drain);
       mbar_wait(drain, 0, nullptr, ctl, p.timeout_ns);
     } else if (warp >= 2) {
-    // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
-    // or a NaN in the product, so these are cleared here and the row tile is marked.
     const int t64 = threadIdx.x - 64;
     int slot = 1;
     uint32_t phase = 0, item = 0;
     bool ok = true;
+    Unit w;
+    int cur = -1;
     while (walk.len > 0 && walk.u < units && ok) {
-      const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
+      if (walk.u != cur) w = load_unit<C::BMT>(a, p.row_tiles, cur = walk.u, false);
       if (w.cnt == 0) { ++walk.u; continue; }
+      const int h = walk.h;
       int k0, k1;
       walk.part(w.cnt, k0, k1);
       walk.next(w.cnt, hkv);
       if (k0 == k1) continue;
+      // The query rows, 16 bytes a copy, swizzled as the MMA reads them; the scores before
+      // have read theirs. Rows that there are none of keep what they held: no other row's
+      // result depends on them.
+      if (item > 0 && !warp_wait(q_free, (item - 1u) & 1u, s_abort, ctl, p.timeout_ns)) break;
+      {
+        const int x = t64 & (8 * KB - 1);
+        if (x * 8 < a.D)
+          for (int r = t64 / (8 * KB); r < w.rows; r += 64 / (8 * KB)) {
+            const int pr = w.r0 + r, i = pr / G;
+            const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + ((int64_t)(w.q0 + i) * a.hq + h * G + (pr - i * G)) * a.D + x * 8;
+            const uint32_t dst = smem_u32(sQ) + (uint32_t)((r >> 7) * C::kQBytes + (x >> 3) * (128 * 128) + (r & 127) * 128 +
+                                                           (((x & 7) ^ (r & 7)) << 4));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+          }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
+      }
+      // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
+      // or a NaN in the product, so these are cleared here and the row tile is marked.
       for (int k = k0; k < k1; ++k) {
         if (!mbar_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
         if (!all_seen(a, w, w.kt.slot(k, kBN))) {
@@ -580,47 +635,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)(g * 128);
     const uint32_t o_col = tmem + lanes + kOCol + (uint32_t)(g * C::DP);
-    uint8_t* q_tile = sQ + (NQ == 2 ? (size_t)g * C::kQBytes : 0);
-    // 16-byte chunk x of row r of the query tile, swizzled as the MMA reads it.
-    auto chunk_at = [&](int r, int x) { return q_tile + (x >> 3) * (128 * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4); };
+    uint8_t* my_stage = stage + (warp - 4) * 2048;
     uint32_t item = 0, tiles = 0;
     bool ok = true;
+    Unit w;
+    int cur = -1, i = 0, low = 0;
+    bool live = false;
+    int64_t row0 = 0;  // this thread's row for kv head 0, in rows of head_dim
+    const uint8_t* mask_row = nullptr;
     while (walk.len > 0 && walk.u < units && ok) {
-      const Unit w = load_unit<C::BMT>(a, p.row_tiles, walk.u, false);
-      if (w.cnt == 0) { ++walk.u; continue; }
       const int b = walk.u / p.row_tiles, h = walk.h;
+      if (walk.u != cur) {
+        w = load_unit<C::BMT>(a, p.row_tiles, cur = walk.u, false);
+        if (w.cnt > 0) {
+          live = r_in < w.rows;
+          const int pr = w.r0 + min(r_in, w.rows - 1);
+          i = pr / G;
+          row0 = (int64_t)(w.q0 + i) * a.hq + (pr - i * G);
+          low = a.window == 0 ? 0 : window_low(a.rows.positions ? __ldg(a.rows.positions + w.q0 + i) : w.ctx + i, a.window);
+          mask_row = a.mask ? a.mask + ((int64_t)b * a.rows.max_q + i) * a.rows.max_q : nullptr;
+        }
+      }
+      if (w.cnt == 0) { ++walk.u; continue; }
       const int64_t first_x = walk.x - walk.k + kItem, last_x = first_x + w.cnt - 1;
       int k0, k1;
       walk.part(w.cnt, k0, k1);
       walk.next(w.cnt, hkv);
       if (k0 == k1) continue;
-      const bool live = r_in < w.rows;
-      const int pr = w.r0 + min(r_in, w.rows - 1), i = pr / G;
-      const int64_t row = (int64_t)(w.q0 + i) * a.hq + h * G + (pr - i * G);
-      // The query tile, coalesced: neighbouring lanes take the chunks of a row. The last scores
-      // of the item before are done: the products after them were waited for.
-      {
-        constexpr int kPer = 32 / (8 * KB);  // rows per load of the warp
-        constexpr int kRows = NQ == 2 ? 32 : 16;
-        const int x = lane & (8 * KB - 1), rr = lane / (8 * KB);
-        uint4 y[kRows / kPer];
-        const int base = NQ == 2 ? quarter * 32 : quarter * 32 + g * 16;
-#pragma unroll
-        for (int j = 0; j < kRows / kPer; ++j) {
-          const int r = base + j * kPer + rr;
-          const int64_t row_r = __shfl_sync(0xffffffffu, row, r & 31);
-          y[j] = make_uint4(0, 0, 0, 0);
-          if ((NQ == 2 ? g * 128 : 0) + r < w.rows && x * 8 < a.D)
-            y[j] = *(const uint4*)((const __nv_bfloat16*)a.q + row_r * a.D + x * 8);
-        }
-#pragma unroll
-        for (int j = 0; j < kRows / kPer; ++j) *(uint4*)chunk_at(base + j * kPer + rr, x) = y[j];
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_ready[NQ == 2 ? g : 0]);
-      }
-      const int low = a.window == 0 ? 0 : window_low(a.rows.positions ? __ldg(a.rows.positions + w.q0 + i) : w.ctx + i, a.window);
-      const uint8_t* mask_row = a.mask ? a.mask + ((int64_t)b * a.rows.max_q + i) * a.rows.max_q : nullptr;
+      const int64_t row = row0 + h * G;
       float m = -INFINITY, l = 0.0f;  // m: log2 units
       bool first = true;
       for (int k = NQ == 2 ? k0 : k0 + g; k < k1; k += NQ == 2 ? 1 : 2, ++tiles, first = false) {
@@ -722,8 +764,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       const bool two = NQ == 1 && k1 - k0 > 1;  // the second O has been written
       // CTA c holds list places [list c / ctas, list (c + 1) / ctas).
-      const int c_first = (int)(((first_x + 1) * ctas - 1) / list), c_last = (int)(((last_x + 1) * ctas - 1) / list);
-      const int pieces = c_last - c_first + 1;
+      int c_first = blockIdx.x, pieces = 1;
+      if (k0 > 0 || k1 < w.cnt) {
+        c_first = (int)(((first_x + 1) * ctas - 1) / list);
+        pieces = (int)(((last_x + 1) * ctas - 1) / list) - c_first + 1;
+      }
       const int64_t mine_at = (int64_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first ? 1 : 0);
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : NAN);
       constexpr int kCols = NQ == 2 ? C::DP : C::DP / 2;
@@ -760,30 +805,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                                          __uint_as_float(o[4 * e + 3]));
           }
         } else {
-          // Over the query tile, which nothing reads any more, so that the rows leave coalesced.
+          uint4 y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint32_t y[4];
+            uint32_t z[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              y[j] = pack_bf16(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
-            *(uint4*)chunk_at(trow, (col0 + c) / 8 + e) = make_uint4(y[0], y[1], y[2], y[3]);
+              z[j] = pack_bf16(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
+            y[e] = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+          if (NQ == 2) {
+            // Through shared memory, so that 64 bytes of a row leave together.
+#pragma unroll
+            for (int e = 0; e < 4; ++e) *(uint4*)(my_stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) = y[e];
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = j * 8 + (lane >> 2), x = lane & 3;
+              const int64_t row_r = __shfl_sync(0xffffffffu, row, r);
+              if (g * 128 + quarter * 32 + r < w.rows && c + x * 8 < a.D)
+                *(uint4*)((__nv_bfloat16*)a.out + row_r * a.D + c + x * 8) = *(const uint4*)(my_stage + r * 64 + ((x ^ ((r >> 1) & 3)) << 4));
+            }
+            __syncwarp();
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col0 + c + 8 * e < a.D) *(uint4*)((__nv_bfloat16*)a.out + row * a.D + col0 + c + 8 * e) = y[e];
           }
         }
       }
       tc_fence_before();  // these reads of O before the next item's first product
       if (pieces == 1) {
-        __syncwarp();
-        constexpr int kCh = kCols / 8;  // chunks of a row
-        constexpr int kPer = 32 / kCh;  // rows per store of the warp
-        const int x = col0 / 8 + (lane & (kCh - 1)), rr = lane / kCh;
-#pragma unroll
-        for (int j = 0; j < 32 / kPer; ++j) {
-          const int r = j * kPer + rr;
-          const int64_t row_r = __shfl_sync(0xffffffffu, row, r);
-          if ((NQ == 2 ? g * 128 : 0) + quarter * 32 + r < w.rows && x * 8 < a.D)
-            *(uint4*)((__nv_bfloat16*)a.out + row_r * a.D + x * 8) = *(const uint4*)chunk_at(quarter * 32 + r, x);
-        }
         if (live && a.lse && (NQ == 2 || g == 0)) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
         if (live && (NQ == 2 || g == 0)) p.ml[mine_at * C::BMT + r_in] = make_float2(m, l);
@@ -892,12 +944,12 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   p.timeout_ns = wait_timeout_ns();
   // A scale of 0 still has to leave a masked score at -inf.
   p.c = fmaxf(a.scale * kLog2e, 1e-30f);
-  const uint32_t budget = 227 * 1024 - 4096;
-  int slots = (int)((budget - NQ * C::kQBytes) / C::kTile);
+  const uint32_t budget = 227 * 1024 - 3072;
+  int slots = (int)((budget - NQ * C::kQBytes - C::kStage) / C::kTile);
   // Even: a buffer is always a key or always a value buffer, so every phase of a value
   // buffer is waited for by those who clear it.
   p.slots = slots > 12 ? 12 : slots & ~1;
-  const size_t smem = 1024 + (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + 3072;
+  const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + 3072;
   const int grid = num_sms();
   if ((size_t)grid * NQ * 4 > kArrivedBytes || (int64_t)a.rows.batch * p.row_tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
   uint8_t* w = (uint8_t*)a.scratch;
