@@ -1,14 +1,16 @@
 // Attention of a block's rows over the cache on the tensor cores
 // (domino_block_attention; the definition is in domino.h): bf16, head_dim <= 128.
 //
-// One pass over the keys with the running maximum and sum of the softmax. Per key
-// tile of 128 slots and query tile of 128 packed rows (row and query head of one kv
-// head): S = Q K^T (tcgen05.mma, fp32 in TMEM), a thread per row takes its 128
+// One pass over the keys with the running maximum and sum of the softmax. Per half key
+// tile of 64 slots and query tile of 128 packed rows (row and query head of one kv
+// head): S = Q K^T (tcgen05.mma, fp32 in TMEM), a thread per row takes its 64
 // scores to registers, P = 2^(S c - m) goes back over S in TMEM as bf16, and
 // O += P V with P as the TMEM operand and V as it lies in the cache (slots x head_dim,
-// head_dim contiguous: the MN-major operand). O stays in TMEM; it is rescaled only
-// when a row's maximum has grown by more than 2^8 since the last time (P then stays
-// below 2^8, and l and O carry the same factor), which after the first tiles is rare.
+// head_dim contiguous: the MN-major operand). The two halves of a key tile have an S each,
+// so one's product and the next tile's scores run under the other's softmax. O stays in
+// TMEM; it is rescaled only when a row's maximum has grown by more than 2^8 since the last
+// time (P then stays below 2^8, and l and O carry the same factor), which after the first
+// tiles is rare.
 //
 //   warp 0       TMA: key and value tiles into one ring of buffers
 //   warp 1       TMEM and the MMAs. The whole warp runs the loop and one elected thread issues:
@@ -41,7 +43,8 @@ namespace domino {
 
 namespace {
 
-constexpr int kBN = 128;
+constexpr int kBN = 128;   // slots of a key tile
+constexpr int kHalf = 64;  // and of a half, the unit of scores and products
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;  // growth of the maximum (log2) that forces a rescale of O
@@ -97,11 +100,11 @@ __device__ __forceinline__ Unit load_unit(const AttnArgs& a, int row_tiles, int 
   return w;
 }
 
-// Whether every row of the tile sees every slot of the key tile at s0.
-__device__ __forceinline__ bool all_seen(const AttnArgs& a, const Unit& w, int s0) {
+// Whether every row of the tile sees every one of the `len` slots from s0.
+__device__ __forceinline__ bool all_seen(const AttnArgs& a, const Unit& w, int s0, int len) {
   const int hi = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_first + 1 : a.mode == DOMINO_MASK_FULL ? w.ctx + w.n : w.ctx;
   const int low = a.mode == DOMINO_MASK_CAUSAL ? w.low_max : min(w.low_max, w.ctx);
-  return s0 + kBN <= hi && (s0 >= low || s0 + kBN <= a.sinks);
+  return s0 + len <= hi && (s0 >= low || s0 + len <= a.sinks);
 }
 
 // A bounded wait that all lanes of a warp leave together, with one answer.
@@ -231,9 +234,9 @@ __device__ __forceinline__ bool bad16(uint32_t x) {  // a bf16 pair with an infi
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
-// Visibility of the 128 slots from s0 for one row, as bits.
+// Visibility of the 64 slots from s0 for one row, as bits.
 __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int i, int low, const uint8_t* mask_row, int s0,
-                                          uint32_t (&bits)[4]) {
+                                          uint32_t (&bits)[2]) {
   const int end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + i + 1 : a.mode == DOMINO_MASK_FULL ? w.ctx + w.n : w.ctx;
   const int from = a.mode == DOMINO_MASK_CAUSAL ? low : min(low, w.ctx);
   auto below = [&](int x, int word) -> uint32_t {  // slots of the word below slot x
@@ -241,14 +244,14 @@ __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int 
     return d <= 0 ? 0u : d >= 32 ? 0xffffffffu : (1u << d) - 1u;
   };
 #pragma unroll
-  for (int j = 0; j < 4; ++j) bits[j] = (~below(from, j) | below(a.sinks, j)) & below(end, j);
+  for (int j = 0; j < 2; ++j) bits[j] = (~below(from, j) | below(a.sinks, j)) & below(end, j);
   if (a.mode == DOMINO_MASK_TREE) {
-    const int j0 = max(0, s0 - w.ctx), j1 = min(w.n, s0 + kBN - w.ctx);
+    const int j0 = max(0, s0 - w.ctx), j1 = min(w.n, s0 + kHalf - w.ctx);
     for (int j = j0; j < j1; ++j) {
       const int at = w.ctx + j - s0;
       const uint32_t bit = __ldg(mask_row + j) ? 1u << (at & 31) : 0u;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) bits[q] |= (at >> 5) == q ? bit : 0u;
+      for (int q = 0; q < 2; ++q) bits[q] |= (at >> 5) == q ? bit : 0u;
     }
   }
 }
@@ -259,12 +262,12 @@ __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int 
 __device__ __noinline__ void add_non_finite(const AttnArgs& a, const Unit& w, int b, int h, int k0, int k1, int i, int low,
                                             const uint8_t* mask_row, int e0, float* o) {
   const uint16_t* v = (const uint16_t*)a.v + (int64_t)b * a.rs + (int64_t)h * a.hs;
-  for (int k = k0; k < k1; ++k) {
-    const int s0 = w.kt.slot(k, kBN);
-    if (all_seen(a, w, s0)) continue;
-    uint32_t bits[4];
+  for (int k = 2 * k0; k < 2 * k1; ++k) {
+    const int tile0 = w.kt.slot(k >> 1, kBN), s0 = tile0 + (k & 1) * kHalf;
+    if (all_seen(a, w, tile0, kBN)) continue;
+    uint32_t bits[2];
     seen_bits(a, w, i, low, mask_row, s0, bits);
-    for (int j = 0; j < kBN; ++j) {
+    for (int j = 0; j < kHalf; ++j) {
       if (!((bits[j >> 5] >> (j & 31)) & 1u)) continue;
       const uint16_t* row = v + (int64_t)(s0 + j) * a.ss;
       for (int e = 0; e < 32 && e0 + e < a.D; ++e) {
@@ -281,7 +284,7 @@ struct Cfg {
   static constexpr int BMT = 128 * NQ;
   static constexpr uint32_t kTile = (uint32_t)KB * kBN * 128;    // bytes of a key or value tile
   static constexpr uint32_t kQBytes = (uint32_t)KB * 128 * 128;  // bytes of a query tile
-  static constexpr uint32_t kStage = NQ == 2 ? 8 * 2048 : 0;     // output on its way out
+  static constexpr uint32_t kStage = NQ == 2 ? 8 * 4096 : 0;     // output on its way out
 };
 constexpr int kThreads = 384;
 constexpr uint32_t kOCol = 256;  // TMEM: S of group g at 128 g, O of group g at kOCol + DP g
@@ -293,21 +296,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   uint8_t* sQ = smem;
   uint8_t* ring = sQ + NQ * C::kQBytes;
   const int slots = p.slots;
-  uint8_t* stage = ring + (size_t)slots * C::kTile;  // NQ = 2: 2 KB per softmax warp
+  uint8_t* stage = ring + (size_t)slots * C::kTile;  // NQ = 2: 4 KB per softmax warp
   uint64_t* full = (uint64_t*)(stage + C::kStage);
   uint64_t* empty = full + slots;
   uint64_t* v_clean = empty + slots;
-  uint64_t* s_ready = v_clean + slots;  // [2]: per group
-  uint64_t* p_ready = s_ready + 2;      // [2]
-  uint64_t* o_done = p_ready + 2;       // [2]
-  uint64_t* q_ready = o_done + 2;
+  uint64_t* s_ready = v_clean + slots;  // [4]: per group and half
+  uint64_t* p_ready = s_ready + 4;      // [4]
+  uint64_t* o_done = p_ready + 4;       // [4]
+  uint64_t* q_ready = o_done + 4;
   uint64_t* q_free = q_ready + 1;
   uint64_t* drain = q_free + 1;
   int64_t* s_prefix = (int64_t*)(drain + 1);
   int64_t* s_scan = s_prefix + 1;       // [kThreads / 32]
   float2* s_ml = (float2*)(s_scan + kThreads / 32);  // [2][128] NQ = 1: the groups' (m, l)
   int* s_unit = (int*)(s_ml + 256);
-  int* s_last = s_unit + 1;             // [2]
+  int* s_cnt = s_unit + 1;
+  int* s_last = s_cnt + 1;              // [2]
   volatile int* s_bad = s_last + 2;     // [2][kBadRing]
   uint32_t* tmem_slot = (uint32_t*)(s_last + 2 + 2 * kBadRing);
   volatile int* s_abort = (volatile int*)(tmem_slot + 1);
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mbar_init(&empty[s], 1);
       mbar_init(&v_clean[s], 2);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&s_ready[s], 1);
       mbar_init(&p_ready[s], 4);
       mbar_init(&o_done[s], 1);
@@ -353,8 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   const int chunk = (units + kThreads - 1) / kThreads;
   const int u_begin = min(units, (int)threadIdx.x * chunk), u_end = min(units, u_begin + chunk);
   int64_t mine = 0;
-  for (int u = u_begin; u < u_end; ++u)
-    mine += places(load_unit<C::BMT>(a, p.row_tiles, u, blockIdx.x == 0 && u % p.row_tiles == 0));
+  int last_places = 0;
+  for (int u = u_begin; u < u_end; ++u) {
+    last_places = places(load_unit<C::BMT>(a, p.row_tiles, u, blockIdx.x == 0 && u % p.row_tiles == 0));
+    mine += last_places;
+  }
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -382,9 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   if (!idle && mine > 0 && before <= x0 / hkv && x0 / hkv < before + mine) {
     int64_t at = before;
     for (int u = u_begin; u < u_end; ++u) {
-      const int c = places(load_unit<C::BMT>(a, p.row_tiles, u, false));
+      const int c = u + 1 == u_end ? last_places : places(load_unit<C::BMT>(a, p.row_tiles, u, false));
       if (x0 < (at + c) * hkv) {
         *s_unit = u;
+        *s_cnt = c;
         *s_prefix = at;
         break;
       }
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   walk.u = 0; walk.h = 0; walk.k = 0;
   if (walk.len > 0) {
     walk.u = *s_unit;
-    const int c = places(load_unit<C::BMT>(a, p.row_tiles, walk.u, false));
+    const int c = *s_cnt;
     const int64_t in = x0 - *s_prefix * hkv;
     walk.h = (int)(in / c);
     walk.k = (int)(in - (int64_t)walk.h * c);
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           mbar_wait(&full[j % slots], (uint32_t)((j / slots) & 1), nullptr, ctl, p.timeout_ns);
       }
     } else if (warp == 1) {
-      const uint32_t id_s = idesc_bf16_f32(128, kBN);
+      const uint32_t id_s = idesc_bf16_f32(128, kHalf);
       const uint32_t id_o = idesc_bf16_f32(128, C::DP) | (1u << 16);  // B is MN-major
       const bool leader = elect_one();
       uint32_t item = 0, done[2] = {0, 0};  // key tiles each group has had
@@ -462,29 +470,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (s >= slots) { s -= slots; ph ^= 1u; }
       };
       const uint32_t q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
-      auto scores = [&](int qt, int g, uint64_t* then) {  // S_g = Q K^T
+      auto scores = [&](int qt, int g, int half, uint64_t* then) {  // S = Q K^T of half a key tile
         const uint64_t ad = sdesc_k_sw128(q_addr + (uint32_t)qt * C::kQBytes);
-        const uint64_t bd = sdesc_k_sw128(ring_addr + (uint32_t)ks * C::kTile);
+        const uint64_t bd = sdesc_k_sw128(ring_addr + (uint32_t)ks * C::kTile + (uint32_t)(half * kHalf * 128));
         if (leader) {
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_bf16(tmem + (uint32_t)(g * 128), ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k),
+              umma_bf16(tmem + (uint32_t)(g * 128 + half * kHalf), ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k),
                         bd + (uint64_t)(kb * (kBN * 128 / 16) + 2 * k), id_s, (kb | k) ? 1u : 0u);
-          umma_commit(&s_ready[g]);
+          umma_commit(&s_ready[g * 2 + half]);
           if (then) umma_commit(then);
         }
         __syncwarp();
       };
-      auto values = [&](int g, bool first) {  // O_g += P_g V
-        const uint64_t bd = sdesc_mn_sw128(ring_addr + (uint32_t)vs * C::kTile);
+      auto values = [&](int g, int half, bool first) {  // O += P V of half a key tile
+        const uint64_t bd = sdesc_mn_sw128(ring_addr + (uint32_t)vs * C::kTile + (uint32_t)(half * kHalf * 128));
         if (leader) {
 #pragma unroll
-          for (int k = 0; k < kBN / 16; ++k)
-            umma_bf16_ts(tmem + kOCol + (uint32_t)(g * C::DP), tmem + (uint32_t)(g * 128 + 8 * k),
+          for (int k = 0; k < kHalf / 16; ++k)
+            umma_bf16_ts(tmem + kOCol + (uint32_t)(g * C::DP), tmem + (uint32_t)(g * 128 + half * kHalf + 8 * k),
                          bd + (uint64_t)(k * (16 * 128 / 16)), id_o, (first && k == 0) ? 0u : 1u);
-          umma_commit(&o_done[g]);
+          umma_commit(&o_done[g * 2 + half]);
         }
         __syncwarp();
       };
@@ -503,56 +511,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int n = k1 - k0;
         if (n == 0) continue;
         wait(q_ready, item & 1u);
-        if (NQ == 2) {
+        // A half's scores go out once the product of the tile before in its S has been issued:
+        // NQ = 2: tile t + 1 of both groups after tile t; NQ = 1: tile t + 2 after tile t.
+        constexpr int kAhead = NQ == 2 ? 1 : 2;
+        for (int t = 0; t < kAhead && t < n && ok; ++t) {
           wait(&full[ks], kph);
           if (!ok) break;
-          scores(0, 0, nullptr);
-          scores(1, 1, n == 1 ? q_free : nullptr);
-          release(&empty[ks]);
-          step(ks, kph);
-          for (int t = 0; t < n && ok; ++t) {
-            const bool more = t + 1 < n;
-            wait(&v_clean[vs], vph);
-            wait(&full[vs], vph);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              wait(&p_ready[g], done[g]++ & 1u);
-              if (!ok) break;
-              values(g, t == 0);
-              if (more) {
-                if (g == 0) wait(&full[ks], kph);
-                if (!ok) break;
-                scores(g, g, g == 1 && t + 2 == n ? q_free : nullptr);
-              }
-            }
-            if (!ok) break;
-            release(&empty[vs]);
-            step(vs, vph);
-            if (more) {
-              release(&empty[ks]);
-              step(ks, kph);
+          for (int half = 0; half < 2; ++half) {
+            uint64_t* then = half == 1 && t + 1 == n ? q_free : nullptr;
+            if (NQ == 2) {
+              scores(0, 0, half, nullptr);
+              scores(1, 1, half, then);
+            } else {
+              scores(0, t, half, then);
             }
           }
-        } else {
-          for (int t = 0; t < n + 2 && ok; ++t) {
-            // Tile t's scores go out once tile t - 2, the one before it in its S, is done.
-            const int g = t & 1;
-            if (t >= 2) {
-              wait(&v_clean[vs], vph);
-              wait(&full[vs], vph);
-              wait(&p_ready[g], done[g]++ & 1u);
+          release(&empty[ks]);
+          step(ks, kph);
+        }
+        for (int t = 0; t < n && ok; ++t) {
+          const bool more = t + kAhead < n;
+          wait(&v_clean[vs], vph);
+          wait(&full[vs], vph);
+          if (more) wait(&full[ks], kph);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint64_t* then = half == 1 && t + kAhead + 1 == n ? q_free : nullptr;
+            if (NQ == 2) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                wait(&p_ready[g * 2 + half], done[0] & 1u);
+                if (!ok) break;
+                values(g, half, t == 0 && half == 0);
+                if (more) scores(g, g, half, g == 1 ? then : nullptr);
+              }
+            } else {
+              const int g = t & 1;
+              wait(&p_ready[g * 2 + half], done[g] & 1u);
               if (!ok) break;
-              values(g, t < 4);
-              release(&empty[vs]);
-              step(vs, vph);
+              values(g, half, t < 2 && half == 0);
+              if (more) scores(0, g, half, then);
             }
-            if (t < n) {
-              wait(&full[ks], kph);
-              if (!ok) break;
-              scores(0, g, t + 1 == n ? q_free : nullptr);
-              release(&empty[ks]);
-              step(ks, kph);
-            }
+          }
+          if (!ok) break;
+          ++done[NQ == 2 ? 0 : t & 1];
+          release(&empty[vs]);
+          step(vs, vph);
+          if (more) {
+            release(&empty[ks]);
+            step(ks, kph);
           }
         }
         ++item;
@@ -598,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       // or a NaN in the product, so these are cleared here and the row tile is marked.
       for (int k = k0; k < k1; ++k) {
         if (!mbar_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
-        if (!all_seen(a, w, w.kt.slot(k, kBN))) {
+        if (!all_seen(a, w, w.kt.slot(k, kBN), kBN)) {
           uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
           bool bad = false;
 #pragma unroll 8
@@ -635,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)(g * 128);
     const uint32_t o_col = tmem + lanes + kOCol + (uint32_t)(g * C::DP);
-    uint8_t* my_stage = stage + (warp - 4) * 2048;
+    uint8_t* my_stage = stage + (warp - 4) * 4096;
     uint32_t item = 0, tiles = 0;
     bool ok = true;
     Unit w;
@@ -643,6 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     bool live = false;
     int64_t row0 = 0;  // this thread's row for kv head 0, in rows of head_dim
     const uint8_t* mask_row = nullptr;
+    // NQ = 2: where this lane stores 16 bytes of 8 of its warp's rows (kv head 0), and which there are.
+    int64_t out_at[8] = {};
+    uint32_t out_rows = 0;
     while (walk.len > 0 && walk.u < units && ok) {
       const int b = walk.u / p.row_tiles, h = walk.h;
       if (walk.u != cur) {
@@ -654,6 +665,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           row0 = (int64_t)(w.q0 + i) * a.hq + (pr - i * G);
           low = a.window == 0 ? 0 : window_low(a.rows.positions ? __ldg(a.rows.positions + w.q0 + i) : w.ctx + i, a.window);
           mask_row = a.mask ? a.mask + ((int64_t)b * a.rows.max_q + i) * a.rows.max_q : nullptr;
+          if (NQ == 2) {
+            out_rows = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int r = j * 4 + (lane >> 3);
+              out_at[j] = __shfl_sync(0xffffffffu, row0, r) * a.D + (lane & 7) * 8;
+              out_rows |= g * 128 + quarter * 32 + r < w.rows ? 1u << j : 0u;
+            }
+          }
         }
       }
       if (w.cnt == 0) { ++walk.u; continue; }
@@ -665,86 +685,81 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const int64_t row = row0 + h * G;
       float m = -INFINITY, l = 0.0f;  // m: log2 units
       bool first = true;
-      for (int k = NQ == 2 ? k0 : k0 + g; k < k1; k += NQ == 2 ? 1 : 2, ++tiles, first = false) {
-        const int s0 = w.kt.slot(k, kBN);
-        ok = warp_wait(&s_ready[g], tiles & 1u, s_abort, ctl, p.timeout_ns);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_col + 32 * c, s + 32 * c);
-        tmem_wait_ld();
-        if (!all_seen(a, w, s0)) {
-          uint32_t bits[4];
-          seen_bits(a, w, i, low, mask_row, s0, bits);
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
-        }
-        float m4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) m4[c] = max3(__uint_as_float(s[c]), __uint_as_float(s[c + 4]), __uint_as_float(s[c + 8]));
-#pragma unroll
-        for (int c = 12; c < 124; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(s[124 + e]));
-        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * p.c;
-        const bool grow = live && mx > m + kLazy;  // from -inf: any finite maximum
-        bool o_free = first;                       // the group's product before this tile's is done
-        if (__any_sync(0xffffffffu, grow)) {
-          const float m_new = grow ? mx : m;
-          const float f = m == m_new || m == -INFINITY ? 1.0f : ex2(m - m_new);
-          m = m_new;
-          l *= f;
-          if (!first) {
-            o_free = true;
-            ok = warp_wait(&o_done[g], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < C::DP; c += 32) {
-              uint32_t o[32];
-              tmem_ld32_nowait(o_col + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_col + c, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        const float m_use = m == -INFINITY ? 0.0f : m;
-        const float2 c2 = make_float2(p.c, p.c), n2 = make_float2(-m_use, -m_use);
-        float2 sum2[2] = {make_float2(0, 0), make_float2(0, 0)};
+      for (int k = NQ == 2 ? k0 : k0 + g; k < k1 && ok; k += NQ == 2 ? 1 : 2, ++tiles) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          const int s0 = w.kt.slot(k, kBN) + half * kHalf;
+          const uint32_t col = s_col + (uint32_t)(half * kHalf);
+          // With these scores the group's product before the last one is done too.
+          ok = warp_wait(&s_ready[g * 2 + half], tiles & 1u, s_abort, ctl, p.timeout_ns);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t s[kHalf];
+          tmem_ld32_nowait(col, s);
+          tmem_ld32_nowait(col + 32, s + 32);
+          tmem_wait_ld();
+          if (!all_seen(a, w, s0, kHalf)) {
+            uint32_t bits[2];
+            seen_bits(a, w, i, low, mask_row, s0, bits);
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c)
+              if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+          }
+          float m4[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) m4[c] = max3(__uint_as_float(s[c]), __uint_as_float(s[c + 4]), __uint_as_float(s[c + 8]));
+#pragma unroll
+          for (int c = 12; c < 60; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(s[60 + e]));
+          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * p.c;
+          const bool grow = live && mx > m + kLazy;  // from -inf: any finite maximum
+          if (__any_sync(0xffffffffu, grow)) {
+            const float m_new = grow ? mx : m;
+            const float f = m == m_new || m == -INFINITY ? 1.0f : ex2(m - m_new);
+            m = m_new;
+            l *= f;
+            if (half > 0 || !first) {
+              // The product before this one; the next waits for this half's weights.
+              ok = warp_wait(&o_done[g * 2 + (half ^ 1)], half ? tiles & 1u : (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < C::DP; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_nowait(o_col + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(o_col + c, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float m_use = m == -INFINITY ? 0.0f : m;
+          const float2 c2 = make_float2(p.c, p.c), n2 = make_float2(-m_use, -m_use);
+          float2 sum2[2] = {make_float2(0, 0), make_float2(0, 0)};
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const int e = half * 64 + 2 * c;
-            float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, n2);
+            float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), c2, n2);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
             pk[c] = pack_bf16(x.x, x.y);
             sum2[c & 1] = add2(sum2[c & 1], x);
           }
-          tmem_st32(s_col + 32 * half, pk);
+          tmem_st32(col, pk);
+          l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[g * 2 + half]);
         }
-        l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
-        tmem_wait_st();
-        tc_fence_before();
-        // Every phase of o_done is waited for: a wait for a later one would take an earlier
-        // one of the same parity for it.
-        if (!o_free) {
-          ok = warp_wait(&o_done[g], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
-          if (!ok) break;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[g]);
+        first = false;
       }
-      if (ok && !first) ok = warp_wait(&o_done[g], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+      if (ok && !first) ok = warp_wait(&o_done[g * 2 + 1], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
       // Whoever shares the epilogue goes on together or not at all: nobody is left at a barrier.
       if (NQ == 1) s_ml[g * 128 + trow] = make_float2(m, l);
       ok = NQ == 1 ? group_all<256>(1, ok) : group_all<128>(1 + g, ok);
@@ -772,42 +787,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const int64_t mine_at = (int64_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first ? 1 : 0);
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : NAN);
       constexpr int kCols = NQ == 2 ? C::DP : C::DP / 2;
+      constexpr int kPart = NQ == 2 ? 64 : 32;  // columns at a time
       const int col0 = NQ == 2 ? 0 : g * kCols;
       const uint32_t o_base = tmem + lanes + kOCol + (uint32_t)(NQ == 2 ? g * C::DP : col0);
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
-        uint32_t o[32];
-        tmem_ld32_nowait(o_base + c, o);
+      for (int c = 0; c < kCols; c += kPart) {
+        uint32_t o[kPart];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < kPart; e += 32) tmem_ld32_nowait(o_base + c + e, o + e);
         tmem_wait_ld();
         if (NQ == 1) {
-          uint32_t o1[32];
+          uint32_t o1[kPart];
           if (two) tmem_ld32_nowait(o_base + C::DP + c, o1);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < kPart; ++e)
             o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + (two ? __uint_as_float(o1[e]) * f1 : 0.0f));
         }
         if (bad && live) {
-          float y[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]);
-          add_non_finite(a, w, b, h, k0, k1, i, low, mask_row, col0 + c, y);
+          for (int e0 = 0; e0 < kPart; e0 += 32) {
+            float y[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(y[e]);
+            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e0 + e]);
+            add_non_finite(a, w, b, h, k0, k1, i, low, mask_row, col0 + c + e0, y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e0 + e] = __float_as_uint(y[e]);
+          }
         }
         __syncwarp();
         if (pieces > 1) {
           if (live) {
             float4* dst = p.o + ((mine_at * NQ + (NQ == 2 ? g : 0)) * (C::DP / 4) + (col0 + c) / 4) * 128 + trow;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < kPart / 4; ++e)
               dst[e * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
                                          __uint_as_float(o[4 * e + 3]));
           }
         } else {
-          uint4 y[4];
+          uint4 y[kPart / 8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < kPart / 8; ++e) {
             uint32_t z[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -815,21 +836,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             y[e] = make_uint4(z[0], z[1], z[2], z[3]);
           }
           if (NQ == 2) {
-            // Through shared memory, so that 64 bytes of a row leave together.
+            // Through shared memory, so that 128 bytes of a row leave together.
 #pragma unroll
-            for (int e = 0; e < 4; ++e) *(uint4*)(my_stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) = y[e];
+            for (int e = 0; e < kPart / 8; ++e) *(uint4*)(my_stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = y[e];
             __syncwarp();
+            const int x = lane & 7;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int r = j * 8 + (lane >> 2), x = lane & 3;
-              const int64_t row_r = __shfl_sync(0xffffffffu, row, r);
-              if (g * 128 + quarter * 32 + r < w.rows && c + x * 8 < a.D)
-                *(uint4*)((__nv_bfloat16*)a.out + row_r * a.D + c + x * 8) = *(const uint4*)(my_stage + r * 64 + ((x ^ ((r >> 1) & 3)) << 4));
+            for (int j = 0; j < 8; ++j) {
+              const int r = j * 4 + (lane >> 3);
+              if (((out_rows >> j) & 1) && c + x * 8 < a.D)
+                *(uint4*)((__nv_bfloat16*)a.out + out_at[j] + h * G * a.D + c) = *(const uint4*)(my_stage + r * 128 + ((x ^ (r & 7)) << 4));
             }
             __syncwarp();
           } else if (live) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < kPart / 8; ++e)
               if (col0 + c + 8 * e < a.D) *(uint4*)((__nv_bfloat16*)a.out + row * a.D + col0 + c + 8 * e) = y[e];
           }
         }
@@ -858,32 +879,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         group_all<kGroup>(bar_id, true);
         if (s_last[NQ == 2 ? g : 0]) {
           __threadfence();
-          // The pieces in order; rows over neighbouring threads.
-          const int rows_q = min(128, w.rows - (NQ == 2 ? g * 128 : 0));
+          // The pieces in order. Neighbouring threads take rows, a thread the same row in every round.
           const int qt = NQ == 2 ? g : 0;
-          for (int x = me; x < rows_q * (C::DP / 4); x += kGroup) {
-            const int e4 = x / rows_q, r = x - e4 * rows_q;
-            auto piece_at = [&](int pc) { return (int64_t)(c_first + pc) * 2 + (pc == 0 ? 1 : 0); };
+          const int rows_q = min(128, w.rows - qt * 128);
+          int rp = 1;
+          while (rp < rows_q) rp <<= 1;
+          const int r = me & (rp - 1);
+          auto piece_at = [&](int pc) { return (int64_t)(c_first + pc) * 2 + (pc == 0 ? 1 : 0); };
+          if (r < rows_q && me / rp < C::DP / 4) {
             float mm = -INFINITY, ll = 0.0f;
 #pragma unroll 8
             for (int pc = 0; pc < pieces; ++pc) mm = fmaxf(mm, __ldcg(&p.ml[piece_at(pc) * C::BMT + qt * 128 + r]).x);
-            float4 acc = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-            for (int pc = 0; pc < pieces; ++pc) {
-              const float2 v = __ldcg(&p.ml[piece_at(pc) * C::BMT + qt * 128 + r]);
-              const float4 y = __ldcg(p.o + ((piece_at(pc) * NQ + qt) * (C::DP / 4) + e4) * 128 + r);
-              if (v.x == -INFINITY && v.y == 0.0f) continue;  // saw nothing
-              const float f = v.x == mm ? 1.0f : ex2(v.x - mm);
-              ll += v.y * f;
-              acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
-            }
             const int prr = w.r0 + qt * 128 + r, ii = prr / G;
             const int64_t orow = (int64_t)(w.q0 + ii) * a.hq + h * G + (prr - ii * G);
-            const float iv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN);
-            if (e4 * 4 < a.D)
-              *(uint2*)((__nv_bfloat16*)a.out + orow * a.D + e4 * 4) =
-                  make_uint2(pack_bf16(acc.x * iv, acc.y * iv), pack_bf16(acc.z * iv, acc.w * iv));
-            if (e4 == 0 && a.lse) a.lse[orow] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            constexpr int kE = 4;  // groups of four columns in flight
+            for (int e4 = me / rp; e4 < C::DP / 4; e4 += kE * (kGroup / rp)) {
+              float4 acc[kE];
+              ll = 0.0f;
+#pragma unroll
+              for (int e = 0; e < kE; ++e) acc[e] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+              for (int pc = 0; pc < pieces; ++pc) {
+                const float2 v = __ldcg(&p.ml[piece_at(pc) * C::BMT + qt * 128 + r]);
+                const float4* src = p.o + ((piece_at(pc) * NQ + qt) * (C::DP / 4)) * 128 + r;
+                const bool none = v.x == -INFINITY && v.y == 0.0f;  // saw nothing
+                const float f = none ? 0.0f : v.x == mm ? 1.0f : ex2(v.x - mm);
+                ll += none ? 0.0f : v.y * f;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                  const int at = e4 + e * (kGroup / rp);
+                  if (at < C::DP / 4 && !none) {
+                    const float4 y = __ldcg(src + at * 128);
+                    acc[e].x += y.x * f; acc[e].y += y.y * f; acc[e].z += y.z * f; acc[e].w += y.w * f;
+                  }
+                }
+              }
+              const float iv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN);
+#pragma unroll
+              for (int e = 0; e < kE; ++e) {
+                const int at = e4 + e * (kGroup / rp);
+                if (at * 4 < a.D)
+                  *(uint2*)((__nv_bfloat16*)a.out + orow * a.D + at * 4) =
+                      make_uint2(pack_bf16(acc[e].x * iv, acc[e].y * iv), pack_bf16(acc[e].z * iv, acc[e].w * iv));
+              }
+            }
+            if (me / rp == 0 && a.lse) a.lse[orow] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
           }
         }
       }
