@@ -13,13 +13,13 @@ namespace domino {
 // read one kv head), so that all the rows that need a key tile share its load.
 //
 // Which slots a tile sees: [0, sinks) and [low, end), taken in key tiles of BN
-// slots: first the sink tiles, then the tiles from floor(low / BN) on.
+// slots: first the tiles from floor(low / BN) on, then the sink tiles (few of their
+// slots are seen, so a maximum begun there would have to be raised).
 struct KeyTiles {
-  int sink_tiles;  // tiles 0 .. sink_tiles - 1 first
-  int main_begin;  // then tiles main_begin ..
-  int count;
+  int main_begin, main_count;  // tiles main_begin .. main_begin + main_count - 1 first
+  int count;                   // then tiles 0 .. count - main_count - 1
   __device__ __forceinline__ int slot(int k, int BN) const {
-    return (k < sink_tiles ? k : main_begin + k - sink_tiles) * BN;
+    return (k < main_count ? main_begin + k : k - main_count) * BN;
   }
 };
 
@@ -37,9 +37,8 @@ __device__ __forceinline__ KeyTiles key_tiles(int mode, int sinks, int low, int 
   const int start = mode == DOMINO_MASK_CAUSAL ? min(low, end) : min(low, ctx);
   KeyTiles k;
   k.main_begin = start / BN;
-  const int main = start < end ? (end + BN - 1) / BN - k.main_begin : 0;
-  k.sink_tiles = min((min(sinks, end) + BN - 1) / BN, k.main_begin);
-  k.count = k.sink_tiles + main;
+  k.main_count = start < end ? (end + BN - 1) / BN - k.main_begin : 0;
+  k.count = k.main_count + min((min(sinks, end) + BN - 1) / BN, k.main_begin);
   return k;
 }
 

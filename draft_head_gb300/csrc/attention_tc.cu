@@ -1,16 +1,17 @@
 // Attention of a block's rows over the cache on the tensor cores
 // (domino_block_attention; the definition is in domino.h): bf16, head_dim <= 128.
 //
-// One pass over the keys with the running maximum and sum of the softmax. Per half key
-// tile of 64 slots and query tile of 128 packed rows (row and query head of one kv
-// head): S = Q K^T (tcgen05.mma, fp32 in TMEM), a thread per row takes its 64
+// One pass over the keys with the running maximum and sum of the softmax. Per key
+// tile of 128 slots and query tile of 128 packed rows (row and query head of one kv
+// head): S = Q K^T (tcgen05.mma, fp32 in TMEM), a thread per row takes its 128
 // scores to registers, P = 2^(S c - m) goes back over S in TMEM as bf16, and
 // O += P V with P as the TMEM operand and V as it lies in the cache (slots x head_dim,
-// head_dim contiguous: the MN-major operand). The two halves of a key tile have an S each,
-// so one's product and the next tile's scores run under the other's softmax. O stays in
-// TMEM; it is rescaled only when a row's maximum has grown by more than 2^8 since the last
-// time (P then stays below 2^8, and l and O carry the same factor), which after the first
-// tiles is rare.
+// head_dim contiguous: the MN-major operand). P is handed over in two halves, so the first
+// half's product runs under the second half's exponentials. (Scores in halves of 64 slots with
+// an S each, so that nothing waits for a product, measured slower: an N = 64 MMA takes 48
+// cycles, not 32, and every hand-over costs the MMA warp about 150.) O stays in TMEM; it is
+// rescaled only when a row's maximum has grown by more than 2^kLazy since the last time: P is
+// then up to 2^kLazy, which fp32 sums and bf16 (fp32's exponents) hold without loss.
 //
 //   warp 0       TMA: key and value tiles into one ring of buffers
 //   warp 1       TMEM and the MMAs. The whole warp runs the loop and one elected thread issues:
@@ -44,10 +45,10 @@ namespace domino {
 namespace {
 
 constexpr int kBN = 128;   // slots of a key tile
-constexpr int kHalf = 64;  // and of a half, the unit of scores and products
+constexpr int kHalf = 64;  // and of the halves in which the weights are handed over
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.0f;  // growth of the maximum (log2) that forces a rescale of O
+constexpr float kLazy = 32.0f;  // growth of the maximum (log2) that forces a rescale of O
 constexpr int kItem = 2;       // list places of a row tile beside its key tiles
 constexpr int kBadRing = 8;    // items the roles may be apart, at most (the ring holds fewer tiles)
 
@@ -100,11 +101,11 @@ __device__ __forceinline__ Unit load_unit(const AttnArgs& a, int row_tiles, int 
   return w;
 }
 
-// Whether every row of the tile sees every one of the `len` slots from s0.
-__device__ __forceinline__ bool all_seen(const AttnArgs& a, const Unit& w, int s0, int len) {
+// Whether every row of the tile sees every slot of the key tile at s0.
+__device__ __forceinline__ bool all_seen(const AttnArgs& a, const Unit& w, int s0) {
   const int hi = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_first + 1 : a.mode == DOMINO_MASK_FULL ? w.ctx + w.n : w.ctx;
   const int low = a.mode == DOMINO_MASK_CAUSAL ? w.low_max : min(w.low_max, w.ctx);
-  return s0 + len <= hi && (s0 >= low || s0 + len <= a.sinks);
+  return s0 + kBN <= hi && (s0 >= low || s0 + kBN <= a.sinks);
 }
 
 // A bounded wait that all lanes of a warp leave together, with one answer.
@@ -234,9 +235,9 @@ __device__ __forceinline__ bool bad16(uint32_t x) {  // a bf16 pair with an infi
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
-// Visibility of the 64 slots from s0 for one row, as bits.
+// Visibility of the 128 slots from s0 for one row, as bits.
 __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int i, int low, const uint8_t* mask_row, int s0,
-                                          uint32_t (&bits)[2]) {
+                                          uint32_t (&bits)[4]) {
   const int end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + i + 1 : a.mode == DOMINO_MASK_FULL ? w.ctx + w.n : w.ctx;
   const int from = a.mode == DOMINO_MASK_CAUSAL ? low : min(low, w.ctx);
   auto below = [&](int x, int word) -> uint32_t {  // slots of the word below slot x
@@ -244,14 +245,14 @@ __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int 
     return d <= 0 ? 0u : d >= 32 ? 0xffffffffu : (1u << d) - 1u;
   };
 #pragma unroll
-  for (int j = 0; j < 2; ++j) bits[j] = (~below(from, j) | below(a.sinks, j)) & below(end, j);
+  for (int j = 0; j < 4; ++j) bits[j] = (~below(from, j) | below(a.sinks, j)) & below(end, j);
   if (a.mode == DOMINO_MASK_TREE) {
-    const int j0 = max(0, s0 - w.ctx), j1 = min(w.n, s0 + kHalf - w.ctx);
+    const int j0 = max(0, s0 - w.ctx), j1 = min(w.n, s0 + kBN - w.ctx);
     for (int j = j0; j < j1; ++j) {
       const int at = w.ctx + j - s0;
       const uint32_t bit = __ldg(mask_row + j) ? 1u << (at & 31) : 0u;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) bits[q] |= (at >> 5) == q ? bit : 0u;
+      for (int q = 0; q < 4; ++q) bits[q] |= (at >> 5) == q ? bit : 0u;
     }
   }
 }
@@ -262,12 +263,12 @@ __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int 
 __device__ __noinline__ void add_non_finite(const AttnArgs& a, const Unit& w, int b, int h, int k0, int k1, int i, int low,
                                             const uint8_t* mask_row, int e0, float* o) {
   const uint16_t* v = (const uint16_t*)a.v + (int64_t)b * a.rs + (int64_t)h * a.hs;
-  for (int k = 2 * k0; k < 2 * k1; ++k) {
-    const int tile0 = w.kt.slot(k >> 1, kBN), s0 = tile0 + (k & 1) * kHalf;
-    if (all_seen(a, w, tile0, kBN)) continue;
-    uint32_t bits[2];
+  for (int k = k0; k < k1; ++k) {
+    const int s0 = w.kt.slot(k, kBN);
+    if (all_seen(a, w, s0)) continue;
+    uint32_t bits[4];
     seen_bits(a, w, i, low, mask_row, s0, bits);
-    for (int j = 0; j < kHalf; ++j) {
+    for (int j = 0; j < kBN; ++j) {
       if (!((bits[j >> 5] >> (j & 31)) & 1u)) continue;
       const uint16_t* row = v + (int64_t)(s0 + j) * a.ss;
       for (int e = 0; e < 32 && e0 + e < a.D; ++e) {
@@ -300,10 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   uint64_t* full = (uint64_t*)(stage + C::kStage);
   uint64_t* empty = full + slots;
   uint64_t* v_clean = empty + slots;
-  uint64_t* s_ready = v_clean + slots;  // [4]: per group and half
-  uint64_t* p_ready = s_ready + 4;      // [4]
-  uint64_t* o_done = p_ready + 4;       // [4]
-  uint64_t* q_ready = o_done + 4;
+  uint64_t* s_ready = v_clean + slots;  // [2]: per group
+  uint64_t* p_ready = s_ready + 2;      // [4]: per group and half
+  uint64_t* o_done = p_ready + 4;       // [2]: per group, once per row tile
+  uint64_t* q_ready = o_done + 2;
   uint64_t* q_free = q_ready + 1;
   uint64_t* drain = q_free + 1;
   int64_t* s_prefix = (int64_t*)(drain + 1);
@@ -327,9 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mbar_init(&empty[s], 1);
       mbar_init(&v_clean[s], 2);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&s_ready[s], 1);
-      mbar_init(&p_ready[s], 4);
+      mbar_init(&p_ready[2 * s], 4);
+      mbar_init(&p_ready[2 * s + 1], 4);
       mbar_init(&o_done[s], 1);
     }
     mbar_init(q_ready, 2);
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           mbar_wait(&full[j % slots], (uint32_t)((j / slots) & 1), nullptr, ctl, p.timeout_ns);
       }
     } else if (warp == 1) {
-      const uint32_t id_s = idesc_bf16_f32(128, kHalf);
+      const uint32_t id_s = idesc_bf16_f32(128, kBN);
       const uint32_t id_o = idesc_bf16_f32(128, C::DP) | (1u << 16);  // B is MN-major
       const bool leader = elect_one();
       uint32_t item = 0, done[2] = {0, 0};  // key tiles each group has had
@@ -470,31 +472,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (s >= slots) { s -= slots; ph ^= 1u; }
       };
       const uint32_t q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
-      auto scores = [&](int qt, int g, int half, uint64_t* then) {  // S = Q K^T of half a key tile
+      auto scores = [&](int qt, int g) {  // S_g = Q K^T
         const uint64_t ad = sdesc_k_sw128(q_addr + (uint32_t)qt * C::kQBytes);
-        const uint64_t bd = sdesc_k_sw128(ring_addr + (uint32_t)ks * C::kTile + (uint32_t)(half * kHalf * 128));
+        const uint64_t bd = sdesc_k_sw128(ring_addr + (uint32_t)ks * C::kTile);
         if (leader) {
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_bf16(tmem + (uint32_t)(g * 128 + half * kHalf), ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k),
+              umma_bf16(tmem + (uint32_t)(g * 128), ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k),
                         bd + (uint64_t)(kb * (kBN * 128 / 16) + 2 * k), id_s, (kb | k) ? 1u : 0u);
-          umma_commit(&s_ready[g * 2 + half]);
-          if (then) umma_commit(then);
+          umma_commit(&s_ready[g]);
         }
         __syncwarp();
       };
-      auto values = [&](int g, int half, bool first) {  // O += P V of half a key tile
-        const uint64_t bd = sdesc_mn_sw128(ring_addr + (uint32_t)vs * C::kTile + (uint32_t)(half * kHalf * 128));
-        if (leader) {
+      auto values = [&](int g, bool first, bool last) {  // O_g += P_g V
 #pragma unroll
-          for (int k = 0; k < kHalf / 16; ++k)
-            umma_bf16_ts(tmem + kOCol + (uint32_t)(g * C::DP), tmem + (uint32_t)(g * 128 + half * kHalf + 8 * k),
-                         bd + (uint64_t)(k * (16 * 128 / 16)), id_o, (first && k == 0) ? 0u : 1u);
-          umma_commit(&o_done[g * 2 + half]);
+        for (int half = 0; half < 2; ++half) {
+          wait(&p_ready[g * 2 + half], done[g] & 1u);
+          if (!ok) return;
+          const uint64_t bd = sdesc_mn_sw128(ring_addr + (uint32_t)vs * C::kTile + (uint32_t)(half * kHalf * 128));
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < kHalf / 16; ++k)
+              umma_bf16_ts(tmem + kOCol + (uint32_t)(g * C::DP), tmem + (uint32_t)(g * 128 + half * (kHalf / 2) + 8 * k),
+                           bd + (uint64_t)(k * (16 * 128 / 16)), id_o, (first && half == 0 && k == 0) ? 0u : 1u);
+            if (half == 1 && last) umma_commit(&o_done[g]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        ++done[g];
       };
       auto release = [&](uint64_t* bar) {
         if (leader) umma_commit(bar);
@@ -511,54 +518,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int n = k1 - k0;
         if (n == 0) continue;
         wait(q_ready, item & 1u);
-        // A half's scores go out once the product of the tile before in its S has been issued:
+        // A tile's scores go out once the product of the tile before in its S has been issued:
         // NQ = 2: tile t + 1 of both groups after tile t; NQ = 1: tile t + 2 after tile t.
         constexpr int kAhead = NQ == 2 ? 1 : 2;
         for (int t = 0; t < kAhead && t < n && ok; ++t) {
           wait(&full[ks], kph);
           if (!ok) break;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint64_t* then = half == 1 && t + 1 == n ? q_free : nullptr;
-            if (NQ == 2) {
-              scores(0, 0, half, nullptr);
-              scores(1, 1, half, then);
-            } else {
-              scores(0, t, half, then);
-            }
+          if (NQ == 2) {
+            scores(0, 0);
+            scores(1, 1);
+          } else {
+            scores(0, t);
           }
+          if (t + 1 == n) release(q_free);
           release(&empty[ks]);
           step(ks, kph);
         }
         for (int t = 0; t < n && ok; ++t) {
           const bool more = t + kAhead < n;
-          wait(&v_clean[vs], vph);
-          wait(&full[vs], vph);
-          if (more) wait(&full[ks], kph);
+          wait(&v_clean[vs], vph);  // and so it is full
+          if (NQ == 2) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint64_t* then = half == 1 && t + kAhead + 1 == n ? q_free : nullptr;
-            if (NQ == 2) {
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                wait(&p_ready[g * 2 + half], done[0] & 1u);
-                if (!ok) break;
-                values(g, half, t == 0 && half == 0);
-                if (more) scores(g, g, half, g == 1 ? then : nullptr);
-              }
-            } else {
-              const int g = t & 1;
-              wait(&p_ready[g * 2 + half], done[g] & 1u);
+            for (int g = 0; g < 2; ++g) {
+              values(g, t == 0, t + 1 == n);
+              if (more && g == 0) wait(&full[ks], kph);
               if (!ok) break;
-              values(g, half, t < 2 && half == 0);
-              if (more) scores(0, g, half, then);
+              if (more) scores(g, g);
             }
+          } else {
+            const int g = t & 1;
+            values(g, t < 2, t + 2 >= n);
+            if (more) wait(&full[ks], kph);
+            if (!ok) break;
+            if (more) scores(0, g);
           }
           if (!ok) break;
-          ++done[NQ == 2 ? 0 : t & 1];
           release(&empty[vs]);
           step(vs, vph);
           if (more) {
+            if (t + kAhead + 1 == n) release(q_free);
             release(&empty[ks]);
             step(ks, kph);
           }
@@ -606,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       // or a NaN in the product, so these are cleared here and the row tile is marked.
       for (int k = k0; k < k1; ++k) {
         if (!mbar_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
-        if (!all_seen(a, w, w.kt.slot(k, kBN), kBN)) {
+        if (!all_seen(a, w, w.kt.slot(k, kBN))) {
           uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
           bool bad = false;
 #pragma unroll 8
@@ -644,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const uint32_t s_col = tmem + lanes + (uint32_t)(g * 128);
     const uint32_t o_col = tmem + lanes + kOCol + (uint32_t)(g * C::DP);
     uint8_t* my_stage = stage + (warp - 4) * 4096;
-    uint32_t item = 0, tiles = 0;
+    uint32_t item = 0, tiles = 0, done_items = 0;
     bool ok = true;
     Unit w;
     int cur = -1, i = 0, low = 0;
@@ -652,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     int64_t row0 = 0;  // this thread's row for kv head 0, in rows of head_dim
     const uint8_t* mask_row = nullptr;
     // NQ = 2: where this lane stores 16 bytes of 8 of its warp's rows (kv head 0), and which there are.
-    int64_t out_at[8] = {};
+    int out_at[8] = {};  // from the row tile's first row
     uint32_t out_rows = 0;
     while (walk.len > 0 && walk.u < units && ok) {
       const int b = walk.u / p.row_tiles, h = walk.h;
@@ -670,7 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int r = j * 4 + (lane >> 3);
-              out_at[j] = __shfl_sync(0xffffffffu, row0, r) * a.D + (lane & 7) * 8;
+              const int pq = w.r0 + g * 128 + quarter * 32 + r;
+              out_at[j] = ((pq / G - w.i_first) * a.hq + pq % G) * a.D + (lane & 7) * 8;
               out_rows |= g * 128 + quarter * 32 + r < w.rows ? 1u << j : 0u;
             }
           }
@@ -683,83 +682,79 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       walk.next(w.cnt, hkv);
       if (k0 == k1) continue;
       const int64_t row = row0 + h * G;
+      __nv_bfloat16* out_tile = (__nv_bfloat16*)a.out + ((int64_t)(w.q0 + w.i_first) * a.hq + h * G) * a.D;
       float m = -INFINITY, l = 0.0f;  // m: log2 units
       bool first = true;
-      for (int k = NQ == 2 ? k0 : k0 + g; k < k1 && ok; k += NQ == 2 ? 1 : 2, ++tiles) {
+      for (int k = NQ == 2 ? k0 : k0 + g; k < k1; k += NQ == 2 ? 1 : 2, ++tiles, first = false) {
+        const int s0 = w.kt.slot(k, kBN);
+        // With these scores the group's product before is done too: it was issued before them.
+        ok = warp_wait(&s_ready[g], tiles & 1u, s_abort, ctl, p.timeout_ns);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[kBN];
+#pragma unroll
+        for (int c = 0; c < kBN; c += 32) tmem_ld32_nowait(s_col + c, s + c);
+        tmem_wait_ld();
+        if (!all_seen(a, w, s0)) {
+          uint32_t bits[4];
+          seen_bits(a, w, i, low, mask_row, s0, bits);
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+        }
+        float m4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) m4[c] = max3(__uint_as_float(s[c]), __uint_as_float(s[c + 4]), __uint_as_float(s[c + 8]));
+#pragma unroll
+        for (int c = 12; c < 124; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(s[124 + e]));
+        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * p.c;
+        const bool grow = live && mx > m + kLazy;  // from -inf: any finite maximum
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = grow ? mx : m;
+          const float f = m == m_new || m == -INFINITY ? 1.0f : ex2(m - m_new);
+          m = m_new;
+          l *= f;
+          if (!first) {
+#pragma unroll 1
+            for (int c = 0; c < C::DP; c += 32) {
+              uint32_t o[32];
+              tmem_ld32_nowait(o_col + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_col + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float m_use = m == -INFINITY ? 0.0f : m;
+        const float2 c2 = make_float2(p.c, p.c), n2 = make_float2(-m_use, -m_use);
+        float2 sum2[2] = {make_float2(0, 0), make_float2(0, 0)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int s0 = w.kt.slot(k, kBN) + half * kHalf;
-          const uint32_t col = s_col + (uint32_t)(half * kHalf);
-          // With these scores the group's product before the last one is done too.
-          ok = warp_wait(&s_ready[g * 2 + half], tiles & 1u, s_abort, ctl, p.timeout_ns);
-          if (!ok) break;
-          tc_fence_after();
-          uint32_t s[kHalf];
-          tmem_ld32_nowait(col, s);
-          tmem_ld32_nowait(col + 32, s + 32);
-          tmem_wait_ld();
-          if (!all_seen(a, w, s0, kHalf)) {
-            uint32_t bits[2];
-            seen_bits(a, w, i, low, mask_row, s0, bits);
-#pragma unroll
-            for (int c = 0; c < kHalf; ++c)
-              if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
-          }
-          float m4[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) m4[c] = max3(__uint_as_float(s[c]), __uint_as_float(s[c + 4]), __uint_as_float(s[c + 8]));
-#pragma unroll
-          for (int c = 12; c < 60; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(s[60 + e]));
-          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * p.c;
-          const bool grow = live && mx > m + kLazy;  // from -inf: any finite maximum
-          if (__any_sync(0xffffffffu, grow)) {
-            const float m_new = grow ? mx : m;
-            const float f = m == m_new || m == -INFINITY ? 1.0f : ex2(m - m_new);
-            m = m_new;
-            l *= f;
-            if (half > 0 || !first) {
-              // The product before this one; the next waits for this half's weights.
-              ok = warp_wait(&o_done[g * 2 + (half ^ 1)], half ? tiles & 1u : (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < C::DP; c += 32) {
-                uint32_t o[32];
-                tmem_ld32_nowait(o_col + c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(o_col + c, o);
-              }
-              tmem_wait_st();
-            }
-          }
-          const float m_use = m == -INFINITY ? 0.0f : m;
-          const float2 c2 = make_float2(p.c, p.c), n2 = make_float2(-m_use, -m_use);
-          float2 sum2[2] = {make_float2(0, 0), make_float2(0, 0)};
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), c2, n2);
+            const int e = half * kHalf + 2 * c;
+            float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, n2);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
             pk[c] = pack_bf16(x.x, x.y);
             sum2[c & 1] = add2(sum2[c & 1], x);
           }
-          tmem_st32(col, pk);
-          l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+          tmem_st32(s_col + 32 * half, pk);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_ready[g * 2 + half]);
         }
-        first = false;
+        l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
       }
-      if (ok && !first) ok = warp_wait(&o_done[g * 2 + 1], (tiles - 1u) & 1u, s_abort, ctl, p.timeout_ns);
+      if (ok && !first) ok = warp_wait(&o_done[g], done_items++ & 1u, s_abort, ctl, p.timeout_ns);
       // Whoever shares the epilogue goes on together or not at all: nobody is left at a barrier.
       if (NQ == 1) s_ml[g * 128 + trow] = make_float2(m, l);
       ok = NQ == 1 ? group_all<256>(1, ok) : group_all<128>(1 + g, ok);
@@ -845,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             for (int j = 0; j < 8; ++j) {
               const int r = j * 4 + (lane >> 3);
               if (((out_rows >> j) & 1) && c + x * 8 < a.D)
-                *(uint4*)((__nv_bfloat16*)a.out + out_at[j] + h * G * a.D + c) = *(const uint4*)(my_stage + r * 128 + ((x ^ (r & 7)) << 4));
+                *(uint4*)(out_tile + out_at[j] + c) = *(const uint4*)(my_stage + r * 128 + ((x ^ (r & 7)) << 4));
             }
             __syncwarp();
           } else if (live) {
