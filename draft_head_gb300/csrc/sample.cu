@@ -33,7 +33,7 @@ namespace {
 constexpr int kThr = 256, kWarps = kThr / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kBins = 1024, kNear = 768;  // 64 bins a nat up to 12 nats, then 2 a nat; the last: the rest
-constexpr int kList = 1536, kPer = kList / kThr;
+constexpr int kList = 2048, kPer = kList / kThr;
 constexpr int kMaxSlice = 48 * 1024;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -192,25 +192,50 @@ __device__ __forceinline__ void find(Smem& s, bool by_mass, double target, int& 
 __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t size) {
   cluster_sync();
   const int per = kBins / (int)size;
-  for (int x = threadIdx.x; x < per; x += kThr) {
+  // A thread sums up to four CTAs' counts of a bin, all loads in flight at once.
+  const int tpb = size > 4 ? (int)size / 4 : 1;  // threads per bin
+  const int first = threadIdx.x % tpb;
+  for (int x = threadIdx.x / tpb; x < per; x += kThr / tpb) {
     const int b = (int)rank * per + x;
-    uint32_t c = 0, hi = 0, lo = 0;
-    u64 m = 0;
-    for (uint32_t k = 0; k < size; ++k) {
-      c += ld_u32(dsmem(&s.hist[0][b], k));
-      hi = ld_u32(dsmem(&s.hist[1][b], k));
-      lo = ld_u32(dsmem(&s.hist[2][b], k));
-      m += ((u64)hi << 15) + lo;
+    uint32_t c[4], hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t k = (uint32_t)(first + tpb * j);
+      const bool on = k < size;
+      c[j] = on ? ld_u32(dsmem(&s.hist[0][b], k)) : 0u;
+      hi[j] = on ? ld_u32(dsmem(&s.hist[1][b], k)) : 0u;
+      lo[j] = on ? ld_u32(dsmem(&s.hist[2][b], k)) : 0u;
     }
-    s.cnt[b] = c;
-    s.mass[b] = m;
+    uint32_t cs = c[0] + c[1] + c[2] + c[3];
+    u64 m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m += ((u64)hi[j] << 15) + lo[j];
+    for (int o = 1; o < tpb; o <<= 1) {
+      cs += __shfl_xor_sync(0xffffffffu, cs, o);
+      m += __shfl_xor_sync(0xffffffffu, m, o);
+    }
+    if (first == 0) {
+      s.cnt[b] = cs;
+      s.mass[b] = m;
+    }
   }
   cluster_sync();
-  for (int b = threadIdx.x; b < kBins; b += kThr) {
-    const uint32_t k = (uint32_t)(b / per);
-    if (k != rank) {
-      s.cnt[b] = ld_u32(dsmem(&s.cnt[b], k));
-      s.mass[b] = ld_u64(dsmem(&s.mass[b], k));
+  if (size > 1) {
+    uint32_t c[kBins / kThr];
+    u64 m[kBins / kThr];
+#pragma unroll
+    for (int j = 0; j < kBins / kThr; ++j) {
+      const int b = threadIdx.x + j * kThr;
+      c[j] = ld_u32(dsmem(&s.cnt[b], (uint32_t)(b / per)));
+      m[j] = ld_u64(dsmem(&s.mass[b], (uint32_t)(b / per)));
+    }
+#pragma unroll
+    for (int j = 0; j < kBins / kThr; ++j) {
+      const int b = threadIdx.x + j * kThr;
+      if ((uint32_t)(b / per) != rank) {
+        s.cnt[b] = c[j];
+        s.mass[b] = m[j];
+      }
     }
   }
   __syncthreads();
@@ -238,28 +263,40 @@ __device__ __forceinline__ void gather(Smem& s, const float* vals, int n, int id
   }
 }
 
-// CTA 0: orders the list (largest key first), in place. kPer keys a thread, each ranked against all.
+// CTA 0: orders the list (largest key first), in place. Up to a key per thread, each is ranked
+// against all; beyond, a bitonic sort (66 short steps for 2048 keys).
 __device__ __forceinline__ void order_list(Smem& s, int n) {
-  u64 key[kPer];
-  int rank[kPer];
+  if (n <= kThr) {
+    const u64 key = (int)threadIdx.x < n ? s.list[threadIdx.x] : 0;
+    int rank = 0, x = 0;
+    for (; x + 8 <= n; x += 8) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int x = threadIdx.x + j * kThr;
-    key[j] = x < n ? s.list[x] : 0;
-    rank[j] = 0;
+      for (int j = 0; j < 8; ++j) rank += s.list[x + j] > key;
+    }
+    for (; x < n; ++x) rank += s.list[x] > key;
+    __syncthreads();
+    if ((int)threadIdx.x < n) s.list[rank] = key;
+    __syncthreads();
+    return;
   }
-  const int each = (n + kThr - 1) / kThr;
-  for (int x = 0; x < n; ++x) {
-    const u64 k = s.list[x];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (j < each) rank[j] += k > key[j];
+  int size = 2 * kThr;
+  while (size < n) size <<= 1;
+  for (int x = n + threadIdx.x; x < size; x += kThr) s.list[x] = 0;
+  __syncthreads();
+  for (int k = 2; k <= size; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < size / 2; i += kThr) {
+        const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1)), hi = lo | j;
+        const u64 x = s.list[lo], y = s.list[hi];
+        if ((x < y) == ((lo & k) == 0)) {
+          s.list[lo] = y;
+          s.list[hi] = x;
+        }
+      }
+      __syncthreads();
+    }
   }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (threadIdx.x + j * kThr < n) s.list[rank[j]] = key[j];
-  __syncthreads();
 }
 
 // CTA 0, ordered list of n keys: the key of the last that stays, when `cnt` more may stay (cnt > 0),
@@ -309,7 +346,8 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
   const int skew = (int)(((uintptr_t)src & 15u) / sizeof(T));
   const uint4* vec = (const uint4*)(src - skew);
   const int id0 = s0 - skew, n = s1 > s0 ? (skew + s1 - s0 + kVec - 1) / kVec * kVec : 0;
-  u64 best = 0;
+  float top = -INFINITY;
+  int top_id = 0;  // the lowest id of this thread's largest logit: its ids rise
   constexpr int kUnroll = 8;
   for (int q0 = t; q0 < n / kVec; q0 += kThr * kUnroll) {
     uint4 x[kUnroll];
@@ -330,9 +368,9 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
         const int id = id0 + q * kVec + e;
         if (id < s0 || id >= s1) {
           f[e] = __uint_as_float(0x7fffffffu);
-        } else {
-          const u64 k = value_id_key(f[e], (uint32_t)id);
-          best = k > best ? k : best;
+        } else if (f[e] > top) {
+          top = f[e];
+          top_id = id;
         }
       }
 #pragma unroll
@@ -355,7 +393,7 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
     }
     return;
   }
-  best = block_max(best, s.red);
+  u64 best = block_max(value_id_key(top, (uint32_t)top_id), s.red);
   if (t < (int)size) st_u64(dsmem(&s.part_key[rank], (uint32_t)t), best);
   if (t == 0) s.n_list = 0;
   clear_histogram(s);
