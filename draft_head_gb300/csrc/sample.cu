@@ -10,16 +10,20 @@
 // A cluster of up to 16 CTAs takes a row, each a slice that it reads once from
 // memory and keeps in shared memory (fp32). Steps, each over the slice:
 //   maximum            merged over the cluster; ends a greedy row
-//   histogram          of (max - logit) / T: 1/64 nat a bin up to 12, then half
-//                      a nat, with counts and weights (integers of 2^-30, so that no order
-//                      of the atomics changes them); summed over the cluster, and
-//                      every CTA finds the bins of the two bounds in the sums
+//   histogram          of (max - logit) / T in kNear bins, and one for the rest, with
+//                      counts and (top-p without top-k) weights; integers, so that no
+//                      order of the atomics changes them. A bin's weight is kept as what its
+//                      tokens lack to the weight at its edge, 2^-21 of that a unit: one 32-bit
+//                      atomic, where a sum of weights would need two. Summed over the
+//                      cluster; every CTA finds the bounds' bins in the sums
 //   short list         when all that can stay are at most kList tokens (peaked
-//                      rows): they go to CTA 0, which orders them and does the rest
+//                      rows): they go to CTA 0, which does the rest by itself
 //   otherwise          the bin of each bound alone goes to CTA 0, which finds the
 //                      exact key; a bin of more than kList tokens (equal logits, say)
 //                      is first split by the bits of the keys. Every CTA then draws
 //                      from what stayed of its slice, reading its noise.
+// In CTA 0's list, which it holds in registers, a bound is found by histograms over the keys' bits,
+// each 1024 times finer than the one before.
 // Bound by memory (the logits once, the noise where tokens stay) when there are many
 // rows, and by the cluster's barriers (about a microsecond each) for one row.
 #include <math.h>
@@ -32,7 +36,7 @@ namespace {
 
 constexpr int kThr = 256, kWarps = kThr / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kBins = 1024, kNear = 768;  // 64 bins a nat up to 12 nats, then 2 a nat; the last: the rest
+constexpr int kBins = 1024, kNear = 1023;  // the first histogram: kNear bins, then one for the rest
 constexpr int kList = 2048, kPer = kList / kThr;
 constexpr int kMaxSlice = 48 * 1024;
 
@@ -70,18 +74,12 @@ __device__ __forceinline__ void st_u32(uint32_t a, uint32_t v) {
 __device__ __forceinline__ void st_u64(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t add_u32(uint32_t a, uint32_t v) {
-  uint32_t o;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(o) : "r"(a), "r"(v) : "memory");
-  return o;
-}
-
 typedef unsigned long long u64;
 
 // Shared memory of a CTA before its slice.
 struct Smem {
   union {
-    uint32_t hist[3][kBins];  // counts; weights in two 15-bit halves
+    uint32_t hist[3][kBins];  // counts; lacks, or weights in two 15-bit halves
     u64 list[kList];          // CTA 0: keys gathered from the cluster
   };
   u64 mass[kBins];  // sums over the cluster (a CTA holds those of its bins before they are shared)
@@ -91,16 +89,19 @@ struct Smem {
   float part_sum[kMaxCluster];
   u64 red[kWarps];
   u64 red2[kWarps];
+  int part_n[kMaxCluster];
   float redf[kWarps];
   u64 result[4];  // CTA 0's answer
-  int n_list;
+  int n_local;
   int found_bin;
-  u64 found_cnt, found_mass;
+  u64 found_cnt, found_mass, found_here;
+  u64 rest_w;
 };
 
 struct Row {
   float lmax, inv_t, temp;
   float min_p;
+  float scale;  // bins per nat
   __device__ __forceinline__ float dist(float l) const { return l == lmax ? 0.0f : (lmax - l) * inv_t; }
   // Weight of a token in units of 2^-30.
   __device__ __forceinline__ uint32_t fixed(float d) const {
@@ -108,15 +109,26 @@ struct Row {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(d * -1.4426950408889634f));
     return (uint32_t)__float2uint_rn(w * 1073741824.0f);
   }
+  // Monotone in d, so in the order of the logits.
+  __device__ __forceinline__ int bin(float d) const {
+    const float b = d * scale;
+    return b < (float)kNear ? (int)b : kNear;
+  }
+  __device__ __forceinline__ float near_weight(float l) const {  // to 2^-22 and 2^-24 of (max - l) / T
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((l - lmax) * (inv_t * 1.4426950408889634f)));
+    return l == lmax ? 1.0f : w;
+  }
+  // Weight at a bin's upper edge, and what a token of the bin lacks to it, in units of 2^-21 of it
+  // (a bin is at most 1/16 nat, so below 2^17).
+  __device__ __forceinline__ float edge(int b) const { return exp2f((float)b * (-1.4426950408889634f / scale)); }
+  __device__ __forceinline__ uint32_t lack(float d, int b) const {
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(((float)b - d * scale) * (1.4426950408889634f / scale)));
+    return (uint32_t)__float2uint_rn((1.0f - w) * 2097152.0f);
+  }
   __device__ __forceinline__ float weight(float l) const { return l == lmax ? 1.0f : expf((l - lmax) * inv_t); }
 };
-
-__device__ __forceinline__ int bin_of(float d) {
-  // Monotone in d, so in the order of the logits.
-  if (d < 12.0f) return (int)(d * 64.0f);
-  const float b = (d - 12.0f) * 2.0f + (float)kNear;
-  return b < (float)(kBins - 1) ? (int)b : kBins - 1;
-}
 
 __device__ __forceinline__ u64 block_max(u64 v, u64* red) {
   v = warp_max_u64(v);
@@ -158,38 +170,52 @@ __device__ __forceinline__ void block_scan(u64& a, u64& b, u64* red, u64* red2) 
   b = by + y - b;
 }
 
-// First place in cnt / mass (as `by_mass` says) where the sum up to and with it reaches
-// `target` (the last one if none does). All threads get it, and the sums before it.
-__device__ __forceinline__ void find(Smem& s, bool by_mass, double target, int& bin, u64& cnt_before, u64& mass_before) {
+// First bin where the sum up to and with it reaches `target` (the last one if none does), of kBins
+// bins whose count and weight `at(bin, count, weight)` gives. All threads get the bin, the sums before it
+// and its count.
+template <typename At>
+__device__ __forceinline__ void find(Smem& s, At at, bool by_mass, double target, int& bin, u64& cnt_before, u64& mass_before, u64& here) {
   constexpr int kEach = kBins / kThr;
   const int b0 = threadIdx.x * kEach;
-  u64 c = 0, m = 0;
+  u64 c[kEach], m[kEach], cs = 0, ms = 0;
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) { c += s.cnt[b0 + j]; m += s.mass[b0 + j]; }
-  u64 cb = c, mb = m;
+  for (int j = 0; j < kEach; ++j) {
+    at(b0 + j, c[j], m[j]);
+    cs += c[j];
+    ms += m[j];
+  }
+  u64 cb = cs, mb = ms;
   block_scan(cb, mb, s.red, s.red2);
-  const double before = by_mass ? (double)mb : (double)cb, after = by_mass ? (double)(mb + m) : (double)(cb + c);
+  const double before = by_mass ? (double)mb : (double)cb, after = by_mass ? (double)(mb + ms) : (double)(cb + cs);
   if ((threadIdx.x == 0 || before < target) && (after >= target || threadIdx.x == kThr - 1)) {
-    int j = 0;
-    for (; j < kEach - 1; ++j) {
-      const u64 nc = cb + s.cnt[b0 + j], nm = mb + s.mass[b0 + j];
-      if ((by_mass ? (double)nm : (double)nc) >= target) break;
-      cb = nc;
-      mb = nm;
+    bool done = false;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      if (!done) {
+        done = (by_mass ? (double)(mb + m[j]) : (double)(cb + c[j])) >= target || j == kEach - 1;
+        if (done) {
+          s.found_bin = b0 + j;
+          s.found_cnt = cb;
+          s.found_mass = mb;
+          s.found_here = c[j];
+        }
+        cb += c[j];
+        mb += m[j];
+      }
     }
-    s.found_bin = b0 + j;
-    s.found_cnt = cb;
-    s.found_mass = mb;
   }
   __syncthreads();
   bin = s.found_bin;
   cnt_before = s.found_cnt;
   mass_before = s.found_mass;
+  here = s.found_here;
   __syncthreads();
 }
 
-// Sums the CTAs' histograms: each CTA takes kBins / size bins, then all read all sums.
-__device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t size) {
+// Sums the CTAs' histograms (their first `arrays` arrays): each CTA takes kBins / size bins, `mass_of`
+// gives a bin's weight from the sums, then all read all.
+template <typename MassOf>
+__device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t size, int arrays, MassOf mass_of) {
   cluster_sync();
   const int per = kBins / (int)size;
   // A thread sums up to four CTAs' counts of a bin, all loads in flight at once.
@@ -197,26 +223,23 @@ __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t
   const int first = threadIdx.x % tpb;
   for (int x = threadIdx.x / tpb; x < per; x += kThr / tpb) {
     const int b = (int)rank * per + x;
-    uint32_t c[4], hi[4], lo[4];
+    uint32_t v[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t k = (uint32_t)(first + tpb * j);
-      const bool on = k < size;
-      c[j] = on ? ld_u32(dsmem(&s.hist[0][b], k)) : 0u;
-      hi[j] = on ? ld_u32(dsmem(&s.hist[1][b], k)) : 0u;
-      lo[j] = on ? ld_u32(dsmem(&s.hist[2][b], k)) : 0u;
-    }
-    uint32_t cs = c[0] + c[1] + c[2] + c[3];
-    u64 m = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m += ((u64)hi[j] << 15) + lo[j];
-    for (int o = 1; o < tpb; o <<= 1) {
-      cs += __shfl_xor_sync(0xffffffffu, cs, o);
-      m += __shfl_xor_sync(0xffffffffu, m, o);
+      for (int y = 0; y < 3; ++y) v[y][j] = k < size && y < arrays ? ld_u32(dsmem(&s.hist[y][b], k)) : 0u;
+    }
+    u64 sum[3];
+#pragma unroll
+    for (int y = 0; y < 3; ++y) {
+      sum[y] = (u64)v[y][0] + v[y][1] + v[y][2] + v[y][3];
+      if (y < arrays)
+        for (int o = 1; o < tpb; o <<= 1) sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], o);
     }
     if (first == 0) {
-      s.cnt[b] = cs;
-      s.mass[b] = m;
+      s.cnt[b] = (uint32_t)sum[0];
+      s.mass[b] = arrays > 1 ? mass_of(b, sum[0], sum[1], sum[2]) : 0;
     }
   }
   cluster_sync();
@@ -227,7 +250,7 @@ __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t
     for (int j = 0; j < kBins / kThr; ++j) {
       const int b = threadIdx.x + j * kThr;
       c[j] = ld_u32(dsmem(&s.cnt[b], (uint32_t)(b / per)));
-      m[j] = ld_u64(dsmem(&s.mass[b], (uint32_t)(b / per)));
+      m[j] = arrays > 1 ? ld_u64(dsmem(&s.mass[b], (uint32_t)(b / per))) : 0;
     }
 #pragma unroll
     for (int j = 0; j < kBins / kThr; ++j) {
@@ -246,89 +269,122 @@ __device__ __forceinline__ void add_weight(Smem& s, int b, uint32_t w) {
   if (w >> 15) atomicAdd(&s.hist[1][b], w >> 15);
   if (w & 0x7fffu) atomicAdd(&s.hist[2][b], w & 0x7fffu);
 }
+__device__ __forceinline__ u64 whole_mass(int, u64, u64 hi, u64 lo) { return (hi << 15) + lo; }
 __device__ __forceinline__ void clear_histogram(Smem& s) {
   for (int x = threadIdx.x; x < 3 * kBins; x += kThr) (&s.hist[0][0])[x] = 0u;
 }
 
-// Gathers the keys for which `in` holds in CTA 0's list.
+// Gathers the keys for which `in` holds, kList at most in all, in CTA 0's list, CTA after CTA;
+// returns their number. Two barriers: the CTAs' numbers, and the copies.
 template <typename In>
-__device__ __forceinline__ void gather(Smem& s, const float* vals, int n, int id0, In in) {
-  const uint32_t counter = dsmem(&s.n_list, 0);
-  for (int p = threadIdx.x; p < n; p += kThr) {
-    const float l = vals[p];
-    if (l == l && in(l, id0 + p)) {
-      const uint32_t at = add_u32(counter, 1u);
-      if (at < (uint32_t)kList) st_u64(dsmem(&s.list[at], 0), value_id_key(l, (uint32_t)(id0 + p)));
-    }
-  }
-}
-
-// CTA 0: orders the list (largest key first), in place. Up to a key per thread, each is ranked
-// against all; beyond, a bitonic sort (66 short steps for 2048 keys).
-__device__ __forceinline__ void order_list(Smem& s, int n) {
-  if (n <= kThr) {
-    const u64 key = (int)threadIdx.x < n ? s.list[threadIdx.x] : 0;
-    int rank = 0, x = 0;
-    for (; x + 8 <= n; x += 8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) rank += s.list[x + j] > key;
-    }
-    for (; x < n; ++x) rank += s.list[x] > key;
-    __syncthreads();
-    if ((int)threadIdx.x < n) s.list[rank] = key;
-    __syncthreads();
-    return;
-  }
-  int size = 2 * kThr;
-  while (size < n) size <<= 1;
-  for (int x = n + threadIdx.x; x < size; x += kThr) s.list[x] = 0;
+__device__ __forceinline__ int gather(Smem& s, const float* vals, int n, int id0, uint32_t rank, uint32_t size, In in) {
+  if (threadIdx.x == 0) s.n_local = 0;
   __syncthreads();
-  for (int k = 2; k <= size; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-#pragma unroll 4
-      for (int i = threadIdx.x; i < size / 2; i += kThr) {
-        const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1)), hi = lo | j;
-        const u64 x = s.list[lo], y = s.list[hi];
-        if ((x < y) == ((lo & k) == 0)) {
-          s.list[lo] = y;
-          s.list[hi] = x;
+  for (int p0 = threadIdx.x; p0 < n; p0 += kThr * 8) {
+    float l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) l[j] = p0 + j * kThr < n ? vals[p0 + j * kThr] : __uint_as_float(0x7fffffffu);
+    unsigned hits = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) hits |= l[j] == l[j] && in(l[j], id0 + p0 + j * kThr) ? 1u << j : 0u;
+    if (hits) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((hits >> j) & 1u) {
+          const int at = atomicAdd(&s.n_local, 1);
+          if (at < kList) s.list[at] = value_id_key(l[j], (uint32_t)(id0 + p0 + j * kThr));
         }
-      }
-      __syncthreads();
     }
+  }
+  __syncthreads();
+  const int mine = min(s.n_local, kList);
+  if (size == 1) return mine;
+  if (threadIdx.x < size) st_u32(dsmem(&s.part_n[rank], threadIdx.x), (uint32_t)mine);
+  cluster_sync();
+  int base = 0, all = 0;
+  for (uint32_t k = 0; k < size; ++k) {
+    base += k < rank ? s.part_n[k] : 0;
+    all += s.part_n[k];
+  }
+  if (rank > 0)
+    for (int x = threadIdx.x; x < mine && base + x < kList; x += kThr) st_u64(dsmem(&s.list[base + x], 0), s.list[x]);
+  cluster_sync();
+  return min(all, kList);
+}
+
+// CTA 0's list of n keys, each thread's in registers, with their weights.
+struct List {
+  u64 key[kPer];
+  uint32_t w[kPer];
+};
+
+// The key of the last that stays of the list, and the weight of what stays: the largest key with
+// `cnt` keys at or above it, or (by_mass) with the weight `aim`; 0 if the whole list has less.
+// The list's shared memory is taken for the histograms.
+__device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, uint32_t cnt, double aim, u64* mass_out) {
+  u64 lo = 0, hi = ~0ull, mass = 0;
+  double target = by_mass ? aim : (double)cnt;
+  while (true) {
+    u64 top = 0, bottom = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (v.key[j] && v.key[j] >= lo && v.key[j] <= hi) {
+        top = v.key[j] > top ? v.key[j] : top;
+        bottom = ~v.key[j] > bottom ? ~v.key[j] : bottom;
+      }
+    }
+    hi = block_max(top, s.red);
+    lo = ~block_max(bottom, s.red2);
+    if (top == 0 && hi == 0) {  // an empty list
+      *mass_out = 0;
+      return 0;
+    }
+    int shift = 0;
+    while (((hi - lo) >> shift) >= (u64)kBins) ++shift;
+    clear_histogram(s);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (v.key[j] && v.key[j] >= lo && v.key[j] <= hi) add_weight(s, (int)((hi - v.key[j]) >> shift), v.w[j]);
+    __syncthreads();
+    int bin;
+    u64 c, m, here;
+    find(s, [&](int b, u64& cc, u64& mm) {
+      cc = s.hist[0][b];
+      mm = ((u64)s.hist[1][b] << 15) + s.hist[2][b];
+    }, by_mass, target, bin, c, m, here);
+    const u64 in_bin = ((u64)s.hist[1][bin] << 15) + s.hist[2][bin];
+    target -= by_mass ? (double)m : (double)c;
+    mass += m;
+    if (here == 0) {  // the whole list has less: the last bin, and nothing in it
+      *mass_out = mass;
+      return 0;
+    }
+    hi -= (u64)bin << shift;
+    lo = hi - (((u64)1 << shift) - 1) > hi ? 0 : hi - (((u64)1 << shift) - 1);
+    if (here == 1 || shift == 0) {
+      u64 k = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (v.key[j] && v.key[j] >= lo && v.key[j] <= hi) k = v.key[j];
+      *mass_out = mass + in_bin;
+      return block_max(k, s.red);
+    }
+    __syncthreads();  // before the histogram is cleared
   }
 }
 
-// CTA 0, ordered list of n keys: the key of the last that stays, when `cnt` more may stay (cnt > 0),
-// or when those stay whose weight before them is below `aim` (by_mass). In `mass`, the weight of what stays.
-__device__ __forceinline__ u64 cut_list(Smem& s, const Row& r, int n, bool by_mass, u64 cnt, double aim, u64* mass) {
-  u64 own[kPer], c = 0, m = 0;
-  const int x0 = threadIdx.x * kPer;
+__device__ __forceinline__ void load_list(const Smem& s, const Row& r, int n, List& v) {
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    own[j] = x0 + j < n ? (u64)r.fixed(r.dist(key_value(s.list[x0 + j]))) : 0;
-    m += own[j];
+    const int x = threadIdx.x + j * kThr;
+    v.key[j] = x < n ? s.list[x] : 0;
+    v.w[j] = x < n ? r.fixed(r.dist(key_value(v.key[j]))) : 0;
   }
-  block_scan(m, c, s.red, s.red2);
-  u64 last = ~0ull, sum = 0;  // smallest key that stays
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int x = x0 + j;
-    const bool stays = x < n && (by_mass ? (double)m < aim : (u64)x < cnt);
-    if (stays) {
-      last = s.list[x];
-      sum = m + own[j];
-    }
-    m += own[j];
-  }
-  // The keys fall and the sums grow with the place, so the last one has the extremes.
-  const u64 inv = block_max(~last, s.red);
-  *mass = block_max(sum, s.red);
-  return ~inv;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int slice) {
+__global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int slice) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& s = *(Smem*)smem_raw;
   float* vals = (float*)(smem_raw + ((sizeof(Smem) + 15) & ~(size_t)15));
@@ -395,7 +451,6 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
   }
   u64 best = block_max(value_id_key(top, (uint32_t)top_id), s.red);
   if (t < (int)size) st_u64(dsmem(&s.part_key[rank], (uint32_t)t), best);
-  if (t == 0) s.n_list = 0;
   clear_histogram(s);
   cluster_sync();
   best = 0;
@@ -410,38 +465,60 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
   }
   r.inv_t = 1.0f / r.temp;
   if (top_k >= V) top_k = 0;
+  // 32 nats, and 64 where many tokens may stay, so that a bound inside a peaked row's bulk still
+  // falls into a bin of few; a flat row of 150,000 tokens has about 1,500 in its fullest bin.
+  r.scale = top_k > 128 ? 16.0f : 32.0f;
 
   u64 bound = 0;  // keys from here on stay
   if (top_k > 0 || top_p < 1.0f) {
+    const bool weigh = top_k == 0;  // with a top-k, its set is weighed once it is known
     uint32_t rest = 0;
     u64 rest_w = 0;
-    for (int p = t; p < n; p += kThr) {
-      const float l = vals[p];
-      if (l != l) continue;
-      const float d = r.dist(l);
-      const int b = bin_of(d);
-      if (b < kBins - 1) {
-        if (top_p < 1.0f)
-          add_weight(s, b, r.fixed(d));
-        else
+    if (t == 0) s.rest_w = 0;
+    __syncthreads();
+    for (int p0 = t; p0 < n; p0 += kThr * 4) {
+      float l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) l[j] = p0 + j * kThr < n ? vals[p0 + j * kThr] : __uint_as_float(0x7fffffffu);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (l[j] != l[j]) continue;
+        const float d = r.dist(l[j]);
+        const int b = r.bin(d);
+        if (b < kNear) {
           atomicAdd(&s.hist[0][b], 1u);
-      } else {
-        ++rest;
-        rest_w += r.fixed(d);
+          if (weigh) atomicAdd(&s.hist[1][b], r.lack(d, b));
+        } else {
+          ++rest;
+          if (weigh) rest_w += r.fixed(d);
+        }
       }
     }
-    if (rest) {
-      atomicAdd(&s.hist[0][kBins - 1], rest);
-      atomicAdd(&s.hist[1][kBins - 1], (uint32_t)(rest_w >> 15));
-      atomicAdd(&s.hist[2][kBins - 1], (uint32_t)(rest_w & 0x7fffu));
+    rest = __reduce_add_sync(0xffffffffu, rest);
+    const uint32_t rest_hi = __reduce_add_sync(0xffffffffu, (uint32_t)(rest_w >> 15));
+    const uint32_t rest_lo = __reduce_add_sync(0xffffffffu, (uint32_t)(rest_w & 0x7fffu));
+    if (rest && (t & 31) == 0) {
+      atomicAdd(&s.hist[0][kNear], rest);
+      atomicAdd(&s.rest_w, ((u64)rest_hi << 15) + rest_lo);
     }
-    share_histogram(s, rank, size);
-    int bin_k = kBins - 1, bin_p = kBins - 1;
-    u64 cnt_k = 0, mass_k = 0, cnt_p = 0, mass_p = 0;
-    if (top_k > 0) find(s, false, (double)top_k, bin_k, cnt_k, mass_k);
+    share_histogram(s, rank, size, weigh ? 2 : 1, [&](int b, u64 c, u64 lack, u64) {
+      if (b == kNear) {
+        u64 m = 0;
+        for (uint32_t k = 0; k < size; ++k) m += ld_u64(dsmem(&s.rest_w, k));
+        return m;
+      }
+      return (u64)llrint(((double)c - (double)lack * (1.0 / 2097152.0)) * (double)r.edge(b) * 1073741824.0);
+    });
+    auto sums = [&](int b, u64& c, u64& m) {
+      c = s.cnt[b];
+      m = s.mass[b];
+    };
+    int bin_k = kNear, bin_p = kNear;
+    u64 cnt_k = 0, mass_k = 0, cnt_p = 0, mass_p = 0, here_k = 0, here_p = 0;
+    if (top_k > 0) find(s, sums, false, (double)top_k, bin_k, cnt_k, mass_k, here_k);
     // With no top-k the whole weight is the sum of all bins.
     double total = 0.0;
-    if (top_p < 1.0f && top_k == 0) {
+    if (weigh) {
       u64 m = 0, z = 0;
       for (int b = t; b < kBins; b += kThr) m += s.mass[b];
       u64 before = m;
@@ -450,36 +527,38 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
       __syncthreads();
       total = (double)s.found_mass;
       __syncthreads();
-      find(s, true, (double)top_p * total, bin_p, cnt_p, mass_p);
+      find(s, sums, true, (double)top_p * total, bin_p, cnt_p, mass_p, here_p);
     }
     const int bin_all = min(bin_k, bin_p);
-    const u64 most = (top_k > 0 ? cnt_k + s.cnt[bin_k] : cnt_p + s.cnt[bin_p]);
+    const u64 most = top_k > 0 ? cnt_k + here_k : cnt_p + here_p;
     if (most <= (u64)kList) {
       // All that can stay, to CTA 0.
-      gather(s, vals, n, id0, [&](float l, int) { return bin_of(r.dist(l)) <= bin_all; });
-      cluster_sync();
+      const int m = gather(s, vals, n, id0, rank, size, [&](float l, int) { return r.bin(r.dist(l)) <= bin_all; });
       if (rank != 0) return;
-      int m = s.n_list;
-      order_list(s, m);
+      List v;
+      load_list(s, r, m, v);
       u64 mass;
       if (top_k > 0) {
-        bound = cut_list(s, r, m, false, (u64)top_k, 0.0, &mass);
-        m = min(m, top_k);
+        bound = cut_list(s, v, false, (uint32_t)top_k, 0.0, &mass);
         total = (double)mass;
       }
       if (top_p < 1.0f) {
-        const u64 k = cut_list(s, r, m, true, 0, (double)top_p * total, &mass);
+        if (top_k > 0) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            if (v.key[j] < bound) v.key[j] = 0, v.w[j] = 0;
+        }
+        const u64 k = cut_list(s, v, true, 0, (double)top_p * total, &mass);
         bound = k > bound ? k : bound;
       }
       u64 key = 0;
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int x = t + j * kThr;
-        if (x < m && s.list[x] >= bound) {
-          const float l = key_value(s.list[x]), w = r.weight(l);
+        if (v.key[j] && v.key[j] >= bound) {
+          const float l = key_value(v.key[j]), w = r.weight(l);
           if (w >= r.min_p) {
-            const uint32_t id = key_id(s.list[x]);
+            const uint32_t id = key_id(v.key[j]);
             const u64 c = value_id_key(l / r.temp + g[id], id);
             key = c > key ? c : key;
             sum += w;
@@ -488,12 +567,11 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
       }
       sum = block_sum(sum, s.redf);
       key = block_max(key, s.red);
-      // The drawn token's logit, from the thread that has it.
+      // From the thread that has the drawn token's logit.
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int x = t + j * kThr;
-        if (x < m && key_id(s.list[x]) == key_id(key)) {
-          const float l = key_value(s.list[x]);
+        if (v.key[j] && key_id(v.key[j]) == key_id(key)) {
+          const float l = key_value(v.key[j]);
           a.tokens[row] = (int)key_id(key);
           if (a.logprob) a.logprob[row] = (l == r.lmax ? 0.0f : (l - r.lmax) * r.inv_t) - logf(sum);
         }
@@ -502,16 +580,15 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
     }
 
     // The bound of one of the two filters: the bin's keys in CTA 0's list, ordered.
-    auto select = [&](int bin, u64 cnt_before, u64 mass_before, bool by_mass, u64 count, double aim, u64 floor_key, u64* mass_out) {
+    auto select = [&](int bin, u64 in_bin, u64 cnt_before, u64 mass_before, bool by_mass, u64 count, double aim, u64 floor_key, u64* mass_out) {
       u64 lo = 0, hi = ~0ull;  // keys of the bin in question
-      u64 in_bin = s.cnt[bin];
       bool whole = true;       // all keys of the bin
       while (in_bin > (u64)kList) {
         // Split the keys between the smallest and the largest by their bits.
         u64 kmax = 0, kmin = 0;
         for (int p = t; p < n; p += kThr) {
           const float l = vals[p];
-          if (l != l || bin_of(r.dist(l)) != bin) continue;
+          if (l != l || r.bin(r.dist(l)) != bin) continue;
           const u64 k = value_id_key(l, (uint32_t)(id0 + p));
           if (!whole && (k < lo || k > hi)) continue;
           kmax = k > kmax ? k : kmax;
@@ -539,39 +616,37 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
           const float l = vals[p];
           if (l != l) continue;
           const float d = r.dist(l);
-          if (bin_of(d) != bin) continue;
+          if (r.bin(d) != bin) continue;
           const u64 k = value_id_key(l, (uint32_t)(id0 + p));
           if (k < lo || k > hi) continue;
           add_weight(s, (int)((hi - k) >> shift), r.fixed(d));
         }
-        share_histogram(s, rank, size);
+        share_histogram(s, rank, size, 3, whole_mass);
         int sub;
         u64 c, m;
-        find(s, by_mass, by_mass ? aim - (double)mass_before : (double)(count - cnt_before), sub, c, m);
+        find(s, sums, by_mass, by_mass ? aim - (double)mass_before : (double)(count - cnt_before), sub, c, m, in_bin);
         cnt_before += c;
         mass_before += m;
-        in_bin = s.cnt[sub];
         const u64 top = hi - ((u64)sub << shift);
         const u64 width = ((u64)1 << shift) - 1;
         hi = top;
         lo = top > width ? top - width : 0;
         whole = false;
       }
-      gather(s, vals, n, id0, [&](float l, int id) {
-        if (bin_of(r.dist(l)) != bin) return false;
+      const int m = gather(s, vals, n, id0, rank, size, [&](float l, int id) {
+        if (r.bin(r.dist(l)) != bin) return false;
         const u64 k = value_id_key(l, (uint32_t)id);
         return k >= floor_key && (whole || (k >= lo && k <= hi));
       });
-      cluster_sync();
       if (rank == 0) {
-        const int m = s.n_list;
-        order_list(s, m);
+        List v;
+        load_list(s, r, m, v);
         u64 mass;
-        const u64 k = cut_list(s, r, m, by_mass, by_mass ? 0 : count - cnt_before, by_mass ? aim - (double)mass_before : 0.0, &mass);
+        const u64 k = cut_list(s, v, by_mass, by_mass ? 0u : (uint32_t)(count - cnt_before),
+                               by_mass ? aim - (double)mass_before : 0.0, &mass);
         if (t == 0) {
           s.result[0] = k;
           s.result[1] = mass_before + mass;
-          s.n_list = 0;
         }
       }
       cluster_sync();
@@ -582,62 +657,63 @@ __global__ void __launch_bounds__(kThr) sample_kernel(const SampleArgs a, int sl
     };
     u64 mass;
     if (top_k > 0) {
-      // The sums that the second search needs are replaced if this one has to split a bin.
+      bound = select(bin_k, here_k, cnt_k, 0, false, (u64)top_k, 0.0, 0, &mass);
       if (top_p < 1.0f) {
-        const bool splits = s.cnt[bin_k] > (uint32_t)kList;
-        bound = select(bin_k, cnt_k, mass_k, false, (u64)top_k, 0.0, 0, &mass);
-        total = (double)mass;
-        if (splits) {
-          clear_histogram(s);
-          cluster_sync();
-          for (int p = t; p < n; p += kThr) {
-            const float l = vals[p];
-            if (l != l) continue;
-            const float d = r.dist(l);
-            const int b = bin_of(d);
-            if (value_id_key(l, (uint32_t)(id0 + p)) >= bound) add_weight(s, b, r.fixed(d));
-          }
-          share_histogram(s, rank, size);
+        // Weigh the top-k set.
+        clear_histogram(s);
+        cluster_sync();
+        for (int p = t; p < n; p += kThr) {
+          const float l = vals[p];
+          if (l != l) continue;
+          const float d = r.dist(l);
+          if (value_id_key(l, (uint32_t)(id0 + p)) >= bound) add_weight(s, r.bin(d), r.fixed(d));
         }
-        find(s, true, (double)top_p * total, bin_p, cnt_p, mass_p);
-        bin_p = min(bin_p, bin_k);
-      } else {
-        bound = select(bin_k, cnt_k, mass_k, false, (u64)top_k, 0.0, 0, &mass);
+        share_histogram(s, rank, size, 3, whole_mass);
+        u64 m = 0, z = 0;
+        for (int b = t; b < kBins; b += kThr) m += s.mass[b];
+        u64 before = m;
+        block_scan(before, z, s.red, s.red2);
+        if (t == kThr - 1) s.found_mass = before + m;
+        __syncthreads();
+        total = (double)s.found_mass;
+        __syncthreads();
+        find(s, sums, true, (double)top_p * total, bin_p, cnt_p, mass_p, here_p);
       }
     }
     if (top_p < 1.0f) {
-      const u64 k = select(bin_p, cnt_p, mass_p, true, 0, (double)top_p * total, bound, &mass);
+      const u64 k = select(bin_p, here_p, cnt_p, mass_p, true, 0, (double)top_p * total, bound, &mass);
       bound = k > bound ? k : bound;
     }
   }
 
   // The draw over what stayed of the slice.
-  u64 key = 0;
-  float sum = 0.0f;
+  const float b_val = bound ? key_value(bound) : -INFINITY;
+  const int b_id = bound ? (int)key_id(bound) : V;
+  float sum = 0.0f, top_score = -INFINITY;
+  int drawn = -1;
   for (int p0 = t; p0 < n; p0 += kThr * 8) {
-    float z[8];
-    bool in[8];
+    float l[8], z[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int p = p0 + j * kThr;
-      in[j] = false;
-      if (p < n) {
-        const float l = vals[p];
-        in[j] = l == l && value_id_key(l, (uint32_t)(id0 + p)) >= bound;
-      }
-      z[j] = in[j] ? __ldcs(g + id0 + p) : 0.0f;
+      l[j] = p < n ? vals[p] : __uint_as_float(0x7fffffffu);
+      const bool in = l[j] > b_val || (l[j] == b_val && id0 + p <= b_id);
+      if (!in) l[j] = __uint_as_float(0x7fffffffu);
+      z[j] = in ? __ldcs(g + id0 + p) : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (!in[j]) continue;
-      const int p = p0 + j * kThr;
-      const float l = vals[p], w = r.weight(l);
-      if (w < r.min_p) continue;
+      const float w = r.near_weight(l[j]);
+      if (!(w >= r.min_p)) continue;  // what did not stay is a NaN
       sum += w;
-      const u64 c = value_id_key(l / r.temp + z[j], (uint32_t)(id0 + p));
-      key = c > key ? c : key;
+      const float score = l[j] / r.temp + z[j];
+      if (score > top_score || drawn < 0) {  // a thread's ids rise: ties stay with the lowest
+        top_score = score;
+        drawn = id0 + p0 + j * kThr;
+      }
     }
   }
+  u64 key = drawn < 0 ? 0 : value_id_key(top_score, (uint32_t)drawn);
   sum = block_sum(sum, s.redf);
   key = block_max(key, s.red);
   if (t == 0) {
