@@ -34,7 +34,7 @@ namespace domino {
 
 namespace {
 
-constexpr int kThr = 256, kWarps = kThr / 32;
+constexpr int kThr = 512, kWarps = kThr / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kBins = 1024, kNear = 1023;  // the first histogram: kNear bins, then one for the rest
 constexpr int kList = 2048, kPer = kList / kThr;
@@ -91,7 +91,7 @@ struct Smem {
   u64 red2[kWarps];
   int part_n[kMaxCluster];
   float redf[kWarps];
-  u64 result[4];  // CTA 0's answer
+  u64 result;  // CTA 0's answer
   int n_local;
   int found_bin;
   u64 found_cnt, found_mass, found_here;
@@ -109,7 +109,13 @@ struct Row {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(d * -1.4426950408889634f));
     return (uint32_t)__float2uint_rn(w * 1073741824.0f);
   }
-  // Monotone in d, so in the order of the logits.
+  // The place of a logit among the bins: bin b holds [b, b + 1), bin kNear all from kNear on.
+  // Monotone, so in the order of the logits.
+  __device__ __forceinline__ float place(float l) const { return dist(l) * scale; }
+  __device__ __forceinline__ bool in_bin(float l, int b) const {
+    const float x = place(l);
+    return x >= (float)b && (x < (float)(b + 1) || b == kNear);
+  }
   __device__ __forceinline__ int bin(float d) const {
     const float b = d * scale;
     return b < (float)kNear ? (int)b : kNear;
@@ -130,24 +136,26 @@ struct Row {
   __device__ __forceinline__ float weight(float l) const { return l == lmax ? 1.0f : expf((l - lmax) * inv_t); }
 };
 
+__device__ __forceinline__ u64 warp_max(u64 v) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((u64)hi << 32) | lo;
+}
 __device__ __forceinline__ u64 block_max(u64 v, u64* red) {
-  v = warp_max_u64(v);
+  v = warp_max(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) v = red[w] > v ? red[w] : v;
-  return v;
+  return warp_max(red[threadIdx.x & (kWarps - 1)]);
 }
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0f;
+  v = red[threadIdx.x & (kWarps - 1)];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += red[w];
+  for (int o = kWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 // Exclusive prefix sums of (a, b) over the block's threads, in thread order.
@@ -174,7 +182,7 @@ __device__ __forceinline__ void block_scan(u64& a, u64& b, u64* red, u64* red2) 
 // bins whose count and weight `at(bin, count, weight)` gives. All threads get the bin, the sums before it
 // and its count.
 template <typename At>
-__device__ __forceinline__ void find(Smem& s, At at, bool by_mass, double target, int& bin, u64& cnt_before, u64& mass_before, u64& here) {
+__device__ __forceinline__ void find(Smem& s, At at, bool by_mass, u64 target, int& bin, u64& cnt_before, u64& mass_before, u64& here) {
   constexpr int kEach = kBins / kThr;
   const int b0 = threadIdx.x * kEach;
   u64 c[kEach], m[kEach], cs = 0, ms = 0;
@@ -186,13 +194,13 @@ __device__ __forceinline__ void find(Smem& s, At at, bool by_mass, double target
   }
   u64 cb = cs, mb = ms;
   block_scan(cb, mb, s.red, s.red2);
-  const double before = by_mass ? (double)mb : (double)cb, after = by_mass ? (double)(mb + ms) : (double)(cb + cs);
+  const u64 before = by_mass ? mb : cb, after = by_mass ? mb + ms : cb + cs;
   if ((threadIdx.x == 0 || before < target) && (after >= target || threadIdx.x == kThr - 1)) {
     bool done = false;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
       if (!done) {
-        done = (by_mass ? (double)(mb + m[j]) : (double)(cb + c[j])) >= target || j == kEach - 1;
+        done = (by_mass ? mb + m[j] : cb + c[j]) >= target || j == kEach - 1;
         if (done) {
           s.found_bin = b0 + j;
           s.found_cnt = cb;
@@ -269,6 +277,8 @@ __device__ __forceinline__ void add_weight(Smem& s, int b, uint32_t w) {
   if (w >> 15) atomicAdd(&s.hist[1][b], w >> 15);
   if (w & 0x7fffu) atomicAdd(&s.hist[2][b], w & 0x7fffu);
 }
+// top_p of a whole weight: what has at least this before it does not stay.
+__device__ __forceinline__ u64 share_of(float top_p, u64 whole) { return (u64)ceil((double)top_p * (double)whole); }
 __device__ __forceinline__ u64 whole_mass(int, u64, u64 hi, u64 lo) { return (hi << 15) + lo; }
 __device__ __forceinline__ void clear_histogram(Smem& s) {
   for (int x = threadIdx.x; x < 3 * kBins; x += kThr) (&s.hist[0][0])[x] = 0u;
@@ -319,11 +329,10 @@ struct List {
 };
 
 // The key of the last that stays of the list, and the weight of what stays: the largest key with
-// `cnt` keys at or above it, or (by_mass) with the weight `aim`; 0 if the whole list has less.
+// `target` keys at or above it, or (by_mass) with that weight; 0 if the whole list has less.
 // The list's shared memory is taken for the histograms.
-__device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, uint32_t cnt, double aim, u64* mass_out) {
+__device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, u64 target, u64* mass_out) {
   u64 lo = 0, hi = ~0ull, mass = 0;
-  double target = by_mass ? aim : (double)cnt;
   while (true) {
     u64 top = 0, bottom = 0;
 #pragma unroll
@@ -354,7 +363,7 @@ __device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, ui
       mm = ((u64)s.hist[1][b] << 15) + s.hist[2][b];
     }, by_mass, target, bin, c, m, here);
     const u64 in_bin = ((u64)s.hist[1][bin] << 15) + s.hist[2][bin];
-    target -= by_mass ? (double)m : (double)c;
+    target -= by_mass ? m : c;
     mass += m;
     if (here == 0) {  // the whole list has less: the last bin, and nothing in it
       *mass_out = mass;
@@ -384,7 +393,7 @@ __device__ __forceinline__ void load_list(const Smem& s, const Row& r, int n, Li
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int slice) {
+__global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int slice) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& s = *(Smem*)smem_raw;
   float* vals = (float*)(smem_raw + ((sizeof(Smem) + 15) & ~(size_t)15));
@@ -515,9 +524,9 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
     };
     int bin_k = kNear, bin_p = kNear;
     u64 cnt_k = 0, mass_k = 0, cnt_p = 0, mass_p = 0, here_k = 0, here_p = 0;
-    if (top_k > 0) find(s, sums, false, (double)top_k, bin_k, cnt_k, mass_k, here_k);
+    if (top_k > 0) find(s, sums, false, (u64)top_k, bin_k, cnt_k, mass_k, here_k);
     // With no top-k the whole weight is the sum of all bins.
-    double total = 0.0;
+    u64 aim = 0;  // the weight before which a token stays; in whole units, so the least integer not below
     if (weigh) {
       u64 m = 0, z = 0;
       for (int b = t; b < kBins; b += kThr) m += s.mass[b];
@@ -525,22 +534,22 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
       block_scan(before, z, s.red, s.red2);
       if (t == kThr - 1) s.found_mass = before + m;
       __syncthreads();
-      total = (double)s.found_mass;
+      aim = share_of(top_p, s.found_mass);
       __syncthreads();
-      find(s, sums, true, (double)top_p * total, bin_p, cnt_p, mass_p, here_p);
+      find(s, sums, true, aim, bin_p, cnt_p, mass_p, here_p);
     }
     const int bin_all = min(bin_k, bin_p);
     const u64 most = top_k > 0 ? cnt_k + here_k : cnt_p + here_p;
     if (most <= (u64)kList) {
       // All that can stay, to CTA 0.
-      const int m = gather(s, vals, n, id0, rank, size, [&](float l, int) { return r.bin(r.dist(l)) <= bin_all; });
+      const int m = gather(s, vals, n, id0, rank, size, [&](float l, int) { return r.place(l) < (float)(bin_all + 1) || bin_all == kNear; });
       if (rank != 0) return;
       List v;
       load_list(s, r, m, v);
       u64 mass;
       if (top_k > 0) {
-        bound = cut_list(s, v, false, (uint32_t)top_k, 0.0, &mass);
-        total = (double)mass;
+        bound = cut_list(s, v, false, (u64)top_k, &mass);
+        aim = share_of(top_p, mass);
       }
       if (top_p < 1.0f) {
         if (top_k > 0) {
@@ -548,7 +557,7 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
           for (int j = 0; j < kPer; ++j)
             if (v.key[j] < bound) v.key[j] = 0, v.w[j] = 0;
         }
-        const u64 k = cut_list(s, v, true, 0, (double)top_p * total, &mass);
+        const u64 k = cut_list(s, v, true, aim, &mass);
         bound = k > bound ? k : bound;
       }
       u64 key = 0;
@@ -580,7 +589,7 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
     }
 
     // The bound of one of the two filters: the bin's keys in CTA 0's list, ordered.
-    auto select = [&](int bin, u64 in_bin, u64 cnt_before, u64 mass_before, bool by_mass, u64 count, double aim, u64 floor_key, u64* mass_out) {
+    auto select = [&](int bin, u64 in_bin, u64 before, bool by_mass, u64 target, u64 floor_key) {
       u64 lo = 0, hi = ~0ull;  // keys of the bin in question
       bool whole = true;       // all keys of the bin
       while (in_bin > (u64)kList) {
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
         u64 kmax = 0, kmin = 0;
         for (int p = t; p < n; p += kThr) {
           const float l = vals[p];
-          if (l != l || r.bin(r.dist(l)) != bin) continue;
+          if (l != l || !r.in_bin(l, bin)) continue;
           const u64 k = value_id_key(l, (uint32_t)(id0 + p));
           if (!whole && (k < lo || k > hi)) continue;
           kmax = k > kmax ? k : kmax;
@@ -615,18 +624,16 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
         for (int p = t; p < n; p += kThr) {
           const float l = vals[p];
           if (l != l) continue;
-          const float d = r.dist(l);
-          if (r.bin(d) != bin) continue;
+          if (!r.in_bin(l, bin)) continue;
           const u64 k = value_id_key(l, (uint32_t)(id0 + p));
           if (k < lo || k > hi) continue;
-          add_weight(s, (int)((hi - k) >> shift), r.fixed(d));
+          add_weight(s, (int)((hi - k) >> shift), r.fixed(r.dist(l)));
         }
         share_histogram(s, rank, size, 3, whole_mass);
         int sub;
         u64 c, m;
-        find(s, sums, by_mass, by_mass ? aim - (double)mass_before : (double)(count - cnt_before), sub, c, m, in_bin);
-        cnt_before += c;
-        mass_before += m;
+        find(s, sums, by_mass, target - before, sub, c, m, in_bin);
+        before += by_mass ? m : c;
         const u64 top = hi - ((u64)sub << shift);
         const u64 width = ((u64)1 << shift) - 1;
         hi = top;
@@ -634,7 +641,7 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
         whole = false;
       }
       const int m = gather(s, vals, n, id0, rank, size, [&](float l, int id) {
-        if (r.bin(r.dist(l)) != bin) return false;
+        if (!r.in_bin(l, bin)) return false;
         const u64 k = value_id_key(l, (uint32_t)id);
         return k >= floor_key && (whole || (k >= lo && k <= hi));
       });
@@ -642,22 +649,16 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
         List v;
         load_list(s, r, m, v);
         u64 mass;
-        const u64 k = cut_list(s, v, by_mass, by_mass ? 0u : (uint32_t)(count - cnt_before),
-                               by_mass ? aim - (double)mass_before : 0.0, &mass);
-        if (t == 0) {
-          s.result[0] = k;
-          s.result[1] = mass_before + mass;
-        }
+        const u64 k = cut_list(s, v, by_mass, target - before, &mass);
+        if (t == 0) s.result = k;
       }
       cluster_sync();
-      *mass_out = ld_u64(dsmem(&s.result[1], 0));
-      const u64 k = ld_u64(dsmem(&s.result[0], 0));
+      const u64 k = ld_u64(dsmem(&s.result, 0));
       cluster_sync();
       return k;
     };
-    u64 mass;
     if (top_k > 0) {
-      bound = select(bin_k, here_k, cnt_k, 0, false, (u64)top_k, 0.0, 0, &mass);
+      bound = select(bin_k, here_k, cnt_k, false, (u64)top_k, 0);
       if (top_p < 1.0f) {
         // Weigh the top-k set.
         clear_histogram(s);
@@ -675,13 +676,13 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
         block_scan(before, z, s.red, s.red2);
         if (t == kThr - 1) s.found_mass = before + m;
         __syncthreads();
-        total = (double)s.found_mass;
+        aim = share_of(top_p, s.found_mass);
         __syncthreads();
-        find(s, sums, true, (double)top_p * total, bin_p, cnt_p, mass_p, here_p);
+        find(s, sums, true, aim, bin_p, cnt_p, mass_p, here_p);
       }
     }
     if (top_p < 1.0f) {
-      const u64 k = select(bin_p, here_p, cnt_p, mass_p, true, 0, (double)top_p * total, bound, &mass);
+      const u64 k = select(bin_p, here_p, mass_p, true, aim, bound);
       bound = k > bound ? k : bound;
     }
   }
@@ -739,10 +740,11 @@ __global__ void __launch_bounds__(kThr, 3) sample_kernel(const SampleArgs a, int
 
 template <typename T>
 cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
-  // Slices of about 10,000 tokens: short enough for several CTAs on an SM and for one row to
-  // be read by many SMs, long enough that the barriers do not outweigh the passes.
+  // Slices of up to 20,480 tokens, two on an SM; when the rows do not fill the SMs, of half that,
+  // so that more of them read a row.
   int size = 1;
-  while (size < kMaxCluster && (a.V + size - 1) / size > 10240) size <<= 1;
+  while (size < kMaxCluster && (a.V + size - 1) / size > 20480) size <<= 1;
+  if (size < kMaxCluster && a.V > 4096 * size && (int64_t)a.rows * size * 2 <= num_sms()) size <<= 1;
   const int slice = ((a.V + size - 1) / size + 31) / 32 * 32;
   if (slice > kMaxSlice || (int64_t)a.rows * size > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const size_t smem = ((sizeof(Smem) + 15) & ~(size_t)15) + (size_t)(slice + 16) * 4;
