@@ -9,7 +9,13 @@
 //
 // A cluster of up to 16 CTAs takes a row, each a slice that it reads once from
 // memory and keeps in shared memory (fp32). Steps, each over the slice:
-//   maximum            merged over the cluster; ends a greedy row
+//   maximum            of the slice and of 256 groups of the row's tokens, merged over the
+//                      cluster; ends a greedy row
+//   candidates         a top-k of up to 128: k groups reach the k-th largest group maximum, so
+//                      no token below it stays, and about as many tokens as k are not below
+//                      it (n of 256 (1 - exp(-n / 256)) = k). top-p alone tries the 128th:
+//                      in a peaked row these tokens have the weight that stays. They go to
+//                      CTA 0, which does the rest by itself. All other rows:
 //   histogram          of (max - logit) / T in kNear bins, and one for the rest, with
 //                      counts and (top-p without top-k) weights; integers, so that no
 //                      order of the atomics changes them. A bin's weight is kept as what its
@@ -36,6 +42,7 @@ namespace {
 
 constexpr int kThr = 512, kWarps = kThr / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kGroups = 256;  // groups of a row's tokens with a maximum each
 constexpr int kBins = 1024, kNear = 1023;  // the first histogram: kNear bins, then one for the rest
 constexpr int kList = 2048, kPer = kList / kThr;
 constexpr int kMaxSlice = 48 * 1024;
@@ -90,12 +97,16 @@ struct Smem {
   u64 red[kWarps];
   u64 red2[kWarps];
   int part_n[kMaxCluster];
+  u64 part_all[kMaxCluster], part_in[kMaxCluster];  // weight of the slice, and of what was gathered
+  alignas(16) float group[kGroups];
+  float redg[kGroups];
   float redf[kWarps];
   u64 result;  // CTA 0's answer
+  float floor;
   int n_local;
   int found_bin;
   u64 found_cnt, found_mass, found_here;
-  u64 rest_w;
+  u64 rest_w, all_w, in_w;
 };
 
 struct Row {
@@ -135,6 +146,9 @@ struct Row {
   }
   __device__ __forceinline__ float weight(float l) const { return l == lmax ? 1.0f : expf((l - lmax) * inv_t); }
 };
+
+// top_p of a whole weight: what has at least this before it does not stay.
+__device__ __forceinline__ u64 share_of(float top_p, u64 whole) { return (u64)ceil((double)top_p * (double)whole); }
 
 __device__ __forceinline__ u64 warp_max(u64 v) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
@@ -277,26 +291,34 @@ __device__ __forceinline__ void add_weight(Smem& s, int b, uint32_t w) {
   if (w >> 15) atomicAdd(&s.hist[1][b], w >> 15);
   if (w & 0x7fffu) atomicAdd(&s.hist[2][b], w & 0x7fffu);
 }
-// top_p of a whole weight: what has at least this before it does not stay.
-__device__ __forceinline__ u64 share_of(float top_p, u64 whole) { return (u64)ceil((double)top_p * (double)whole); }
 __device__ __forceinline__ u64 whole_mass(int, u64, u64 hi, u64 lo) { return (hi << 15) + lo; }
 __device__ __forceinline__ void clear_histogram(Smem& s) {
   for (int x = threadIdx.x; x < 3 * kBins; x += kThr) (&s.hist[0][0])[x] = 0u;
 }
 
-// Gathers the keys for which `in` holds, kList at most in all, in CTA 0's list, CTA after CTA;
-// returns their number. Two barriers: the CTAs' numbers, and the copies.
+// Gathers the keys for which `in` holds in this CTA's list, and makes their number known to the
+// cluster, with the weights `all` and `inside` of the whole block. Returns how many the cluster has.
 template <typename In>
-__device__ __forceinline__ int gather(Smem& s, const float* vals, int n, int id0, uint32_t rank, uint32_t size, In in) {
+__device__ __forceinline__ int collect(Smem& s, const float* vals, int n, int id0, uint32_t rank, uint32_t size, In in, bool weigh,
+                                       const Row& r) {
   if (threadIdx.x == 0) s.n_local = 0;
   __syncthreads();
+  u64 all = 0, inside = 0;
   for (int p0 = threadIdx.x; p0 < n; p0 += kThr * 8) {
     float l[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) l[j] = p0 + j * kThr < n ? vals[p0 + j * kThr] : __uint_as_float(0x7fffffffu);
     unsigned hits = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) hits |= l[j] == l[j] && in(l[j], id0 + p0 + j * kThr) ? 1u << j : 0u;
+    for (int j = 0; j < 8; ++j) {
+      const bool hit = l[j] == l[j] && in(l[j], id0 + p0 + j * kThr);
+      hits |= hit ? 1u << j : 0u;
+      if (weigh && l[j] == l[j]) {
+        const uint32_t w = r.fixed(r.dist(l[j]));
+        all += w;
+        inside += hit ? w : 0u;
+      }
+    }
     if (hits) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -306,20 +328,34 @@ __device__ __forceinline__ int gather(Smem& s, const float* vals, int n, int id0
         }
     }
   }
-  __syncthreads();
-  const int mine = min(s.n_local, kList);
-  if (size == 1) return mine;
-  if (threadIdx.x < size) st_u32(dsmem(&s.part_n[rank], threadIdx.x), (uint32_t)mine);
-  cluster_sync();
-  int base = 0, all = 0;
-  for (uint32_t k = 0; k < size; ++k) {
-    base += k < rank ? s.part_n[k] : 0;
-    all += s.part_n[k];
+  if (weigh) {
+    u64 a = all, b = inside;
+    block_scan(a, b, s.red, s.red2);
+    if (threadIdx.x == kThr - 1) {
+      s.all_w = a + all;
+      s.in_w = b + inside;
+    }
   }
-  if (rank > 0)
-    for (int x = threadIdx.x; x < mine && base + x < kList; x += kThr) st_u64(dsmem(&s.list[base + x], 0), s.list[x]);
+  __syncthreads();
+  if (threadIdx.x < size) {
+    st_u32(dsmem(&s.part_n[rank], threadIdx.x), (uint32_t)s.n_local);
+    if (weigh) {
+      st_u64(dsmem(&s.part_all[rank], threadIdx.x), s.all_w);
+      st_u64(dsmem(&s.part_in[rank], threadIdx.x), s.in_w);
+    }
+  }
   cluster_sync();
-  return min(all, kList);
+  int sum = 0;
+  for (uint32_t k = 0; k < size; ++k) sum += s.part_n[k];
+  return sum;
+}
+// The CTAs' lists (kList keys at most in all) to CTA 0's, CTA after CTA.
+__device__ __forceinline__ void join(Smem& s, uint32_t rank) {
+  int base = 0;
+  for (uint32_t k = 0; k < rank; ++k) base += s.part_n[k];
+  if (rank > 0)
+    for (int x = threadIdx.x; x < s.n_local; x += kThr) st_u64(dsmem(&s.list[base + x], 0), s.list[x]);
+  cluster_sync();
 }
 
 // CTA 0's list of n keys, each thread's in registers, with their weights.
@@ -348,8 +384,7 @@ __device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, u6
       *mass_out = 0;
       return 0;
     }
-    int shift = 0;
-    while (((hi - lo) >> shift) >= (u64)kBins) ++shift;
+    const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);
     clear_histogram(s);
     __syncthreads();
 #pragma unroll
@@ -389,6 +424,97 @@ __device__ __forceinline__ void load_list(const Smem& s, const Row& r, int n, Li
     const int x = threadIdx.x + j * kThr;
     v.key[j] = x < n ? s.list[x] : 0;
     v.w[j] = x < n ? r.fixed(r.dist(key_value(v.key[j]))) : 0;
+  }
+}
+
+// CTA 0: the draw from a list that holds all that can stay. `aim` is the weight for top-p when no top-k
+// fixes it.
+__device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs& a, const Row& r, int row, int m, int top_k, float top_p,
+                                               u64 aim) {
+  const float* g = a.gumbel + (int64_t)row * a.gs;
+  u64 key = 0;
+  float sum = 0.0f;
+  if (m <= kThr / 2) {
+    // A key per thread, each ranked against all; then every bound is a matter of places and sums.
+    u64 own = (int)threadIdx.x < m ? s.list[threadIdx.x] : 0;
+    int rank = 0;
+    if ((threadIdx.x & ~31u) < (unsigned)m) {
+      int x = 0;
+      for (; x + 8 <= m; x += 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rank += s.list[x + j] > own;
+      }
+      for (; x < m; ++x) rank += s.list[x] > own;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < m) s.list[rank] = own;
+    __syncthreads();
+    own = (int)threadIdx.x < m ? s.list[threadIdx.x] : 0;
+    if (top_k > 0 && (int)threadIdx.x >= top_k) own = 0;
+    const float l = key_value(own);
+    const u64 w = own ? (u64)r.fixed(r.dist(l)) : 0;
+    u64 before = w, z = 0;
+    block_scan(before, z, s.red, s.red2);
+    if (top_k > 0 && top_p < 1.0f) {
+      if (threadIdx.x == kThr - 1) s.found_mass = before + w;
+      __syncthreads();
+      aim = share_of(top_p, s.found_mass);
+    }
+    if (own && (top_p >= 1.0f || before < aim)) {
+      const float wt = r.weight(l);
+      if (wt >= r.min_p) {
+        const uint32_t id = key_id(own);
+        key = value_id_key(l / r.temp + g[id], id);
+        sum = wt;
+      }
+    }
+    const u64 mine = key;
+    sum = block_sum(sum, s.redf);
+    key = block_max(key, s.red);
+    if (mine && mine == key) {
+      a.tokens[row] = (int)key_id(key);
+      if (a.logprob) a.logprob[row] = (l == r.lmax ? 0.0f : (l - r.lmax) * r.inv_t) - logf(sum);
+    }
+    return;
+  }
+  List v;
+  load_list(s, r, m, v);
+  u64 mass, bound = 0;
+  if (top_k > 0) {
+    bound = cut_list(s, v, false, (u64)top_k, &mass);
+    aim = share_of(top_p, mass);
+  }
+  if (top_p < 1.0f) {
+    if (top_k > 0) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (v.key[j] < bound) v.key[j] = 0, v.w[j] = 0;
+    }
+    const u64 k = cut_list(s, v, true, aim, &mass);
+    bound = k > bound ? k : bound;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (v.key[j] && v.key[j] >= bound) {
+      const float l = key_value(v.key[j]), w = r.weight(l);
+      if (w >= r.min_p) {
+        const uint32_t id = key_id(v.key[j]);
+        const u64 c = value_id_key(l / r.temp + g[id], id);
+        key = c > key ? c : key;
+        sum += w;
+      }
+    }
+  }
+  sum = block_sum(sum, s.redf);
+  key = block_max(key, s.red);
+  // From the thread that has the drawn token's logit.
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (v.key[j] && key_id(v.key[j]) == key_id(key)) {
+      const float l = key_value(v.key[j]);
+      a.tokens[row] = (int)key_id(key);
+      if (a.logprob) a.logprob[row] = (l == r.lmax ? 0.0f : (l - r.lmax) * r.inv_t) - logf(sum);
+    }
   }
 }
 
@@ -458,6 +584,16 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
     }
     return;
   }
+  {
+    // The groups: the same number of neighbouring threads' tokens each, kGroups / size in a CTA.
+    const int lanes = kThr * (int)size / kGroups, per = kGroups / (int)size;
+    float m = top;
+    for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (t % lanes == 0) s.redg[t / lanes] = m;
+    __syncthreads();
+    if (t < kGroups)
+      st_u32(dsmem(&s.group[(int)rank * per + t % per], (uint32_t)(t / per)), __float_as_uint(s.redg[t % per]));
+  }
   u64 best = block_max(value_id_key(top, (uint32_t)top_id), s.red);
   if (t < (int)size) st_u64(dsmem(&s.part_key[rank], (uint32_t)t), best);
   clear_histogram(s);
@@ -479,6 +615,44 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
   r.scale = top_k > 128 ? 16.0f : 32.0f;
 
   u64 bound = 0;  // keys from here on stay
+  if (top_k > 0 ? top_k <= kGroups / 2 : top_p < 1.0f) {
+    // The candidates: tokens not below the k-th largest group maximum.
+    const int k = top_k > 0 ? top_k : kGroups / 2;
+    if (t < kGroups) {
+      const float own = s.group[t];
+      int before = 0;
+#pragma unroll 8
+      for (int x = 0; x < kGroups; x += 4) {
+        const float4 y = *(const float4*)&s.group[x];
+        before += (y.x > own || (y.x == own && x < t)) + (y.y > own || (y.y == own && x + 1 < t)) +
+                  (y.z > own || (y.z == own && x + 2 < t)) + (y.w > own || (y.w == own && x + 3 < t));
+      }
+      if (before == k - 1) s.floor = own;
+    }
+    __syncthreads();
+    const float floor_l = s.floor;
+    // top-p alone: a flat row's tokens below the candidates would hold most of its weight.
+    const bool likely = top_k > 0 || r.near_weight(floor_l) * (float)V < 20.0f;
+    if (likely) {
+    const int m = collect(s, vals, n, id0, rank, size, [&](float l, int) { return l >= floor_l; }, top_k == 0, r);
+    u64 aim = 0, inside = 0;
+    if (top_k == 0) {
+      u64 all = 0;
+      for (uint32_t q = 0; q < size; ++q) {
+        all += s.part_all[q];
+        inside += s.part_in[q];
+      }
+      aim = share_of(top_p, all);
+    }
+    if (m <= kList && inside >= aim) {
+      join(s, rank);
+      if (rank == 0) draw_from_list(s, a, r, row, m, top_k, top_p, aim);
+      return;
+    }
+    cluster_sync();  // the numbers are read before the next ones arrive
+    clear_histogram(s);
+    }
+  }
   if (top_k > 0 || top_p < 1.0f) {
     const bool weigh = top_k == 0;  // with a top-k, its set is weighed once it is known
     uint32_t rest = 0;
@@ -542,49 +716,10 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
     const u64 most = top_k > 0 ? cnt_k + here_k : cnt_p + here_p;
     if (most <= (u64)kList) {
       // All that can stay, to CTA 0.
-      const int m = gather(s, vals, n, id0, rank, size, [&](float l, int) { return r.place(l) < (float)(bin_all + 1) || bin_all == kNear; });
-      if (rank != 0) return;
-      List v;
-      load_list(s, r, m, v);
-      u64 mass;
-      if (top_k > 0) {
-        bound = cut_list(s, v, false, (u64)top_k, &mass);
-        aim = share_of(top_p, mass);
-      }
-      if (top_p < 1.0f) {
-        if (top_k > 0) {
-#pragma unroll
-          for (int j = 0; j < kPer; ++j)
-            if (v.key[j] < bound) v.key[j] = 0, v.w[j] = 0;
-        }
-        const u64 k = cut_list(s, v, true, aim, &mass);
-        bound = k > bound ? k : bound;
-      }
-      u64 key = 0;
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (v.key[j] && v.key[j] >= bound) {
-          const float l = key_value(v.key[j]), w = r.weight(l);
-          if (w >= r.min_p) {
-            const uint32_t id = key_id(v.key[j]);
-            const u64 c = value_id_key(l / r.temp + g[id], id);
-            key = c > key ? c : key;
-            sum += w;
-          }
-        }
-      }
-      sum = block_sum(sum, s.redf);
-      key = block_max(key, s.red);
-      // From the thread that has the drawn token's logit.
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (v.key[j] && key_id(v.key[j]) == key_id(key)) {
-          const float l = key_value(v.key[j]);
-          a.tokens[row] = (int)key_id(key);
-          if (a.logprob) a.logprob[row] = (l == r.lmax ? 0.0f : (l - r.lmax) * r.inv_t) - logf(sum);
-        }
-      }
+      const int m = collect(s, vals, n, id0, rank, size,
+                            [&](float l, int) { return r.place(l) < (float)(bin_all + 1) || bin_all == kNear; }, false, r);
+      join(s, rank);
+      if (rank == 0) draw_from_list(s, a, r, row, m, top_k, top_p, aim);
       return;
     }
 
@@ -619,8 +754,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
           lo = s.part_lo[k] > lo ? s.part_lo[k] : lo;
         }
         lo = ~lo;
-        int shift = 0;
-        while (((hi - lo) >> shift) >= (u64)kBins) ++shift;
+        const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);
         for (int p = t; p < n; p += kThr) {
           const float l = vals[p];
           if (l != l) continue;
@@ -640,11 +774,12 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
         lo = top > width ? top - width : 0;
         whole = false;
       }
-      const int m = gather(s, vals, n, id0, rank, size, [&](float l, int id) {
+      const int m = collect(s, vals, n, id0, rank, size, [&](float l, int id) {
         if (!r.in_bin(l, bin)) return false;
         const u64 k = value_id_key(l, (uint32_t)id);
         return k >= floor_key && (whole || (k >= lo && k <= hi));
-      });
+      }, false, r);
+      join(s, rank);
       if (rank == 0) {
         List v;
         load_list(s, r, m, v);
