@@ -251,8 +251,9 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
   p.part = partials_at(a.scratch, simt_want(), kBM);
   const size_t smem = sizeof(float) * (kBM * (a.D + 4) + kBN * (a.D + 4) + kBN * a.D + kBM * (kBN + 1)) + 8 * kBM;
   const dim3 grid((unsigned)(p.row_tiles * p.splits), (unsigned)a.hkv, (unsigned)a.rows.batch);
-  const void* fn = a.dtype == DOMINO_BF16 ? (const void*)attn_simt_kernel<__nv_bfloat16> : (const void*)attn_simt_kernel<float>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 120 * 1024);
+  static FuncOnce once_bf16, once_f32;
+  const cudaError_t e = a.dtype == DOMINO_BF16 ? once_bf16.set((const void*)attn_simt_kernel<__nv_bfloat16>, 120 * 1024, false)
+                                               : once_f32.set((const void*)attn_simt_kernel<float>, 120 * 1024, false);
   if (e != cudaSuccess) return e;
   if (a.dtype == DOMINO_BF16)
     attn_simt_kernel<__nv_bfloat16><<<grid, kThr, smem, stream>>>(p);

@@ -39,6 +39,7 @@
 #include <mutex>
 
 #include "attention.cuh"
+#include "packed.cuh"
 
 namespace domino {
 
@@ -178,37 +179,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int s, int h, int b, uint64_t* bar,
                                             uint64_t policy, bool hint) {
   if (hint)
@@ -991,7 +961,8 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   p.arrived = (unsigned int*)w;
   p.ml = (float2*)(w + kArrivedBytes);
   p.o = (float4*)(w + kArrivedBytes + (size_t)2 * grid * C::BMT * 8);
-  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NQ, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  static FuncOnce once;
+  cudaError_t e = once.set((const void*)attn_tc_kernel<NQ, KB>, 227 * 1024, false);
   if (e != cudaSuccess) return e;
   attn_tc_kernel<NQ, KB><<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <atomic>
 
 #include "../../include/domino.h"
 
@@ -169,6 +170,22 @@ cudaError_t launch_tree_marginal(const float* cand_val, const int32_t* cand_id, 
                                  int P, int V, int N, int M, float inv_tau, int32_t* node_token,
                                  int32_t* node_parent, int32_t* node_depth, float* node_score, Ctl* ctl,
                                  cudaStream_t stream);
+
+// A kernel's attributes, set on the first launch on each device (a call costs about half a
+// microsecond each time otherwise). Setting them twice does no harm.
+struct FuncOnce {
+  std::atomic<uint64_t> devices{0};
+  cudaError_t set(const void* fn, int smem, bool wide_cluster) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (devices.load() >> dev) & 1u) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && wide_cluster) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && dev < 64) devices.fetch_or((uint64_t)1 << dev);
+    return e;
+  }
+};
 
 // The target's side of a cycle (declarations and meaning: domino.h).
 struct RowsArgs {

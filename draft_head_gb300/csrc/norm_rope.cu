@@ -2,130 +2,286 @@
 // place in the cache, in one pass (domino_qk_norm_rope; the definition is in
 // domino.h).
 //
-// Memory bound: every element is read once and written once. One CTA takes a
-// row of the block. A group of lanes holds one head, eight elements a lane (16
-// bytes of bf16), and the CTA's groups take the row's q, k and v heads in turn.
-// Mean square by shuffles within the group; the rotation's partner elements
-// come from the group's own fp32 copy in shared memory. All arithmetic is fp32,
-// rounded once on the store.
+// Memory bound: every element is read once and written once. A CTA takes a row
+// of the block. A group of lanes holds one head, eight elements a lane (16 bytes of
+// bf16), and the CTA's groups take the row's heads in turn, the loads of several in flight at
+// once. A lane has the same eight places of every head, so the row's cosines and sines
+// and the weights are read once and multiplied once. The mean square and the
+// rotation's partners come by shuffles within the group; only where half of rot_dim is
+// no multiple of eight do the partners go through shared memory. All arithmetic is fp32,
+// rounded once on the store. With few rows the heads are spread over more CTAs; with many a CTA
+// takes a run of rows, whose lengths it looks up once a request.
 #include "common.cuh"
+#include "packed.cuh"
 #include "rows.cuh"
 
 namespace domino {
 
 namespace {
 
-constexpr int kNrThreads = 256;
+constexpr int kNrThreads = 128;
 
+// Eight elements as they lie in memory; in arithmetic, four fp32 pairs.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
+struct Raw8;
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-  const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = ((const float4*)p)[0];
+    b = ((const float4*)p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float2 (&x)[4]) const {
+    x[0] = make_float2(a.x, a.y); x[1] = make_float2(a.z, a.w);
+    x[2] = make_float2(b.x, b.y); x[3] = make_float2(b.z, b.w);
+  }
+  __device__ __forceinline__ void set(const float2 (&x)[4]) {
+    a = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    b = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+  }
+  __device__ __forceinline__ Raw8 of(int lane) const {  // another lane's
+    Raw8 o;
+    const float* x = (const float*)&a;
+    float* y = (float*)&o.a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], lane);
+    x = (const float*)&b;
+    y = (float*)&o.b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], lane);
+    return o;
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    ((float4*)p)[0] = a;
+    ((float4*)p)[1] = b;
+  }
+};
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *(const uint4*)p;
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *(const uint4*)p; }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float2 (&x)[4]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  ((float4*)p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  ((float4*)p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *(const uint32_t*)&h;
+  __device__ __forceinline__ void set(const float2 (&x)[4]) {
+    u = make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y));
   }
-  *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
-}
+  __device__ __forceinline__ Raw8 of(int lane) const {  // another lane's
+    Raw8 o;
+    o.u.x = __shfl_sync(0xffffffffu, u.x, lane);
+    o.u.y = __shfl_sync(0xffffffffu, u.y, lane);
+    o.u.z = __shfl_sync(0xffffffffu, u.z, lane);
+    o.u.w = __shfl_sync(0xffffffffu, u.w, lane);
+    return o;
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *(uint4*)p = u; }
+};
 
-template <typename T>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeArgs a, int width) {
-  extern __shared__ float s_y[];  // [groups][D]
-  const int t = blockIdx.x;
-  int b, i, ctx;
-  if (!find_row(a.rows, t, b, i, ctx, a.ctl)) return;
-  const int pos = a.rows.positions ? a.rows.positions[t] : ctx + i;
-  if (a.rot > 0 && (pos < 0 || pos >= a.max_pos)) {
-    if (threadIdx.x == 0) dev_error(a.ctl, DEV_ERR_DATA);
-    return;
-  }
-  const float* cs = a.rope + (int64_t)pos * a.rot;
-  const int group = threadIdx.x / width, lane = threadIdx.x % width, groups = kNrThreads / width;
+enum { kPairs = 0, kHalves = 1, kHalvesShared = 2 };
+
+template <typename T, int MODE, int kWidth>
+__global__ void __launch_bounds__(kNrThreads, 6) norm_rope_kernel(const NormRopeArgs a, int chunk) {
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // q heads in flight, beside one of k and one of v
+  extern __shared__ __align__(16) float s_w[];    // [2][D] weights; kHalvesShared: [groups][D] heads
+  constexpr int groups = kNrThreads / kWidth;
+  const int group = threadIdx.x / kWidth, lane = threadIdx.x % kWidth;
   const int e0 = lane * 8;
   const bool live = e0 < a.D;
-  const int half = a.rot / 2, heads = a.hq + 2 * a.hkv;
-  const int64_t slot = (int64_t)b * a.rs + (int64_t)(ctx + i) * a.ss;
-  float* y = s_y + group * a.D;
-  for (int h0 = 0; h0 < heads; h0 += groups) {  // block-uniform bounds: every lane meets every shuffle
-    const int h = h0 + group;
-    const bool on = live && h < heads;
-    const bool is_v = h >= a.hq + a.hkv, is_q = h < a.hq;
-    float x[8] = {};
-    const T* src = is_q ? (const T*)a.q + (int64_t)t * a.q_stride + (int64_t)h * a.D
-                        : is_v ? (const T*)a.v + (int64_t)t * a.v_stride + (int64_t)(h - a.hq - a.hkv) * a.D
-                               : (const T*)a.k + (int64_t)t * a.k_stride + (int64_t)(h - a.hq) * a.D;
-    if (on) load8<T>(src + e0, x);
-    float ss = 0.0f;
+  const int half = a.rot / 2;
+  const int first = blockIdx.y * groups + group, step = groups * gridDim.y;
+  // Loops over heads have the same bounds for the whole block: every lane meets every shuffle.
+  const int first_u = blockIdx.y * groups;
+  const float inv_d = 1.0f / (float)a.D;
+  float* x_all = s_w + 2 * a.D + group * a.D;
+  int t = blockIdx.x * chunk;
+  const int t_end = min(a.rows.tokens, t + chunk);
+  Raw8<T> xq[kBatch], xk, xv;
+  auto fetch_q = [&](int h0) {
+    const T* p = (const T*)a.q + (int64_t)t * a.q_stride + e0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-    for (int o = width / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (on && !is_v) {
-      const float rstd = rsqrtf(ss / (float)a.D + a.eps);
-      const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
-      float wt[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-      if (w) load8<T>(w + e0, wt);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[e0 + j] = x[j] * rstd * wt[j];
+    for (int j = 0; j < kBatch; ++j)
+      if (live && h0 + j * step < a.hq) xq[j].load(p + (h0 + j * step) * a.D);
+  };
+  auto fetch_kv = [&](int h) {
+    if (live && h < a.hkv) {
+      xk.load((const T*)a.k + (int64_t)t * a.k_stride + h * a.D + e0);
+      xv.load((const T*)a.v + (int64_t)t * a.v_stride + h * a.D + e0);
     }
-    __syncwarp();
-    if (on) {
-      if (!is_v) {
+  };
+  fetch_q(first);  // these need no lengths
+  fetch_kv(first);
+  // A place's partner in the rotation (itself where it does not turn), and both places' weights.
+  const bool low = e0 < half;
+  auto partner_of = [&](int e) { return e >= a.rot ? e : MODE == kPairs ? e ^ 1 : e < half ? e + half : e - half; };
+  for (int e = threadIdx.x; e < 2 * a.D; e += kNrThreads) {
+    const T* w = (const T*)(e < a.D ? a.q_weight : a.k_weight);
+    s_w[e] = w ? to_f<T>(w[e < a.D ? e : e - a.D]) : 1.0f;
+  }
+  const int partner_lane = (threadIdx.x & 31) + (e0 >= a.rot ? 0 : low ? half : -half) / 8;
+  int b, i, ctx, rows;
+  bool mine = find_row(a.rows, t, b, i, ctx, rows, a.ctl);
+  __syncthreads();
+  while (true) {
+    const int pos = !mine ? 0 : a.rows.positions ? a.rows.positions[t] : ctx + i;
+    const bool placed = mine && (a.rot == 0 || (pos >= 0 && pos < a.max_pos));
+    if (mine && !placed && threadIdx.x == 0) dev_error(a.ctl, DEV_ERR_DATA);
+    if (placed) {
+      // The angle of each of the lane's places: eight neighbours of a half, or four pairs.
+      float c[8], s[8];
+      const float* cs = a.rope + (int64_t)pos * a.rot;
+      if (MODE == kHalves || (MODE == kPairs && a.rot % 8 == 0)) {
+        constexpr int kN = MODE == kHalves ? 8 : 4;
+        const float* at = cs + (MODE == kPairs ? e0 / 2 : low ? e0 : e0 - half);
+        float c4[kN], s4[kN];
+#pragma unroll
+        for (int j = 0; j < kN; j += 4) {
+          const bool turns = e0 < a.rot;
+          const float4 x4 = turns ? __ldg((const float4*)(at + j)) : make_float4(1, 1, 1, 1);
+          const float4 y4 = turns ? __ldg((const float4*)(at + half + j)) : make_float4(0, 0, 0, 0);
+          c4[j] = x4.x; c4[j + 1] = x4.y; c4[j + 2] = x4.z; c4[j + 3] = x4.w;
+          s4[j] = y4.x; s4[j + 1] = y4.y; s4[j + 2] = y4.z; s4[j + 3] = y4.w;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j;
-          if (e >= a.rot) {
-            x[j] = y[e];
-          } else if (a.interleaved) {
-            const float c = cs[e >> 1], s = cs[half + (e >> 1)];
-            x[j] = (e & 1) ? y[e] * c + y[e - 1] * s : y[e] * c - y[e + 1] * s;
-          } else {
-            const int p = e < half ? e : e - half;
-            const float c = cs[p], s = cs[half + p];
-            x[j] = e < half ? y[e] * c - y[e + half] * s : y[e] * c + y[e - half] * s;
-          }
+          c[j] = c4[MODE == kPairs ? j / 2 : j];
+          s[j] = s4[MODE == kPairs ? j / 2 : j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = e0 + j, p = MODE == kPairs ? e >> 1 : e < half ? e : e - half;
+          c[j] = e < a.rot ? __ldg(cs + p) : 1.0f;
+          s[j] = e < a.rot ? __ldg(cs + half + p) : 0.0f;
         }
       }
-      T* dst = is_q ? (T*)a.q_out + ((int64_t)t * a.hq + h) * a.D
-                    : is_v ? (T*)a.v_cache + slot + (int64_t)(h - a.hq - a.hkv) * a.hs
-                           : (T*)a.k_cache + slot + (int64_t)(h - a.hq) * a.hs;
-      store8(dst + e0, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (MODE == kPairs ? (j & 1) == 0 : e0 + j < half) s[j] = -s[j];
+      // Weights times cosines and the partners' weights times sines, first for k, then for q.
+      float2 wc[4], ws[4];
+      auto weigh = [&](const float* w) {
+        const int e = live ? e0 : 0;
+        float x[8], y[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) *(float4*)&x[j] = *(const float4*)&w[e + j];
+        if (MODE == kHalves) {
+          const int p = partner_of(e);
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) *(float4*)&y[j] = *(const float4*)&w[p + j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = MODE == kPairs ? x[j ^ 1] : w[partner_of(e + j)];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          wc[j] = make_float2(x[2 * j] * c[2 * j], x[2 * j + 1] * c[2 * j + 1]);
+          ws[j] = make_float2(y[2 * j] * s[2 * j], y[2 * j + 1] * s[2 * j + 1]);
+        }
+      };
+      // z = rstd (x (w c) + x' (w' s)), x' the partner. (An infinity makes rstd 0 and a NaN makes it a
+      // NaN, so that a partner's value times 0 adds nothing to what the head's own values do.)
+      auto turn = [&](Raw8<T>& v, bool on, T* dst) {
+        float2 x[4], y[4];
+        if (!on) v.zero();
+        v.get(x);
+        float2 sq = mul2(x[0], x[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) sq = fma2(x[e], x[e], sq);
+        float ss = sq.x + sq.y;
+#pragma unroll
+        for (int o = kWidth / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float rstd = rsqrtf(ss * inv_d + a.eps);
+        if (MODE == kPairs) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = make_float2(x[e].y, x[e].x);
+        } else if (MODE == kHalves) {
+          v.of(partner_lane).get(y);
+        } else {
+          __syncwarp();
+          if (on) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x_all[e0 + 2 * e] = x[e].x;
+              x_all[e0 + 2 * e + 1] = x[e].y;
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = on ? make_float2(x_all[partner_of(e0 + 2 * e)], x_all[partner_of(e0 + 2 * e + 1)]) : make_float2(0, 0);
+        }
+        const float2 r2 = make_float2(rstd, rstd);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = mul2(r2, fma2(x[e], wc[e], mul2(y[e], ws[e])));
+        v.set(x);
+        if (on) v.store(dst);
+      };
+      const int64_t slot = (int64_t)b * a.rs + (int64_t)(ctx + i) * a.ss + e0;
+      weigh(s_w + a.D);
+      for (int h0 = first_u; h0 < a.hkv; h0 += step) {
+        const int h = h0 + group;
+        if (h0 > first_u) fetch_kv(h);
+        const bool on = live && h < a.hkv;
+        if (on) xv.store((T*)a.v_cache + slot + (int64_t)h * a.hs);
+        turn(xk, on, (T*)a.k_cache + slot + (int64_t)h * a.hs);
+      }
+      weigh(s_w);
+      T* q_out = (T*)a.q_out + (int64_t)t * a.hq * a.D + e0;
+      for (int h0 = first_u; h0 < a.hq; h0 += kBatch * step) {
+        if (h0 > first_u) fetch_q(h0 + group);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          // All of the batch at once, so that the heads' chains overlap; one beyond the last is not stored.
+          const int h = h0 + j * step + group;
+          turn(xq[j], live && h < a.hq, q_out + h * a.D);
+        }
+      }
     }
-    __syncwarp();
+    if (++t == t_end) break;
+    fetch_q(first);
+    fetch_kv(first);
+    if (mine && i + 1 < rows)
+      ++i;
+    else
+      mine = find_row(a.rows, t, b, i, ctx, rows, a.ctl);
   }
+}
+
+template <typename T, int MODE>
+cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
+  // Lanes per head: 8 (a head of up to 64), 16 or 32.
+  const int width = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, groups = kNrThreads / width;
+  const int rounds = ((a.hq > a.hkv ? a.hq : a.hkv) + groups - 1) / groups;
+  // A row's heads over several CTAs while the rows do not fill the SMs; past ten CTAs on an SM, a CTA
+  // takes neighbouring rows one after the other: their lengths are then at hand.
+  const int most = 10 * num_sms();
+  const int chunk = (a.rows.tokens + most - 1) / most;
+  const dim3 grid((unsigned)((a.rows.tokens + chunk - 1) / chunk),
+                  (int64_t)a.rows.tokens * rounds <= 2 * num_sms() ? (unsigned)rounds : 1u);
+  const size_t smem = (size_t)(2 + (MODE == kHalvesShared ? groups : 0)) * a.D * 4;
+  if (width == 8)
+    norm_rope_kernel<T, MODE, 8><<<grid, kNrThreads, smem, stream>>>(a, chunk);
+  else if (width == 16)
+    norm_rope_kernel<T, MODE, 16><<<grid, kNrThreads, smem, stream>>>(a, chunk);
+  else
+    norm_rope_kernel<T, MODE, 32><<<grid, kNrThreads, smem, stream>>>(a, chunk);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
+  if (a.interleaved) return launch<T, kPairs>(a, stream);
+  return a.rot % 16 == 0 ? launch<T, kHalves>(a, stream) : launch<T, kHalvesShared>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
-  int width = 1;
-  while (width * 8 < a.D) width <<= 1;
-  const size_t smem = (size_t)(kNrThreads / width) * a.D * 4;
-  if (a.dtype == DOMINO_BF16)
-    norm_rope_kernel<__nv_bfloat16><<<a.rows.tokens, kNrThreads, smem, stream>>>(a, width);
-  else
-    norm_rope_kernel<float><<<a.rows.tokens, kNrThreads, smem, stream>>>(a, width);
-  return cudaGetLastError();
+  return a.dtype == DOMINO_BF16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
 }
 
 }  // namespace domino

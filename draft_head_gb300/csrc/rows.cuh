@@ -30,29 +30,43 @@ __device__ __forceinline__ bool request_rows(const RowsArgs& r, int b, int& q0, 
   return true;
 }
 
-// The request b and place i of packed row t, and the request's past. Called by
+// The request b and place i of packed row t, and the request's past and rows. Called by
 // whole warps; every lane gets the result. A 32-way search: each round, the
-// lanes look at 32 requests spread over what is left.
-__device__ __forceinline__ bool find_row(const RowsArgs& r, int t, int& b, int& i, int& ctx, Ctl* ctl) {
+// lanes look at 32 requests spread over what is left; in the last round a lane
+// has its request's lengths at hand.
+__device__ __forceinline__ bool find_row(const RowsArgs& r, int t, int& b, int& i, int& ctx, int& rows, Ctl* ctl) {
   const int lane = threadIdx.x & 31;
-  if (r.q_start) {
-    int lo = 0, n = r.batch;  // the last b in [lo, lo + n) with q_start[b] <= t
-    while (n > 1) {
-      const int step = (n + 31) / 32;
-      const int at = lane * step;
-      const unsigned m = __ballot_sync(0xffffffffu, at < n && r.q_start[lo + at] <= t);
-      const int k = m ? 31 - __clz(m) : 0;
-      lo += k * step;
-      n = min(step, n - k * step);
-    }
-    b = lo;
-  } else {
+  if (!r.q_start) {
     b = t / r.max_q;
+    int q0;
+    if (!request_rows(r, b, q0, rows, ctx, lane == 0, ctl)) return false;
+    i = t - q0;
+    return i >= 0 && i < rows;
   }
-  int q0, rows;
-  if (!request_rows(r, b, q0, rows, ctx, lane == 0, ctl)) return false;
-  i = t - q0;
-  return i >= 0 && i < rows;  // a row of no request
+  int lo = 0, n = r.batch;  // the last b in [lo, lo + n) with q_start[b] <= t
+  while (n > 32) {
+    const int step = (n + 31) / 32;
+    const int at = lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, at < n && r.q_start[lo + at] <= t);
+    const int k = m ? 31 - __clz(m) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  int q0 = 0, c = 0;
+  rows = 0;
+  bool fine = true;
+  if (lane < n) fine = request_rows(r, lo + lane, q0, rows, c, false, ctl);
+  const unsigned m = __ballot_sync(0xffffffffu, lane < n && q0 <= t);
+  const int k = m ? 31 - __clz(m) : 0;
+  b = lo + k;
+  i = t - __shfl_sync(0xffffffffu, q0, k);
+  ctx = __shfl_sync(0xffffffffu, c, k);
+  rows = __shfl_sync(0xffffffffu, rows, k);
+  if (!__shfl_sync(0xffffffffu, (int)fine, k)) {
+    if (lane == 0) dev_error(ctl, DEV_ERR_DATA);
+    return false;
+  }
+  return i >= 0 && i < rows;  // or a row of no request
 }
 
 }  // namespace domino

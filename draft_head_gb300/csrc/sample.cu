@@ -883,9 +883,8 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   const int slice = ((a.V + size - 1) / size + 31) / 32 * 32;
   if (slice > kMaxSlice || (int64_t)a.rows * size > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const size_t smem = ((sizeof(Smem) + 15) & ~(size_t)15) + (size_t)(slice + 16) * 4;
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static FuncOnce once;
+  cudaError_t e = once.set((const void*)sample_kernel<T>, 227 * 1024, true);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * size));
