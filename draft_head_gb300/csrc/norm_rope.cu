@@ -84,7 +84,7 @@ struct Raw8<__nv_bfloat16> {
 enum { kPairs = 0, kHalves = 1, kHalvesShared = 2 };
 
 template <typename T, int MODE, int kWidth>
-__global__ void __launch_bounds__(kNrThreads, 6) norm_rope_kernel(const NormRopeArgs a, int chunk) {
+__global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRopeArgs a, int chunk) {
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // q heads in flight, beside one of k and one of v
   extern __shared__ __align__(16) float s_w[];    // [2][D] weights; kHalvesShared: [groups][D] heads
   constexpr int groups = kNrThreads / kWidth;
@@ -256,9 +256,9 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
   // Lanes per head: 8 (a head of up to 64), 16 or 32.
   const int width = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, groups = kNrThreads / width;
   const int rounds = ((a.hq > a.hkv ? a.hq : a.hkv) + groups - 1) / groups;
-  // A row's heads over several CTAs while the rows do not fill the SMs; past ten CTAs on an SM, a CTA
+  // A row's heads over several CTAs while the rows do not fill the SMs; past the five CTAs that an SM holds, a CTA
   // takes neighbouring rows one after the other: their lengths are then at hand.
-  const int most = 10 * num_sms();
+  const int most = 5 * num_sms();
   const int chunk = (a.rows.tokens + most - 1) / most;
   const dim3 grid((unsigned)((a.rows.tokens + chunk - 1) / chunk),
                   (int64_t)a.rows.tokens * rounds <= 2 * num_sms() ? (unsigned)rounds : 1u);
