@@ -8,7 +8,8 @@
 // argmax of logit / T + noise over what stayed.
 //
 // A cluster of up to 16 CTAs takes a row, each a slice that it reads once from
-// memory and keeps in shared memory (fp32). Steps, each over the slice:
+// memory; it keeps it in shared memory, or with many rows reads it again from L2. Steps, each
+// over the slice:
 //   maximum            of the slice and of 256 groups of the row's tokens, merged over the
 //                      cluster; ends a greedy row
 //   candidates         a top-k of up to 128: k groups reach the k-th largest group maximum, so
@@ -40,11 +41,11 @@ namespace domino {
 
 namespace {
 
-constexpr int kThr = 512, kWarps = kThr / 32;
+constexpr int kMaxWarps = 16;
 constexpr int kMaxCluster = 16;
 constexpr int kGroups = 256;  // groups of a row's tokens with a maximum each
 constexpr int kBins = 1024, kNear = 1023;  // the first histogram: kNear bins, then one for the rest
-constexpr int kList = 2048, kPer = kList / kThr;
+constexpr int kList = 2048;
 constexpr int kMaxSlice = 48 * 1024;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -94,13 +95,13 @@ struct Smem {
   u64 part_key[kMaxCluster];  // from each CTA
   u64 part_lo[kMaxCluster];
   float part_sum[kMaxCluster];
-  u64 red[kWarps];
-  u64 red2[kWarps];
+  u64 red[kMaxWarps];
+  u64 red2[kMaxWarps];
   int part_n[kMaxCluster];
   u64 part_all[kMaxCluster], part_in[kMaxCluster];  // weight of the slice, and of what was gathered
   alignas(16) float group[kGroups];
   float redg[kGroups];
-  float redf[kWarps];
+  float redf[kMaxWarps];
   u64 result;  // CTA 0's answer
   float floor;
   int n_local;
@@ -155,14 +156,69 @@ __device__ __forceinline__ u64 warp_max(u64 v) {
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
   return ((u64)hi << 32) | lo;
 }
-__device__ __forceinline__ u64 block_max(u64 v, u64* red) {
+// A CTA's slice of a row, in 16-byte units from the one that holds its first element. kStage: raw in
+// shared memory; otherwise read again, from L2.
+template <typename T, int kThr, bool kStage>
+struct Slice {
+  static constexpr int kVec = 16 / (int)sizeof(T), kUnits = 16 / kVec;
+  const uint4* from;
+  uint4* stage;
+  int units, id0, s0, s1;
+
+  __device__ __forceinline__ void decode(uint4 x, int q, float* l) const {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      l[e] = sizeof(T) == 4 ? __uint_as_float(w[e & 3])
+                            : __uint_as_float((e & 1) ? w[(e >> 1) & 3] & 0xffff0000u : w[(e >> 1) & 3] << 16);
+      l[e] = fmaxf(l[e], -INFINITY);  // NaN counts as -inf
+    }
+    if (q == 0 || q == units - 1) {  // what lies outside the slice is marked with a NaN
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const int id = id0 + q * kVec + e;
+        if (id < s0 || id >= s1) l[e] = __uint_as_float(0x7fffffffu);
+      }
+    }
+  }
+  // f(16 values, their ids) until the slice is through; a thread's ids rise.
+  template <typename F>
+  __device__ __forceinline__ void batches(F f) const {
+    for (int q0 = threadIdx.x; q0 < units; q0 += kThr * kUnits) {
+      uint4 x[kUnits];
+      float l[16];
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) {
+        const int q = q0 + j * kThr;
+        x[j] = q < units ? (kStage ? stage[q] : __ldcg(from + q)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) {
+        const int q = q0 + j * kThr;
+        decode(x[j], q, l + j * kVec);
+        if (q >= units) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) l[j * kVec + e] = __uint_as_float(0x7fffffffu);
+        }
+      }
+      f(l, [&](int x16) { return id0 + (q0 + x16 / kVec * kThr) * kVec + x16 % kVec; });
+    }
+  }
+};
+
+// What a block of kThr threads does together.
+template <int kThr>
+struct Block {
+static constexpr int kWarps = kThr / 32, kPer = kList / kThr;
+
+static __device__ __forceinline__ u64 block_max(u64 v, u64* red) {
   v = warp_max(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   return warp_max(red[threadIdx.x & (kWarps - 1)]);
 }
-__device__ __forceinline__ float block_sum(float v, float* red) {
+static __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
@@ -173,7 +229,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return v;
 }
 // Exclusive prefix sums of (a, b) over the block's threads, in thread order.
-__device__ __forceinline__ void block_scan(u64& a, u64& b, u64* red, u64* red2) {
+static __device__ __forceinline__ void block_scan(u64& a, u64& b, u64* red, u64* red2) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   u64 x = a, y = b;
 #pragma unroll
@@ -196,7 +252,7 @@ __device__ __forceinline__ void block_scan(u64& a, u64& b, u64* red, u64* red2) 
 // bins whose count and weight `at(bin, count, weight)` gives. All threads get the bin, the sums before it
 // and its count.
 template <typename At>
-__device__ __forceinline__ void find(Smem& s, At at, bool by_mass, u64 target, int& bin, u64& cnt_before, u64& mass_before, u64& here) {
+static __device__ __forceinline__ void find(Smem& s, At at, bool by_mass, u64 target, int& bin, u64& cnt_before, u64& mass_before, u64& here) {
   constexpr int kEach = kBins / kThr;
   const int b0 = threadIdx.x * kEach;
   u64 c[kEach], m[kEach], cs = 0, ms = 0;
@@ -237,7 +293,7 @@ __device__ __forceinline__ void find(Smem& s, At at, bool by_mass, u64 target, i
 // Sums the CTAs' histograms (their first `arrays` arrays): each CTA takes kBins / size bins, `mass_of`
 // gives a bin's weight from the sums, then all read all.
 template <typename MassOf>
-__device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t size, int arrays, MassOf mass_of) {
+static __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t size, int arrays, MassOf mass_of) {
   cluster_sync();
   const int per = kBins / (int)size;
   // A thread sums up to four CTAs' counts of a bin, all loads in flight at once.
@@ -286,32 +342,28 @@ __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t
   __syncthreads();
 }
 
-__device__ __forceinline__ void add_weight(Smem& s, int b, uint32_t w) {
+static __device__ __forceinline__ void add_weight(Smem& s, int b, uint32_t w) {
   atomicAdd(&s.hist[0][b], 1u);
   if (w >> 15) atomicAdd(&s.hist[1][b], w >> 15);
   if (w & 0x7fffu) atomicAdd(&s.hist[2][b], w & 0x7fffu);
 }
-__device__ __forceinline__ u64 whole_mass(int, u64, u64 hi, u64 lo) { return (hi << 15) + lo; }
-__device__ __forceinline__ void clear_histogram(Smem& s) {
+static __device__ __forceinline__ u64 whole_mass(int, u64, u64 hi, u64 lo) { return (hi << 15) + lo; }
+static __device__ __forceinline__ void clear_histogram(Smem& s) {
   for (int x = threadIdx.x; x < 3 * kBins; x += kThr) (&s.hist[0][0])[x] = 0u;
 }
 
 // Gathers the keys for which `in` holds in this CTA's list, and makes their number known to the
 // cluster, with the weights `all` and `inside` of the whole block. Returns how many the cluster has.
-template <typename In>
-__device__ __forceinline__ int collect(Smem& s, const float* vals, int n, int id0, uint32_t rank, uint32_t size, In in, bool weigh,
-                                       const Row& r) {
+template <typename S, typename In>
+static __device__ __forceinline__ int collect(Smem& s, const S& slice, uint32_t rank, uint32_t size, In in, bool weigh, const Row& r) {
   if (threadIdx.x == 0) s.n_local = 0;
   __syncthreads();
   u64 all = 0, inside = 0;
-  for (int p0 = threadIdx.x; p0 < n; p0 += kThr * 8) {
-    float l[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) l[j] = p0 + j * kThr < n ? vals[p0 + j * kThr] : __uint_as_float(0x7fffffffu);
+  slice.batches([&](const float(&l)[16], auto id_of) {
     unsigned hits = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool hit = l[j] == l[j] && in(l[j], id0 + p0 + j * kThr);
+    for (int j = 0; j < 16; ++j) {
+      const bool hit = l[j] == l[j] && in(l[j], id_of(j));
       hits |= hit ? 1u << j : 0u;
       if (weigh && l[j] == l[j]) {
         const uint32_t w = r.fixed(r.dist(l[j]));
@@ -321,13 +373,13 @@ __device__ __forceinline__ int collect(Smem& s, const float* vals, int n, int id
     }
     if (hits) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 16; ++j)
         if ((hits >> j) & 1u) {
           const int at = atomicAdd(&s.n_local, 1);
-          if (at < kList) s.list[at] = value_id_key(l[j], (uint32_t)(id0 + p0 + j * kThr));
+          if (at < kList) s.list[at] = value_id_key(l[j], (uint32_t)id_of(j));
         }
     }
-  }
+  });
   if (weigh) {
     u64 a = all, b = inside;
     block_scan(a, b, s.red, s.red2);
@@ -350,7 +402,7 @@ __device__ __forceinline__ int collect(Smem& s, const float* vals, int n, int id
   return sum;
 }
 // The CTAs' lists (kList keys at most in all) to CTA 0's, CTA after CTA.
-__device__ __forceinline__ void join(Smem& s, uint32_t rank) {
+static __device__ __forceinline__ void join(Smem& s, uint32_t rank) {
   int base = 0;
   for (uint32_t k = 0; k < rank; ++k) base += s.part_n[k];
   if (rank > 0)
@@ -367,7 +419,7 @@ struct List {
 // The key of the last that stays of the list, and the weight of what stays: the largest key with
 // `target` keys at or above it, or (by_mass) with that weight; 0 if the whole list has less.
 // The list's shared memory is taken for the histograms.
-__device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, u64 target, u64* mass_out) {
+static __device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, u64 target, u64* mass_out) {
   u64 lo = 0, hi = ~0ull, mass = 0;
   while (true) {
     u64 top = 0, bottom = 0;
@@ -418,7 +470,7 @@ __device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, u6
   }
 }
 
-__device__ __forceinline__ void load_list(const Smem& s, const Row& r, int n, List& v) {
+static __device__ __forceinline__ void load_list(const Smem& s, const Row& r, int n, List& v) {
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int x = threadIdx.x + j * kThr;
@@ -429,12 +481,12 @@ __device__ __forceinline__ void load_list(const Smem& s, const Row& r, int n, Li
 
 // CTA 0: the draw from a list that holds all that can stay. `aim` is the weight for top-p when no top-k
 // fixes it.
-__device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs& a, const Row& r, int row, int m, int top_k, float top_p,
+static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs& a, const Row& r, int row, int m, int top_k, float top_p,
                                                u64 aim) {
   const float* g = a.gumbel + (int64_t)row * a.gs;
   u64 key = 0;
   float sum = 0.0f;
-  if (m <= kThr / 2) {
+  if (m <= 256) {
     // A key per thread, each ranked against all; then every bound is a matter of places and sums.
     u64 own = (int)threadIdx.x < m ? s.list[threadIdx.x] : 0;
     int rank = 0;
@@ -517,56 +569,63 @@ __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs& a, con
     }
   }
 }
+};
 
-template <typename T>
-__global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int slice) {
+template <typename T, int kThr, bool kStage>
+__global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const SampleArgs a, int length) {
+  using B = Block<kThr>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& s = *(Smem*)smem_raw;
-  float* vals = (float*)(smem_raw + ((sizeof(Smem) + 15) & ~(size_t)15));
   const uint32_t rank = cluster_rank(), size = cluster_size();
   // All CTAs of the cluster are there before one writes to another (waited for below).
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int row = blockIdx.x / (int)size, t = threadIdx.x, V = a.V;
-  const int s0 = min(V, (int)rank * slice), s1 = min(V, s0 + slice);
+  const int s0 = min(V, (int)rank * length), s1 = min(V, s0 + length);
   const T* src = (const T*)a.logits + (int64_t)row * a.ls + s0;
   const float* g = a.gumbel ? a.gumbel + (int64_t)row * a.gs : nullptr;
 
-  // The slice, in 16-byte units from the one that holds its first element: position p of
-  // `vals` is token id0 + p; what lies outside the slice is marked with a NaN.
   constexpr int kVec = 16 / (int)sizeof(T);
   const int skew = (int)(((uintptr_t)src & 15u) / sizeof(T));
-  const uint4* vec = (const uint4*)(src - skew);
-  const int id0 = s0 - skew, n = s1 > s0 ? (skew + s1 - s0 + kVec - 1) / kVec * kVec : 0;
+  Slice<T, kThr, kStage> slice;
+  slice.from = (const uint4*)(src - skew);
+  slice.stage = (uint4*)(smem_raw + ((sizeof(Smem) + 15) & ~(size_t)15));
+  slice.units = s1 > s0 ? (skew + s1 - s0 + kVec - 1) / kVec : 0;
+  slice.id0 = s0 - skew;
+  slice.s0 = s0;
+  slice.s1 = s1;
   float top = -INFINITY;
   int top_id = 0;  // the lowest id of this thread's largest logit: its ids rise
-  constexpr int kUnroll = 8;
-  for (int q0 = t; q0 < n / kVec; q0 += kThr * kUnroll) {
-    uint4 x[kUnroll];
+  if (kStage) {
+    constexpr int kLoads = 8;  // in flight
+    for (int q0 = t; q0 < slice.units; q0 += kThr * kLoads) {
+      uint4 x[kLoads];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
-      if (q0 + j * kThr < n / kVec) x[j] = __ldcs(vec + q0 + j * kThr);
+      for (int j = 0; j < kLoads; ++j)
+        if (q0 + j * kThr < slice.units) x[j] = __ldcs(slice.from + q0 + j * kThr);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const int q = q0 + j * kThr;
-      if (q >= n / kVec) break;
-      float f[kVec];
-      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      for (int j = 0; j < kLoads; ++j) {
+        const int q = q0 + j * kThr;
+        if (q >= slice.units) break;
+        slice.stage[q] = x[j];
+        float l[kVec];
+        slice.decode(x[j], q, l);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        f[e] = sizeof(T) == 4 ? __uint_as_float(w[e & 3])
-                              : __uint_as_float((e & 1) ? w[(e >> 1) & 3] & 0xffff0000u : w[(e >> 1) & 3] << 16);
-        f[e] = fmaxf(f[e], -INFINITY);  // NaN counts as -inf
-        const int id = id0 + q * kVec + e;
-        if (id < s0 || id >= s1) {
-          f[e] = __uint_as_float(0x7fffffffu);
-        } else if (f[e] > top) {
-          top = f[e];
-          top_id = id;
-        }
+        for (int e = 0; e < kVec; ++e)
+          if (l[e] > top) {
+            top = l[e];
+            top_id = slice.id0 + q * kVec + e;
+          }
       }
-#pragma unroll
-      for (int e = 0; e < kVec; e += 4) *(float4*)(vals + q * kVec + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
     }
+  } else {
+    slice.batches([&](const float(&l)[16], auto id_of) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (l[j] > top) {
+          top = l[j];
+          top_id = id_of(j);
+        }
+    });
   }
   Row r;
   r.temp = a.temperature ? a.temperature[row] : 1.0f;
@@ -594,9 +653,9 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
     if (t < kGroups)
       st_u32(dsmem(&s.group[(int)rank * per + t % per], (uint32_t)(t / per)), __float_as_uint(s.redg[t % per]));
   }
-  u64 best = block_max(value_id_key(top, (uint32_t)top_id), s.red);
+  u64 best = B::block_max(value_id_key(top, (uint32_t)top_id), s.red);
   if (t < (int)size) st_u64(dsmem(&s.part_key[rank], (uint32_t)t), best);
-  clear_histogram(s);
+  B::clear_histogram(s);
   cluster_sync();
   best = 0;
   for (uint32_t k = 0; k < size; ++k) best = s.part_key[k] > best ? s.part_key[k] : best;
@@ -634,7 +693,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
     // top-p alone: a flat row's tokens below the candidates would hold most of its weight.
     const bool likely = top_k > 0 || r.near_weight(floor_l) * (float)V < 20.0f;
     if (likely) {
-    const int m = collect(s, vals, n, id0, rank, size, [&](float l, int) { return l >= floor_l; }, top_k == 0, r);
+    const int m = B::collect(s, slice, rank, size, [&](float l, int) { return l >= floor_l; }, top_k == 0, r);
     u64 aim = 0, inside = 0;
     if (top_k == 0) {
       u64 all = 0;
@@ -645,12 +704,12 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
       aim = share_of(top_p, all);
     }
     if (m <= kList && inside >= aim) {
-      join(s, rank);
-      if (rank == 0) draw_from_list(s, a, r, row, m, top_k, top_p, aim);
+      B::join(s, rank);
+      if (rank == 0) B::draw_from_list(s, a, r, row, m, top_k, top_p, aim);
       return;
     }
     cluster_sync();  // the numbers are read before the next ones arrive
-    clear_histogram(s);
+    B::clear_histogram(s);
     }
   }
   if (top_k > 0 || top_p < 1.0f) {
@@ -659,12 +718,9 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
     u64 rest_w = 0;
     if (t == 0) s.rest_w = 0;
     __syncthreads();
-    for (int p0 = t; p0 < n; p0 += kThr * 4) {
-      float l[4];
+    slice.batches([&](const float(&l)[16], auto) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) l[j] = p0 + j * kThr < n ? vals[p0 + j * kThr] : __uint_as_float(0x7fffffffu);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 16; ++j) {
         if (l[j] != l[j]) continue;
         const float d = r.dist(l[j]);
         const int b = r.bin(d);
@@ -676,7 +732,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
           if (weigh) rest_w += r.fixed(d);
         }
       }
-    }
+    });
     rest = __reduce_add_sync(0xffffffffu, rest);
     const uint32_t rest_hi = __reduce_add_sync(0xffffffffu, (uint32_t)(rest_w >> 15));
     const uint32_t rest_lo = __reduce_add_sync(0xffffffffu, (uint32_t)(rest_w & 0x7fffu));
@@ -684,7 +740,7 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
       atomicAdd(&s.hist[0][kNear], rest);
       atomicAdd(&s.rest_w, ((u64)rest_hi << 15) + rest_lo);
     }
-    share_histogram(s, rank, size, weigh ? 2 : 1, [&](int b, u64 c, u64 lack, u64) {
+    B::share_histogram(s, rank, size, weigh ? 2 : 1, [&](int b, u64 c, u64 lack, u64) {
       if (b == kNear) {
         u64 m = 0;
         for (uint32_t k = 0; k < size; ++k) m += ld_u64(dsmem(&s.rest_w, k));
@@ -698,28 +754,28 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
     };
     int bin_k = kNear, bin_p = kNear;
     u64 cnt_k = 0, mass_k = 0, cnt_p = 0, mass_p = 0, here_k = 0, here_p = 0;
-    if (top_k > 0) find(s, sums, false, (u64)top_k, bin_k, cnt_k, mass_k, here_k);
+    if (top_k > 0) B::find(s, sums, false, (u64)top_k, bin_k, cnt_k, mass_k, here_k);
     // With no top-k the whole weight is the sum of all bins.
     u64 aim = 0;  // the weight before which a token stays; in whole units, so the least integer not below
     if (weigh) {
       u64 m = 0, z = 0;
       for (int b = t; b < kBins; b += kThr) m += s.mass[b];
       u64 before = m;
-      block_scan(before, z, s.red, s.red2);
+      B::block_scan(before, z, s.red, s.red2);
       if (t == kThr - 1) s.found_mass = before + m;
       __syncthreads();
       aim = share_of(top_p, s.found_mass);
       __syncthreads();
-      find(s, sums, true, aim, bin_p, cnt_p, mass_p, here_p);
+      B::find(s, sums, true, aim, bin_p, cnt_p, mass_p, here_p);
     }
     const int bin_all = min(bin_k, bin_p);
     const u64 most = top_k > 0 ? cnt_k + here_k : cnt_p + here_p;
     if (most <= (u64)kList) {
       // All that can stay, to CTA 0.
-      const int m = collect(s, vals, n, id0, rank, size,
+      const int m = B::collect(s, slice, rank, size,
                             [&](float l, int) { return r.place(l) < (float)(bin_all + 1) || bin_all == kNear; }, false, r);
-      join(s, rank);
-      if (rank == 0) draw_from_list(s, a, r, row, m, top_k, top_p, aim);
+      B::join(s, rank);
+      if (rank == 0) B::draw_from_list(s, a, r, row, m, top_k, top_p, aim);
       return;
     }
 
@@ -730,22 +786,24 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
       while (in_bin > (u64)kList) {
         // Split the keys between the smallest and the largest by their bits.
         u64 kmax = 0, kmin = 0;
-        for (int p = t; p < n; p += kThr) {
-          const float l = vals[p];
-          if (l != l || !r.in_bin(l, bin)) continue;
-          const u64 k = value_id_key(l, (uint32_t)(id0 + p));
-          if (!whole && (k < lo || k > hi)) continue;
-          kmax = k > kmax ? k : kmax;
-          kmin = ~k > kmin ? ~k : kmin;
-        }
-        kmax = block_max(kmax, s.red);
-        kmin = block_max(kmin, s.red);
+        slice.batches([&](const float(&l)[16], auto id_of) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (l[j] != l[j] || !r.in_bin(l[j], bin)) continue;
+            const u64 k = value_id_key(l[j], (uint32_t)id_of(j));
+            if (!whole && (k < lo || k > hi)) continue;
+            kmax = k > kmax ? k : kmax;
+            kmin = ~k > kmin ? ~k : kmin;
+          }
+        });
+        kmax = B::block_max(kmax, s.red);
+        kmin = B::block_max(kmin, s.red);
         __syncthreads();
         if (t < (int)size) {
           st_u64(dsmem(&s.part_key[rank], (uint32_t)t), kmax);
           st_u64(dsmem(&s.part_lo[rank], (uint32_t)t), kmin);
         }
-        clear_histogram(s);
+        B::clear_histogram(s);
         cluster_sync();
         hi = 0;
         lo = 0;
@@ -755,18 +813,18 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
         }
         lo = ~lo;
         const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);
-        for (int p = t; p < n; p += kThr) {
-          const float l = vals[p];
-          if (l != l) continue;
-          if (!r.in_bin(l, bin)) continue;
-          const u64 k = value_id_key(l, (uint32_t)(id0 + p));
-          if (k < lo || k > hi) continue;
-          add_weight(s, (int)((hi - k) >> shift), r.fixed(r.dist(l)));
-        }
-        share_histogram(s, rank, size, 3, whole_mass);
+        slice.batches([&](const float(&l)[16], auto id_of) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (l[j] != l[j] || !r.in_bin(l[j], bin)) continue;
+            const u64 k = value_id_key(l[j], (uint32_t)id_of(j));
+            if (k >= lo && k <= hi) B::add_weight(s, (int)((hi - k) >> shift), r.fixed(r.dist(l[j])));
+          }
+        });
+        B::share_histogram(s, rank, size, 3, B::whole_mass);
         int sub;
         u64 c, m;
-        find(s, sums, by_mass, target - before, sub, c, m, in_bin);
+        B::find(s, sums, by_mass, target - before, sub, c, m, in_bin);
         before += by_mass ? m : c;
         const u64 top = hi - ((u64)sub << shift);
         const u64 width = ((u64)1 << shift) - 1;
@@ -774,17 +832,17 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
         lo = top > width ? top - width : 0;
         whole = false;
       }
-      const int m = collect(s, vals, n, id0, rank, size, [&](float l, int id) {
+      const int m = B::collect(s, slice, rank, size, [&](float l, int id) {
         if (!r.in_bin(l, bin)) return false;
         const u64 k = value_id_key(l, (uint32_t)id);
         return k >= floor_key && (whole || (k >= lo && k <= hi));
       }, false, r);
-      join(s, rank);
+      B::join(s, rank);
       if (rank == 0) {
-        List v;
-        load_list(s, r, m, v);
+        typename B::List v;
+        B::load_list(s, r, m, v);
         u64 mass;
-        const u64 k = cut_list(s, v, by_mass, target - before, &mass);
+        const u64 k = B::cut_list(s, v, by_mass, target - before, &mass);
         if (t == 0) s.result = k;
       }
       cluster_sync();
@@ -796,24 +854,26 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
       bound = select(bin_k, here_k, cnt_k, false, (u64)top_k, 0);
       if (top_p < 1.0f) {
         // Weigh the top-k set.
-        clear_histogram(s);
+        B::clear_histogram(s);
         cluster_sync();
-        for (int p = t; p < n; p += kThr) {
-          const float l = vals[p];
-          if (l != l) continue;
-          const float d = r.dist(l);
-          if (value_id_key(l, (uint32_t)(id0 + p)) >= bound) add_weight(s, r.bin(d), r.fixed(d));
-        }
-        share_histogram(s, rank, size, 3, whole_mass);
+        slice.batches([&](const float(&l)[16], auto id_of) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (l[j] != l[j] || value_id_key(l[j], (uint32_t)id_of(j)) < bound) continue;
+            const float d = r.dist(l[j]);
+            B::add_weight(s, r.bin(d), r.fixed(d));
+          }
+        });
+        B::share_histogram(s, rank, size, 3, B::whole_mass);
         u64 m = 0, z = 0;
         for (int b = t; b < kBins; b += kThr) m += s.mass[b];
         u64 before = m;
-        block_scan(before, z, s.red, s.red2);
+        B::block_scan(before, z, s.red, s.red2);
         if (t == kThr - 1) s.found_mass = before + m;
         __syncthreads();
         aim = share_of(top_p, s.found_mass);
         __syncthreads();
-        find(s, sums, true, aim, bin_p, cnt_p, mass_p, here_p);
+        B::find(s, sums, true, aim, bin_p, cnt_p, mass_p, here_p);
       }
     }
     if (top_p < 1.0f) {
@@ -827,31 +887,31 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
   const int b_id = bound ? (int)key_id(bound) : V;
   float sum = 0.0f, top_score = -INFINITY;
   int drawn = -1;
-  for (int p0 = t; p0 < n; p0 += kThr * 8) {
-    float l[8], z[8];
+  slice.batches([&](const float(&l)[16], auto id_of) {
+    float z[16];
+    unsigned in = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int p = p0 + j * kThr;
-      l[j] = p < n ? vals[p] : __uint_as_float(0x7fffffffu);
-      const bool in = l[j] > b_val || (l[j] == b_val && id0 + p <= b_id);
-      if (!in) l[j] = __uint_as_float(0x7fffffffu);
-      z[j] = in ? __ldcs(g + id0 + p) : 0.0f;
+    for (int j = 0; j < 16; ++j) {
+      const bool stays = l[j] > b_val || (l[j] == b_val && id_of(j) <= b_id);
+      in |= stays ? 1u << j : 0u;
+      z[j] = stays ? __ldcs(g + id_of(j)) : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 16; ++j) {
+      if (!((in >> j) & 1u)) continue;
       const float w = r.near_weight(l[j]);
-      if (!(w >= r.min_p)) continue;  // what did not stay is a NaN
+      if (w < r.min_p) continue;
       sum += w;
       const float score = l[j] / r.temp + z[j];
-      if (score > top_score || drawn < 0) {  // a thread's ids rise: ties stay with the lowest
+      if (score > top_score || drawn < 0) {  // ties stay with the lowest id
         top_score = score;
-        drawn = id0 + p0 + j * kThr;
+        drawn = id_of(j);
       }
     }
-  }
+  });
   u64 key = drawn < 0 ? 0 : value_id_key(top_score, (uint32_t)drawn);
-  sum = block_sum(sum, s.redf);
-  key = block_max(key, s.red);
+  sum = B::block_sum(sum, s.redf);
+  key = B::block_max(key, s.red);
   if (t == 0) {
     st_u64(dsmem(&s.part_lo[rank], 0), key);
     st_u32(dsmem(&s.part_sum[rank], 0), __float_as_uint(sum));
@@ -873,18 +933,13 @@ __global__ void __launch_bounds__(kThr, 2) sample_kernel(const SampleArgs a, int
   }
 }
 
-template <typename T>
-cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
-  // Slices of up to 20,480 tokens, two on an SM; when the rows do not fill the SMs, of half that,
-  // so that more of them read a row.
-  int size = 1;
-  while (size < kMaxCluster && (a.V + size - 1) / size > 20480) size <<= 1;
-  if (size < kMaxCluster && a.V > 4096 * size && (int64_t)a.rows * size * 2 <= num_sms()) size <<= 1;
-  const int slice = ((a.V + size - 1) / size + 31) / 32 * 32;
-  if (slice > kMaxSlice || (int64_t)a.rows * size > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const size_t smem = ((sizeof(Smem) + 15) & ~(size_t)15) + (size_t)(slice + 16) * 4;
+template <typename T, int kThr, bool kStage>
+cudaError_t launch(const SampleArgs& a, int size, cudaStream_t stream) {
+  const int length = ((a.V + size - 1) / size + 31) / 32 * 32;
+  const size_t smem = ((sizeof(Smem) + 15) & ~(size_t)15) + (kStage ? (size_t)(length + 16) * sizeof(T) : 0);
+  if (length > kMaxSlice || smem > 227 * 1024 || (int64_t)a.rows * size > 0x7fffffff) return cudaErrorInvalidConfiguration;
   static FuncOnce once;
-  cudaError_t e = once.set((const void*)sample_kernel<T>, 227 * 1024, true);
+  cudaError_t e = once.set((const void*)sample_kernel<T, kThr, kStage>, 227 * 1024, true);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * size));
@@ -898,7 +953,22 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, slice);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, kThr, kStage>, a, length);
+}
+
+template <typename T>
+cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
+  // Slices of up to 20,480 tokens; when the rows do not fill the SMs, of half that, so that more of
+  // them read a row.
+  int size = 1;
+  while (size < kMaxCluster && (a.V + size - 1) / size > 20480) size <<= 1;
+  const int64_t ctas = (int64_t)a.rows * size;
+  if (size < kMaxCluster && a.V > 4096 * size && ctas * 2 <= num_sms()) size <<= 1;
+  // Few rows: the slices stay in shared memory, two CTAs on an SM. Many: a row's time is mostly barriers,
+  // and what hides them is more rows in flight than shared memory holds, so the slices are read again
+  // from L2 (four CTAs on an SM).
+  if (ctas > 2 * (int64_t)num_sms()) return launch<T, 256, false>(a, size, stream);
+  return launch<T, 512, true>(a, size, stream);
 }
 
 }  // namespace
