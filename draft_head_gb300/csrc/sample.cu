@@ -677,16 +677,19 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
   if (top_k > 0 ? top_k <= kGroups / 2 : top_p < 1.0f) {
     // The candidates: tokens not below the k-th largest group maximum.
     const int k = top_k > 0 ? top_k : kGroups / 2;
-    if (t < kGroups) {
-      const float own = s.group[t];
-      int before = 0;
-#pragma unroll 8
-      for (int x = 0; x < kGroups; x += 4) {
-        const float4 y = *(const float4*)&s.group[x];
-        before += (y.x > own || (y.x == own && x < t)) + (y.y > own || (y.y == own && x + 1 < t)) +
-                  (y.z > own || (y.z == own && x + 2 < t)) + (y.w > own || (y.w == own && x + 3 < t));
+    if (t < 32) {
+      // The largest order key that k maxima reach, bit by bit; a warp, eight maxima a lane.
+      uint32_t own[kGroups / 32], key = 0;
+#pragma unroll
+      for (int j = 0; j < kGroups / 32; ++j) own[j] = float_order_key(s.group[t + 32 * j]);
+      for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = key | (1u << bit);
+        uint32_t reach = 0;
+#pragma unroll
+        for (int j = 0; j < kGroups / 32; ++j) reach += own[j] >= c;
+        if (__reduce_add_sync(0xffffffffu, reach) >= (uint32_t)k) key = c;
       }
-      if (before == k - 1) s.floor = own;
+      if (t == 0) s.floor = order_key_float(key);
     }
     __syncthreads();
     const float floor_l = s.floor;
