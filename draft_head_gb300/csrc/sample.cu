@@ -36,6 +36,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "packed.cuh"
 
 namespace domino {
 
@@ -156,6 +157,13 @@ __device__ __forceinline__ u64 warp_max(u64 v) {
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
   return ((u64)hi << 32) | lo;
 }
+__device__ __forceinline__ float max16(const float (&l)[16]) {  // NaNs are passed over
+  float m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = max3(l[j], l[j + 4], fmaxf(l[j + 8], l[j + 12]));
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
 // A CTA's slice of a row, in 16-byte units from the one that holds its first element. kStage: raw in
 // shared memory; otherwise read again, from L2.
 template <typename T, int kThr, bool kStage>
@@ -165,25 +173,30 @@ struct Slice {
   uint4* stage;
   int units, id0, s0, s1;
 
+  // What lies outside the slice is marked with one NaN; a NaN logit counts as -inf.
+  static __device__ __forceinline__ float outside() { return __uint_as_float(0x7fffffffu); }
+  static __device__ __forceinline__ float cleared(float l) {
+    return __float_as_uint(l) == 0x7fffffffu ? l : fmaxf(l, -INFINITY);
+  }
   __device__ __forceinline__ void decode(uint4 x, int q, float* l) const {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       l[e] = sizeof(T) == 4 ? __uint_as_float(w[e & 3])
                             : __uint_as_float((e & 1) ? w[(e >> 1) & 3] & 0xffff0000u : w[(e >> 1) & 3] << 16);
-      l[e] = fmaxf(l[e], -INFINITY);  // NaN counts as -inf
     }
-    if (q == 0 || q == units - 1) {  // what lies outside the slice is marked with a NaN
+    if (q == 0 || q == units - 1) {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const int id = id0 + q * kVec + e;
-        if (id < s0 || id >= s1) l[e] = __uint_as_float(0x7fffffffu);
+        if (id < s0 || id >= s1) l[e] = outside();
       }
     }
   }
-  // f(16 values, their ids) until the slice is through; a thread's ids rise.
+  // f(16 values, their ids) until the slice is through, where one of the 16 is `least` at the least; a
+  // thread's ids rise.
   template <typename F>
-  __device__ __forceinline__ void batches(F f) const {
+  __device__ __forceinline__ void batches(float least, F f) const {
     for (int q0 = threadIdx.x; q0 < units; q0 += kThr * kUnits) {
       uint4 x[kUnits];
       float l[16];
@@ -198,9 +211,12 @@ struct Slice {
         decode(x[j], q, l + j * kVec);
         if (q >= units) {
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) l[j * kVec + e] = __uint_as_float(0x7fffffffu);
+          for (int e = 0; e < kVec; ++e) l[j * kVec + e] = outside();
         }
       }
+      if (least > -INFINITY && !(max16(l) >= least)) continue;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) l[j] = cleared(l[j]);
       f(l, [&](int x16) { return id0 + (q0 + x16 / kVec * kThr) * kVec + x16 % kVec; });
     }
   }
@@ -355,11 +371,12 @@ static __device__ __forceinline__ void clear_histogram(Smem& s) {
 // Gathers the keys for which `in` holds in this CTA's list, and makes their number known to the
 // cluster, with the weights `all` and `inside` of the whole block. Returns how many the cluster has.
 template <typename S, typename In>
-static __device__ __forceinline__ int collect(Smem& s, const S& slice, uint32_t rank, uint32_t size, In in, bool weigh, const Row& r) {
+static __device__ __forceinline__ int collect(Smem& s, const S& slice, uint32_t rank, uint32_t size, float least, In in, bool weigh,
+                                              const Row& r) {
   if (threadIdx.x == 0) s.n_local = 0;
   __syncthreads();
   u64 all = 0, inside = 0;
-  slice.batches([&](const float(&l)[16], auto id_of) {
+  slice.batches(weigh ? -INFINITY : least, [&](const float(&l)[16], auto id_of) {
     unsigned hits = 0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -607,24 +624,28 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
         const int q = q0 + j * kThr;
         if (q >= slice.units) break;
         slice.stage[q] = x[j];
-        float l[kVec];
+        float l[kVec], m = -INFINITY;
         slice.decode(x[j], q, l);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          if (l[e] > top) {
-            top = l[e];
-            top_id = slice.id0 + q * kVec + e;
-          }
+        for (int e = 0; e < kVec; ++e) m = fmaxf(m, l[e]);
+        if (m > top) {
+          top = m;
+#pragma unroll
+          for (int e = kVec - 1; e >= 0; --e)
+            if (l[e] == m) top_id = slice.id0 + q * kVec + e;
+        }
       }
     }
   } else {
-    slice.batches([&](const float(&l)[16], auto id_of) {
+    // Before the first batch `top` is -inf, and a batch of nothing but -inf changes nothing.
+    slice.batches(-INFINITY, [&](const float(&l)[16], auto id_of) {
+      const float m = max16(l);
+      if (m > top) {
+        top = m;
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (l[j] > top) {
-          top = l[j];
-          top_id = id_of(j);
-        }
+        for (int j = 15; j >= 0; --j)
+          if (l[j] == m) top_id = id_of(j);
+      }
     });
   }
   Row r;
@@ -696,7 +717,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
     // top-p alone: a flat row's tokens below the candidates would hold most of its weight.
     const bool likely = top_k > 0 || r.near_weight(floor_l) * (float)V < 20.0f;
     if (likely) {
-    const int m = B::collect(s, slice, rank, size, [&](float l, int) { return l >= floor_l; }, top_k == 0, r);
+    const int m = B::collect(s, slice, rank, size, floor_l, [&](float l, int) { return l >= floor_l; }, top_k == 0, r);
     u64 aim = 0, inside = 0;
     if (top_k == 0) {
       u64 all = 0;
@@ -721,7 +742,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
     u64 rest_w = 0;
     if (t == 0) s.rest_w = 0;
     __syncthreads();
-    slice.batches([&](const float(&l)[16], auto) {
+    slice.batches(-INFINITY, [&](const float(&l)[16], auto) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         if (l[j] != l[j]) continue;
@@ -775,7 +796,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
     const u64 most = top_k > 0 ? cnt_k + here_k : cnt_p + here_p;
     if (most <= (u64)kList) {
       // All that can stay, to CTA 0.
-      const int m = B::collect(s, slice, rank, size,
+      const int m = B::collect(s, slice, rank, size, -INFINITY,
                             [&](float l, int) { return r.place(l) < (float)(bin_all + 1) || bin_all == kNear; }, false, r);
       B::join(s, rank);
       if (rank == 0) B::draw_from_list(s, a, r, row, m, top_k, top_p, aim);
@@ -789,7 +810,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
       while (in_bin > (u64)kList) {
         // Split the keys between the smallest and the largest by their bits.
         u64 kmax = 0, kmin = 0;
-        slice.batches([&](const float(&l)[16], auto id_of) {
+        slice.batches(-INFINITY, [&](const float(&l)[16], auto id_of) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if (l[j] != l[j] || !r.in_bin(l[j], bin)) continue;
@@ -816,7 +837,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
         }
         lo = ~lo;
         const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);
-        slice.batches([&](const float(&l)[16], auto id_of) {
+        slice.batches(-INFINITY, [&](const float(&l)[16], auto id_of) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if (l[j] != l[j] || !r.in_bin(l[j], bin)) continue;
@@ -835,7 +856,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
         lo = top > width ? top - width : 0;
         whole = false;
       }
-      const int m = B::collect(s, slice, rank, size, [&](float l, int id) {
+      const int m = B::collect(s, slice, rank, size, -INFINITY, [&](float l, int id) {
         if (!r.in_bin(l, bin)) return false;
         const u64 k = value_id_key(l, (uint32_t)id);
         return k >= floor_key && (whole || (k >= lo && k <= hi));
@@ -859,7 +880,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
         // Weigh the top-k set.
         B::clear_histogram(s);
         cluster_sync();
-        slice.batches([&](const float(&l)[16], auto id_of) {
+        slice.batches(-INFINITY, [&](const float(&l)[16], auto id_of) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if (l[j] != l[j] || value_id_key(l[j], (uint32_t)id_of(j)) < bound) continue;
@@ -890,12 +911,15 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
   const int b_id = bound ? (int)key_id(bound) : V;
   float sum = 0.0f, top_score = -INFINITY;
   int drawn = -1;
-  slice.batches([&](const float(&l)[16], auto id_of) {
+  // Nothing below this passes min_p either (with room for the rounding; the test itself follows), so its
+  // noise is not read.
+  const float least = r.min_p > 0.0f ? fmaxf(b_val, r.lmax + r.temp * (logf(r.min_p) - 1e-3f) - 1e-5f * fabsf(r.lmax)) : b_val;
+  slice.batches(least, [&](const float(&l)[16], auto id_of) {
     float z[16];
     unsigned in = 0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const bool stays = l[j] > b_val || (l[j] == b_val && id_of(j) <= b_id);
+      const bool stays = l[j] >= least && (l[j] > b_val || id_of(j) <= b_id);
       in |= stays ? 1u << j : 0u;
       z[j] = stays ? __ldcs(g + id_of(j)) : 0.0f;
     }
@@ -905,6 +929,9 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const Samp
       const float w = r.near_weight(l[j]);
       if (w < r.min_p) continue;
       sum += w;
+      // The exact score only where one within rounding of it does not lose.
+      const float near = l[j] * r.inv_t;
+      if (near + z[j] + 1e-6f * (fabsf(near) + fabsf(z[j])) < top_score) continue;
       const float score = l[j] / r.temp + z[j];
       if (score > top_score || drawn < 0) {  // ties stay with the lowest id
         top_score = score;
