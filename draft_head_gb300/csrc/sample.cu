@@ -589,7 +589,7 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
 };
 
 template <typename T, int kThr, bool kStage>
-__global__ void __launch_bounds__(kThr, kStage ? 2 : 4) sample_kernel(const SampleArgs a, int length) {
+__global__ void __launch_bounds__(kThr, kStage ? 2 : 5) sample_kernel(const SampleArgs a, int length) {
   using B = Block<kThr>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& s = *(Smem*)smem_raw;
@@ -996,7 +996,7 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   if (size < kMaxCluster && a.V > 4096 * size && ctas * 2 <= num_sms()) size <<= 1;
   // Few rows: the slices stay in shared memory, two CTAs on an SM. Many: a row's time is mostly barriers,
   // and what hides them is more rows in flight than shared memory holds, so the slices are read again
-  // from L2 (four CTAs on an SM).
+  // from L2 (five CTAs on an SM; six and eight spill in the draw).
   if (ctas > 2 * (int64_t)num_sms()) return launch<T, 256, false>(a, size, stream);
   return launch<T, 512, true>(a, size, stream);
 }
