@@ -237,11 +237,16 @@ int simt_row_tiles(const AttnArgs& a) {
 
 }  // namespace
 
+// Of every kernel that a block with these bounds or smaller ones may run on.
 size_t attn_ws_bytes(const AttnArgs& a) {
-  return attn_tc_applies(a) ? attn_tc_ws_bytes(a) : partial_bytes(simt_want(), kBM, a.D);
+  const size_t simt = partial_bytes(simt_want(), kBM, a.D);
+  if (a.dtype != DOMINO_BF16 || a.D > 128) return simt;
+  const size_t rows = attn_rows_ws_bytes(a), rest = attn_tc_applies(a) ? attn_tc_ws_bytes(a) : simt;
+  return rows > rest ? rows : rest;
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
+  if (attn_rows_applies(a)) return launch_attention_rows(a, stream);
   if (attn_tc_applies(a)) return launch_attention_tc(a, stream);
   SimtP p;
   p.a = a;

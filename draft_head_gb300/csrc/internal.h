@@ -223,6 +223,10 @@ struct AttnArgs {
 };
 size_t attn_ws_bytes(const AttnArgs& a);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
+// At most 16 packed rows of a kv head: bf16, head_dim <= 128.
+bool attn_rows_applies(const AttnArgs& a);
+size_t attn_rows_ws_bytes(const AttnArgs& a);
+cudaError_t launch_attention_rows(const AttnArgs& a, cudaStream_t stream);
 // On the tensor cores: bf16, head_dim <= 128.
 bool attn_tc_applies(const AttnArgs& a);
 size_t attn_tc_ws_bytes(const AttnArgs& a);
