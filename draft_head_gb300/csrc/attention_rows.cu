@@ -27,7 +27,8 @@ namespace domino {
 namespace {
 
 constexpr int kBN = 16, kWarps = 4, kThr = 32 * kWarps;
-constexpr int kLeast = 4;  // key tiles per CTA at least: one per warp
+constexpr int kLeast = 8;  // key tiles per CTA at least: two per warp
+constexpr int kMostPieces = 64;  // of a row tile: their join takes a round trip for every eight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 32.0f;
@@ -225,22 +226,16 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
       }
       if (mend) {
         for (int x = 0; x < kBN && s0 + x < end; ++x)
-          for (int d = 0; d < 8 * JJ; ++d) {
-            const int col = 64 * (d >> 3) + 8 * n + (d & 7);
-            if (col >= a.D) continue;
-            const float v = __bfloat162float(vb[(int64_t)(s0 + x) * a.ss + col]);
-            if (isfinite(v)) continue;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = g * 8 + 2 * c + e;
-              if (!sees(a.mode, a.sinks, s_low[r], ctx, rows_n, s_i[r], mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, s0 + x))
-                continue;
+          for (int e = 0; e < 2; ++e) {
+            const int r = g * 8 + 2 * c + e;
+            const bool sees_it = sees(a.mode, a.sinks, s_low[r], ctx, rows_n, s_i[r],
+                                      mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, s0 + x);
 #pragma unroll
-              for (int t = 0; t < 4 * JJ; ++t)
-                if (t == (d >> 3) * 4 + ((d & 7) >> 1)) {
-                  if (d & 1) o[g][t][2 + e] += v;
-                  else o[g][t][e] += v;
-                }
+            for (int d = 0; d < 8 * JJ; ++d) {
+              const int col = 64 * (d >> 3) + 8 * n + (d & 7);
+              const float v = col < a.D ? __bfloat162float(vb[(int64_t)(s0 + x) * a.ss + col]) : 0.0f;
+              if (sees_it && !isfinite(v)) o[g][(d >> 3) * 4 + ((d & 7) >> 1)][(d & 1) * 2 + e] += v;
             }
           }
       }
@@ -306,51 +301,66 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  for (int x = threadIdx.x; x < rows * (DP / 4); x += kThr) {
-    const int r = x / (DP / 4), e = (x - r * (DP / 4)) * 4;
-    if (e >= a.D) continue;
-    const int64_t first = tile * p.splits * kRows + r;
-    // One pass over the pieces in order, eight in flight, the maximum raised as they come.
-    float mm = -INFINITY, ll = 0.0f;
-    float4 acc = make_float4(0, 0, 0, 0);
-    for (int s = 0; s < used; s += 8) {
-      float2 ml[8];
-      float4 y[8];
+  // A thread has up to kX groups of four columns, in rows that are kThr / (DP / 4) apart: one pass over the
+  // pieces in order, kU in flight for every group, the maximum raised as they come.
+  constexpr int kX = kRows * (DP / 4) / kThr, kApart = kThr / (DP / 4), kU = kX > 2 ? 4 : 8;
+  const int e = (threadIdx.x % (DP / 4)) * 4, r0 = threadIdx.x / (DP / 4);
+  if (e >= a.D) return;
+  float mm[kX], ll[kX];
+  float4 acc[kX];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        ml[u] = make_float2(-INFINITY, 0.0f);
-        if (s + u < used) {
-          ml[u] = __ldcg(&p.part.ml[first + (int64_t)(s + u) * kRows]);
-          y[u] = __ldcg((const float4*)(p.part.o + (first + (int64_t)(s + u) * kRows) * a.D + e));
+  for (int x = 0; x < kX; ++x) {
+    mm[x] = -INFINITY;
+    ll[x] = 0.0f;
+    acc[x] = make_float4(0, 0, 0, 0);
+  }
+  for (int s = 0; s < used; s += kU) {
+    float2 ml[kX][kU];
+    float4 y[kX][kU];
+#pragma unroll
+    for (int x = 0; x < kX; ++x)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        ml[x][u] = make_float2(-INFINITY, 0.0f);
+        if (s + u < used && r0 + x * kApart < rows) {
+          const int64_t at = (tile * p.splits + s + u) * kRows + r0 + x * kApart;
+          ml[x][u] = __ldcg(&p.part.ml[at]);
+          y[x][u] = __ldcg((const float4*)(p.part.o + at * a.D + e));
         }
       }
-      float now = mm;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) now = fmaxf(now, ml[u].x);
-      const float keep = now == mm || mm == -INFINITY ? 1.0f : ex2(mm - now);
-      ll *= keep;
-      acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
-      mm = now;
+    for (int x = 0; x < kX; ++x) {
+      float now = mm[x];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (ml[u].x == -INFINITY && ml[u].y == 0.0f) continue;  // saw nothing
-        const float f = ml[u].x == mm || ml[u].x == -INFINITY ? 1.0f : ex2(ml[u].x - mm);
-        ll += ml[u].y * f;
-        acc.x += y[u].x * f; acc.y += y[u].y * f; acc.z += y[u].z * f; acc.w += y[u].w * f;
+      for (int u = 0; u < kU; ++u) now = fmaxf(now, ml[x][u].x);
+      const float keep = now == mm[x] || mm[x] == -INFINITY ? 1.0f : ex2(mm[x] - now);
+      ll[x] *= keep;
+      acc[x].x *= keep; acc[x].y *= keep; acc[x].z *= keep; acc[x].w *= keep;
+      mm[x] = now;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (ml[x][u].x == -INFINITY && ml[x][u].y == 0.0f) continue;  // saw nothing
+        const float f = ml[x][u].x == now || ml[x][u].x == -INFINITY ? 1.0f : ex2(ml[x][u].x - now);
+        ll[x] += ml[x][u].y * f;
+        acc[x].x += y[x][u].x * f; acc[x].y += y[x][u].y * f; acc[x].z += y[x][u].z * f; acc[x].w += y[x][u].w * f;
       }
     }
-    finish(r, e, acc, mm, ll);
   }
+#pragma unroll
+  for (int x = 0; x < kX; ++x)
+    if (r0 + x * kApart < rows) finish(r0 + x * kApart, e, acc[x], mm[x], ll[x]);
 }
 
-int64_t want_ctas() { return 4 * (int64_t)num_sms(); }
+int64_t want_ctas() { return 2 * (int64_t)num_sms(); }  // what is resident at once
 
 template <int NT, int KS, int JJ>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   RowsP p;
   p.a = a;
   p.c = fmaxf(a.scale * kLog2e, 1e-30f);  // a scale of 0 still has to leave a masked score at -inf
-  p.splits = splits_for((int64_t)a.hkv * a.rows.batch, want_ctas(), ((int64_t)a.rows.max_ctx + a.rows.max_q) / kBN / kLeast);
+  int64_t most = ((int64_t)a.rows.max_ctx + a.rows.max_q) / kBN / kLeast;
+  most = most < kMostPieces ? most : kMostPieces;
+  p.splits = splits_for((int64_t)a.hkv * a.rows.batch, want_ctas(), most);
   p.part = partials_at(a.scratch, want_ctas(), 16);
   const dim3 grid((unsigned)p.splits, (unsigned)a.hkv, (unsigned)a.rows.batch);
   attn_rows_kernel<NT, KS, JJ><<<grid, kThr, 0, stream>>>(p);
