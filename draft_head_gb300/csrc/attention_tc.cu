@@ -227,11 +227,11 @@ __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int 
   }
 }
 
-// Adds the non-finite values that the row sees in the piece's partly seen tiles to
-// columns [e0, e0 + 32) of its sums: the tiles had them cleared, because the product
+// Adds the non-finite values that the row sees in the piece's partly seen tiles to columns [e0, e1) of its
+// result in memory (bf16 `out`, or the piece's sums `sums`): the tiles had them cleared, because the product
 // with V would have spread them to the rows that do not see them.
 __device__ __noinline__ void add_non_finite(const AttnArgs& a, const Unit& w, int b, int h, int k0, int k1, int i, int low,
-                                            const uint8_t* mask_row, int e0, float* o) {
+                                            const uint8_t* mask_row, int e0, int e1, __nv_bfloat16* out, float4* sums) {
   const uint16_t* v = (const uint16_t*)a.v + (int64_t)b * a.rs + (int64_t)h * a.hs;
   for (int k = k0; k < k1; ++k) {
     const int s0 = w.kt.slot(k, kBN);
@@ -239,11 +239,16 @@ __device__ __noinline__ void add_non_finite(const AttnArgs& a, const Unit& w, in
     uint32_t bits[4];
     seen_bits(a, w, i, low, mask_row, s0, bits);
     for (int j = 0; j < kBN; ++j) {
-      if (!((bits[j >> 5] >> (j & 31)) & 1u)) continue;
+      const uint32_t word = j < 32 ? bits[0] : j < 64 ? bits[1] : j < 96 ? bits[2] : bits[3];
+      if (!((word >> (j & 31)) & 1u)) continue;
       const uint16_t* row = v + (int64_t)(s0 + j) * a.ss;
-      for (int e = 0; e < 32 && e0 + e < a.D; ++e) {
-        const uint32_t x = row[e0 + e];
-        if ((x & 0x7f80u) == 0x7f80u) o[e] += __uint_as_float(x << 16);
+      for (int e = e0; e < e1 && e < a.D; ++e) {
+        const uint32_t x = row[e];
+        if ((x & 0x7f80u) != 0x7f80u) continue;
+        if (out)
+          out[e] = __float2bfloat16(__bfloat162float(out[e]) + __uint_as_float(x << 16));
+        else
+          ((float*)(sums + (e >> 2) * 128))[e & 3] += __uint_as_float(x << 16);
       }
     }
   }
@@ -770,17 +775,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           for (int e = 0; e < kPart; ++e)
             o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + (two ? __uint_as_float(o1[e]) * f1 : 0.0f));
         }
-        if (bad && live) {
-#pragma unroll
-          for (int e0 = 0; e0 < kPart; e0 += 32) {
-            float y[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e0 + e]);
-            add_non_finite(a, w, b, h, k0, k1, i, low, mask_row, col0 + c + e0, y);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e0 + e] = __float_as_uint(y[e]);
-          }
-        }
         __syncwarp();
         if (pieces > 1) {
           if (live) {
@@ -821,6 +815,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
       }
       tc_fence_before();  // these reads of O before the next item's first product
+      if (bad) {
+        __threadfence_block();
+        __syncwarp();  // a row's result may have been stored by other lanes
+        if (live)
+          add_non_finite(a, w, b, h, k0, k1, i, low, mask_row, col0, col0 + kCols,
+                         pieces > 1 ? nullptr : (__nv_bfloat16*)a.out + row * a.D,
+                         p.o + (mine_at * NQ + (NQ == 2 ? g : 0)) * (C::DP / 4) * 128 + trow);
+      }
       if (pieces == 1) {
         if (live && a.lse && (NQ == 2 || g == 0)) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
