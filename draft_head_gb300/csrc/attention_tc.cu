@@ -54,7 +54,9 @@ constexpr int kItem = 2;       // list places of a row tile beside its key tiles
 constexpr int kBadRing = 8;    // items the roles may be apart, at most (the ring holds fewer tiles)
 
 struct TcAttnP {
-  CUtensorMap tmK, tmV;
+  CUtensorMap tmK, tmV, tmQ, tmO;
+  int q_boxes;    // 1: a query tile is one box of tmQ (the group divides 128)
+  int o_boxes;    // 1: 32 packed rows of the output are one box of tmO (it divides 32)
   AttnArgs a;
   int row_tiles;  // per request, of 128 NQ packed rows
   int slots;      // ring buffers
@@ -194,6 +196,18 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
         "l"((uint64_t)tmap), "r"(x), "r"(s), "r"(h), "r"(b), "r"(smem_u32(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"((uint64_t)tmap), "r"(x),
+               "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
 // Shared-memory descriptor of an MN-major operand with 128-byte swizzle: rows of 64
 // elements of N, 8 rows (of K) per 1024-byte atom; the next 8 rows follow at the
 // stride offset, the next 64 elements of N at the leading offset (a whole 128-row block).
@@ -309,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mbar_init(&p_ready[2 * s + 1], 4);
       mbar_init(&o_done[s], 1);
     }
-    mbar_init(q_ready, 2);
+    mbar_init(q_ready, p.q_boxes ? 1 : 2);
     mbar_init(q_free, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -317,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     mbar_fence_init();
     tma_prefetch_desc(&p.tmK);
     tma_prefetch_desc(&p.tmV);
+    if (p.q_boxes) tma_prefetch_desc(&p.tmQ);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -556,19 +571,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       walk.part(w.cnt, k0, k1);
       walk.next(w.cnt, hkv);
       if (k0 == k1) continue;
-      // The query rows, 16 bytes a copy, swizzled as the MMA reads them; the scores before
-      // have read theirs. Rows that there are none of keep what they held: no other row's
-      // result depends on them.
+      // The query rows, swizzled as the MMA reads them; the scores before have read theirs. Rows that
+      // there are none of hold anything: no other row's result depends on them.
       if (item > 0 && !warp_wait(q_free, (item - 1u) & 1u, s_abort, ctl, p.timeout_ns)) break;
-      {
+      if (p.q_boxes) {
+        // Packed rows of a tile are `G` heads of each of 128 / G rows: one box.
+        if (threadIdx.x == 64) {
+          mbar_expect_tx(q_ready, NQ * C::kQBytes);
+#pragma unroll
+          for (int g = 0; g < NQ; ++g)
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+              tma_load_3d(sQ + g * C::kQBytes + kb * (128 * 128), &p.tmQ, kb * 64, h * G, w.q0 + w.i_first + g * (128 / G), q_ready);
+        }
+      } else {
         const int x = t64 & (8 * KB - 1);
+        constexpr int kStep = 64 / (8 * KB);
+        int r = t64 / (8 * KB), i = (w.r0 + r) / G, gq = w.r0 + r - i * G;
         if (x * 8 < a.D)
-          for (int r = t64 / (8 * KB); r < w.rows; r += 64 / (8 * KB)) {
-            const int pr = w.r0 + r, i = pr / G;
-            const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + ((int64_t)(w.q0 + i) * a.hq + h * G + (pr - i * G)) * a.D + x * 8;
+          for (; r < w.rows; r += kStep) {
+            const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + ((int64_t)(w.q0 + i) * a.hq + h * G + gq) * a.D + x * 8;
             const uint32_t dst = smem_u32(sQ) + (uint32_t)((r >> 7) * C::kQBytes + (x >> 3) * (128 * 128) + (r & 127) * 128 +
                                                            (((x & 7) ^ (r & 7)) << 4));
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+            for (gq += kStep; gq >= G; gq -= G) ++i;
           }
         asm volatile("cp.async.wait_all;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -748,6 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         l = x.y * f0 + (f1 != 0.0f ? y.y * f1 : 0.0f);
       }
       const bool two = NQ == 1 && k1 - k0 > 1;  // the second O has been written
+      const bool o_boxes = p.o_boxes && !bad && g * 128 + quarter * 32 + 32 <= w.rows;
       // CTA c holds list places [list c / ctas, list (c + 1) / ctas).
       int c_first = blockIdx.x, pieces = 1;
       if (k0 > 0 || k1 < w.cnt) {
@@ -794,8 +821,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               z[j] = pack_bf16(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
             y[e] = make_uint4(z[0], z[1], z[2], z[3]);
           }
-          if (NQ == 2) {
+          if (NQ == 2 && o_boxes) {
+            // As a box, from shared memory.
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < kPart / 8; ++e) *(uint4*)(my_stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = y[e];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&p.tmO, c, h * G, w.q0 + w.i_first + (g * 128 + quarter * 32) / G, my_stage);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          } else if (NQ == 2) {
             // Through shared memory, so that 128 bytes of a row leave together.
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
 #pragma unroll
             for (int e = 0; e < kPart / 8; ++e) *(uint4*)(my_stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = y[e];
             __syncwarp();
@@ -896,6 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       ++item;
     }
+    if (NQ == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -938,6 +980,20 @@ bool make_tmap(CUtensorMap* tm, const void* base, const AttnArgs& a) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries or the output as {head_dim, head, row}, boxes of 64 elements of a group's heads of
+// packed / G rows.
+bool make_row_tmap(CUtensorMap* tm, const void* base, int packed, const AttnArgs& a) {
+  EncodeTiledFn fn = encode_fn();
+  const int G = a.hq / a.hkv;
+  if (!fn || packed % G) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.hq, (cuuint64_t)a.rows.tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.hq * a.D * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(packed / G)}, estr[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr size_t kArrivedBytes = 4096;
 
 template <int NQ, int KB>
@@ -946,6 +1002,8 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   TcAttnP p;
   memset(&p, 0, sizeof(p));
   if (!make_tmap(&p.tmK, a.k, a) || !make_tmap(&p.tmV, a.v, a)) return cudaErrorInvalidValue;
+  p.q_boxes = make_row_tmap(&p.tmQ, a.q, 128, a) ? 1 : 0;
+  p.o_boxes = NQ == 2 && make_row_tmap(&p.tmO, a.out, 32, a) ? 1 : 0;
   p.a = a;
   p.row_tiles = (int)(((int64_t)a.rows.max_q * (a.hq / a.hkv) + C::BMT - 1) / C::BMT);
   p.timeout_ns = wait_timeout_ns();
