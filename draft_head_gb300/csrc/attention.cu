@@ -13,6 +13,7 @@
 #include <math.h>
 
 #include "attention.cuh"
+#include "packed.cuh"
 
 namespace domino {
 
@@ -28,6 +29,13 @@ struct SimtP {
   Partials part;
   int splits, row_tiles;
 };
+
+__device__ __forceinline__ float4 load4(const float* p) { return *(const float4*)p; }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = *(const uint2*)p;
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__ SimtP p) {
@@ -56,13 +64,37 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
     s_low[t] = window_low(pos, a.window);
   }
   const T* q = (const T*)a.q;
-  for (int x = t; x < kBM * D; x += kThr) {
-    const int r = x / D, e = x - r * D, pr = r0 + r;
-    sq[r * ldq + e] = r < rows ? to_f<T>(q[((int64_t)(q0 + pr / G) * a.hq + h * G + pr % G) * D + e]) * (a.scale * kLog2e) : 0.0f;
-  }
+  // Four elements a thread; its place moves on by kThr of them without a division.
+  const int nv = D / 4, row_step = kThr / nv, col_step = kThr - row_step * nv, row_1 = t / nv, col_1 = t - row_1 * nv;
+  auto each = [&](int rows_of, auto f) {
+    for (int r = row_1, e = col_1; r < rows_of;) {
+      f(r, e * 4);
+      r += row_step;
+      e += col_step;
+      if (e >= nv) {
+        e -= nv;
+        ++r;
+      }
+    }
+  };
+  each(kBM, [&](int r, int e) {
+    float4 x = make_float4(0, 0, 0, 0);
+    if (r < rows) {
+      const int pr = r0 + r;
+      x = load4(q + ((int64_t)(q0 + pr / G) * a.hq + h * G + pr % G) * D + e);
+    }
+    const float c = a.scale * kLog2e;
+    *(float4*)(sq + r * ldq + e) = make_float4(x.x * c, x.y * c, x.z * c, x.w * c);
+  });
   __syncthreads();
-  int low = 0x7fffffff;
-  for (int r = 0; r < rows; ++r) low = min(low, s_low[r]);
+  int low = 0x7fffffff, low_max = 0;
+  for (int r = 0; r < rows; ++r) {
+    low = min(low, s_low[r]);
+    low_max = max(low_max, s_low[r]);
+  }
+  // Slots that every row sees: from all_low (or among the sinks) up to all_hi.
+  const int all_hi = a.mode == DOMINO_MASK_CAUSAL ? ctx + s_i[0] + 1 : a.mode == DOMINO_MASK_FULL ? ctx + n : ctx;
+  const int all_low = a.mode == DOMINO_MASK_CAUSAL ? low_max : min(low_max, ctx);
   const KeyTiles kt = key_tiles(a.mode, a.sinks, low, ctx, n, s_i[rows - 1], kBN);
   const int used = splits_used(p.splits, kt.count, kLeast);
   if (split >= used) return;
@@ -83,14 +115,15 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
   for (int k = k_begin; k < k_end; ++k) {
     const int s0 = kt.slot(k, kBN);
     __syncthreads();
-    for (int x = t; x < kBN * D; x += kThr) {
-      const int r = x / D, e = x - r * D, s = s0 + r;
+    each(kBN, [&](int r, int e) {
       // Slots past the request's rows are not read.
-      sk[r * ldq + e] = s < ctx + n ? to_f<T>(kb[(int64_t)s * a.ss + e]) : 0.0f;
-      sv[r * D + e] = s < ctx + n ? to_f<T>(vb[(int64_t)s * a.ss + e]) : 0.0f;
-    }
+      const bool in = s0 + r < ctx + n;
+      *(float4*)(sk + r * ldq + e) = in ? load4(kb + (int64_t)(s0 + r) * a.ss + e) : make_float4(0, 0, 0, 0);
+      *(float4*)(sv + r * D + e) = in ? load4(vb + (int64_t)(s0 + r) * a.ss + e) : make_float4(0, 0, 0, 0);
+    });
     __syncthreads();
-    float s[4][2] = {};
+    const bool whole = s0 + kBN <= all_hi && (s0 >= all_low || s0 + kBN <= a.sinks);
+    float2 s2[4][2] = {};  // even and odd terms
     for (int e = 0; e < D; e += 4) {
       float4 kq[2], qq[4];
 #pragma unroll
@@ -101,8 +134,14 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          s[i][j] = fmaf(qq[i].x, kq[j].x, fmaf(qq[i].y, kq[j].y, fmaf(qq[i].z, kq[j].z, fmaf(qq[i].w, kq[j].w, s[i][j]))));
+          s2[i][j] = fma2(make_float2(qq[i].x, qq[i].y), make_float2(kq[j].x, kq[j].y),
+                         fma2(make_float2(qq[i].z, qq[i].w), make_float2(kq[j].z, kq[j].w), s2[i][j]));
     }
+    float s[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = tr * 4 + i;
@@ -111,8 +150,8 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int slot = s0 + tc + 16 * j;
-        in[j] = r < rows && slot < ctx + n &&
-                sees(a.mode, a.sinks, s_low[r], ctx, n, s_i[r], mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, slot);
+        in[j] = r < rows && (whole || (slot < ctx + n &&
+                sees(a.mode, a.sinks, s_low[r], ctx, n, s_i[r], mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, slot)));
         if (in[j]) mx = fmaxf(mx, s[i][j]);
       }
 #pragma unroll
@@ -142,17 +181,26 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
       for (int c = 0; c < 4; ++c) {
         const int e = c * 64 + tc * 4;
         if (e < D) {
-          const float4 v = *(const float4*)(sv + j * D + e);
+          float4 v = *(const float4*)(sv + j * D + e);
+          // What a row does not see has weight 0 and must not be multiplied if it is no number. A slot that
+          // all rows see may be anything.
+          if (!whole && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (w[i] != 0.0f) {
+                o[i][4 * c] = fmaf(w[i], v.x, o[i][4 * c]);
+                o[i][4 * c + 1] = fmaf(w[i], v.y, o[i][4 * c + 1]);
+                o[i][4 * c + 2] = fmaf(w[i], v.z, o[i][4 * c + 2]);
+                o[i][4 * c + 3] = fmaf(w[i], v.w, o[i][4 * c + 3]);
+              }
+            continue;
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // A slot that no row of the tile's row sees has weight 0 and is not
-            // multiplied: its v may hold anything.
-            if (w[i] != 0.0f) {
-              o[i][4 * c] = fmaf(w[i], v.x, o[i][4 * c]);
-              o[i][4 * c + 1] = fmaf(w[i], v.y, o[i][4 * c + 1]);
-              o[i][4 * c + 2] = fmaf(w[i], v.z, o[i][4 * c + 2]);
-              o[i][4 * c + 3] = fmaf(w[i], v.w, o[i][4 * c + 3]);
-            }
+            const float2 w2 = make_float2(w[i], w[i]);
+            const float2 x = fma2(w2, make_float2(v.x, v.y), make_float2(o[i][4 * c], o[i][4 * c + 1]));
+            const float2 y = fma2(w2, make_float2(v.z, v.w), make_float2(o[i][4 * c + 2], o[i][4 * c + 3]));
+            o[i][4 * c] = x.x; o[i][4 * c + 1] = x.y; o[i][4 * c + 2] = y.x; o[i][4 * c + 3] = y.y;
           }
         }
       }

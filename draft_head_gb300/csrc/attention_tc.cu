@@ -50,7 +50,6 @@ constexpr int kHalf = 64;  // and of the halves in which the weights are handed 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 32.0f;  // growth of the maximum (log2) that forces a rescale of O
-constexpr int kItem = 2;       // list places of a row tile beside its key tiles
 constexpr int kBadRing = 8;    // items the roles may be apart, at most (the ring holds fewer tiles)
 
 struct TcAttnP {
@@ -134,6 +133,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The CTA's part of the work list, walked by every role alike.
+template <int kItem>
 struct Walk {
   int u, h, k, len;
   int64_t x;  // place in the list
@@ -272,6 +272,10 @@ template <int NQ, int KB>
 struct Cfg {
   static constexpr int DP = 64 * KB;
   static constexpr int BMT = 128 * NQ;
+  // List places of a row tile beside its key tiles: its start and epilogue take about 11,000 cycles, a key
+  // tile 2,000 (NQ = 1) or 3,200. Two more than that for prompts measured best (2: 497 us, 6: 465, 8: 450,
+  // 10: 460 for two prompts of 8192 rows with a window; 64 blocks 195 us at 2 and 169 at 6).
+  static constexpr int kItem = NQ == 1 ? 6 : 8;
   static constexpr uint32_t kTile = (uint32_t)KB * kBN * 128;    // bytes of a key or value tile
   static constexpr uint32_t kQBytes = (uint32_t)KB * 128 * 128;  // bytes of a query tile
   static constexpr uint32_t kStage = NQ == 2 ? 8 * 4096 : 0;     // output on its way out
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   }
 
   // Count the work list (places of one kv head) and find this CTA's part of it.
-  auto places = [](const Unit& w) { return w.cnt > 0 ? w.cnt + kItem : 0; };
+  auto places = [](const Unit& w) { return w.cnt > 0 ? w.cnt + C::kItem : 0; };
   const int units = a.rows.batch * p.row_tiles;
   const int chunk = (units + kThreads - 1) / kThreads;
   const int u_begin = min(units, (int)threadIdx.x * chunk), u_end = min(units, u_begin + chunk);
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
   }
   __syncthreads();
-  Walk walk;
+  Walk<C::kItem> walk;
   walk.len = (int)(x1 - x0);
   walk.x = x0;
   walk.u = 0; walk.h = 0; walk.k = 0;
@@ -677,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
       }
       if (w.cnt == 0) { ++walk.u; continue; }
-      const int64_t first_x = walk.x - walk.k + kItem, last_x = first_x + w.cnt - 1;
+      const int64_t first_x = walk.x - walk.k + C::kItem, last_x = first_x + w.cnt - 1;
       int k0, k1;
       walk.part(w.cnt, k0, k1);
       walk.next(w.cnt, hkv);
