@@ -232,34 +232,50 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = tr * 4 + i;
-      m[i] = -INFINITY;
-      l[i] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) o[i][c] = 0.0f;
-      if (r >= rows) continue;
+    // Four columns of a row at a time, one pass over the pieces in order, eight in flight, the maximum raised as
+    // they come.
+    for (int x = t; x < rows * nv; x += kThr) {
+      const int r = x / nv, e = (x - r * nv) * 4;
       const int64_t first = tl * p.splits * kBM + r;
-      for (int sp2 = 0; sp2 < used; ++sp2) m[i] = fmaxf(m[i], __ldcg(&p.part.ml[first + (int64_t)sp2 * kBM]).x);
-      if (m[i] == -INFINITY) continue;
-      for (int sp2 = 0; sp2 < used; ++sp2) {
-        const int64_t at = first + (int64_t)sp2 * kBM;
-        const float2 ml = __ldcg(&p.part.ml[at]);
-        if (ml.x == -INFINITY) continue;
-        const float w = ml.x == m[i] ? 1.0f : exp2f(ml.x - m[i]);
-        l[i] += ml.y * w;
+      float mm = -INFINITY, ll = 0.0f;
+      float4 acc = make_float4(0, 0, 0, 0);
+      for (int s = 0; s < used; s += 8) {
+        float2 ml[8];
+        float4 y[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c * 64 + tc * 4 < D) {
-            const float4 v = __ldcg((const float4*)(p.part.o + at * D + c * 64 + tc * 4));
-            o[i][4 * c] += v.x * w;
-            o[i][4 * c + 1] += v.y * w;
-            o[i][4 * c + 2] += v.z * w;
-            o[i][4 * c + 3] += v.w * w;
+        for (int u = 0; u < 8; ++u) {
+          ml[u] = make_float2(-INFINITY, 0.0f);
+          if (s + u < used) {
+            ml[u] = __ldcg(&p.part.ml[first + (int64_t)(s + u) * kBM]);
+            y[u] = __ldcg((const float4*)(p.part.o + (first + (int64_t)(s + u) * kBM) * D + e));
           }
+        }
+        float now = mm;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) now = fmaxf(now, ml[u].x);
+        const float keep = now == mm || mm == -INFINITY ? 1.0f : exp2f(mm - now);
+        ll *= keep;
+        acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+        mm = now;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (ml[u].x == -INFINITY && ml[u].y == 0.0f) continue;  // saw nothing
+          const float f = ml[u].x == mm || ml[u].x == -INFINITY ? 1.0f : exp2f(ml[u].x - mm);
+          ll += ml[u].y * f;
+          acc.x += y[u].x * f; acc.y += y[u].y * f; acc.z += y[u].z * f; acc.w += y[u].w * f;
+        }
       }
+      const int pr = r0 + r;
+      const int64_t row = (int64_t)(q0 + pr / G) * a.hq + h * G + pr % G;
+      const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN);
+      if (a.lse && e == 0) a.lse[row] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      T* dst = out + row * D + e;
+      dst[0] = (T)(acc.x * inv);
+      dst[1] = (T)(acc.y * inv);
+      dst[2] = (T)(acc.z * inv);
+      dst[3] = (T)(acc.w * inv);
     }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
