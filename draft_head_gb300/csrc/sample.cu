@@ -562,6 +562,8 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
     const u64 k = cut_list(s, v, true, aim, &mass);
     bound = k > bound ? k : bound;
   }
+  // The list's order is that of the atomics that filled it, so its weights are summed as integers (of 2^-40).
+  u64 whole = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     if (v.key[j] && v.key[j] >= bound) {
@@ -570,12 +572,15 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
         const uint32_t id = key_id(v.key[j]);
         const u64 c = value_id_key(l / r.temp + g[id], id);
         key = c > key ? c : key;
-        sum += w;
+        whole += __float2ull_rn(w * 1099511627776.0f);
       }
     }
   }
-  sum = block_sum(sum, s.redf);
-  key = block_max(key, s.red);
+  u64 before = whole, z = 0;
+  block_scan(before, z, s.red, s.red2);
+  if (threadIdx.x == kThr - 1) s.found_mass = before + whole;
+  key = block_max(key, s.red);  // a barrier before found_mass is read
+  sum = (float)((double)s.found_mass * (1.0 / 1099511627776.0));
   // From the thread that has the drawn token's logit.
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {

@@ -540,6 +540,21 @@ def test_sample_strides_and_default_settings():
         assert one.sample(x[r:r + 1, 7:1007], gum[r:r + 1, 100:1100]).item() == tok[r].item()
 
 
+@pytest.mark.parametrize("rows", [2, 200])
+def test_sample_gives_the_same_bits_again(rows):
+    """Candidates are gathered in whatever order the atomics take: tokens and log-probabilities do not depend on it."""
+    V = 60000
+    x, gum = rows_of("peaked", rows, V, 9)
+    s = Sampler(rows, V)
+    for k, p in ((1000, 0.99), (2000, 1.0), (300, 0.9), (0, 0.95), (64, 0.9)):
+        kk, pp = ints([k] * rows), torch.full((rows,), p, device="cuda")
+        first = [y.clone() for y in s.sample(x, gum, None, kk, pp, want_logprob=True)]
+        for _ in range(10):
+            tok, lp = s.sample(x, gum, None, kk, pp, want_logprob=True)
+            assert torch.equal(tok, first[0]) and torch.equal(lp, first[1])
+    assert s.last_status() == 0
+
+
 @pytest.mark.parametrize("dt", [F32, BF])
 def test_sample_full_vocabulary_rows(dt):
     """Long rows: filters over 151936 tokens, flat (most of the vocabulary stays) and peaked."""
