@@ -125,6 +125,47 @@ def test_qk_norm_rope(case):
     assert torch.equal(k.transpose(1, 2)[untouched], k0.transpose(1, 2)[untouched])
 
 
+MANY = [
+    # dtype, requests, rows, hq, hkv, D, rot, interleaved, in place
+    (BF, 3, 2000, 8, 2, 64, 64, False, False),
+    (BF, 2, 1700, 5, 1, 128, 128, True, True),
+    (F32, 2, 1700, 14, 2, 80, 40, False, True),
+    (F32, 5, 700, 4, 4, 256, 256, False, False),
+    (BF, 70, 40, 33, 3, 24, 0, False, False),
+    (BF, 4, 1200, 32, 8, 128, 12, True, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_norm_rope_of_many_rows(case):
+    """More rows than the SMs hold at once, of requests of unlike lengths, one of them empty."""
+    dt, b, n, hq, hkv, D, rot, pairs, in_place = MANY[case]
+    g = gen(300 + case)
+    rows = [0 if r == 1 and b > 2 else max(1, n - 17 * r) for r in range(b)]
+    ctx = [(5 * r) % 11 for r in range(b)]
+    st, cap = starts(rows), n + 11
+    k, v = cache_pair(g, dt, b, hkv, cap, D)
+    want_k, want_v = k.to(O.F64), v.to(O.F64)
+    q, kk, vv = ((1.7 * randn(g, st[-1], h, D)).to(dt) for h in (hq, hkv, hkv))
+    table = rope_table(cap, rot) if rot else None
+    qw, kw = (1 + 0.3 * randn(g, D)).to(dt), (1 + 0.3 * randn(g, D)).to(dt)
+    pos = torch.tensor([c + i for m, c in zip(rows, ctx) for i in range(m)], device="cuda")
+    want_q = O.norm_rope(q, qw, 1e-5, table, pos, rot, pairs)
+    new_k = O.norm_rope(kk, kw, 1e-5, table, pos, rot, pairs)
+    out, ws = q if in_place else torch.empty_like(q), B.workspace(256)
+    block = B.block(st[-1], max(rows), max(ctx), ints(ctx), ints(st))
+    B.domino_qk_norm_rope(B.kv_cache(k, v), block, hq, q, hq * D, kk, hkv * D, vv, hkv * D, qw, kw, 1e-5, table,
+                          cap if rot else 0, rot, pairs, out, ws)
+    assert B.domino_last_status(ws) == 0
+    h = H if dt == BF else 0.0
+    for r, m in enumerate(rows):
+        want_k[r, :, ctx[r]:ctx[r] + m] = new_k[st[r]:st[r + 1]].transpose(0, 1)
+        want_v[r, :, ctx[r]:ctx[r] + m] = vv[st[r]:st[r + 1]].to(O.F64).transpose(0, 1)
+    for got, want in ((out, want_q), (k, want_k)):
+        assert bool(((got.to(O.F64) - want).abs() <= h * want.abs() * 1.01 + 64 * U * float(want.abs().max())).all())
+    assert torch.equal(v.to(O.F64), want_v)
+
+
 def test_norm_rope_in_place_and_without_q_start():
     g = gen(7)
     k, v = cache_pair(g, BF, 3, 2, 20, 64)
