@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mbar_init(&p_ready[2 * s + 1], 4);
       mbar_init(&o_done[s], 1);
     }
-    mbar_init(q_ready, p.q_boxes ? 1 : 2);
+    mbar_init(q_ready, 2);
     mbar_init(q_free, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -587,6 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
               tma_load_3d(sQ + g * C::kQBytes + kb * (128 * 128), &p.tmQ, kb * 64, h * G, w.q0 + w.i_first + g * (128 / G), q_ready);
+        } else if (threadIdx.x == 96) {
+          // The other warp counts too: a row tile of a key tile or two has all its scores before any value tile is
+          // asked of it, and q_free could be two phases on before it has seen the one it waits for.
+          mbar_arrive(q_ready);
         }
       } else {
         const int x = t64 & (8 * KB - 1);

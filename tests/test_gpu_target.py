@@ -125,6 +125,26 @@ def test_qk_norm_rope(case):
     assert torch.equal(k.transpose(1, 2)[untouched], k0.transpose(1, 2)[untouched])
 
 
+@pytest.mark.parametrize("mask,window", [("tree", 0), ("full", 90), ("causal", 0)])
+def test_attention_of_short_row_tiles_again_and_again(mask, window):
+    """Row tiles of one or two key tiles, several on every SM, in calls right behind one another: all of them end, and with
+    the same bits."""
+    g = gen(41)
+    b, n, hq, hkv, D = 96, 17, 32, 8, 128
+    ctx = [(37 * r) % 200 for r in range(b)]
+    k, v = cache_pair(g, BF, b, hkv, 220, D)
+    q = randn(g, b * n, hq, D).to(BF)
+    m = (torch.rand(b, n, n, generator=g, device="cuda") < 0.4).to(torch.uint8) if mask == "tree" else None
+    p = BlockAttention(k, v, hq, b * n, n, 200, window=window)
+    past = ints(ctx)
+    first = p.attend(q, past, mask=mask if m is None else m).clone()
+    for _ in range(400):
+        out = p.attend(q, past, mask=mask if m is None else m)
+    torch.cuda.synchronize()
+    assert p.last_status() == 0
+    assert torch.equal(out, first)
+
+
 MANY = [
     # dtype, requests, rows, hq, hkv, D, rot, interleaved, in place
     (BF, 3, 2000, 8, 2, 64, 64, False, False),
