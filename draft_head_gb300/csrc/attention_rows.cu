@@ -17,7 +17,12 @@
 // core kernel: raised only when a score passes them by 2^kLazy.
 // Four warps of a CTA share its slots and join in shared memory; CTAs that share a row tile
 // write their sums to the workspace, and the last one joins them in order.
+//
+// One token, 32 heads of 128 over 8 of the cache: over 4000 slots 12.5 us (20 with the tensor core
+// kernel), over 30,000 slots 29.6 us (4.1 TB/s); 64 tokens over up to 4000 slots each 117 us
+// (4.6 TB/s).
 #include <math.h>
+#include <algorithm>
 
 #include "attention.cuh"
 #include "packed.cuh"
@@ -28,6 +33,11 @@ namespace {
 
 constexpr int kBN = 16, kWarps = 4, kThr = 32 * kWarps;
 constexpr int kLeast = 8;  // key tiles per CTA at least: two per warp
+// From kManyTiles row tiles on, pieces of at least kLeastMany key tiles, about kWaves times as many as are
+// resident at once: the lengths are unlike, and one round and a half of whole row tiles leaves SMs idle. Tokens
+// of 16 / 32 / 64 / 128 requests over up to 4000 slots: 37.8 / 61.6 / 116.7 / 198.8 us; with one round of pieces
+// 42.6 / 69.9 / 126.8 / 206.8. Of 8 requests (64 row tiles, fewer pieces than SMs) 33.8, with the other rule 28.6.
+constexpr int kManyTiles = 96, kLeastMany = 64, kWaves = 4;
 constexpr int kMostPieces = 64;  // of a row tile: their join takes a round trip for every eight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -36,7 +46,7 @@ constexpr float kLazy = 32.0f;
 struct RowsP {
   AttnArgs a;
   Partials part;
-  int splits;
+  int splits, least;  // CTAs per row tile at most; key tiles that each has at least
   float c;  // scale log2(e)
 };
 
@@ -105,7 +115,7 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
     low_max = max(low_max, s_low[r]);
   }
   const KeyTiles kt = key_tiles(a.mode, a.sinks, low_min, ctx, rows_n, rows_n - 1, kBN);
-  const int used = splits_used(p.splits, kt.count, kLeast);
+  const int used = splits_used(p.splits, kt.count, p.least);
   if (split >= used) return;
   const int k_begin = (int)((int64_t)kt.count * split / used), k_end = (int)((int64_t)kt.count * (split + 1) / used);
   // Slots that every row sees: from all_low (or among the sinks) up to all_hi.
@@ -351,16 +361,18 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
     if (r0 + x * kApart < rows) finish(r0 + x * kApart, e, acc[x], mm[x], ll[x]);
 }
 
-int64_t want_ctas() { return 2 * (int64_t)num_sms(); }  // what is resident at once
+int64_t resident() { return 2 * (int64_t)num_sms(); }
+int64_t want_ctas() { return kWaves * resident(); }
 
 template <int NT, int KS, int JJ>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   RowsP p;
   p.a = a;
   p.c = fmaxf(a.scale * kLog2e, 1e-30f);  // a scale of 0 still has to leave a masked score at -inf
-  int64_t most = ((int64_t)a.rows.max_ctx + a.rows.max_q) / kBN / kLeast;
-  most = most < kMostPieces ? most : kMostPieces;
-  p.splits = splits_for((int64_t)a.hkv * a.rows.batch, want_ctas(), most);
+  const int64_t key_tiles = ((int64_t)a.rows.max_ctx + a.rows.max_q) / kBN, row_tiles = (int64_t)a.hkv * a.rows.batch;
+  const bool many = row_tiles >= kManyTiles;
+  p.least = many ? kLeastMany : kLeast;
+  p.splits = splits_for(row_tiles, many ? want_ctas() : resident(), std::min<int64_t>(key_tiles / p.least, kMostPieces));
   p.part = partials_at(a.scratch, want_ctas(), 16);
   const dim3 grid((unsigned)p.splits, (unsigned)a.hkv, (unsigned)a.rows.batch);
   attn_rows_kernel<NT, KS, JJ><<<grid, kThr, 0, stream>>>(p);
@@ -369,8 +381,14 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+// Up to 8 packed rows it is the faster one or as fast (64 tokens over up to 4000 slots 117 us, the tensor core
+// kernel 118; over up to 500 slots 24 and 50). From 9 to 16 its products are twice as many, and with every SM busy over
+// long caches the tensor core kernel wins: 64 requests of 4 rows in groups of 4, up to 4000 slots, 133 and 119 us, up to
+// 500 slots 32 and 48; 16 requests 43.7 and 43.1; one 21 and 21.
 bool attn_rows_applies(const AttnArgs& a) {
-  return a.dtype == DOMINO_BF16 && a.D <= 128 && (int64_t)a.rows.max_q * (a.hq / a.hkv) <= 16;
+  const int64_t rows = (int64_t)a.rows.max_q * (a.hq / a.hkv);
+  if (a.dtype != DOMINO_BF16 || a.D > 128 || rows > 16) return false;
+  return rows <= 8 || a.rows.max_ctx < 2500 || (int64_t)a.hkv * a.rows.batch <= num_sms();
 }
 size_t attn_rows_ws_bytes(const AttnArgs& a) { return partial_bytes(want_ctas(), 16, a.D); }
 

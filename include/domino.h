@@ -488,7 +488,9 @@ typedef enum {
  * bf16 for the product with v. scale is finite and not negative.
  * Workspace: domino_block_attention_workspace_bytes(cache, block, n_q_heads)
  * (0 if the arguments are invalid; block's device pointers are not read),
- * zeroed before its first use; each call leaves it ready for the next.
+ * zeroed before its first use; each call leaves it ready for the next (after
+ * DOMINO_ERR_TIMEOUT it is to be zeroed again). Calls that may overlap need a
+ * workspace each.
  */
 size_t domino_block_attention_workspace_bytes(const domino_kv_cache* cache, const domino_block* block,
                                               int n_q_heads);
@@ -508,7 +510,8 @@ domino_status domino_block_attention(const domino_kv_cache* cache, const domino_
  *   logprob[r] = the log-probability of tokens[r] in that distribution.
  * T = 0: tokens[r] = argmax of the logits, logprob 0, noise not read. A row
  * with no logit above -inf: token -1, logprob -inf. A NaN logit counts as -inf;
- * +inf logits share the whole probability.
+ * +inf logits share the whole probability (the token is the lowest id of those
+ * that stay, logprob -log of their number).
  *   logits      device, dtype (DOMINO_F32 or DOMINO_BF16), row r at r *
  *               logits_stride elements
  *   temperature, top_p, min_p [rows] device fp32, top_k [rows] device int32;
