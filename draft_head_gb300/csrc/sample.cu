@@ -964,9 +964,10 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : 5) sample_kernel(const Samp
       sum += s.part_sum[k];
       key = s.part_lo[k] > key ? s.part_lo[k] : key;
     }
-    const int id = (int)key_id(key);
+    const int id = key ? (int)key_id(key) : -1;  // -1: logits that changed between the passes
     a.tokens[row] = id;
-    if (a.logprob) {
+    if (a.logprob && id < 0) a.logprob[row] = NAN;
+    if (a.logprob && id >= 0) {
       const float l = fmaxf(to_f<T>(((const T*)a.logits)[(int64_t)row * a.ls + id]), -INFINITY);
       a.logprob[row] = (l == r.lmax ? 0.0f : (l - r.lmax) * r.inv_t) - logf(sum);
     }
