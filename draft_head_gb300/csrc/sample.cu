@@ -36,8 +36,8 @@
 // for one row.
 //
 // Vocabulary 151,936, fp32. One row: greedy 4.7 us, top-k 64 with top-p 12.8, all filters 23 us. 1024
-// rows: greedy 116 us (5.4 TB/s), top-k 64 248, min-p 188, top-p alone 462 (peaked rows), mixed settings
-// 349 us; 272 flat rows at top-p 0.9 alone, where two thirds of the vocabulary stay: 338 us.
+// rows: greedy 111 us (5.6 TB/s), top-k 64 223, min-p 200, top-p alone 434 (peaked rows), mixed settings
+// 316 us; 272 flat rows at top-p 0.9 alone, where two thirds of the vocabulary stay: 311 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -52,7 +52,8 @@ constexpr int kMaxCluster = 16;
 constexpr int kGroups = 256;  // groups of a row's tokens with a maximum each
 constexpr int kBins = 1024, kNear = 1023;  // the first histogram: kNear bins, then one for the rest
 constexpr int kList = 2048;
-constexpr int kMaxSlice = 48 * 1024;
+constexpr int kMaxSlice = 48 * 1024;  // shared memory; a bin's lack (below 2^16 a token) stays within 32 bits up to 64 K
+constexpr int kManyCtas = 5;          // on an SM with many rows
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -599,7 +600,7 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
 };
 
 template <typename T, int kThr, bool kStage>
-__global__ void __launch_bounds__(kThr, kStage ? 2 : 5) sample_kernel(const SampleArgs a, int length) {
+__global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(const SampleArgs a, int length) {
   using B = Block<kThr>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& s = *(Smem*)smem_raw;
@@ -1010,7 +1011,13 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   // from L2 (rows of 151,936, mixed settings: 1024 rows 554 us from shared memory and 343 from L2, 272 rows 164
   // and 118, 64 rows 51 and 46, 37 rows 33 and 40, 16 rows 28 and 39; one flat row at top-p 32 and 43). Five CTAs
   // on an SM: six and eight spill in the draw.
-  if (ctas > 2 * (int64_t)num_sms()) return launch<T, 256, false>(a, size, stream);
+  // Where half as many CTAs still fill the SMs, the slices are twice as long: fewer barriers and searches for the same
+  // tokens (1024 rows, mixed settings 342 us and 316 so, 272 flat rows at top-p 337 and 311; four times 330 and 304, but
+  // rows at min-p or a peaked top-p slower). 64 rows, which do not fill them: top-p 64 us and 90.
+  if (ctas > 2 * (int64_t)num_sms()) {
+    const bool longer = size > 1 && ctas / 2 > kManyCtas * num_sms() && (a.V + size / 2 - 1) / (size / 2) <= kMaxSlice - 32;
+    return launch<T, 256, false>(a, longer ? size / 2 : size, stream);
+  }
   return launch<T, 512, true>(a, size, stream);
 }
 

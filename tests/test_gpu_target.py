@@ -637,3 +637,27 @@ def test_sample_full_vocabulary_rows(dt):
                 assert tok[r].item() == want
                 assert abs(lp[r].item() - wlp) <= 2e-5
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind,dt,rows,V", [("flat", F32, 400, 151936), ("equal", F32, 300, 151936), ("ties", BF, 300, 151936),
+                                            ("masked", F32, 900, 45001), ("peaked", BF, 900, 45001), ("wide", F32, 900, 45001)])
+def test_sample_of_many_rows(kind, dt, rows, V):
+    """More rows than the SMs hold at once, in which a block takes a longer part of a row."""
+    x, gum = rows_of(kind, rows, V, 17)
+    x = x.to(dt)
+    sets = [SETTINGS[r % len(SETTINGS)] for r in range(rows)]
+    t, k, p, m = (torch.tensor([s[j] for s in sets], device="cuda", dtype=torch.int32 if j == 1 else F32) for j in range(4))
+    s = Sampler(rows, V, dtype=dt)
+    tok, lp = (y.tolist() for y in s.sample(x, gum, t, k, p, m, want_logprob=True))
+    assert s.last_status() == 0
+    compared = 0
+    for r in range(0, rows, 7 if len(SETTINGS) % 7 else 11):
+        want, wlp, margin = O.sample(x[r], gum[r], float(t[r]), int(k[r]), float(p[r]), float(m[r]))
+        # As in test_sample: fp32 scores of magnitude |logit / T| round at 2^-23 of it.
+        bar = 1e-4 + float(x[r].float().abs().clamp(max=1e30).max()) / max(float(t[r]), 1e-30) * 2.0 ** -22 if t[r] else 0.0
+        if margin <= bar:
+            continue
+        compared += 1
+        assert tok[r] == want, (r, margin)
+        assert lp[r] == wlp or abs(lp[r] - wlp) <= 2e-5 + 4e-6 * abs(wlp) + bar / 16, (r, lp[r], wlp)
+    assert compared >= 1
