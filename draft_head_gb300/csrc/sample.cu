@@ -10,6 +10,7 @@
 // A cluster of up to 16 CTAs takes a row, each a slice that it reads once from
 // memory; it keeps it in shared memory, or with many rows reads it again from L2. Steps, each
 // over the slice:
+//   no filter          one pass over logits and noise with a running maximum and sum, and done
 //   maximum            of the slice and of 256 groups of the row's tokens, merged over the
 //                      cluster; ends a greedy row
 //   candidates         a top-k of up to 128: k groups reach the k-th largest group maximum, so
@@ -36,8 +37,9 @@
 // for one row.
 //
 // Vocabulary 151,936, fp32. One row: greedy 4.7 us, top-k 64 with top-p 12.8, all filters 23 us. 1024
-// rows: greedy 111 us (5.6 TB/s), top-k 64 223, min-p 200, top-p alone 434 (peaked rows), mixed settings
-// 316 us; 272 flat rows at top-p 0.9 alone, where two thirds of the vocabulary stay: 311 us.
+// rows: greedy 111 us (5.6 TB/s), no filter 214 (5.8 TB/s with the noise; in two passes 404), top-k 64 225,
+// min-p 198, top-p alone 443 (peaked rows), mixed settings 322 us; 272 flat rows at top-p 0.9 alone, where two
+// thirds of the vocabulary stay: 312 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -599,8 +601,114 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
 }
 };
 
+// A row without a filter: one pass with a running maximum, the noise read beside the logits. False (and nothing written)
+// for a row with +inf logits. A function of its own, as its registers would be spilled in the other passes' loops.
 template <typename T, int kThr, bool kStage>
-__global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(const SampleArgs a, int length) {
+__device__ __noinline__ bool draw_unfiltered(Smem& s, const SampleArgs& a, const uint4* from, int units, int id0, int s0, int s1, int row,
+                                             float temp) {
+  using B = Block<kThr>;
+  constexpr int kVec = 16 / (int)sizeof(T);
+  const uint32_t rank = cluster_rank(), size = cluster_size();
+  const int t = threadIdx.x;
+  const float* g = a.gumbel + (int64_t)row * a.gs;
+  Slice<T, kThr, kStage> slice;
+  slice.from = from;
+  slice.units = units;
+  slice.id0 = id0;
+  slice.s0 = s0;
+  slice.s1 = s1;
+  Row r;
+  r.temp = temp;
+  r.inv_t = 1.0f / r.temp;
+  const float c = r.inv_t * 1.4426950408889634f;
+  const bool noise4 = ((uintptr_t)(g + slice.id0) & 15u) == 0;
+  float m = -3.402823466e+38f, most = -INFINITY, sum = 0.0f, top_score = -INFINITY;
+  int drawn = -1;
+  constexpr int kN = kStage ? 16 : 8, kU = kN / kVec;  // in flight, of each
+  for (int q0 = t; q0 < slice.units; q0 += kThr * kU) {
+    float l[kN], z[kN], now = -INFINITY;
+    uint4 x[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      const int q = q0 + j * kThr;
+      x[j] = q < slice.units ? __ldcs(slice.from + q) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int e = 0; e < kN; e += 4) {
+      const int id = slice.id0 + (q0 + e / kVec * kThr) * kVec + e % kVec;
+      const bool four = noise4 && id >= s0 && id + 4 <= s1;
+      const float4 n = four ? __ldcs((const float4*)(g + id)) : make_float4(0, 0, 0, 0);
+      z[e] = n.x; z[e + 1] = n.y; z[e + 2] = n.z; z[e + 3] = n.w;
+      if (!four) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (id + k >= s0 && id + k < s1) z[e + k] = __ldcs(g + id + k);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      const int q = q0 + j * kThr;
+      slice.decode(x[j], q, l + j * kVec);
+      if (q >= slice.units) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) l[j * kVec + e] = slice.outside();
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j) now = fmaxf(now, l[j]);  // NaNs are passed over
+    most = fmaxf(most, now);
+    if (now > m) {
+      sum *= ex2((m - now) * c);
+      m = now;
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      if (!(l[j] > -INFINITY)) continue;
+      sum += ex2((l[j] - m) * c);
+      const float near = l[j] * r.inv_t;
+      if (near + z[j] + 1e-6f * (fabsf(near) + fabsf(z[j])) < top_score) continue;  // as in the draw below
+      const float score = l[j] / r.temp + z[j];
+      if (score > top_score || drawn < 0) {
+        top_score = score;
+        drawn = slice.id0 + (q0 + j / kVec * kThr) * kVec + j % kVec;
+      }
+    }
+  }
+  const u64 key = B::block_max(drawn < 0 ? 0 : value_id_key(top_score, (uint32_t)drawn), s.red);
+  const float part = key_value(B::block_max(value_id_key(most, 0u), s.red));
+  sum = B::block_sum(most == -INFINITY ? 0.0f : sum * ex2((m - part) * c), s.redf);
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (t < (int)size) st_u64(dsmem(&s.part_key[rank], (uint32_t)t), value_id_key(part, 0u));
+  if (t == 0) {
+    st_u64(dsmem(&s.part_lo[rank], 0), key);
+    st_u32(dsmem(&s.part_sum[rank], 0), __float_as_uint(sum));
+  }
+  cluster_sync();
+  r.lmax = -INFINITY;
+  for (uint32_t k = 0; k < size; ++k) r.lmax = fmaxf(r.lmax, key_value(s.part_key[k]));
+  if (r.lmax < INFINITY) {
+    if (rank == 0 && t == 0) {
+      u64 best = 0;
+      sum = 0.0f;
+      for (uint32_t k = 0; k < size; ++k) {
+        if (s.part_sum[k] > 0.0f) sum += s.part_sum[k] * ex2((key_value(s.part_key[k]) - r.lmax) * c);
+        best = s.part_lo[k] > best ? s.part_lo[k] : best;
+      }
+      const int id = best ? (int)key_id(best) : -1;  // -1: no logit above -inf
+      a.tokens[row] = id;
+      if (a.logprob) {
+        const float l = id < 0 ? 0.0f : to_f<T>(((const T*)a.logits)[(int64_t)row * a.ls + id]);
+        a.logprob[row] = id < 0 ? -INFINITY : (l == r.lmax ? 0.0f : (l - r.lmax) * r.inv_t) - logf(sum);
+      }
+    }
+    return true;
+  }
+  cluster_sync();  // every CTA has read these
+  return false;
+}
+
+template <typename T, int kThr, bool kStage>
+__global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(const __grid_constant__ SampleArgs a, int length) {
   using B = Block<kThr>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem& s = *(Smem*)smem_raw;
@@ -621,6 +729,16 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
   slice.id0 = s0 - skew;
   slice.s0 = s0;
   slice.s1 = s1;
+  bool there = false;  // all CTAs of the cluster have been seen
+  {
+    const float temp = a.temperature ? a.temperature[row] : 1.0f;
+    const int k = a.top_k ? a.top_k[row] : 0;
+    if (temp > 0.0f && temp < INFINITY && (k == 0 || k >= V) && g && !(a.top_p && a.top_p[row] != 1.0f) &&
+        !(a.min_p && a.min_p[row] != 0.0f)) {
+      if (draw_unfiltered<T, kThr, kStage>(s, a, slice.from, slice.units, slice.id0, s0, s1, row, temp)) return;
+      there = true;
+    }
+  }
   float top = -INFINITY;
   int top_id = 0;  // the lowest id of this thread's largest logit: its ids rise
   if (kStage) {
@@ -664,7 +782,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
   int top_k = a.top_k ? a.top_k[row] : 0;
   const float top_p = a.top_p ? a.top_p[row] : 1.0f;
   r.min_p = a.min_p ? a.min_p[row] : 0.0f;
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (!there) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   // The same for every CTA of the cluster, as every branch on the way to a cluster barrier.
   if (!(r.temp >= 0.0f && r.temp < INFINITY) || top_k < 0 || !(top_p > 0.0f && top_p <= 1.0f) ||
       !(r.min_p >= 0.0f && r.min_p <= 1.0f) || (r.temp > 0.0f && !g)) {
