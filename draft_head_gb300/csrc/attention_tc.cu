@@ -1026,12 +1026,12 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   p.timeout_ns = wait_timeout_ns();
   // A scale of 0 still has to leave a masked score at -inf.
   p.c = fmaxf(a.scale * kLog2e, 1e-30f);
-  const uint32_t budget = 227 * 1024 - 3072;
+  const uint32_t budget = (227 - 3) * 1024;
   int slots = (int)((budget - NQ * C::kQBytes - C::kStage) / C::kTile);
   // Even: a buffer is always a key or always a value buffer, so every phase of a value
   // buffer is waited for by those who clear it.
   p.slots = slots > 12 ? 12 : slots & ~1;
-  const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + 3072;
+  const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + 3 * 1024;
   const int grid = num_sms();
   if ((size_t)grid * NQ * 4 > kArrivedBytes || (int64_t)a.rows.batch * p.row_tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
   uint8_t* w = (uint8_t*)a.scratch;
