@@ -36,8 +36,9 @@ __device__ __forceinline__ KeyTiles key_tiles(int mode, int sinks, int low, int 
   // Outside the causal mode the window does not reach into the block.
   const int start = mode == DOMINO_MASK_CAUSAL ? min(low, end) : min(low, ctx);
   KeyTiles k;
-  k.main_begin = start / BN;
-  k.main_count = start < end ? (end + BN - 1) / BN - k.main_begin : 0;
+  // A window that begins past the row itself (positions ahead of the slots) leaves all tiles to the sinks.
+  k.main_begin = start < end ? start / BN : (end + BN - 1) / BN;
+  k.main_count = (end + BN - 1) / BN - k.main_begin;
   k.count = k.main_count + min((min(sinks, end) + BN - 1) / BN, k.main_begin);
   return k;
 }
