@@ -75,8 +75,8 @@ struct TcAttnP {
   float4* o;              // [2 grid][NQ][DP / 4][128]: four columns of a row, rows next to each other
 };
 
-// A row tile of one request: its rows and the slots they see. `cnt` is 0 when there
-// is nothing to do.
+// A row tile of one request: its rows and the slots they see. `cnt` is 0 when it has
+// no rows.
 struct Unit {
   int q0, n, ctx, r0, rows, i_first, i_last, low_min, low_max, cnt;
   KeyTiles kt;
@@ -108,6 +108,8 @@ __device__ __forceinline__ Unit load_unit(const AttnArgs& a, int row_tiles, int 
     w.low_max = window_low(w.ctx + w.i_last, a.window);
   }
   w.kt = key_tiles(a.mode, a.sinks, w.low_min, w.ctx, w.n, w.i_last, kBN);
+  // Rows that see nothing at all take a key tile, masked whole, on the way to their output of 0 and lse of -inf.
+  if (w.kt.count == 0) w.kt.main_begin = 0, w.kt.main_count = w.kt.count = 1;
   w.cnt = w.kt.count;
   return w;
 }

@@ -55,3 +55,13 @@ def test_first_tokens_when_positions_run_ahead_of_the_slots(kernel, ctx, window,
     for n, shift in enumerate((lambda i: 650, lambda i: -20, lambda i: window - 1, lambda i: 650 if i % 3 else 0)):
         seen = causal_at(kernel, ctx, shift, window, sinks, 40 + n)
         assert n != 0 or all(int(s.sum(1).max()) <= sinks for s in seen)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("ctx", [0, 100, 300])
+def test_rows_whose_window_lies_past_their_slots_see_nothing(kernel, ctx):
+    """No first tokens, and a window that begins past the row itself: output 0 and lse -inf, for whole row tiles and for
+    some of their rows."""
+    for n, shift in enumerate((lambda i: 650, lambda i: 650 if i % 3 else 0, lambda i: 650 if i > 30 else 0)):
+        seen = causal_at(kernel, ctx, shift, 40, 0, 50 + n)
+        assert n != 0 or not any(bool(s.any()) for s in seen)
