@@ -68,22 +68,26 @@ struct Partials {
   unsigned int* arrived;  // per tile, zero between calls
 };
 
-// Splits of each of `tiles` tiles so that about `want` CTAs run; 1 from `want`
-// tiles on. tiles * splits stays below 2 * want, which sizes the workspace for
-// every smaller block too.
+// Splits of each of `tiles` tiles so that about `want` CTAs run (kCountersPerSm per SM at most); 1 from
+// `want` tiles on. tiles * splits stays below 2 * want, which sizes the workspace for every smaller
+// block too.
 inline int splits_for(int64_t tiles, int64_t want, int64_t most) {
   int64_t s = (want + tiles - 1) / tiles;
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s);
 }
+// The workspace behind its control block: the counters, whose place is the same for every attention kernel (they are
+// zero between calls, and a workspace may go from one kernel to another), then what a kernel needs for itself.
+constexpr int kCountersPerSm = 8;  // tiles that are cut, at most, for each SM
+inline size_t counter_bytes() { return ((size_t)kCountersPerSm * num_sms() * 4 + 255) & ~(size_t)255; }
 inline size_t partial_bytes(int64_t want, int BM, int D) {
-  return (((size_t)want * 4 + 255) & ~(size_t)255) + (size_t)(2 * want) * BM * (8 + (size_t)D * 4);
+  return counter_bytes() + (size_t)(2 * want) * BM * (8 + (size_t)D * 4);
 }
 inline Partials partials_at(void* scratch, int64_t want, int BM) {
   uint8_t* w = (uint8_t*)scratch;
   Partials p;
   p.arrived = (unsigned int*)w;
-  w += ((size_t)want * 4 + 255) & ~(size_t)255;
+  w += counter_bytes();
   p.ml = (float2*)w;
   p.o = (float*)(w + (size_t)(2 * want) * BM * 8);
   return p;

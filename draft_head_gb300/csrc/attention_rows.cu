@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
 
 int64_t resident() { return 2 * (int64_t)num_sms(); }
 int64_t want_ctas() { return kWaves * resident(); }
+static_assert(2 * kWaves <= kCountersPerSm, "a counter for every tile that is cut");
 
 template <int NT, int KS, int JJ>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {

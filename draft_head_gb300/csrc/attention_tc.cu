@@ -1013,8 +1013,6 @@ bool make_row_tmap(CUtensorMap* tm, const void* base, int packed, const AttnArgs
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kArrivedBytes = 4096;
-
 template <int NQ, int KB>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   using C = Cfg<NQ, KB>;
@@ -1035,11 +1033,13 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   p.slots = slots > 12 ? 12 : slots & ~1;
   const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + 3 * 1024;
   const int grid = num_sms();
-  if ((size_t)grid * NQ * 4 > kArrivedBytes || (int64_t)a.rows.batch * p.row_tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
+  static_assert(NQ <= kCountersPerSm, "a counter for every tile that is cut");
+  if ((int64_t)a.rows.batch * p.row_tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
   uint8_t* w = (uint8_t*)a.scratch;
   p.arrived = (unsigned int*)w;
-  p.ml = (float2*)(w + kArrivedBytes);
-  p.o = (float4*)(w + kArrivedBytes + (size_t)2 * grid * C::BMT * 8);
+  w += counter_bytes();
+  p.ml = (float2*)w;
+  p.o = (float4*)(w + (size_t)2 * grid * C::BMT * 8);
   static FuncOnce once;
   cudaError_t e = once.set((const void*)attn_tc_kernel<NQ, KB>, 227 * 1024, false);
   if (e != cudaSuccess) return e;
@@ -1051,7 +1051,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
 
 size_t attn_tc_ws_bytes(const AttnArgs& a) {
   const size_t dp = a.D > 64 ? 128 : 64;
-  return kArrivedBytes + (size_t)2 * num_sms() * 256 * (8 + dp * 4);
+  return counter_bytes() + (size_t)2 * num_sms() * 256 * (8 + dp * 4);
 }
 
 // bf16, head_dim <= 128, and a cache that a tensor map can describe: no axis of more than

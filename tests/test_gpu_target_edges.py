@@ -65,3 +65,36 @@ def test_rows_whose_window_lies_past_their_slots_see_nothing(kernel, ctx):
     for n, shift in enumerate((lambda i: 650, lambda i: 650 if i % 3 else 0, lambda i: 650 if i > 30 else 0)):
         seen = causal_at(kernel, ctx, shift, 40, 0, 50 + n)
         assert n != 0 or not any(bool(s.any()) for s in seen)
+
+
+def test_kernels_share_a_workspace():
+    """Calls that run on different kernels, one after another on one workspace: each leaves it ready for the next."""
+    g = T.gen(60)
+    calls = []
+    for dt, b, rows, past, hq, hkv, D in ((F32, 1, 1, 2900, 1, 1, 80),      # its key tiles over many blocks
+                                          (BF, 64, 1, 2900, 8, 8, 64),      # few rows, more tiles than SMs, each cut
+                                          (BF, 3, 40, 2900, 8, 2, 128),     # one query tile
+                                          (BF, 2, 1, 2900, 4, 2, 256),      # wide heads
+                                          (BF, 2, 300, 2900, 8, 2, 128),    # two query tiles
+                                          (BF, 1, 2, 2900, 8, 2, 128)):     # few rows, one request
+        k, v = T.cache_pair(g, dt, b, hkv, past + rows, D)
+        q = T.randn(g, b * rows, hq, D).to(dt)
+        ctx = T.ints([past] * b)
+        cache, block = B.kv_cache(k, v), B.block(b * rows, rows, past, ctx)
+        calls.append((cache, block, hq, q, D ** -0.5, ctx, k, v))
+    size = max(B.domino_block_attention_workspace_bytes(c[0], c[1], c[2]) for c in calls)
+
+    def run(c, ws):
+        out, lse = torch.full_like(c[3], 7.0), torch.full(c[3].shape[:2], 7.0, device="cuda")
+        B.domino_block_attention(c[0], c[1], c[2], c[3], c[4], B.MASK_CAUSAL, None, 0, 0, out, lse, ws)
+        return out, lse
+
+    want = [run(c, B.workspace(size)) for c in calls]
+    ws = B.workspace(size)
+    n = len(calls)
+    for first in range(n):
+        for second in range(n):
+            for x in (first, second):
+                out, lse = run(calls[x], ws)
+                assert torch.equal(out, want[x][0]) and torch.equal(lse, want[x][1]), (first, second, x)
+    assert B.domino_last_status(ws) == 0
