@@ -623,7 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
       // or a NaN in the product, so these are cleared here and the row tile is marked.
       for (int k = k0; k < k1; ++k) {
-        if (!mbar_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
+        ok = warp_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns);
+        if (!ok) break;
         if (!all_seen(a, w, w.kt.slot(k, kBN))) {
           uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
           bool bad = false;

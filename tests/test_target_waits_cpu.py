@@ -1,0 +1,33 @@
+"""The bounded waits of the target-side kernels, by reading their source: a wait that runs out must not happen on a GPU
+that others use, so what a kernel does then is held to rules that can be read."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "draft_head_gb300", "csrc")
+
+
+def source(name):
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def part(text, start, end):
+    assert text.count(start) == 1, start
+    text = text[text.index(start) + len(start):]
+    return text[:text.index(end)]
+
+
+# A wait whose answer decides where the lane goes on.
+DECIDES = re.compile(r"(!|=|&&|\breturn)\s*mbar_wait\(")
+
+
+def test_whole_warps_leave_a_wait_with_one_answer():
+    """Where whole warps wait and go on to a warp's or a block's barrier, a lane's own answer may differ from its
+    neighbours' (one sees the phase, another its limit), and the warp would be split at the barrier: they go by the vote."""
+    text = source("attention_tc.cu")
+    assert DECIDES.search("if (!mbar_wait(") and DECIDES.search("ok = mbar_wait(")
+    roles = {"mma": part(text, "} else if (warp == 1) {", "} else if (warp >= 2) {"),
+             "queries and values": part(text, "} else if (warp >= 2) {", "setmaxnreg.inc"),
+             "softmax": part(text, "setmaxnreg.inc", "tmem_dealloc(tmem, 512)")}
+    for name, role in roles.items():
+        assert "warp_wait(" in role and not DECIDES.search(role), name
