@@ -454,11 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         walk.next(w.cnt, hkv);
       }
-      if (!ok) {
-        // Give up, but first let the copies already in flight land.
-        for (long j = issued - 1; j >= 0 && j >= issued - slots; --j)
-          mbar_wait(&full[j % slots], (uint32_t)((j / slots) & 1), nullptr, ctl, p.timeout_ns);
-      }
+      // The last copies land before the block ends, also where those who wait for them have given up.
+      for (long j = issued - 1; j >= 0 && j >= issued - slots; --j)
+        mbar_land(&full[j % slots], (uint32_t)((j / slots) & 1), ctl);
     } else if (warp == 1) {
       const uint32_t id_s = idesc_bf16_f32(128, kBN);
       const uint32_t id_o = idesc_bf16_f32(128, C::DP) | (1u << 16);  // B is MN-major
@@ -570,11 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       // Every MMA issued above has finished before TMEM is freed.
       release(drain);
-      mbar_wait(drain, 0, nullptr, ctl, p.timeout_ns);
+      mbar_land(drain, 0, ctl);
     } else if (warp >= 2) {
     const int t64 = threadIdx.x - 64;
     int slot = 1;
-    uint32_t phase = 0, item = 0;
+    uint32_t phase = 0, item = 0, boxes = 0;
     bool ok = true;
     Unit w;
     int cur = -1;
@@ -592,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       if (p.q_boxes) {
         // Packed rows of a tile are `G` heads of each of 128 / G rows: one box.
         if (threadIdx.x == 64) {
+          ++boxes;
           mbar_expect_tx(q_ready, NQ * C::kQBytes);
 #pragma unroll
           for (int g = 0; g < NQ; ++g)
@@ -653,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       ++item;
     }
+    if (boxes > 0) mbar_land(q_ready, (boxes - 1u) & 1u, ctl);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");

@@ -31,3 +31,17 @@ def test_whole_warps_leave_a_wait_with_one_answer():
              "softmax": part(text, "setmaxnreg.inc", "tmem_dealloc(tmem, 512)")}
     for name, role in roles.items():
         assert "warp_wait(" in role and not DECIDES.search(role), name
+
+
+def test_copies_land_before_attention_gives_up_its_memory():
+    """Key, value and query boxes and products in flight are waited for on every way out, also by a role that is through while
+    another has given up, and with a limit that is not the caller's."""
+    text = source("attention_tc.cu")
+    keys = part(text, "if (warp == 0 && lane == 0) {", "} else if (warp == 1) {")
+    after = keys[keys.index("walk.next("):]
+    assert "mbar_land(&full[" in after and "if (!ok)" not in after
+    assert "mbar_land(drain" in part(text, "} else if (warp == 1) {", "} else if (warp >= 2) {")
+    queries = part(text, "} else if (warp >= 2) {", "setmaxnreg.inc")
+    assert "mbar_land(q_ready" in queries[queries.index("++item;"):]
+    land = part(source("common.cuh"), "void mbar_land(", "\n}")
+    assert "timeout" not in land
