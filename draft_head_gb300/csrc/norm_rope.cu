@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
   int st = 0;
   uint32_t phase = 0;
   bool ok = true;
-  for (int t = t0; t < t_end; ++t) {
+  int t = t0;
+  for (; t < t_end; ++t) {
     const int64_t slot = (int64_t)b * a.rs + (int64_t)(ctx + i) * a.ss + e0;
     const bool on_row = placed;
     if (on_row) at.set_angles(raw);
@@ -345,8 +346,8 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
         mine = find_row(a.rows, t + 1, b, i, ctx, rows, a.ctl);
       look(t + 1);
     }
-    ok = mbar_wait(&full[st], phase, nullptr, a.ctl, timeout_ns);
-    if (!__syncthreads_and(ok)) break;
+    ok = __syncthreads_and(mbar_wait(&full[st], phase, nullptr, a.ctl, timeout_ns));
+    if (!ok) break;
     if (on_row) {
       const T* x = ring + (int64_t)st * row + e0;
       at.weigh(s_w + a.D);
@@ -382,9 +383,10 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
       phase ^= 1u;
     }
   }
-  if (!ok)  // copies in flight end before the memory is given up
-    for (int k = 0; k < stages; ++k) {
-      if (threadIdx.x == 0) mbar_wait(&full[st], phase, nullptr, a.ctl, timeout_ns);
+  // After a wait that ran out for any thread: the rows on their way land before the memory is given up.
+  if (!ok && threadIdx.x == 0)
+    for (int k = 0; k < stages && t + k < t_end; ++k) {
+      mbar_land(&full[st], phase, a.ctl);
       if (++st == stages) {
         st = 0;
         phase ^= 1u;

@@ -45,3 +45,13 @@ def test_copies_land_before_attention_gives_up_its_memory():
     assert "mbar_land(q_ready" in queries[queries.index("++item;"):]
     land = part(source("common.cuh"), "void mbar_land(", "\n}")
     assert "timeout" not in land
+
+
+def test_rows_on_their_way_land_before_the_ring_is_given_up():
+    """The block leaves the loop when any of its threads gives up; the thread that waits for the copies then goes by the block's
+    answer, not by its own, waits for the rows that were asked for and no others, and not with the caller's limit."""
+    run = part(source("norm_rope.cu"), "norm_rope_run_kernel(const NormRopeArgs a", "template <typename T, int MODE>\ncudaError_t")
+    assert re.search(r"\bok = __syncthreads_and\(mbar_wait\(", run)
+    assert len(re.findall(r"\bok = ", run)) == 2  # its first value, and the block's answer
+    land = run[run.index("if (!ok && threadIdx.x == 0)"):]
+    assert "t + k < t_end" in land and "mbar_land(&full[st]" in land and "mbar_wait(" not in land
