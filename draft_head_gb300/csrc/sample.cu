@@ -96,7 +96,7 @@ typedef unsigned long long u64;
 // Shared memory of a CTA before its slice.
 struct Smem {
   union {
-    uint32_t hist[3][kBins];  // counts; lacks, or weights in two 15-bit halves
+    uint32_t hist[4][kBins];  // counts; lacks, or weights in parts
     u64 list[kList];          // CTA 0: keys gathered from the cluster
   };
   u64 mass[kBins];  // sums over the cluster (a CTA holds those of its bins before they are shared)
@@ -116,20 +116,29 @@ struct Smem {
   int n_local;
   int found_bin;
   u64 found_cnt, found_mass, found_here;
-  u64 rest_w, all_w, in_w;
+  u64 all_w, in_w;
 };
+
+// A weight of up to 16 in units of 2^-kUnit, in two halves that convert as 32 bits.
+constexpr int kUnit = 40;
+__device__ __forceinline__ u64 units(float w) {
+  const float high = floorf(w * 1048576.0f);
+  return ((u64)__float2uint_rz(high) << 20) + __float2uint_rn(fmaf(w, 1048576.0f, -high) * 1048576.0f);
+}
 
 struct Row {
   float lmax, inv_t, temp;
   float min_p;
   float scale;  // bins per nat
   __device__ __forceinline__ float dist(float l) const { return l == lmax ? 0.0f : (lmax - l) * inv_t; }
-  // Weight of a token in units of 2^-30.
-  __device__ __forceinline__ uint32_t fixed(float d) const {
+  // Weight of a token at distance d, and in the units in which top-p counts: sums of them are the same in any order, and
+  // a whole vocabulary's rounding is below what fp32 tells of a top-p.
+  static __device__ __forceinline__ float falling(float d) {
     float w;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(d * -1.4426950408889634f));
-    return (uint32_t)__float2uint_rn(w * 1073741824.0f);
+    return w;
   }
+  static __device__ __forceinline__ u64 fixed(float d) { return units(falling(d)); }
   // The place of a logit among the bins: bin b holds [b, b + 1), bin kNear all from kNear on.
   // Monotone, so in the order of the logits.
   __device__ __forceinline__ float place(float l) const { return dist(l) * scale; }
@@ -272,9 +281,9 @@ static __device__ __forceinline__ void block_scan(u64& a, u64& b, u64* red, u64*
   b = by + y - b;
 }
 
-// First bin where the sum up to and with it reaches `target` (the last one if none does), of kBins
-// bins whose count and weight `at(bin, count, weight)` gives. All threads get the bin, the sums before it
-// and its count.
+// First bin where the sum up to and with it reaches `target` (the last one with a count if none does: the sums of two
+// passes may differ in their last bits), of kBins bins whose count and weight `at(bin, count, weight)` gives. All threads
+// get the bin, the sums before it and its count.
 template <typename At>
 static __device__ __forceinline__ void find(Smem& s, At at, bool by_mass, u64 target, int& bin, u64& cnt_before, u64& mass_before, u64& here) {
   constexpr int kEach = kBins / kThr;
@@ -288,36 +297,46 @@ static __device__ __forceinline__ void find(Smem& s, At at, bool by_mass, u64 ta
   }
   u64 cb = cs, mb = ms;
   block_scan(cb, mb, s.red, s.red2);
-  const u64 before = by_mass ? mb : cb, after = by_mass ? mb + ms : cb + cs;
-  if ((threadIdx.x == 0 || before < target) && (after >= target || threadIdx.x == kThr - 1)) {
-    bool done = false;
+  while (true) {
+    const u64 before = by_mass ? mb : cb, after = by_mass ? mb + ms : cb + cs;
+    if (threadIdx.x == kThr - 1 && after < target) {
+      s.found_bin = -1;
+      s.found_cnt = cb + cs;
+    }
+    if ((threadIdx.x == 0 || before < target) && after >= target) {
+      u64 x = cb, y = mb;
+      bool done = false;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      if (!done) {
-        done = (by_mass ? mb + m[j] : cb + c[j]) >= target || j == kEach - 1;
-        if (done) {
-          s.found_bin = b0 + j;
-          s.found_cnt = cb;
-          s.found_mass = mb;
-          s.found_here = c[j];
+      for (int j = 0; j < kEach; ++j) {
+        if (!done) {
+          done = (by_mass ? y + m[j] : x + c[j]) >= target;
+          if (done) {
+            s.found_bin = b0 + j;
+            s.found_cnt = x;
+            s.found_mass = y;
+            s.found_here = c[j];
+          }
+          x += c[j];
+          y += m[j];
         }
-        cb += c[j];
-        mb += m[j];
       }
     }
+    __syncthreads();
+    bin = s.found_bin;
+    cnt_before = s.found_cnt;
+    mass_before = s.found_mass;
+    here = s.found_here;
+    __syncthreads();
+    if (bin >= 0) return;
+    by_mass = false;
+    target = cnt_before;
   }
-  __syncthreads();
-  bin = s.found_bin;
-  cnt_before = s.found_cnt;
-  mass_before = s.found_mass;
-  here = s.found_here;
-  __syncthreads();
 }
 
-// Sums the CTAs' histograms (their first `arrays` arrays): each CTA takes kBins / size bins, `mass_of`
+// Sums the CTAs' histograms (their first kArrays arrays): each CTA takes kBins / size bins, `mass_of`
 // gives a bin's weight from the sums, then all read all.
-template <typename MassOf>
-static __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t size, int arrays, MassOf mass_of) {
+template <int kArrays, typename MassOf>
+static __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, uint32_t size, MassOf mass_of) {
   cluster_sync();
   const int per = kBins / (int)size;
   // A thread sums up to four CTAs' counts of a bin, all loads in flight at once.
@@ -325,23 +344,22 @@ static __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, u
   const int first = threadIdx.x % tpb;
   for (int x = threadIdx.x / tpb; x < per; x += kThr / tpb) {
     const int b = (int)rank * per + x;
-    uint32_t v[3][4];
+    uint32_t v[kArrays][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t k = (uint32_t)(first + tpb * j);
 #pragma unroll
-      for (int y = 0; y < 3; ++y) v[y][j] = k < size && y < arrays ? ld_u32(dsmem(&s.hist[y][b], k)) : 0u;
+      for (int y = 0; y < kArrays; ++y) v[y][j] = k < size ? ld_u32(dsmem(&s.hist[y][b], k)) : 0u;
     }
-    u64 sum[3];
+    u64 sum[kArrays];
 #pragma unroll
-    for (int y = 0; y < 3; ++y) {
+    for (int y = 0; y < kArrays; ++y) {
       sum[y] = (u64)v[y][0] + v[y][1] + v[y][2] + v[y][3];
-      if (y < arrays)
-        for (int o = 1; o < tpb; o <<= 1) sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], o);
+      for (int o = 1; o < tpb; o <<= 1) sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], o);
     }
     if (first == 0) {
       s.cnt[b] = (uint32_t)sum[0];
-      s.mass[b] = arrays > 1 ? mass_of(b, sum[0], sum[1], sum[2]) : 0;
+      s.mass[b] = mass_of(b, sum);
     }
   }
   cluster_sync();
@@ -352,7 +370,7 @@ static __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, u
     for (int j = 0; j < kBins / kThr; ++j) {
       const int b = threadIdx.x + j * kThr;
       c[j] = ld_u32(dsmem(&s.cnt[b], (uint32_t)(b / per)));
-      m[j] = arrays > 1 ? ld_u64(dsmem(&s.mass[b], (uint32_t)(b / per))) : 0;
+      m[j] = kArrays > 1 ? ld_u64(dsmem(&s.mass[b], (uint32_t)(b / per))) : 0;
     }
 #pragma unroll
     for (int j = 0; j < kBins / kThr; ++j) {
@@ -366,14 +384,27 @@ static __device__ __forceinline__ void share_histogram(Smem& s, uint32_t rank, u
   __syncthreads();
 }
 
-static __device__ __forceinline__ void add_weight(Smem& s, int b, uint32_t w) {
+// A token of weight w in bin b: 16 bits of it an array (a slice's sums of 2^16 tokens stay within 32 bits).
+static __device__ __forceinline__ void add_weight(Smem& s, int b, u64 w) {
   atomicAdd(&s.hist[0][b], 1u);
-  if (w >> 15) atomicAdd(&s.hist[1][b], w >> 15);
-  if (w & 0x7fffu) atomicAdd(&s.hist[2][b], w & 0x7fffu);
+#pragma unroll
+  for (int y = 1; y < 4; ++y) {
+    const uint32_t part = (uint32_t)(w >> (48 - 16 * y)) & 0xffffu;
+    if (part) atomicAdd(&s.hist[y][b], part);
+  }
 }
-static __device__ __forceinline__ u64 whole_mass(int, u64, u64 hi, u64 lo) { return (hi << 15) + lo; }
+static __device__ __forceinline__ u64 whole_mass(int, const u64 (&sum)[4]) { return (sum[1] << 32) + (sum[2] << 16) + sum[3]; }
+// The same for a token of a list of up to 2^11: two arrays hold its weights.
+static __device__ __forceinline__ void add_listed(Smem& s, int b, u64 w) {
+  atomicAdd(&s.hist[0][b], 1u);
+  const uint32_t high = (uint32_t)(w >> 20), low = (uint32_t)w & 0xfffffu;
+  if (high) atomicAdd(&s.hist[1][b], high);
+  if (low) atomicAdd(&s.hist[2][b], low);
+}
+static __device__ __forceinline__ u64 listed_mass(const Smem& s, int b) { return ((u64)s.hist[1][b] << 20) + s.hist[2][b]; }
+template <int kArrays>
 static __device__ __forceinline__ void clear_histogram(Smem& s) {
-  for (int x = threadIdx.x; x < 3 * kBins; x += kThr) (&s.hist[0][0])[x] = 0u;
+  for (int x = threadIdx.x; x < kArrays * kBins; x += kThr) (&s.hist[0][0])[x] = 0u;
 }
 
 // Gathers the keys for which `in` holds in this CTA's list, and makes their number known to the
@@ -386,20 +417,19 @@ static __device__ __forceinline__ int collect(Smem& s, const S& slice, uint32_t 
   u64 all = 0, inside = 0;
   slice.batches(weigh ? -INFINITY : least, [&](const float(&l)[16], auto id_of) {
     unsigned hits = 0;
+    float part = 0.0f;  // a batch's sum has the weights' own precision
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const bool hit = l[j] == l[j] && in(l[j], id_of(j));
       hits |= hit ? 1u << j : 0u;
-      if (weigh && l[j] == l[j]) {
-        const uint32_t w = r.fixed(r.dist(l[j]));
-        all += w;
-        inside += hit ? w : 0u;
-      }
+      if (weigh && l[j] == l[j]) part += r.falling(r.dist(l[j]));
     }
+    if (weigh) all += units(part);
     if (hits) {
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if ((hits >> j) & 1u) {
+          if (weigh) inside += r.fixed(r.dist(l[j]));
           const int at = atomicAdd(&s.n_local, 1);
           if (at < kList) s.list[at] = value_id_key(l[j], (uint32_t)id_of(j));
         }
@@ -435,16 +465,15 @@ static __device__ __forceinline__ void join(Smem& s, uint32_t rank) {
   cluster_sync();
 }
 
-// CTA 0's list of n keys, each thread's in registers, with their weights.
+// CTA 0's list of n keys, each thread's in registers.
 struct List {
   u64 key[kPer];
-  uint32_t w[kPer];
 };
 
 // The key of the last that stays of the list, and the weight of what stays: the largest key with
-// `target` keys at or above it, or (by_mass) with that weight; 0 if the whole list has less.
+// `target` keys at or above it, or (by_mass) with that weight; the smallest if the whole list has less.
 // The list's shared memory is taken for the histograms.
-static __device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_mass, u64 target, u64* mass_out) {
+static __device__ __forceinline__ u64 cut_list(Smem& s, const Row& r, const List& v, bool by_mass, u64 target, u64* mass_out) {
   u64 lo = 0, hi = ~0ull, mass = 0;
   while (true) {
     u64 top = 0, bottom = 0;
@@ -462,25 +491,22 @@ static __device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_m
       return 0;
     }
     const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);
-    clear_histogram(s);
+    clear_histogram<3>(s);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (v.key[j] && v.key[j] >= lo && v.key[j] <= hi) add_weight(s, (int)((hi - v.key[j]) >> shift), v.w[j]);
+      if (v.key[j] && v.key[j] >= lo && v.key[j] <= hi)
+        add_listed(s, (int)((hi - v.key[j]) >> shift), r.fixed(r.dist(key_value(v.key[j]))));
     __syncthreads();
     int bin;
     u64 c, m, here;
     find(s, [&](int b, u64& cc, u64& mm) {
       cc = s.hist[0][b];
-      mm = ((u64)s.hist[1][b] << 15) + s.hist[2][b];
+      mm = listed_mass(s, b);
     }, by_mass, target, bin, c, m, here);
-    const u64 in_bin = ((u64)s.hist[1][bin] << 15) + s.hist[2][bin];
+    const u64 in_bin = listed_mass(s, bin);
     target -= by_mass ? m : c;
     mass += m;
-    if (here == 0) {  // the whole list has less: the last bin, and nothing in it
-      *mass_out = mass;
-      return 0;
-    }
     hi -= (u64)bin << shift;
     lo = hi - (((u64)1 << shift) - 1) > hi ? 0 : hi - (((u64)1 << shift) - 1);
     if (here == 1 || shift == 0) {
@@ -495,12 +521,11 @@ static __device__ __forceinline__ u64 cut_list(Smem& s, const List& v, bool by_m
   }
 }
 
-static __device__ __forceinline__ void load_list(const Smem& s, const Row& r, int n, List& v) {
+static __device__ __forceinline__ void load_list(const Smem& s, int n, List& v) {
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int x = threadIdx.x + j * kThr;
     v.key[j] = x < n ? s.list[x] : 0;
-    v.w[j] = x < n ? r.fixed(r.dist(key_value(v.key[j]))) : 0;
   }
 }
 
@@ -529,7 +554,7 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
     own = (int)threadIdx.x < m ? s.list[threadIdx.x] : 0;
     if (top_k > 0 && (int)threadIdx.x >= top_k) own = 0;
     const float l = key_value(own);
-    const u64 w = own ? (u64)r.fixed(r.dist(l)) : 0;
+    const u64 w = own ? r.fixed(r.dist(l)) : 0;
     u64 before = w, z = 0;
     block_scan(before, z, s.red, s.red2);
     if (top_k > 0 && top_p < 1.0f) {
@@ -555,22 +580,22 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
     return;
   }
   List v;
-  load_list(s, r, m, v);
+  load_list(s, m, v);
   u64 mass, bound = 0;
   if (top_k > 0) {
-    bound = cut_list(s, v, false, (u64)top_k, &mass);
+    bound = cut_list(s, r, v, false, (u64)top_k, &mass);
     aim = share_of(top_p, mass);
   }
   if (top_p < 1.0f) {
     if (top_k > 0) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (v.key[j] < bound) v.key[j] = 0, v.w[j] = 0;
+        if (v.key[j] < bound) v.key[j] = 0;
     }
-    const u64 k = cut_list(s, v, true, aim, &mass);
+    const u64 k = cut_list(s, r, v, true, aim, &mass);
     bound = k > bound ? k : bound;
   }
-  // The list's order is that of the atomics that filled it, so its weights are summed as integers (of 2^-40).
+  // The list's order is that of the atomics that filled it, so its weights are summed as integers.
   u64 whole = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -580,7 +605,7 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
         const uint32_t id = key_id(v.key[j]);
         const u64 c = value_id_key(l / r.temp + g[id], id);
         key = c > key ? c : key;
-        whole += __float2ull_rn(w * 1099511627776.0f);
+        whole += units(w);
       }
     }
   }
@@ -588,7 +613,7 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
   block_scan(before, z, s.red, s.red2);
   if (threadIdx.x == kThr - 1) s.found_mass = before + whole;
   key = block_max(key, s.red);  // a barrier before found_mass is read
-  sum = (float)((double)s.found_mass * (1.0 / 1099511627776.0));
+  sum = (float)((double)s.found_mass * (1.0 / (double)(1ull << kUnit)));
   // From the thread that has the drawn token's logit.
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -805,7 +830,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
   }
   u64 best = B::block_max(value_id_key(top, (uint32_t)top_id), s.red);
   if (t < (int)size) st_u64(dsmem(&s.part_key[rank], (uint32_t)t), best);
-  B::clear_histogram(s);
+  B::template clear_histogram<2>(s);
   cluster_sync();
   best = 0;
   for (uint32_t k = 0; k < size; ++k) best = s.part_key[k] > best ? s.part_key[k] : best;
@@ -862,14 +887,12 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
       return;
     }
     cluster_sync();  // the numbers are read before the next ones arrive
-    B::clear_histogram(s);
+    B::template clear_histogram<2>(s);
     }
   }
   if (top_k > 0 || top_p < 1.0f) {
     const bool weigh = top_k == 0;  // with a top-k, its set is weighed once it is known
     uint32_t rest = 0;
-    u64 rest_w = 0;
-    if (t == 0) s.rest_w = 0;
     __syncthreads();
     slice.batches(-INFINITY, [&](const float(&l)[16], auto) {
 #pragma unroll
@@ -882,25 +905,21 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
           if (weigh) atomicAdd(&s.hist[1][b], r.lack(d, b));
         } else {
           ++rest;
-          if (weigh) rest_w += r.fixed(d);
         }
       }
     });
     rest = __reduce_add_sync(0xffffffffu, rest);
-    const uint32_t rest_hi = __reduce_add_sync(0xffffffffu, (uint32_t)(rest_w >> 15));
-    const uint32_t rest_lo = __reduce_add_sync(0xffffffffu, (uint32_t)(rest_w & 0x7fffu));
-    if (rest && (t & 31) == 0) {
-      atomicAdd(&s.hist[0][kNear], rest);
-      atomicAdd(&s.rest_w, ((u64)rest_hi << 15) + rest_lo);
+    if (rest && (t & 31) == 0) atomicAdd(&s.hist[0][kNear], rest);
+    if (weigh) {
+      // Tokens past the last near bin, 32 nats down, weigh nothing: a whole vocabulary of them is less than 2^-26 of a row,
+      // and no fp32 top-p below 1 is as near to it.
+      B::template share_histogram<2>(s, rank, size, [&](int b, const u64 (&sum)[2]) {
+        const double w = ((double)sum[0] - (double)sum[1] * (1.0 / 2097152.0)) * (double)r.edge(b);
+        return b == kNear ? 0 : (u64)llrint(w * (double)(1ull << kUnit));
+      });
+    } else {
+      B::template share_histogram<1>(s, rank, size, [](int, const u64 (&)[1]) { return (u64)0; });
     }
-    B::share_histogram(s, rank, size, weigh ? 2 : 1, [&](int b, u64 c, u64 lack, u64) {
-      if (b == kNear) {
-        u64 m = 0;
-        for (uint32_t k = 0; k < size; ++k) m += ld_u64(dsmem(&s.rest_w, k));
-        return m;
-      }
-      return (u64)llrint(((double)c - (double)lack * (1.0 / 2097152.0)) * (double)r.edge(b) * 1073741824.0);
-    });
     auto sums = [&](int b, u64& c, u64& m) {
       c = s.cnt[b];
       m = s.mass[b];
@@ -956,7 +975,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
           st_u64(dsmem(&s.part_key[rank], (uint32_t)t), kmax);
           st_u64(dsmem(&s.part_lo[rank], (uint32_t)t), kmin);
         }
-        B::clear_histogram(s);
+        B::template clear_histogram<4>(s);
         cluster_sync();
         hi = 0;
         lo = 0;
@@ -974,7 +993,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
             if (k >= lo && k <= hi) B::add_weight(s, (int)((hi - k) >> shift), r.fixed(r.dist(l[j])));
           }
         });
-        B::share_histogram(s, rank, size, 3, B::whole_mass);
+        B::template share_histogram<4>(s, rank, size, B::whole_mass);
         int sub;
         u64 c, m;
         B::find(s, sums, by_mass, target - before, sub, c, m, in_bin);
@@ -993,9 +1012,9 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
       B::join(s, rank);
       if (rank == 0) {
         typename B::List v;
-        B::load_list(s, r, m, v);
+        B::load_list(s, m, v);
         u64 mass;
-        const u64 k = B::cut_list(s, v, by_mass, target - before, &mass);
+        const u64 k = B::cut_list(s, r, v, by_mass, target - before, &mass);
         if (t == 0) s.result = k;
       }
       cluster_sync();
@@ -1007,7 +1026,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
       bound = select(bin_k, here_k, cnt_k, false, (u64)top_k, 0);
       if (top_p < 1.0f) {
         // Weigh the top-k set.
-        B::clear_histogram(s);
+        B::template clear_histogram<4>(s);
         cluster_sync();
         slice.batches(-INFINITY, [&](const float(&l)[16], auto id_of) {
 #pragma unroll
@@ -1017,7 +1036,7 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
             B::add_weight(s, r.bin(d), r.fixed(d));
           }
         });
-        B::share_histogram(s, rank, size, 3, B::whole_mass);
+        B::template share_histogram<4>(s, rank, size, B::whole_mass);
         u64 m = 0, z = 0;
         for (int b = t; b < kBins; b += kThr) m += s.mass[b];
         u64 before = m;

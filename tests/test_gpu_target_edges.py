@@ -98,3 +98,73 @@ def test_kernels_share_a_workspace():
                 out, lse = run(calls[x], ws)
                 assert torch.equal(out, want[x][0]) and torch.equal(lse, want[x][1]), (first, second, x)
     assert B.domino_last_status(ws) == 0
+
+
+def far_down(V, tied, low, high, seed):
+    """A row with one likely token and `tied` tokens each at `high` and at `low` nats below it (the rest masked), at random
+    places, and noise that only a few tokens have."""
+    g = T.gen(seed)
+    at = torch.randperm(V, generator=g, device="cuda")[:2 * tied + 1]
+    x = torch.full((V,), float("-inf"), device="cuda")
+    x[at[0]] = 3.0
+    x[at[1:tied + 1]] = 3.0 - high
+    x[at[tied + 1:]] = 3.0 - low
+    return x, at[1:tied + 1].sort()[0], at[tied + 1:].sort()[0]
+
+
+@pytest.mark.parametrize("rows", [3, 800])
+@pytest.mark.parametrize("high,low,share", [(17.0, 18.0, 0.995), (17.0, 18.0, 0.6), (20.0, 20.5, 0.98), (19.0, 21.4, 0.9),
+                                            (16.0, 25.0, 0.999)])
+def test_top_p_whose_bound_lies_far_down(rows, high, low, share):
+    """The bound falls among equal logits far below the maximum: the tokens before it stay, no other does. Each row's noise
+    would have a token drawn that does not stay, after one that does."""
+    V, tied = 120000, 50000
+    x, upper, lower = far_down(V, tied, low, high, 70)
+    total = 1.0 + tied * (math.exp(-high) + math.exp(-low))
+    top_p = torch.tensor((1.0 + share * tied * math.exp(-high)) / total, dtype=F32).item()
+    stay = (top_p * total - 1.0) / math.exp(-high)  # of the upper tokens, in the order of their ids
+    # Masses are good to 2^-20 of themselves (the exponential's argument, of up to 32, rounds at 2^-19 of a nat) and to 2^-22 of the whole.
+    slack = 4 + tied * 2.0 ** -18 + total * 2.0 ** -22 / math.exp(-high)
+    assert slack < 0.05 * tied and 0 < stay < tied
+    inside, outside = int(upper[int(stay - slack)]), int(upper[min(tied - 1, int(stay + slack) + 2)])
+    noise = torch.zeros(rows, V, device="cuda")
+    noise[:, inside] = 60.0
+    noise[0::2, lower[:5]] = 90.0
+    noise[1::2, int(lower[-1])] = 90.0
+    if stay + slack + 2 < tied - 1:
+        noise[:, outside] = 80.0
+    p = torch.full((rows,), top_p, device="cuda")
+    s = Sampler(rows, V)
+    tok, lp = s.sample(x.expand(rows, V).contiguous(), noise, None, None, p, want_logprob=True)
+    assert s.last_status() == 0
+    assert tok.tolist() == [inside] * rows
+    assert bool(((lp + high + math.log(1.0 + stay * math.exp(-high))).abs() <= 1e-5).all())
+
+
+@pytest.mark.parametrize("rows", [3, 800])
+@pytest.mark.parametrize("top_k", [0, 60000])
+@pytest.mark.parametrize("spread", [0.0, 1.4])
+def test_top_p_counts_the_weight_of_a_long_tail(rows, top_k, spread):
+    """150,000 tokens 22 nats down are some 1e-5 of a row together, and each less than 2^-31 of its largest weight: they
+    count in what top-p takes its share of."""
+    V, n = 151936, 150000
+    g = T.gen(71)
+    at = torch.randperm(V, generator=g, device="cuda")[:n + 1]
+    x = torch.full((V,), float("-inf"), device="cuda")
+    x[at[0]] = 0.0
+    x[at[1:]] = -22.0 - spread * torch.rand(n, generator=g, device="cuda")
+    value, order = x.to(O.F64).sort(descending=True, stable=True)
+    before = (value.exp().cumsum(0) - value.exp())[:top_k or n + 1]
+    total = float(before[-1] + value[len(before) - 1].exp())
+    top_p = torch.tensor((1.0 + 0.5 * (total - 1.0)) / total, dtype=F32).item()
+    # Masses are good to 2^-18 of themselves and to 2^-22 of the whole.
+    room = 2.0 ** -22 * total + 2.0 ** -18 * (total - 1.0) + 4 * math.exp(-22.0)
+    assert room < 0.2 * (total - 1.0)
+    inside = order[int((before < top_p * total - room).sum()) - 1].item()
+    outside = order[int((before < top_p * total + room).sum())].item()
+    noise = torch.zeros(rows, V, device="cuda")
+    noise[:, inside], noise[:, outside] = 60.0, 80.0
+    s = Sampler(rows, V)
+    tok = s.sample(x.expand(rows, V).contiguous(), noise, None, T.ints([top_k] * rows), torch.full((rows,), top_p, device="cuda"))
+    assert s.last_status() == 0
+    assert tok.tolist() == [inside] * rows
