@@ -188,17 +188,19 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
         const int e = c * 64 + tc * 4;
         if (e < D) {
           float4 v = *(const float4*)(sv + j * D + e);
-          // What a row does not see has weight 0 and must not be multiplied if it is no number. A slot that
-          // all rows see may be anything.
+          // What a row does not see has weight 0 and must not be multiplied if it is no number; what it sees is added as
+          // it is then, as the weight may have vanished. A slot that all rows see may be anything.
           if (!whole && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {
+            const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (w[i] != 0.0f) {
-                o[i][4 * c] = fmaf(w[i], v.x, o[i][4 * c]);
-                o[i][4 * c + 1] = fmaf(w[i], v.y, o[i][4 * c + 1]);
-                o[i][4 * c + 2] = fmaf(w[i], v.z, o[i][4 * c + 2]);
-                o[i][4 * c + 3] = fmaf(w[i], v.w, o[i][4 * c + 3]);
+            for (int i = 0; i < 4; ++i) {
+              const int r = tr * 4 + i, slot = s0 + j;
+              if (r < rows && slot < ctx + n &&
+                  sees(a.mode, a.sinks, s_low[r], ctx, n, s_i[r], mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, slot)) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[i][4 * c + y] = isfinite(x[y]) ? fmaf(w[i], x[y], o[i][4 * c + y]) : o[i][4 * c + y] + x[y];
               }
+            }
             continue;
           }
 #pragma unroll

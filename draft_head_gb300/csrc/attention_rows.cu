@@ -288,8 +288,7 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
     for (int w = 0; w < kWarps; ++w) {
       const float2 v = s_ml[w][r];
       const float4 y = *(const float4*)&s_o[w][r][e];
-      const float f = v.x == -INFINITY ? (v.y == 0.0f ? 0.0f : 1.0f) : v.x == mm ? 1.0f : ex2(v.x - mm);
-      if (f == 0.0f) continue;
+      const float f = v.x == -INFINITY || v.x == mm ? 1.0f : ex2(v.x - mm);  // a warp that saw nothing has sums of 0
       ll += v.y * f;
       acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
     }

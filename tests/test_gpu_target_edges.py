@@ -168,3 +168,30 @@ def test_top_p_counts_the_weight_of_a_long_tail(rows, top_k, spread):
     tok = s.sample(x.expand(rows, V).contiguous(), noise, None, T.ints([top_k] * rows), torch.full((rows,), top_p, device="cuda"))
     assert s.last_status() == 0
     assert tok.tolist() == [inside] * rows
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_non_finite_value_reaches_rows_in_which_its_weight_vanishes(kernel, value):
+    """Slots of scores so low that their weights are 0 in fp32, in key tiles that all rows see and in one that some see:
+    a seen NaN or infinity still is not lost."""
+    dt, _, hq, hkv, D = KERNELS[kernel]
+    rows, past = {"few_rows": 4, "one_query_tile": 20, "two_query_tiles": 150}.get(kernel, 12), 400
+    g = T.gen(80)
+    k, v = T.cache_pair(g, dt, 1, hkv, past + rows, D)
+    q = torch.ones(rows, hq, D, dtype=dt, device="cuda")
+    far = ((torch.arange(past + rows, device="cuda") // 16) % 4 == 1)
+    far[past + 2] = True
+    k[0, :, far] = -200.0 * D ** -0.5
+    p = BlockAttention(k, v, hq, rows, rows, past)
+    out0, lse0 = (x.clone() for x in p.attend(q, T.ints([past]), want_lse=True))
+    for slot in (85, past + 2):
+        keep = v[0, 1, slot, 5].clone()
+        v[0, 1, slot, 5] = value
+        out, lse = p.attend(q, T.ints([past]), want_lse=True)
+        v[0, 1, slot, 5] = keep
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[max(0, slot - past):, hq // hkv:, 5] = True
+        assert not bool(torch.isfinite(out[hit]).any())
+        assert torch.equal(out[~hit], out0[~hit]) and torch.equal(lse, lse0)
+    assert p.last_status() == 0
