@@ -790,8 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const float2 x = s_ml[trow], y = s_ml[128 + trow];
         m = fmaxf(x.x, y.x);
         f0 = x.x == m ? 1.0f : ex2(x.x - m);
-        f1 = y.x == -INFINITY ? 0.0f : y.x == m ? 1.0f : ex2(y.x - m);
-        l = x.y * f0 + (f1 != 0.0f ? y.y * f1 : 0.0f);
+        f1 = y.x == m ? 1.0f : ex2(y.x - m);
+        l = x.y * f0 + y.y * f1;  // a sum may be NaN (of NaN scores) beside a maximum of -inf
       }
       const bool two = NQ == 1 && k1 - k0 > 1;  // the second O has been written
       const bool o_boxes = p.o_boxes && !bad && g * 128 + quarter * 32 + 32 <= w.rows;

@@ -195,3 +195,19 @@ def test_a_non_finite_value_reaches_rows_in_which_its_weight_vanishes(kernel, va
         assert not bool(torch.isfinite(out[hit]).any())
         assert torch.equal(out[~hit], out0[~hit]) and torch.equal(lse, lse0)
     assert p.last_status() == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_nan_score_reaches_the_log_sum(kernel):
+    """A row that sees a NaN key, in a key tile of which it sees nothing else: output and lse are NaN. More requests than SMs, so that
+    most have all their key tiles in one block."""
+    dt, _, hq, hkv, D = KERNELS[kernel]
+    rows, past, b = {"few_rows": 4, "one_query_tile": 20, "two_query_tiles": 150}.get(kernel, 12), 128, 200
+    g = T.gen(81)
+    k, v = T.cache_pair(g, dt, b, hkv, past + rows, D)
+    q = T.randn(g, b * rows, hq, D).to(dt)
+    k[:, 0, past] = float("nan")
+    out, lse = BlockAttention(k, v, hq, b * rows, rows, past).attend(q, T.ints([past] * b), want_lse=True)
+    G = hq // hkv
+    assert bool(torch.isnan(out[:, :G]).all()) and bool(torch.isnan(lse[:, :G]).all())
+    assert bool(torch.isfinite(out[:, G:]).all()) and bool(torch.isfinite(lse[:, G:]).all())
