@@ -162,12 +162,12 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
       }
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      // A row that has seen nothing keeps m = -inf and l = 0.
+      // A row that has seen nothing, or scores of -inf alone, keeps m = -inf and l = 0.
       const float keep = mx == -INFINITY || m[i] == mx ? 1.0f : exp2f(m[i] - mx);
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float w = in[j] ? exp2f(s[i][j] - mx) : 0.0f;
+        const float w = in[j] ? exp2f(s[i][j] - (mx == -INFINITY ? 0.0f : mx)) : 0.0f;
         sp[r * (kBN + 1) + tc + 16 * j] = w;
         sum += w;
       }

@@ -211,3 +211,21 @@ def test_a_nan_score_reaches_the_log_sum(kernel):
     G = hq // hkv
     assert bool(torch.isnan(out[:, :G]).all()) and bool(torch.isnan(lse[:, :G]).all())
     assert bool(torch.isfinite(out[:, G:]).all()) and bool(torch.isfinite(lse[:, G:]).all())
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("where", ["first", "last", "all"])
+def test_scores_of_minus_infinity_have_no_weight(kernel, where):
+    """Whole key tiles whose seen scores are -inf: their slots count for nothing; if there are no others, as if none were seen."""
+    dt, _, hq, hkv, D = KERNELS[kernel]
+    rows, past = {"few_rows": 4, "one_query_tile": 20, "two_query_tiles": 150}.get(kernel, 12), 384
+    g = T.gen(82)
+    k, v = T.cache_pair(g, dt, 1, hkv, past + rows, D)
+    q = (0.5 + torch.rand(rows, hq, D, generator=g, device="cuda")).to(dt)
+    dead = torch.zeros(past + rows, dtype=torch.bool)
+    dead[slice(0, 256) if where == "first" else slice(256, None) if where == "last" else slice(None)] = True
+    k[0, :, dead.cuda()] = float("-inf")
+    p = BlockAttention(k, v, hq, rows, rows, past)
+    out, lse = p.attend(q, T.ints([past]), want_lse=True)
+    seen = torch.stack([O.seen_slots("causal", 0, 0, past, rows, i, past + i) for i in range(rows)]) & ~dead
+    T.check_attention((dt, [rows], [past], hq, hkv, D), q, torch.where(torch.isinf(k), torch.zeros_like(k), k), v, p, [seen], [0, rows], out, lse)
