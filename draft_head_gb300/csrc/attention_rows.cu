@@ -368,7 +368,7 @@ template <int NT, int KS, int JJ>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   RowsP p;
   p.a = a;
-  p.c = fmaxf(a.scale * kLog2e, 1e-30f);  // a scale of 0 still has to leave a masked score at -inf
+  p.c = a.scale * kLog2e;
   const int64_t key_tiles = ((int64_t)a.rows.max_ctx + a.rows.max_q) / kBN, row_tiles = (int64_t)a.hkv * a.rows.batch;
   const bool many = row_tiles >= kManyTiles;
   p.least = many ? kLeastMany : kLeast;

@@ -1025,8 +1025,9 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   p.a = a;
   p.row_tiles = (int)(((int64_t)a.rows.max_q * (a.hq / a.hkv) + C::BMT - 1) / C::BMT);
   p.timeout_ns = wait_timeout_ns();
-  // A scale of 0 still has to leave a masked score at -inf.
-  p.c = fmaxf(a.scale * kLog2e, 1e-30f);
+  // Masked scores are -inf before they are multiplied and have to stay so with a scale of 0: the smallest normal factor
+  // instead, which brings products of up to 2^120 to within 2^-6 of 0.
+  p.c = fmaxf(a.scale * kLog2e, 1.17549435e-38f);
   const uint32_t budget = (227 - 3) * 1024;
   int slots = (int)((budget - NQ * C::kQBytes - C::kStage) / C::kTile);
   // Even: a buffer is always a key or always a value buffer, so every phase of a value

@@ -229,3 +229,18 @@ def test_scores_of_minus_infinity_have_no_weight(kernel, where):
     out, lse = p.attend(q, T.ints([past]), want_lse=True)
     seen = torch.stack([O.seen_slots("causal", 0, 0, past, rows, i, past + i) for i in range(rows)]) & ~dead
     T.check_attention((dt, [rows], [past], hq, hkv, D), q, torch.where(torch.isinf(k), torch.zeros_like(k), k), v, p, [seen], [0, rows], out, lse)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_scale_zero_weighs_all_seen_slots_alike(kernel):
+    """Scale 0 makes every score 0, however large the products are (2^100 here)."""
+    dt, _, hq, hkv, D = KERNELS[kernel]
+    rows, past = {"few_rows": 4, "one_query_tile": 20, "two_query_tiles": 150}.get(kernel, 12), 200
+    g = T.gen(83)
+    k, v = T.cache_pair(g, dt, 1, hkv, past + rows, D)
+    k *= 2.0 ** 50
+    q = (2.0 ** 50 * T.randn(g, rows, hq, D)).to(dt)
+    p = BlockAttention(k, v, hq, rows, rows, past, scale=0.0, window=150, sinks=3)
+    out, lse = p.attend(q, T.ints([past]), want_lse=True)
+    seen = torch.stack([O.seen_slots("causal", 150, 3, past, rows, i, past + i) for i in range(rows)])
+    T.check_attention((dt, [rows], [past], hq, hkv, D), q, k, v, p, [seen], [0, rows], out, lse)
