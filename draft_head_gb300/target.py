@@ -14,6 +14,13 @@ from . import binding as B
 _MODES = {"causal": B.MASK_CAUSAL, "full": B.MASK_FULL}
 
 
+def _need(t, dtype, count: int, device: int, what: str):
+    """A device array that the library takes by its address: `count` elements at least, one behind the other."""
+    if t.dtype is not dtype or t.numel() < count or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what}: {count} elements of {dtype} on device {device}, contiguous; not {tuple(t.shape)} of {t.dtype} "
+                         f"on {t.device}")
+
+
 def rope_table(positions: int, rot_dim: int, base: float = 1e6, device="cuda") -> torch.Tensor:
     """The rotation table domino_qk_norm_rope reads, [positions, rot_dim] fp32: the cosines of pos * base^(-2j / rot_dim)
     for j < rot_dim / 2, then the sines (angles in 64 bits)."""
@@ -29,7 +36,8 @@ class BlockAttention:
     first three axes in memory). max_tokens / max_q / max_ctx bound the packed rows of a call, a request's rows and its
     past. scale defaults to head_dim ** -0.5; window 0 is the whole past. rope: a rotation table [max_pos, rot_dim]
     (rope_table); q_weight, k_weight: the norms' weights [head_dim]. Rows are packed request after request; q_start
-    [batch + 1] int32 says where each begins (None: every request has max_q rows)."""
+    [batch + 1] int32 says where each begins (None: every request has max_q rows), ctx_len [batch] int32 how many slots
+    are in use, positions [tokens] int32 where each row is (None: behind the past)."""
 
     def __init__(self, k_cache, v_cache, n_q_heads: int, max_tokens: int, max_q: int, max_ctx: int, window: int = 0,
                  sinks: int = 0, scale=None, rope=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -38,6 +46,7 @@ class BlockAttention:
         self.k_cache, self.v_cache = k_cache, v_cache
         self.hq, self.hkv, self.dim = n_q_heads, self.cache.n_kv_heads, self.cache.head_dim
         self.dev, self.dtype = k_cache.device, k_cache.dtype
+        self.ordinal = k_cache.get_device()
         self.max_tokens, self.max_q, self.max_ctx = max_tokens, max_q, max_ctx
         self.window, self.sinks = window, sinks
         self.scale = float(self.dim ** -0.5 if scale is None else scale)
@@ -58,9 +67,14 @@ class BlockAttention:
     def _set_rows(self, tokens: int, ctx_len, q_start, positions):
         if tokens > self.max_tokens:
             raise ValueError(f"{tokens} rows: made for {self.max_tokens}")
-        r = self.rows
+        r, batch, ordinal = self.rows, self.cache.batch, self.ordinal
+        _need(ctx_len, torch.int32, batch, ordinal, "ctx_len")
+        if q_start is not None:
+            _need(q_start, torch.int32, batch + 1, ordinal, "q_start")
+        if positions is not None:
+            _need(positions, torch.int32, tokens, ordinal, "positions")
         r.tokens = tokens
-        r.max_q = self.max_q if q_start is not None else tokens // self.cache.batch
+        r.max_q = self.max_q if q_start is not None else tokens // batch
         r.ctx_len = ctx_len.data_ptr()
         r.q_start = None if q_start is None else q_start.data_ptr()
         r.positions = None if positions is None else positions.data_ptr()

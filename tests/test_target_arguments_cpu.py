@@ -1,0 +1,61 @@
+"""What BlockAttention and Sampler refuse of the arrays that the library takes by their addresses (no GPU: each call is
+refused before anything is enqueued)."""
+import pytest
+import torch
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module")
+def T():
+    from draft_head_gb300 import build
+    build.build()
+    from draft_head_gb300 import target
+    return target
+
+
+def layer(T, batch=3, dtype=BF, **kw):
+    k = torch.zeros(batch, 2, 20, 64, dtype=dtype)
+    return T.BlockAttention(k, torch.zeros_like(k), n_q_heads=4, max_tokens=12, max_q=4, max_ctx=16, **kw)
+
+
+def ints(*x, dtype=I32):
+    return torch.tensor(x, dtype=dtype)
+
+
+CTX, START, POS = ints(1, 2, 3), ints(0, 4, 8, 12), torch.arange(12, dtype=I32)
+BAD_ROWS = [
+    dict(ctx_len=ints(1, 2, 3, dtype=torch.int64)), dict(ctx_len=ints(1, 2)), dict(ctx_len=ints(1, 1).repeat(3)[::2]),
+    dict(ctx_len=CTX[:1].expand(3)), dict(ctx_len=CTX.float()),
+    dict(q_start=ints(0, 4, 8, 12, dtype=torch.int64)), dict(q_start=ints(0, 4, 8)), dict(q_start=START.repeat(2)[::2]),
+    dict(positions=POS.long()), dict(positions=POS[:11]), dict(positions=POS.repeat(2)[::2]), dict(positions=POS.short()),
+]
+
+
+@pytest.mark.parametrize("i", range(len(BAD_ROWS)))
+def test_lengths_and_positions_that_are_refused(T, i):
+    p = layer(T)
+    a = dict(ctx_len=CTX, q_start=START, positions=POS)
+    a.update(BAD_ROWS[i])
+    with pytest.raises(ValueError, match=next(iter(BAD_ROWS[i]))):
+        p.append(torch.zeros(12, 8 * 64, dtype=BF), **a)
+    with pytest.raises(ValueError, match=next(iter(BAD_ROWS[i]))):
+        p.attend(torch.zeros(12, 4, 64, dtype=BF), **a)
+
+
+@pytest.mark.parametrize("name", ["ctx_len", "q_start", "positions"])
+def test_arrays_on_another_device_are_refused(T, name):
+    p = layer(T)
+    p.ordinal = 0  # a cache on the first GPU
+
+    class OnGpu:  # an array as it would look there
+        def __init__(self, t):
+            self.t, self.dtype, self.shape, self.device = t, t.dtype, t.shape, "cuda:0"
+            self.numel, self.is_contiguous, self.data_ptr = t.numel, t.is_contiguous, t.data_ptr
+
+        def get_device(self):
+            return 0
+
+    a = {k: v if k == name else OnGpu(v) for k, v in dict(ctx_len=CTX, q_start=START, positions=POS).items()}
+    with pytest.raises(ValueError, match=name):
+        p.attend(torch.zeros(12, 4, 64, dtype=BF), **a)
