@@ -109,8 +109,10 @@ class BlockAttention:
             mode, mask_ptr = _MODES[mask], None
         else:
             mode, mask_ptr = B.MASK_TREE, mask.data_ptr()
-            if mask.dtype != torch.uint8 or mask.shape[-1] != self.rows.max_q or not mask.is_contiguous():
-                raise ValueError(f"mask: [batch, {self.rows.max_q}, {self.rows.max_q}] uint8, contiguous")
+            n, batch = self.rows.max_q, self.cache.batch
+            if mask.dim() == 0 or mask.shape[-1] != n:
+                raise ValueError(f"mask: [{batch}, {n}, {n}], not {tuple(mask.shape)}")
+            _need(mask, torch.uint8, batch * n * n, self.ordinal, "mask")
         st = B.lib.domino_block_attention(*self._refs, self.hq, q.data_ptr(), self.scale, mode, mask_ptr, self.window,
                                           self.sinks, self._out[0], self._out[1] if want_lse else None, *self._ws,
                                           B._stream(None))

@@ -59,3 +59,15 @@ def test_arrays_on_another_device_are_refused(T, name):
     a = {k: v if k == name else OnGpu(v) for k, v in dict(ctx_len=CTX, q_start=START, positions=POS).items()}
     with pytest.raises(ValueError, match=name):
         p.attend(torch.zeros(12, 4, 64, dtype=BF), **a)
+
+
+def seen(*shape):
+    return torch.ones(*shape, dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("mask", [seen(4, 4), seen(1, 4, 4), seen(2, 4, 4), seen(3, 3, 4), seen(3, 4, 3), seen(3, 4, 8)[..., ::2],
+                                  seen(4, 4).expand(3, 4, 4), torch.tensor(1, dtype=torch.uint8), seen(3, 4, 4).bool(), seen(3, 4, 4).int()])
+def test_tree_masks_that_are_refused(T, mask):
+    """Among them a mask of one request for three, which the kernels would read past."""
+    with pytest.raises(ValueError, match="mask"):
+        layer(T).attend(torch.zeros(12, 4, 64, dtype=BF), CTX, q_start=START, mask=mask)
