@@ -33,9 +33,9 @@ class BlockAttention:
     """One attention layer of the target (or of the draft backbone) over its cache.
 
     k_cache, v_cache: [batch, n_kv_heads, capacity, head_dim], bfloat16 or float32, the same strides (any order of the
-    first three axes in memory). max_tokens / max_q / max_ctx bound the packed rows of a call, a request's rows and its
+    first three axes in memory), on one device with every other array of a call. max_tokens / max_q / max_ctx bound the packed rows of a call, a request's rows and its
     past. scale defaults to head_dim ** -0.5; window 0 is the whole past. rope: a rotation table [max_pos, rot_dim]
-    (rope_table); q_weight, k_weight: the norms' weights [head_dim]. Rows are packed request after request; q_start
+    (rope_table), float32; q_weight, k_weight: the norms' weights [head_dim], of the cache's type. Rows are packed request after request; q_start
     [batch + 1] int32 says where each begins (None: every request has max_q rows), ctx_len [batch] int32 how many slots
     are in use, positions [tokens] int32 where each row is (None: behind the past)."""
 
@@ -50,6 +50,13 @@ class BlockAttention:
         self.max_tokens, self.max_q, self.max_ctx = max_tokens, max_q, max_ctx
         self.window, self.sinks = window, sinks
         self.scale = float(self.dim ** -0.5 if scale is None else scale)
+        for weight, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if weight is not None:
+                _need(weight, self.dtype, self.dim, self.ordinal, what)
+        if rope is not None:
+            if rope.dim() != 2:
+                raise ValueError(f"rope: [positions, rot_dim], not {tuple(rope.shape)}")
+            _need(rope, torch.float32, 0, self.ordinal, "rope")
         self.rope, self.q_weight, self.k_weight = rope, q_weight, k_weight
         self.eps, self.interleaved = float(eps), int(interleaved)
         self.rows = B.block(max_tokens, max_q, max_ctx, None)

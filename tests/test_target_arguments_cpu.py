@@ -71,3 +71,20 @@ def test_tree_masks_that_are_refused(T, mask):
     """Among them a mask of one request for three, which the kernels would read past."""
     with pytest.raises(ValueError, match="mask"):
         layer(T).attend(torch.zeros(12, 4, 64, dtype=BF), CTX, q_start=START, mask=mask)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weights_and_tables_that_are_refused(T, dtype):
+    """An fp32 weight beside a bf16 cache would be read as twice as many bf16 numbers, a bf16 table past its end."""
+    other = F32 if dtype == BF else BF
+    for name in ("q_weight", "k_weight"):
+        for bad in (torch.ones(64, dtype=other), torch.ones(63, dtype=dtype), torch.ones(128, dtype=dtype)[::2],
+                    torch.ones(1, dtype=dtype).expand(64)):
+            with pytest.raises(ValueError, match=name):
+                layer(T, dtype=dtype, **{name: bad})
+        layer(T, dtype=dtype, **{name: torch.ones(64, dtype=dtype)})
+    for bad in (torch.ones(30, 64, dtype=BF), torch.ones(30, 64, dtype=torch.float64), torch.ones(64), torch.ones(2, 30, 64),
+                torch.ones(30, 128)[:, ::2]):
+        with pytest.raises(ValueError, match="rope"):
+            layer(T, dtype=dtype, rope=bad)
+    layer(T, dtype=dtype, rope=torch.ones(30, 64))
