@@ -330,8 +330,10 @@ def domino_verify_sampled_head(head: Head, draft, L_base, u, lse, target_logits,
 def kv_cache(k, v) -> domino_kv_cache:
     """The struct of a layer's cache from tensors k and v [batch, n_kv_heads, capacity, head_dim] of the same
     strides (any order of the first three axes in memory; the last one contiguous)."""
-    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or k.stride(3) != 1:
-        raise ValueError("k and v: [batch, n_kv_heads, capacity, head_dim] of one type and the same strides, the last 1")
+    if (k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or k.stride(3) != 1 or
+            k.device != v.device):
+        raise ValueError("k and v: [batch, n_kv_heads, capacity, head_dim] of one type and the same strides, the last 1, on one "
+                         "device")
     dt = {torch.bfloat16: BF16, torch.float32: F32}.get(k.dtype)
     if dt is None:
         raise ValueError(f"cache type {k.dtype}: bfloat16 or float32")

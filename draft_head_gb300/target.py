@@ -91,8 +91,9 @@ class BlockAttention:
         normed and rotated queries come back [tokens, n_q_heads, head_dim] (a buffer of this object), keys and values go
         to the cache at slots ctx_len[b] + row."""
         width = (self.hq + 2 * self.hkv) * self.dim
-        if qkv.dtype != self.dtype or qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
-            raise ValueError(f"qkv: [tokens, {width}] of {self.dtype}")
+        if (qkv.dtype != self.dtype or qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1 or
+                qkv.get_device() != self.ordinal):
+            raise ValueError(f"qkv: [tokens, {width}] of {self.dtype} on {self.dev}")
         tokens = qkv.shape[0]
         self._set_rows(tokens, ctx_len, q_start, positions)
         p, stride, size = qkv.data_ptr(), qkv.stride(0), qkv.element_size()
@@ -109,8 +110,9 @@ class BlockAttention:
         [tokens, n_q_heads, head_dim], and with want_lse the rows' log-sum-exp [tokens, n_q_heads] (buffers of this
         object)."""
         tokens = q.shape[0]
-        if q.dtype != self.dtype or q.shape[1:] != self.q.shape[1:] or not q.is_contiguous():
-            raise ValueError(f"q: [tokens, {self.hq}, {self.dim}] of {self.dtype}, contiguous")
+        if (q.dtype != self.dtype or q.shape[1:] != self.q.shape[1:] or not q.is_contiguous() or
+                q.get_device() != self.ordinal):
+            raise ValueError(f"q: [tokens, {self.hq}, {self.dim}] of {self.dtype} on {self.dev}, contiguous")
         self._set_rows(tokens, ctx_len, q_start, positions)
         if isinstance(mask, str):
             mode, mask_ptr = _MODES[mask], None

@@ -58,7 +58,7 @@ def test_arrays_on_another_device_are_refused(T, name):
 
     a = {k: v if k == name else OnGpu(v) for k, v in dict(ctx_len=CTX, q_start=START, positions=POS).items()}
     with pytest.raises(ValueError, match=name):
-        p.attend(torch.zeros(12, 4, 64, dtype=BF), **a)
+        p.attend(OnGpu(torch.zeros(12, 4, 64, dtype=BF)), **a)
 
 
 def seen(*shape):
@@ -88,3 +88,15 @@ def test_weights_and_tables_that_are_refused(T, dtype):
         with pytest.raises(ValueError, match="rope"):
             layer(T, dtype=dtype, rope=bad)
     layer(T, dtype=dtype, rope=torch.ones(30, 64))
+
+
+def test_rows_and_caches_on_another_device_are_refused(T):
+    p = layer(T)
+    p.ordinal = 0
+    with pytest.raises(ValueError, match="qkv"):
+        p.append(torch.zeros(12, 8 * 64, dtype=BF), CTX, q_start=START)
+    with pytest.raises(ValueError, match="^q:"):
+        p.attend(torch.zeros(12, 4, 64, dtype=BF), CTX, q_start=START)
+    k = torch.zeros(3, 2, 20, 64, dtype=BF)
+    with pytest.raises(ValueError, match="one device"):
+        T.B.kv_cache(k, torch.empty_like(k, device="meta"))
