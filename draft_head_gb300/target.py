@@ -143,6 +143,7 @@ class Sampler:
         self.ws = B.workspace(256, device)
         self.tokens = torch.empty(rows, dtype=torch.int32, device=device)
         self.logprob = torch.empty(rows, dtype=torch.float32, device=device)
+        self.dev, self.ordinal = self.tokens.device, self.tokens.get_device()
         self._dt = {torch.bfloat16: B.BF16, torch.float32: B.F32}[dtype]
         self._ws = (self.ws.data_ptr(), self.ws.numel())
         self._out = (self.tokens.data_ptr(), self.logprob.data_ptr())
@@ -151,9 +152,21 @@ class Sampler:
         """tokens [rows] int32 (-1: no logit above -inf), and with want_logprob their log-probabilities in the kept
         distributions. gumbel [rows, V] fp32 may be None when every temperature is 0. Settings: [rows] device tensors
         (fp32; top_k int32), None: 1, off, off, off."""
-        n = logits.shape[0]
-        if n > self.rows or logits.dtype != self.dtype or logits.shape[1] != self.V or logits.stride(1) != 1:
-            raise ValueError(f"logits: [up to {self.rows}, {self.V}] of {self.dtype}")
+        n, V, ordinal = logits.shape[0], self.V, self.ordinal
+        if (n > self.rows or logits.dtype != self.dtype or logits.dim() != 2 or logits.shape[1] != V or logits.stride(1) != 1 or
+                logits.get_device() != ordinal):
+            raise ValueError(f"logits: [up to {self.rows}, {V}] of {self.dtype} on {self.dev}")
+        if gumbel is not None and (gumbel.dtype is not torch.float32 or gumbel.dim() != 2 or gumbel.shape[0] < n or gumbel.shape[1] < V or
+                                   gumbel.stride(1) != 1 or gumbel.get_device() != ordinal):
+            raise ValueError(f"gumbel: [{n}, {V}] of float32 on {self.dev}, not {tuple(gumbel.shape)} of {gumbel.dtype} on {gumbel.device}")
+        if temperature is not None:
+            _need(temperature, torch.float32, n, ordinal, "temperature")
+        if top_k is not None:
+            _need(top_k, torch.int32, n, ordinal, "top_k")
+        if top_p is not None:
+            _need(top_p, torch.float32, n, ordinal, "top_p")
+        if min_p is not None:
+            _need(min_p, torch.float32, n, ordinal, "min_p")
         st = B.lib.domino_sample(self._dt, logits.data_ptr(), logits.stride(0), n, self.V, B._ptr(temperature),
                                  B._ptr(top_k), B._ptr(top_p), B._ptr(min_p), B._ptr(gumbel),
                                  0 if gumbel is None else gumbel.stride(0), self._out[0],

@@ -100,3 +100,42 @@ def test_rows_and_caches_on_another_device_are_refused(T):
     k = torch.zeros(3, 2, 20, 64, dtype=BF)
     with pytest.raises(ValueError, match="one device"):
         T.B.kv_cache(k, torch.empty_like(k, device="meta"))
+
+
+BAD_DRAWS = [
+    dict(gumbel=torch.zeros(4, 50, dtype=BF)), dict(gumbel=torch.zeros(3, 50)), dict(gumbel=torch.zeros(4, 49)),
+    dict(gumbel=torch.zeros(4, 100)[:, ::2]), dict(gumbel=torch.zeros(50, 4).T), dict(gumbel=torch.zeros(4, 50, dtype=torch.float64)),
+    dict(gumbel=torch.zeros(200)),
+    dict(top_k=torch.zeros(4, dtype=torch.int64)), dict(top_k=torch.zeros(3, dtype=I32)), dict(top_k=torch.zeros(8, dtype=I32)[::2]),
+    dict(top_k=torch.zeros(4)), dict(temperature=torch.ones(4, dtype=torch.float64)), dict(temperature=torch.ones(1).expand(4)),
+    dict(top_p=torch.ones(3)), dict(top_p=torch.ones(4, dtype=BF)), dict(min_p=torch.ones(4, dtype=I32)), dict(min_p=torch.ones(1)),
+    dict(logits=torch.zeros(4, 50, 1)), dict(logits=torch.zeros(4, 51)), dict(logits=torch.zeros(5, 50)), dict(logits=torch.zeros(4, 50, dtype=BF)),
+]
+
+
+@pytest.mark.parametrize("i", range(len(BAD_DRAWS)))
+def test_noise_and_settings_that_are_refused(T, i):
+    """Among them an int64 top-k, which turned the filter off for every other row, and noise of fewer rows than the logits."""
+    a = dict(logits=torch.zeros(4, 50), gumbel=torch.zeros(4, 50), temperature=torch.ones(4), top_k=torch.zeros(4, dtype=I32),
+             top_p=torch.ones(4), min_p=torch.zeros(4))
+    a.update(BAD_DRAWS[i])
+    with pytest.raises(ValueError, match=next(iter(BAD_DRAWS[i]))):
+        T.Sampler(4, 50, device="cpu").sample(**a)
+
+
+@pytest.mark.parametrize("name", ["logits", "gumbel"])
+def test_logits_and_noise_on_another_device_are_refused(T, name):
+    s = T.Sampler(4, 50, device="cpu")
+    a = dict(logits=torch.zeros(4, 50), gumbel=torch.zeros(4, 50))
+    a[name] = torch.zeros(4, 50, device="meta")
+    s.ordinal = 0 if name == "logits" else -1
+    if name == "gumbel":  # both look as if they had no device; the noise alone is moved
+        class Away:
+            def __init__(self, t):
+                self.dtype, self.shape, self.device, self.dim, self.stride = t.dtype, t.shape, "cuda:0", t.dim, t.stride
+
+            def get_device(self):
+                return 0
+        a[name] = Away(torch.zeros(4, 50))
+    with pytest.raises(ValueError, match=name):
+        s.sample(**a)
