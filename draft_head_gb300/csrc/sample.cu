@@ -181,32 +181,87 @@ __device__ __forceinline__ float max16(const float (&l)[16]) {  // NaNs are pass
   return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
-// A CTA's slice of a row, in 16-byte units from the one that holds its first element. kStage: raw in
-// shared memory; otherwise read again, from L2.
+// A CTA's slice of a row, in 16-byte units from the one that holds its first element; a unit that lies only partly in
+// the slice is read element by element, so nothing outside the row is. kStage: raw in shared memory; otherwise
+// read again, from L2.
 template <typename T, int kThr, bool kStage>
 struct Slice {
   static constexpr int kVec = 16 / (int)sizeof(T), kUnits = 16 / kVec;
   const uint4* from;
   uint4* stage;
   int units, id0, s0, s1;
+  int whole0, wholes;  // the first unit that lies in the slice whole, and their number
+
+  __device__ __forceinline__ Slice(const T* row, uint4* shared, int begin, int end) : stage(shared), s0(begin), s1(end) {
+    const int skew = (int)(((uintptr_t)(row + s0) & 15u) / sizeof(T));
+    from = (const uint4*)(row + s0 - skew);
+    id0 = s0 - skew;
+    units = s1 > s0 ? (skew + s1 - s0 + kVec - 1) / kVec : 0;
+    whole0 = skew ? 1 : 0;
+    wholes = max(0, (skew + s1 - s0) / kVec - whole0);
+  }
+  __device__ __forceinline__ bool whole(int q) const { return (unsigned)(q - whole0) < (unsigned)wholes; }
+  // A unit that is not whole: its elements in the slice, and zeros.
+  __device__ __forceinline__ uint4 ragged(int q) const {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      const int id = id0 + q * kVec + e;
+      if (id < s0 || id >= s1) continue;
+      if (sizeof(T) == 4)
+        w[e & 3] = __ldcg((const uint32_t*)from + q * kVec + e);
+      else
+        w[(e >> 1) & 3] |= (uint32_t)__ldcg((const unsigned short*)from + q * kVec + e) << (16 * (e & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 
   // What lies outside the slice is marked with one NaN; a NaN logit counts as -inf.
   static __device__ __forceinline__ float outside() { return __uint_as_float(0x7fffffffu); }
   static __device__ __forceinline__ float cleared(float l) {
     return __float_as_uint(l) == 0x7fffffffu ? l : fmaxf(l, -INFINITY);
   }
-  __device__ __forceinline__ void decode(uint4 x, int q, float* l) const {
+  // The values of a whole unit from its bits.
+  static __device__ __forceinline__ void decode(uint4 x, float* l) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       l[e] = sizeof(T) == 4 ? __uint_as_float(w[e & 3])
                             : __uint_as_float((e & 1) ? w[(e >> 1) & 3] & 0xffff0000u : w[(e >> 1) & 3] << 16);
     }
-    if (q == 0 || q == units - 1) {
+  }
+  // What of unit q's values lies outside the slice, marked.
+  __device__ __forceinline__ void mark(int q, float* l) const {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const int id = id0 + q * kVec + e;
-        if (id < s0 || id >= s1) l[e] = outside();
+    for (int e = 0; e < kVec; ++e) {
+      const int id = id0 + q * kVec + e;
+      if (id < s0 || id >= s1) l[e] = outside();
+    }
+  }
+  // The values of units q0, q0 + kThr, ... (kN / kVec of them), which `get` reads where they are whole. Most batches are whole
+  // throughout, and go without a test a unit.
+  template <int kN, bool kShared, typename Get>
+  __device__ __forceinline__ void read(int q0, Get get, float (&l)[kN]) const {
+    constexpr int kU = kN / kVec, kSpan = (kU - 1) * kThr;
+    uint4 x[kU];
+    if (wholes > kSpan && (unsigned)(q0 - whole0) < (unsigned)(wholes - kSpan)) {
+#pragma unroll
+      for (int j = 0; j < kU; ++j) x[j] = get(q0 + j * kThr);
+#pragma unroll
+      for (int j = 0; j < kU; ++j) decode(x[j], l + j * kVec);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kU; ++j) {
+        const int q = q0 + j * kThr;
+        x[j] = make_uint4(0, 0, 0, 0);
+        if (kShared ? q < units : whole(q)) x[j] = get(q);
+      }
+#pragma unroll
+      for (int j = 0; j < kU; ++j) {
+        const int q = q0 + j * kThr;
+        if (!kShared && q < units && !whole(q)) x[j] = ragged(q);
+        decode(x[j], l + j * kVec);
+        mark(q, l + j * kVec);
       }
     }
   }
@@ -215,22 +270,8 @@ struct Slice {
   template <typename F>
   __device__ __forceinline__ void batches(float least, F f) const {
     for (int q0 = threadIdx.x; q0 < units; q0 += kThr * kUnits) {
-      uint4 x[kUnits];
       float l[16];
-#pragma unroll
-      for (int j = 0; j < kUnits; ++j) {
-        const int q = q0 + j * kThr;
-        x[j] = q < units ? (kStage ? stage[q] : __ldcg(from + q)) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < kUnits; ++j) {
-        const int q = q0 + j * kThr;
-        decode(x[j], q, l + j * kVec);
-        if (q >= units) {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) l[j * kVec + e] = outside();
-        }
-      }
+      read<16, kStage>(q0, [&](int q) { return kStage ? stage[q] : __ldcg(from + q); }, l);
       if (least > -INFINITY && !(max16(l) >= least)) continue;
 #pragma unroll
       for (int j = 0; j < 16; ++j) l[j] = cleared(l[j]);
@@ -629,19 +670,13 @@ static __device__ __forceinline__ void draw_from_list(Smem& s, const SampleArgs&
 // A row without a filter: one pass with a running maximum, the noise read beside the logits. False (and nothing written)
 // for a row with +inf logits. A function of its own, as its registers would be spilled in the other passes' loops.
 template <typename T, int kThr, bool kStage>
-__device__ __noinline__ bool draw_unfiltered(Smem& s, const SampleArgs& a, const uint4* from, int units, int id0, int s0, int s1, int row,
-                                             float temp) {
+__device__ __noinline__ bool draw_unfiltered(Smem& s, const SampleArgs& a, int s0, int s1, int row, float temp) {
   using B = Block<kThr>;
   constexpr int kVec = 16 / (int)sizeof(T);
   const uint32_t rank = cluster_rank(), size = cluster_size();
   const int t = threadIdx.x;
   const float* g = a.gumbel + (int64_t)row * a.gs;
-  Slice<T, kThr, kStage> slice;
-  slice.from = from;
-  slice.units = units;
-  slice.id0 = id0;
-  slice.s0 = s0;
-  slice.s1 = s1;
+  const Slice<T, kThr, kStage> slice((const T*)a.logits + (int64_t)row * a.ls, nullptr, s0, s1);
   Row r;
   r.temp = temp;
   r.inv_t = 1.0f / r.temp;
@@ -652,12 +687,7 @@ __device__ __noinline__ bool draw_unfiltered(Smem& s, const SampleArgs& a, const
   constexpr int kN = kStage ? 16 : 8, kU = kN / kVec;  // in flight, of each
   for (int q0 = t; q0 < slice.units; q0 += kThr * kU) {
     float l[kN], z[kN], now = -INFINITY;
-    uint4 x[kU];
-#pragma unroll
-    for (int j = 0; j < kU; ++j) {
-      const int q = q0 + j * kThr;
-      x[j] = q < slice.units ? __ldcs(slice.from + q) : make_uint4(0, 0, 0, 0);
-    }
+    slice.template read<kN, false>(q0, [&](int q) { return __ldcs(slice.from + q); }, l);
 #pragma unroll
     for (int e = 0; e < kN; e += 4) {
       const int id = slice.id0 + (q0 + e / kVec * kThr) * kVec + e % kVec;
@@ -668,15 +698,6 @@ __device__ __noinline__ bool draw_unfiltered(Smem& s, const SampleArgs& a, const
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (id + k >= s0 && id + k < s1) z[e + k] = __ldcs(g + id + k);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kU; ++j) {
-      const int q = q0 + j * kThr;
-      slice.decode(x[j], q, l + j * kVec);
-      if (q >= slice.units) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) l[j * kVec + e] = slice.outside();
       }
     }
 #pragma unroll
@@ -742,25 +763,18 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int row = blockIdx.x / (int)size, t = threadIdx.x, V = a.V;
   const int s0 = min(V, (int)rank * length), s1 = min(V, s0 + length);
-  const T* src = (const T*)a.logits + (int64_t)row * a.ls + s0;
   const float* g = a.gumbel ? a.gumbel + (int64_t)row * a.gs : nullptr;
 
   constexpr int kVec = 16 / (int)sizeof(T);
-  const int skew = (int)(((uintptr_t)src & 15u) / sizeof(T));
-  Slice<T, kThr, kStage> slice;
-  slice.from = (const uint4*)(src - skew);
-  slice.stage = (uint4*)(smem_raw + ((sizeof(Smem) + 15) & ~(size_t)15));
-  slice.units = s1 > s0 ? (skew + s1 - s0 + kVec - 1) / kVec : 0;
-  slice.id0 = s0 - skew;
-  slice.s0 = s0;
-  slice.s1 = s1;
+  const Slice<T, kThr, kStage> slice((const T*)a.logits + (int64_t)row * a.ls, (uint4*)(smem_raw + ((sizeof(Smem) + 15) & ~(size_t)15)),
+                                     s0, s1);
   bool there = false;  // all CTAs of the cluster have been seen
   {
     const float temp = a.temperature ? a.temperature[row] : 1.0f;
     const int k = a.top_k ? a.top_k[row] : 0;
     if (temp > 0.0f && temp < INFINITY && (k == 0 || k >= V) && g && !(a.top_p && a.top_p[row] != 1.0f) &&
         !(a.min_p && a.min_p[row] != 0.0f)) {
-      if (draw_unfiltered<T, kThr, kStage>(s, a, slice.from, slice.units, slice.id0, s0, s1, row, temp)) return;
+      if (draw_unfiltered<T, kThr, kStage>(s, a, s0, s1, row, temp)) return;
       there = true;
     }
   }
@@ -768,21 +782,41 @@ __global__ void __launch_bounds__(kThr, kStage ? 2 : kManyCtas) sample_kernel(co
   int top_id = 0;  // the lowest id of this thread's largest logit: its ids rise
   if (kStage) {
     constexpr int kLoads = 8;  // in flight
-    for (int q0 = t; q0 < slice.units; q0 += kThr * kLoads) {
+    const int end = slice.whole0 + slice.wholes;
+    for (int q0 = slice.whole0 + t; q0 < end; q0 += kThr * kLoads) {
       uint4 x[kLoads];
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
-        if (q0 + j * kThr < slice.units) x[j] = __ldcs(slice.from + q0 + j * kThr);
+        if (q0 + j * kThr < end) x[j] = __ldcs(slice.from + q0 + j * kThr);
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int q = q0 + j * kThr;
-        if (q >= slice.units) break;
+        if (q >= end) break;
         slice.stage[q] = x[j];
         float l[kVec], m = -INFINITY;
-        slice.decode(x[j], q, l);
+        slice.decode(x[j], l);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) m = fmaxf(m, l[e]);
         if (m > top) {
+          top = m;
+#pragma unroll
+          for (int e = kVec - 1; e >= 0; --e)
+            if (l[e] == m) top_id = slice.id0 + q * kVec + e;
+        }
+      }
+    }
+    // The units that are not whole: the first, of the lowest ids, and the last.
+    if (t < 2 && t < slice.units) {
+      const int q = t == 0 ? 0 : slice.units - 1;
+      if (!slice.whole(q)) {
+        const uint4 x = slice.ragged(q);
+        slice.stage[q] = x;
+        float l[kVec], m = -INFINITY;
+        slice.decode(x, l);
+        slice.mark(q, l);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) m = fmaxf(m, l[e]);
+        if (t == 0 ? m >= top : m > top) {
           top = m;
 #pragma unroll
           for (int e = kVec - 1; e >= 0; --e)

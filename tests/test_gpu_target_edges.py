@@ -244,3 +244,29 @@ def test_scale_zero_weighs_all_seen_slots_alike(kernel):
     out, lse = p.attend(q, T.ints([past]), want_lse=True)
     seen = torch.stack([O.seen_slots("causal", 150, 3, past, rows, i, past + i) for i in range(rows)])
     T.check_attention((dt, [rows], [past], hq, hkv, D), q, k, v, p, [seen], [0, rows], out, lse)
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("rows,V", [(3, 1003), (1, 9), (2, 60001), (700, 20011)])
+def test_rows_at_any_alignment_give_the_same_draw(rows, V, dt):
+    """Rows that begin and end inside 16-byte units, also where a slice is one unit or less: as when they are aligned."""
+    x, gum = T.rows_of("peaked", rows, V, 90)
+    x = x.to(dt)
+    settings = [(0.8, 0, 1.0, 0.0), (0.7, 20, 0.9, 0.0), (1.0, 0, 0.9, 0.0), (0.0, 0, 1.0, 0.0), (1.0, 5000, 0.95, 0.0), (0.9, 0, 1.0, 0.05)]
+    s = Sampler(rows, V, dtype=dt)
+    for t, k, p, m in settings:
+        a = (torch.full((rows,), t, device="cuda"), T.ints([k] * rows), torch.full((rows,), p, device="cuda"),
+             torch.full((rows,), m, device="cuda"))
+        want = None
+        for pad, at in ((16, 0), (16, 1), (13, 3), (17, 7)):
+            stride = (V + pad + 7) // 8 * 8 + (0 if at == 0 else at)
+            buf = torch.full((rows, stride), float("inf"), device="cuda", dtype=dt)  # what is beside a row would win
+            noise = torch.full((rows, stride), 50.0, device="cuda")
+            buf[:, at:at + V], noise[:, at:at + V] = x, gum
+            tok, lp = s.sample(buf[:, at:at + V], noise[:, at:at + V], *a, want_logprob=True)
+            got = tok.clone(), lp.clone()
+            want = got if want is None else want
+            assert torch.equal(got[0], want[0])
+            # The order of a sum's terms goes with the alignment.
+            assert bool(((got[1] - want[1]).abs() <= 1e-5).all())
+    assert s.last_status() == 0
