@@ -136,7 +136,7 @@ class BlockAttention:
 
 class Sampler:
     """Draws from logits [rows, V] (bfloat16 or float32) under per-row temperature, top-k, top-p and min-p with given
-    Gumbel noise. Owns the result buffers for `rows` rows."""
+    Gumbel noise; V up to 786,432. Owns the result buffers for `rows` rows."""
 
     def __init__(self, rows: int, V: int, dtype=torch.float32, device="cuda"):
         self.rows, self.V, self.dtype = rows, V, dtype

@@ -523,6 +523,8 @@ domino_status domino_block_attention(const domino_kv_cache* cache, const domino_
  * A setting outside its range (T < 0 or not finite, top_k < 0, top_p outside
  * (0, 1], min_p outside [0, 1]) records DOMINO_ERR_DEVICE_DATA and gives that
  * row token -1, logprob NaN. ws: any workspace of at least 256 bytes.
+ * V is at most 786,432 (16 blocks of a cluster with 49,152 tokens each):
+ * DOMINO_ERR_UNSUPPORTED above.
  */
 domino_status domino_sample(int dtype, const void* logits, int64_t logits_stride, int rows, int V,
                             const float* temperature, const int32_t* top_k, const float* top_p,

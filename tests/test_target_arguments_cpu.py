@@ -139,3 +139,21 @@ def test_logits_and_noise_on_another_device_are_refused(T, name):
         a[name] = Away(torch.zeros(4, 50))
     with pytest.raises(ValueError, match=name):
         s.sample(**a)
+
+
+@pytest.mark.parametrize("dtype,rows", [(0, 1), (0, 5000), (1, 1), (1, 5000)])
+def test_the_longest_vocabulary_is_the_one_that_is_written_down(T, dtype, rows):
+    """The largest that the header names is not refused for its size (the launch may be, without a GPU), one more is."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "domino.h")).read()
+    most = int(re.search(r"V is at most ([\d,]+)", text).group(1).replace(",", ""))
+    f, unsupported = 0x100000, 2  # an address that nothing reads: without a GPU no kernel runs
+
+    def status(V):
+        return T.B.lib.domino_sample(dtype, f, V, rows, V, None, None, None, None, f, V, f, None, f, 256, None)
+
+    assert status(most + 1) == unsupported
+    if not torch.cuda.is_available():
+        assert status(most) not in (0, unsupported)
