@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRope
   fetch_q(first);  // these need no lengths
   fetch_kv(first);
   read_weights<T>(a, s_w);
+  if (blockIdx.y == 0) report_requests(a.rows, a.ctl);
   int b, i, ctx, rows;
   bool mine = find_row(a.rows, t, b, i, ctx, rows, a.ctl);
   __syncthreads();
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
     for (int st = 0; st < stages && t0 + st < t_end; ++st) bring(t0 + st, st);
   }
   read_weights<T>(a, s_w);
+  report_requests(a.rows, a.ctl);
   int b, i, ctx, rows;
   bool mine, placed;
   float raw[16];

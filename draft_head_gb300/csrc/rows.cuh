@@ -30,6 +30,13 @@ __device__ __forceinline__ bool request_rows(const RowsArgs& r, int b, int& q0, 
   return true;
 }
 
+// Looks at the lengths of all requests, also of those that no row leads to (without rows, or with fewer than none), once over
+// the blocks of a grid's first axis.
+__device__ __forceinline__ void report_requests(const RowsArgs& r, Ctl* ctl) {
+  int q0, n, ctx;
+  for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < r.batch; b += gridDim.x * blockDim.x) request_rows(r, b, q0, n, ctx, true, ctl);
+}
+
 // The request b and place i of packed row t, and the request's past and rows. Called by
 // whole warps; every lane gets the result. A 32-way search: each round, the
 // lanes look at 32 requests spread over what is left; in the last round a lane

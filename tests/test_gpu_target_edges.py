@@ -270,3 +270,32 @@ def test_rows_at_any_alignment_give_the_same_draw(rows, V, dt):
             # The order of a sum's terms goes with the alignment.
             assert bool(((got[1] - want[1]).abs() <= 1e-5).all())
     assert s.last_status() == 0
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("bad", ["past", "negative past", "fewer rows than none", "past the cache"])
+def test_lengths_of_requests_without_rows_are_reported(bad, many):
+    """A bad length of a request that none of the rows leads to is reported by both calls; the rows of the others are served."""
+    n, D = (3000 if many else 4), 64
+    g = T.gen(95)
+    k, v = T.cache_pair(g, BF, 3, 2, n + 16, D)
+    ctx, st = [2, 5, 3], [0, n, n, 2 * n]
+    if bad == "past":
+        ctx[1] = 17
+    elif bad == "negative past":
+        ctx[1] = -1
+    elif bad == "past the cache":
+        ctx[1] = n + 17
+    else:
+        st = [0, n, n - 2, 2 * n - 2]
+    p = BlockAttention(k, v, 4, 2 * n, n, 16)
+    qkv = T.randn(g, 2 * n, 8 * D).to(BF)
+    k0 = k.clone()
+    q = p.append(qkv, T.ints(ctx), q_start=T.ints(st))
+    assert p.last_status() == 6
+    assert not torch.equal(k[0, :, 2:n], k0[0, :, 2:n]) and not torch.equal(k[2], k0[2])
+    p.attend(q, T.ints(ctx), q_start=T.ints(st))
+    assert p.last_status() == 6 and p.last_status() == 0
+    good = [0, n, n, 2 * n]
+    p.append(qkv, T.ints([2, 5, 3]), q_start=T.ints(good))
+    assert p.last_status() == 0
