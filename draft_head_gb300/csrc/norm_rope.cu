@@ -30,10 +30,11 @@ constexpr int kNrThreads = 128;
 constexpr int kRunCtas = 4;     // of the kernel for many rows, on an SM
 constexpr int kMostStages = 2;  // rows in a CTA's ring, at most
 constexpr int kRunSmem = 55 * 1024;
-// Rows per CTA of the kernel for few rows from which the kernel for many is taken. 1500 rows (two) of
-// 32 + 8 + 8 heads of 128: 8.9 us with the first and 9.5 with the second, 2000 rows (three) 11.5 and
-// 11.4, 4000 rows 26.7 and 20.5; fp32 12.3 and 15.4, 18.9 and 19.6, 40.1 and 38.3 us.
-constexpr int kRunRows = 3;
+// Rows per CTA of the kernel for few rows from which the kernel for many is taken. 32 + 8 + 8 heads of 128, first and second
+// kernel: bf16, 1500 rows (two) 8.8 and 9.2 us, 2000 (three) 11.4 and 11.3, 2700 (four) 15.0 and 13.4, 4000 (six) 25.6 and 19.7;
+// fp32, 2000 rows 17.9 and 20.2 us, 2700 27.5 and 28.3, 3300 (five) 33.4 and 33.5, 4000 39.1 and 38.0.
+template <typename T>
+constexpr int kRunRows = sizeof(T) == 2 ? 3 : 6;
 
 // Eight elements as they lie in memory; in arithmetic, four fp32 pairs.
 template <typename T>
@@ -408,7 +409,7 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
   const size_t smem = (size_t)(2 + (MODE == kHalvesShared ? groups : 0)) * a.D * 4;
   const size_t row = (size_t)(a.hq + 2 * a.hkv) * a.D * sizeof(T);
   const int stages = (int)std::min<size_t>(kMostStages, (kRunSmem - smem) / row);
-  if (chunk >= kRunRows && stages >= 2) {
+  if (chunk >= kRunRows<T> && stages >= 2) {
     const int ctas = kRunCtas * num_sms();
     chunk = (a.rows.tokens + ctas - 1) / ctas;
     const unsigned grid = (unsigned)((a.rows.tokens + chunk - 1) / chunk);

@@ -299,3 +299,11 @@ def test_lengths_of_requests_without_rows_are_reported(bad, many):
     good = [0, n, n, 2 * n]
     p.append(qkv, T.ints([2, 5, 3]), q_start=T.ints(good))
     assert p.last_status() == 0
+
+
+@pytest.mark.parametrize("case", [(F32, 3, 2400, 14, 2, 80, 40, False, True), (F32, 5, 1500, 4, 4, 256, 256, False, False),
+                                  (F32, 2, 3000, 8, 2, 64, 64, True, False), (F32, 4, 1500, 6, 3, 48, 20, False, True)])
+def test_norm_rope_of_many_fp32_rows(monkeypatch, case):
+    """As many rows as take the kernel for many in fp32 too."""
+    monkeypatch.setattr(T, "MANY", [case])
+    T.test_norm_rope_of_many_rows(0)
