@@ -164,10 +164,11 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
       for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
       // A row that has seen nothing, or scores of -inf alone, keeps m = -inf and l = 0.
       const float keep = mx == -INFINITY || m[i] == mx ? 1.0f : exp2f(m[i] - mx);
+      const float base = fmaxf(mx, -3.402823466e+38f);  // not -inf: scores of -inf have no weight
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float w = in[j] ? exp2f(s[i][j] - (mx == -INFINITY ? 0.0f : mx)) : 0.0f;
+        const float w = in[j] ? exp2f(s[i][j] - base) : -0.0f;  // the sign says that the slot is not seen
         sp[r * (kBN + 1) + tc + 16 * j] = w;
         sum += w;
       }
@@ -193,14 +194,11 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
           if (!whole && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {
             const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = tr * 4 + i, slot = s0 + j;
-              if (r < rows && slot < ctx + n &&
-                  sees(a.mode, a.sinks, s_low[r], ctx, n, s_i[r], mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, slot)) {
+            for (int i = 0; i < 4; ++i)
+              if (__float_as_int(w[i]) >= 0) {
 #pragma unroll
                 for (int y = 0; y < 4; ++y) o[i][4 * c + y] = isfinite(x[y]) ? fmaf(w[i], x[y], o[i][4 * c + y]) : o[i][4 * c + y] + x[y];
               }
-            }
             continue;
           }
 #pragma unroll
