@@ -49,6 +49,7 @@
 
 #include "attention.cuh"
 #include "packed.cuh"
+#include "waits.cuh"
 
 namespace domino {
 

@@ -212,12 +212,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 
-// Before the memory that an asynchronous operation reads or writes is given up: waits for one that is in flight and needs
-// nobody else to end. Its limit is its own, as the caller's may be shorter than a copy.
-__device__ __forceinline__ void mbar_land(uint64_t* bar, uint32_t parity, Ctl* ctl) {
-  mbar_wait(bar, parity, nullptr, ctl, 2000000000ull);
-}
-
 // 2-D tiled TMA load global -> shared, completing on `bar` (complete_tx).
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const void* tmap, int x, int y,
                                             uint64_t* bar) {

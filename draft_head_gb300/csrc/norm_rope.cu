@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "packed.cuh"
 #include "rows.cuh"
+#include "waits.cuh"
 
 namespace domino {
 

@@ -43,7 +43,7 @@ def test_copies_land_before_attention_gives_up_its_memory():
     assert "mbar_land(drain" in part(text, "} else if (warp == 1) {", "} else if (warp >= 2) {")
     queries = part(text, "} else if (warp >= 2) {", "setmaxnreg.inc")
     assert "mbar_land(q_ready" in queries[queries.index("++item;"):]
-    land = part(source("common.cuh"), "void mbar_land(", "\n}")
+    land = part(source("waits.cuh"), "void mbar_land(", "\n}")
     assert "timeout" not in land
 
 
