@@ -18,8 +18,8 @@
 // Four warps of a CTA share its slots and join in shared memory; CTAs that share a row tile
 // write their sums to the workspace, and the last one joins them in order.
 //
-// One token, 32 heads of 128 over 8 of the cache: over 4000 slots 12.5 us (20 with the tensor core
-// kernel), over 30,000 slots 29.6 us (4.1 TB/s); 64 tokens over up to 4000 slots each 117 us
+// One token, 32 heads of 128 over 8 of the cache: over 4000 slots 12.2 us (20 with the tensor core
+// kernel), over 30,000 slots 28.1 us (4.4 TB/s); 64 tokens over up to 4000 slots each 117 us
 // (4.6 TB/s).
 #include <math.h>
 #include <algorithm>
@@ -383,8 +383,9 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
 
 // Up to 8 packed rows it is the faster one or as fast (64 tokens over up to 4000 slots 117 us, the tensor core
 // kernel 118; over up to 500 slots 24 and 50). From 9 to 16 its products are twice as many, and with every SM busy over
-// long caches the tensor core kernel wins: 64 requests of 4 rows in groups of 4, up to 4000 slots, 133 and 119 us, up to
-// 500 slots 32 and 48; 16 requests 43.7 and 43.1; one 21 and 21.
+// long caches the tensor core kernel wins, from pasts of about 2500 on: 64 requests of 4 rows in groups of 4, up to 500 /
+// 2000 / 2500 / 3000 / 4000 slots, 31 / 76 / 80 / 96 / 120 us and 47 / 76 / 81 / 92 / 112; 32 requests 18 / 47 / 48 / 55 / 72
+// and 28 / 46 / 50 / 54 / 67. Fewer, which leave SMs idle: 16 requests up to 4000 slots 43.7 and 43.1; one 21 and 21.
 bool attn_rows_applies(const AttnArgs& a) {
   const int64_t rows = (int64_t)a.rows.max_q * (a.hq / a.hkv);
   if (a.dtype != DOMINO_BF16 || a.D > 128 || rows > 16) return false;

@@ -13,7 +13,8 @@
 // draft block of 16 rows: 3.6 us, nearly all of it the launch.
 // Many rows: a CTA takes a run of rows; bulk copies bring the next row to shared memory while it
 // works on one, so that the loads wait for nothing. Prompts of 4 requests, 19,700 rows of 32 + 8 + 8
-// heads of 128 in bf16: 86 us, 5.5 TB/s (without the copies ahead 114 us: too few bytes in flight).
+// heads of 128 in bf16: 86 us, 5.5 TB/s (without the copies ahead 114 us: too few bytes in flight; rows of which two
+// do not fit the ring's 55 KB, 55 heads of 128 in fp32 say, go without them).
 // Four CTAs an SM with two rows each measured best (three rows 87, four rows 89, three CTAs 97,
 // five, whose registers spill, 98 us).
 #include <algorithm>

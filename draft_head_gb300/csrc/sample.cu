@@ -36,10 +36,10 @@
 // logits once, the noise where tokens stay), and by the cluster's barriers (about a microsecond each)
 // for one row.
 //
-// Vocabulary 151,936, fp32. One row: greedy 4.7 us, top-k 64 with top-p 12.8, all filters 23 us. 1024
-// rows: greedy 111 us (5.6 TB/s), no filter 214 (5.8 TB/s with the noise; in two passes 404), top-k 64 225,
-// min-p 198, top-p alone 443 (peaked rows), mixed settings 322 us; 272 flat rows at top-p 0.9 alone, where two
-// thirds of the vocabulary stay: 312 us.
+// Vocabulary 151,936, fp32. One row: greedy 4.5 us, top-k 64 with top-p 13, top-k 1000 22 us. 1024 rows: greedy
+// 113 us (5.5 TB/s), no filter 218 (5.7 TB/s with the noise; in two passes 404), top-k 64 227, min-p 210, top-p alone
+// 416 (peaked rows), mixed settings 320 us; 272 flat rows at top-p of 0.8 to 0.95 alone, where most of the vocabulary
+// stays: 317 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -1177,14 +1177,17 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   while (size < kMaxCluster && (a.V + size - 1) / size > 20480) size <<= 1;
   const int64_t ctas = (int64_t)a.rows * size;
   if (size < kMaxCluster && a.V > 4096 * size && ctas * 2 <= num_sms()) size <<= 1;
+  // All figures: rows of 151,936, mixed settings if nothing else is said, the same inputs again and again.
   // Few rows: the slices stay in shared memory, two CTAs on an SM. Many: a row's time is mostly barriers,
   // and what hides them is more rows in flight than shared memory holds, so the slices are read again
-  // from L2 (rows of 151,936, mixed settings: 1024 rows 554 us from shared memory and 343 from L2, 272 rows 164
-  // and 118, 64 rows 51 and 46, 37 rows 33 and 40, 16 rows 28 and 39; one flat row at top-p 32 and 43). Five CTAs
-  // on an SM: six and eight spill in the draw.
+  // from L2 (1024 rows 540 us from shared memory and 292 from L2, 272 rows 160 and 138, 64 rows 51 and 43, 37 rows 32
+  // and 39, 16 rows 28 and 40; one flat row at top-p 32 and 46).
+  // Five CTAs on an SM, whose 48 registers do not hold the filters' passes (750 bytes are spilled): 1024 rows 292 us, 272
+  // 138, flat ones 317, 1024 at min-p 210, without a filter 218, greedy 113. Four: 291, 124, 293, 176, 254 and 119; three:
+  // 322, 119 and 328; six: 355, 169 and 415.
   // Where half as many CTAs still fill the SMs, the slices are twice as long: fewer barriers and searches for the same
-  // tokens (1024 rows, mixed settings 342 us and 316 so, 272 flat rows at top-p 337 and 311; four times 330 and 304, but
-  // rows at min-p or a peaked top-p slower). 64 rows, which do not fill them: top-p 64 us and 90.
+  // tokens (1024 rows 334 us and 292 so, 272 flat rows at top-p 353 and 317, though 272 mixed ones 115 and 138). 64 rows,
+  // which do not fill them: 43 us and 57, flat at top-p 94 and 112.
   if (ctas > 2 * (int64_t)num_sms()) {
     const bool longer = size > 1 && ctas / 2 > kManyCtas * num_sms() && (a.V + size / 2 - 1) / (size / 2) <= kMaxSlice - 32;
     return launch<T, 256, false>(a, longer ? size / 2 : size, stream);

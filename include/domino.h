@@ -483,13 +483,15 @@ typedef enum {
  *   mask    [batch, max_q, max_q] device uint8 (DOMINO_MASK_TREE only)
  *   lse     [tokens, n_q_heads] device fp32 out, or NULL
  * Slots that no row sees are not used, whatever they hold; a seen slot's NaN
- * or infinity reaches the rows that see it, as the formula says.
+ * or infinity reaches the rows that see it, as the formula says. A score of -inf
+ * has weight 0; a row whose seen scores are all -inf is like one that sees none.
  * Scores, softmax and sums are fp32; in bf16 the softmax weights are rounded to
  * bf16 for the product with v. scale is finite and not negative.
  * Workspace: domino_block_attention_workspace_bytes(cache, block, n_q_heads)
  * (0 if the arguments are invalid; block's device pointers are not read),
- * zeroed before its first use; each call leaves it ready for the next (after
- * DOMINO_ERR_TIMEOUT it is to be zeroed again). Calls that may overlap need a
+ * zeroed before its first use; each call leaves it ready for the next, of any
+ * shape and type that it is large enough for (after DOMINO_ERR_TIMEOUT it is to
+ * be zeroed again). Calls that may overlap need a
  * workspace each.
  */
 size_t domino_block_attention_workspace_bytes(const domino_kv_cache* cache, const domino_block* block,
@@ -503,7 +505,8 @@ domino_status domino_block_attention(const domino_kv_cache* cache, const domino_
  * row's temperature, tokens ordered by (logit descending, id ascending):
  *   top_k  the first top_k tokens stay (0: all);
  *   top_p  of those, a token stays iff the probability (softmax of logit / T
- *          over the top_k set) before it in the order is below top_p (1: all);
+ *          over the top_k set) before it in the order is below top_p (1: all;
+ *          weights are counted in units of 2^-40 of the largest);
  *   min_p  of those, a token stays iff exp((logit - max logit) / T) >= min_p;
  *   tokens[r] = argmax over what stayed of logit / T + gumbel[r, v], ties to
  *   the lowest id: a draw from softmax(logit / T) over what stayed;

@@ -1,5 +1,5 @@
-"""The bounded waits of the target-side kernels, by reading their source: a wait that runs out must not happen on a GPU
-that others use, so what a kernel does then is held to rules that can be read."""
+"""The bounded waits of the target-side kernels, by reading their source: no test makes one run out on a GPU, so what a kernel
+does then is held to rules that can be read."""
 import os
 import re
 
