@@ -148,7 +148,7 @@ struct Row {
   }
   __device__ __forceinline__ int bin(float d) const {
     const float b = d * scale;
-    return b < (float)kNear ? (int)b : kNear;
+    return b < (float)kNear ? (int)__float2uint_rz(b) : kNear;  // 0 below 0: a logit that has risen under the call
   }
   __device__ __forceinline__ float near_weight(float l) const {  // to 2^-22 and 2^-24 of (max - l) / T
     float w;
@@ -497,12 +497,13 @@ static __device__ __forceinline__ int collect(Smem& s, const S& slice, uint32_t 
   for (uint32_t k = 0; k < size; ++k) sum += s.part_n[k];
   return sum;
 }
-// The CTAs' lists (kList keys at most in all) to CTA 0's, CTA after CTA.
+// The CTAs' lists (kList keys at most in all, unless logits change under the call: the rest is left out then) to CTA 0's,
+// CTA after CTA.
 static __device__ __forceinline__ void join(Smem& s, uint32_t rank) {
   int base = 0;
   for (uint32_t k = 0; k < rank; ++k) base += s.part_n[k];
   if (rank > 0)
-    for (int x = threadIdx.x; x < s.n_local; x += kThr) st_u64(dsmem(&s.list[base + x], 0), s.list[x]);
+    for (int x = threadIdx.x; x < min(s.n_local, kList - base); x += kThr) st_u64(dsmem(&s.list[base + x], 0), s.list[x]);
   cluster_sync();
 }
 

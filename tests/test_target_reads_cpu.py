@@ -34,3 +34,16 @@ def test_whole_units_lie_inside_the_slice():
                     span = 2 * 2
                     if wholes > span and 0 <= q0 - whole0 < wholes - span:
                         assert all(whole0 <= q0 + 2 * j < whole0 + wholes for j in range(3))
+
+
+def test_changing_logits_cannot_lead_past_shared_memory():
+    """The passes over a slice read it again: a logit that has risen above the maximum, or more keys than were counted, must
+    not become an index outside the histogram or the list."""
+    text = source("sample.cu")
+    bins = part(text, "int bin(float d) const {", "}")
+    assert "__float2uint_rz(b)" in bins  # saturates at 0
+    join = part(text, "static __device__ __forceinline__ void join(", "cluster_sync();")
+    assert "x < min(s.n_local, kList - base)" in join
+    collect = part(text, "collect(Smem& s, const S& slice", "return sum;")
+    assert "if (at < kList) s.list[at]" in collect
+    assert "v.key[j] = x < n ? s.list[x] : 0;" in text and "kPer = kList / kThr" in text
