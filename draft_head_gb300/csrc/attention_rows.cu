@@ -274,12 +274,12 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
     const int i = r / G;
     const int64_t row = (int64_t)(q0 + i) * a.hq + h * G + (r - i * G);
     const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN);
-    if (e < a.D)
-      *(uint2*)((__nv_bfloat16*)a.out + row * a.D + e) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+    *(uint2*)((__nv_bfloat16*)a.out + row * a.D + e) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
     if (e == 0 && a.lse) a.lse[row] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
   };
   for (int x = threadIdx.x; x < rows * (DP / 4); x += kThr) {
     const int r = x / (DP / 4), e = (x - r * (DP / 4)) * 4;
+    if (e >= a.D) continue;  // a piece's rows lie head_dim apart in the workspace
     float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][r].x);

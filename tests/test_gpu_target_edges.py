@@ -307,3 +307,29 @@ def test_norm_rope_of_many_fp32_rows(monkeypatch, case):
     """As many rows as take the kernel for many in fp32 too."""
     monkeypatch.setattr(T, "MANY", [case])
     T.test_norm_rope_of_many_rows(0)
+
+
+@pytest.mark.parametrize("D", [8, 24, 40, 56, 64, 72, 80, 96, 104, 120, 128])
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 8, 1), (3, 10, 2), (1, 2, 2), (4, 8, 2)])
+def test_few_rows_in_pieces_at_every_head_size(D, rows, hq, hkv):
+    """Long caches, whose row tiles are cut: the pieces' rows lie behind one another in the workspace and keep to their place,
+    and to the workspace."""
+    g = T.gen(96)
+    ctx = [2700, 900]
+    k, v = T.cache_pair(g, BF, 2, hkv, max(ctx) + rows, D)
+    q = (2 * T.randn(g, 2 * rows, hq, D)).to(BF)
+    p = BlockAttention(k, v, hq, 2 * rows, rows, max(ctx))
+    n = p.ws.numel()
+    ws = torch.full((n + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    ws[:n] = 0
+    out, lse = torch.empty_like(q), torch.empty(2 * rows, hq, device="cuda")
+    past = T.ints(ctx)
+    block = B.block(2 * rows, rows, max(ctx), past)
+    first = None
+    for _ in range(20):
+        B.domino_block_attention(p.cache, block, hq, q, p.scale, B.MASK_CAUSAL, None, 0, 0, out, lse, ws[:n])
+        first = first or (out.clone(), lse.clone())
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert bool((ws[n:] == 0x5a).all()) and B.domino_last_status(ws[:n]) == 0
+    seen = [torch.stack([O.seen_slots("causal", 0, 0, c, rows, i, c + i) for i in range(rows)]) for c in ctx]
+    T.check_attention((BF, [rows] * 2, ctx, hq, hkv, D), q, k, v, p, seen, [0, rows, 2 * rows], out, lse)
