@@ -148,16 +148,21 @@ def _normal(g, *shape):
 # ---------------------------------------------------------------------------
 # The quantised form: codes and the exponent's byte of vectors along the last axis.
 # ---------------------------------------------------------------------------
+def _power(e):
+    """2^e in 64 bits by its fields: a GPU's pow is a unit off for some."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _quantise(x):
     part, power = torch.frexp(x.abs().amax(-1))  # part in [0.5, 1); 448 = 0.875 * 2^9
     e = (power - 9 + (part > 0.875)).clamp(-100, 120)
-    codes = (x * torch.ldexp(torch.ones_like(part), -e)[..., None]).float().to(torch.float8_e4m3fn)
+    codes = (x * _power(-e).to(x.dtype)[..., None]).float().to(torch.float8_e4m3fn)
     return codes, (e + 127).to(torch.uint8)
 
 
 def _values(codes, scale):
     """What codes and scales stand for, in 32 bits (exact)."""
-    return codes.float() * torch.ldexp(torch.ones_like(scale, dtype=torch.float32), scale.int() - 127)[..., None]
+    return codes.float() * _power(scale.int() - 127).float()[..., None]
 
 
 # ---------------------------------------------------------------------------
@@ -487,29 +492,29 @@ def _exact_slots(s, kind, b, n):
     ids = s["table"][b, : (n + page - 1) // page].tolist()
     pages = [s[kind + "_pages"][i].double() for i in ids]
     if s[kind + "_scale"] is not None:
-        pages = [x * torch.pow(2.0, s[kind + "_scale"][i].double() - 127)[..., None] for x, i in zip(pages, ids)]
+        pages = [x * _power(s[kind + "_scale"][i].int() - 127)[..., None] for x, i in zip(pages, ids)]
     return torch.cat(pages, 1)[:, :n]
 
 
 def _nearest_codes(x):
     """Vectors [..., dim] in 64 bits as (the numbers of their codes, their scales): a search through the 127 magnitudes."""
     grid = torch.arange(127, dtype=torch.uint8, device=x.device).view(torch.float8_e4m3fn).double()
-    e = torch.full(x.shape[:-1], -100.0, dtype=torch.float64, device=x.device)
+    e = torch.full(x.shape[:-1], -100, device=x.device)
     most = x.abs().amax(-1)
-    while bool((most > 448 * torch.pow(2.0, e)).any()):
-        e = torch.where(most > 448 * torch.pow(2.0, e), e + 1, e)
-    y = x / torch.pow(2.0, e)[..., None]
+    while bool((most > 448 * _power(e)).any()):
+        e = torch.where(most > 448 * _power(e), e + 1, e)
+    y = x / _power(e)[..., None]
     between = (grid[1:] + grid[:-1]) / 2
     at = torch.bucketize(y.abs(), between)  # a tie goes below it,
     tie = (y.abs() == between[at.clamp(max=125)]) & (at < 126) & (at % 2 == 1)
-    return torch.copysign(grid[at + tie], y), torch.pow(2.0, e)  # or to the even code
+    return torch.copysign(grid[at + tie], y), _power(e)  # or to the even code
 
 
 def _exact_append(c, s):
     hq, hkv, dim, rot, page = c["hq"], c["hkv"], c["dim"], c["rot"], c["page"]
     heads = s["qkv"].double().view(s["tokens"], hq + 2 * hkv, dim)
     pools = {k: s[k + "_pages"].double() for k in "kv"}
-    scales = {k: None if s[k + "_scale"] is None else torch.pow(2.0, s[k + "_scale"].double() - 127) for k in "kv"}
+    scales = {k: None if s[k + "_scale"] is None else _power(s[k + "_scale"].int() - 127) for k in "kv"}
     first = torch.arange(0, rot, 2, device="cuda") if c["pairs"] else torch.arange(rot // 2, device="cuda")
     second = first + 1 if c["pairs"] else first + rot // 2
     out = torch.empty(s["tokens"], hq, dim, dtype=torch.float64, device="cuda")
