@@ -489,7 +489,7 @@ def exact(case, seed):
 def _exact_slots(s, kind, b, n):
     """The first n slots of request b, [hkv, n, dim] in 64 bits."""
     page = s["case"]["page"]
-    ids = s["table"][b, : (n + page - 1) // page].tolist()
+    ids = s["table"][b, : max(1, (n + page - 1) // page)].clamp(min=0).tolist()
     pages = [s[kind + "_pages"][i].double() for i in ids]
     if s[kind + "_scale"] is not None:
         pages = [x * _power(s[kind + "_scale"][i].int() - 127)[..., None] for x, i in zip(pages, ids)]
