@@ -24,7 +24,7 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 STATUS = {0: "DOMINO_OK", 1: "DOMINO_ERR_INVALID_ARG", 2: "DOMINO_ERR_UNSUPPORTED", 3: "DOMINO_ERR_CUDA",
           4: "DOMINO_ERR_TIMEOUT", 5: "DOMINO_ERR_WORKSPACE", 6: "DOMINO_ERR_DEVICE_DATA", 7: "DOMINO_ERR_INDEX"}
 
@@ -38,6 +38,8 @@ EXPORTED = [
     "domino_draft_chain_stats_supported", "domino_draft_chain_stats",
     "domino_verify_sampled_head_workspace_bytes", "domino_verify_sampled_head",
     "domino_qk_norm_rope", "domino_block_attention_workspace_bytes", "domino_block_attention", "domino_sample",
+    "domino_token_logprobs", "domino_paged_append", "domino_paged_read", "domino_paged_attention_workspace_bytes",
+    "domino_paged_attention",
 ]
 
 
@@ -65,6 +67,15 @@ class domino_kv_cache(ctypes.Structure):
 class domino_block(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_ctx", ctypes.c_int32),
                 ("q_start", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
+class domino_paged_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64)]
 
 
 MASK_CAUSAL, MASK_FULL, MASK_TREE = 0, 1, 2
@@ -119,6 +130,13 @@ _sig("domino_qk_norm_rope", _i32, [_CP, _BP, _i32, _vp, _i64, _vp, _i64, _vp, _i
 _sig("domino_block_attention_workspace_bytes", _sz, [_CP, _BP, _i32])
 _sig("domino_block_attention", _i32, [_CP, _BP, _i32, _vp, _f32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp])
 _sig("domino_sample", _i32, [_i32, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp])
+_PP = ctypes.POINTER(domino_paged_cache)
+_sig("domino_token_logprobs", _i32, [_i32, _vp, _i64, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("domino_paged_append", _i32, [_PP, _BP, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _f32, _vp, _i32, _i32,
+                                   _i32, _vp, _vp, _sz, _vp])
+_sig("domino_paged_read", _i32, [_PP, _vp, _vp, _i32, _CP, _vp, _sz, _vp])
+_sig("domino_paged_attention_workspace_bytes", _sz, [_PP, _BP, _i32])
+_sig("domino_paged_attention", _i32, [_PP, _BP, _i32, _vp, _f32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp])
 
 
 def _ptr(t):
@@ -373,3 +391,64 @@ def domino_sample(logits, rows: int, V: int, temperature, top_k, top_p, min_p, g
                              _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(gumbel),
                              V if gumbel_stride is None else gumbel_stride, _ptr(tokens), _ptr(logprob), _ptr(ws),
                              ws.numel() * ws.element_size(), _stream(stream)), "domino_sample")
+
+
+def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> domino_paged_cache:
+    """The struct of a layer's cache in pages from k and v [n_pages, n_kv_heads, page_size, head_dim] of the same strides (any
+    order of the first three axes in memory; the last one contiguous) and page_table [batch, max_pages] int32. float8_e4m3fn
+    pages have k_scale and v_scale, [n_pages, n_kv_heads, page_size] uint8 (or float8_e8m0fnu), contiguous."""
+    if (k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or k.stride(3) != 1 or
+            k.device != v.device):
+        raise ValueError("k and v: [n_pages, n_kv_heads, page_size, head_dim] of one type and the same strides, the last 1, on one "
+                         "device")
+    dt = {torch.bfloat16: BF16, torch.float32: F32, torch.float8_e4m3fn: E4M3}.get(k.dtype)
+    if dt is None:
+        raise ValueError(f"page type {k.dtype}: float8_e4m3fn, bfloat16 or float32")
+    for scale, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if dt != E4M3:
+            if scale is not None:
+                raise ValueError(f"{what}: only float8_e4m3fn pages have scales")
+        elif (scale is None or scale.dtype not in (torch.uint8, torch.float8_e8m0fnu) or scale.shape != k.shape[:3] or
+              not scale.is_contiguous() or scale.device != k.device):
+            raise ValueError(f"{what}: {list(k.shape[:3])} of uint8 or float8_e8m0fnu on {k.device}, contiguous")
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or page_table.shape[1] == 0 or
+            page_table.device != k.device):
+        raise ValueError(f"page_table: [batch, max_pages] of int32 on {k.device}, its rows contiguous")
+    p, h, s, d = k.shape
+    return domino_paged_cache(dt, page_table.shape[0], h, d, p, s, page_table.shape[1], _ptr(k), _ptr(v), k.stride(0), k.stride(1),
+                              k.stride(2), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), page_table.stride(0))
+
+
+def domino_paged_append(cache: domino_paged_cache, rows: domino_block, n_q_heads: int, q, q_stride: int, k, k_stride: int, v,
+                        v_stride: int, norm: bool, q_weight, k_weight, eps: float, rope, max_pos: int, rot_dim: int,
+                        interleaved: bool, q_out, ws, stream=None):
+    _check(lib.domino_paged_append(ctypes.byref(cache), ctypes.byref(rows), n_q_heads, _ptr(q), q_stride, _ptr(k), k_stride,
+                                   _ptr(v), v_stride, int(norm), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(rope), max_pos,
+                                   rot_dim, int(interleaved), _ptr(q_out), _ptr(ws), ws.numel() * ws.element_size(),
+                                   _stream(stream)), "domino_paged_append")
+
+
+def domino_paged_read(cache: domino_paged_cache, first, count, max_count: int, out: domino_kv_cache, ws, stream=None):
+    _check(lib.domino_paged_read(ctypes.byref(cache), _ptr(first), _ptr(count), max_count, ctypes.byref(out), _ptr(ws),
+                                 ws.numel() * ws.element_size(), _stream(stream)), "domino_paged_read")
+
+
+def domino_paged_attention_workspace_bytes(cache: domino_paged_cache, rows: domino_block, n_q_heads: int) -> int:
+    return lib.domino_paged_attention_workspace_bytes(ctypes.byref(cache), ctypes.byref(rows), n_q_heads)
+
+
+def domino_paged_attention(cache: domino_paged_cache, rows: domino_block, n_q_heads: int, q, scale: float, mask_mode: int, mask,
+                           window: int, sinks: int, out, lse, ws, stream=None):
+    _check(lib.domino_paged_attention(ctypes.byref(cache), ctypes.byref(rows), n_q_heads, _ptr(q), float(scale), mask_mode,
+                                      _ptr(mask), window, sinks, _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
+                                      _stream(stream)), "domino_paged_attention")
+
+
+def domino_token_logprobs(logits, rows: int, V: int, tokens, temperature, top_n: int, logprob, rank, entropy, lse, top_ids,
+                          top_logprob, ws, stream=None, logits_stride=None):
+    """logits: bfloat16 or float32; the row stride defaults to V."""
+    dt = BF16 if logits.dtype == torch.bfloat16 else F32
+    _check(lib.domino_token_logprobs(dt, _ptr(logits), V if logits_stride is None else logits_stride, rows, V, _ptr(tokens),
+                                     _ptr(temperature), top_n, _ptr(logprob), _ptr(rank), _ptr(entropy), _ptr(lse),
+                                     _ptr(top_ids), _ptr(top_logprob), _ptr(ws), ws.numel() * ws.element_size(),
+                                     _stream(stream)), "domino_token_logprobs")

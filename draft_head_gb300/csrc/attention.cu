@@ -1,6 +1,6 @@
-// Attention of a block's rows over the cache (domino_block_attention; the
-// definition is in domino.h): the kernel on CUDA cores, for fp32 and for every
-// head size.
+// Attention of a block's rows over the cache (domino_block_attention and
+// domino_paged_attention; the definitions are in domino.h): the kernel on CUDA cores, for
+// fp32 and for every head size.
 //
 // One pass over the keys with the running maximum m and sum l of the softmax:
 // per key tile s = scale q.k, m' = max(m, s), o = o 2^(m - m') + 2^(s - m') v
@@ -17,9 +17,11 @@
 // by one). Prompts: bound by shared memory (six 16-byte reads for 16 packed multiply-adds of the scores). 2000
 // rows: 8 heads of 128 in fp32 666 us, 8 heads of 256 in bf16 1348 us, 12 TFLOP/s both.
 #include <math.h>
+#include <algorithm>
 
 #include "attention.cuh"
 #include "packed.cuh"
+#include "pages.cuh"
 
 namespace domino {
 
@@ -43,7 +45,18 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
                      __uint_as_float(u.y & 0xffff0000u));
 }
 
-template <typename T>
+// Four elements of slot s of kv head h of request b; zeros where its page is not there (`page` < 0).
+template <typename T, int CACHE>
+__device__ __forceinline__ float4 slot4(const AttnArgs& a, const void* kv, const uint8_t* scale, int page, int h, int s, int e) {
+  if (page < 0) return make_float4(0, 0, 0, 0);
+  const int64_t at = (int64_t)page * a.pages.page_stride + (int64_t)h * a.hs + (int64_t)slot_in_page(a.pages, s) * a.ss + e;
+  if (CACHE == kPaged) return load4((const T*)kv + at);
+  const float4 x = codes_f32(*(const uint32_t*)((const uint8_t*)kv + at));
+  const float f = scale_f32(scale[scale_at(a.pages, a.hkv, page, h, s)]);
+  return make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+}
+
+template <typename T, int CACHE>
 __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__ SimtP p) {
   extern __shared__ float sm[];
   __shared__ int s_last;
@@ -124,8 +137,15 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
     each(kBN, [&](int r, int e) {
       // Slots past the request's rows are not read.
       const bool in = s0 + r < ctx + n;
-      *(float4*)(sk + r * ldq + e) = in ? load4(kb + (int64_t)(s0 + r) * a.ss + e) : make_float4(0, 0, 0, 0);
-      *(float4*)(sv + r * D + e) = in ? load4(vb + (int64_t)(s0 + r) * a.ss + e) : make_float4(0, 0, 0, 0);
+      if (CACHE == kWhole) {
+        *(float4*)(sk + r * ldq + e) = in ? load4(kb + (int64_t)(s0 + r) * a.ss + e) : make_float4(0, 0, 0, 0);
+        *(float4*)(sv + r * D + e) = in ? load4(vb + (int64_t)(s0 + r) * a.ss + e) : make_float4(0, 0, 0, 0);
+      } else {
+        const int page = in ? page_of(a.pages, b, s0 + r) : -1;
+        if (in && page < 0 && e == 0) dev_error(a.ctl, DEV_ERR_DATA);
+        *(float4*)(sk + r * ldq + e) = slot4<T, CACHE>(a, a.k, a.pages.k_scale, page, h, s0 + r, e);
+        *(float4*)(sv + r * D + e) = slot4<T, CACHE>(a, a.v, a.pages.v_scale, page, h, s0 + r, e);
+      }
     });
     __syncthreads();
     const bool whole = s0 + kBN <= all_hi && (s0 >= all_low || s0 + kBN <= a.sinks);
@@ -311,13 +331,14 @@ int simt_row_tiles(const AttnArgs& a) {
 size_t attn_ws_bytes(const AttnArgs& a) {
   const size_t simt = partial_bytes(simt_want(), kBM, a.D);
   if (a.dtype != DOMINO_BF16 || a.D > 128) return simt;
-  const size_t rows = attn_rows_ws_bytes(a), rest = attn_tc_applies(a) ? attn_tc_ws_bytes(a) : simt;
-  return rows > rest ? rows : rest;
+  const size_t rows = attn_rows_ws_bytes(a), tc = attn_tc_ws_bytes(a);
+  if (a.cache != kWhole) return std::max(simt, std::max(rows, tc));
+  return std::max(rows, attn_tc_applies(a) ? tc : simt);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
-  if (attn_rows_applies(a)) return launch_attention_rows(a, stream);
-  if (attn_tc_applies(a)) return launch_attention_tc(a, stream);
+  if (a.cache == kWhole && attn_rows_applies(a)) return launch_attention_rows(a, stream);
+  if (a.cache == kWhole && attn_tc_applies(a)) return launch_attention_tc(a, stream);
   SimtP p;
   p.a = a;
   p.row_tiles = simt_row_tiles(a);
@@ -326,15 +347,19 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
   p.part = partials_at(a.scratch, simt_want(), kBM);
   const size_t smem = sizeof(float) * (kBM * (a.D + 4) + kBN * (a.D + 4) + kBN * a.D + kBM * (kBN + 1)) + 8 * kBM;
   const dim3 grid((unsigned)(p.row_tiles * p.splits), (unsigned)a.hkv, (unsigned)a.rows.batch);
-  static FuncOnce once_bf16, once_f32;
-  const cudaError_t e = a.dtype == DOMINO_BF16 ? once_bf16.set((const void*)attn_simt_kernel<__nv_bfloat16>, 120 * 1024, false)
-                                               : once_f32.set((const void*)attn_simt_kernel<float>, 120 * 1024, false);
-  if (e != cudaSuccess) return e;
-  if (a.dtype == DOMINO_BF16)
-    attn_simt_kernel<__nv_bfloat16><<<grid, kThr, smem, stream>>>(p);
-  else
-    attn_simt_kernel<float><<<grid, kThr, smem, stream>>>(p);
-  return cudaGetLastError();
+  auto run = [&](auto kernel, FuncOnce& once) {
+    const cudaError_t e = once.set((const void*)kernel, 120 * 1024, false);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThr, smem, stream>>>(p);
+    return cudaGetLastError();
+  };
+  static FuncOnce once_bf16, once_f32, once_paged_bf16, once_paged_f32, once_e4m3;
+  if (a.cache == kPagedE4m3) return run(attn_simt_kernel<__nv_bfloat16, kPagedE4m3>, once_e4m3);
+  if (a.cache == kPaged)
+    return a.dtype == DOMINO_BF16 ? run(attn_simt_kernel<__nv_bfloat16, kPaged>, once_paged_bf16)
+                                  : run(attn_simt_kernel<float, kPaged>, once_paged_f32);
+  return a.dtype == DOMINO_BF16 ? run(attn_simt_kernel<__nv_bfloat16, kWhole>, once_bf16)
+                                : run(attn_simt_kernel<float, kWhole>, once_f32);
 }
 
 }  // namespace domino

@@ -194,6 +194,13 @@ struct RowsArgs {
   const int32_t* ctx_len;
   const int32_t* positions;
 };
+// Where the slots of a cache in pages lie (domino_paged_cache).
+struct PagesArgs {
+  const int32_t* table;  // [batch] rows, table_stride apart
+  int64_t table_stride, page_stride;
+  int n_pages, shift;  // 2^shift slots in a page
+  uint8_t *k_scale, *v_scale;
+};
 struct NormRopeArgs {
   RowsArgs rows;
   int dtype, hq, hkv, D, rot, interleaved, max_pos;
@@ -205,8 +212,11 @@ struct NormRopeArgs {
   void *q_out, *k_cache, *v_cache;
   int64_t rs, hs, ss;  // cache strides: request, head, slot
   Ctl* ctl;
+  PagesArgs pages;  // launch_paged_append only
+  int e4m3, norm;
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_append(const NormRopeArgs& a, cudaStream_t stream);
 
 struct AttnArgs {
   RowsArgs rows;
@@ -220,6 +230,8 @@ struct AttnArgs {
   float* lse;
   Ctl* ctl;
   void* scratch;  // behind the control block
+  int cache;      // kWhole, kPaged, kPagedE4m3 (pages.cuh)
+  PagesArgs pages;
 };
 size_t attn_ws_bytes(const AttnArgs& a);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
@@ -231,6 +243,34 @@ cudaError_t launch_attention_rows(const AttnArgs& a, cudaStream_t stream);
 bool attn_tc_applies(const AttnArgs& a);
 size_t attn_tc_ws_bytes(const AttnArgs& a);
 cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t stream);
+
+struct PagedReadArgs {
+  int dtype, e4m3, batch, hkv, D, capacity, max_count;
+  const int32_t *first, *count;
+  const void *k, *v;
+  int64_t hs, ss;
+  PagesArgs pages;
+  void *k_out, *v_out;
+  int out_capacity;
+  int64_t out_rs, out_hs, out_ss;
+  Ctl* ctl;
+};
+cudaError_t launch_paged_read(const PagedReadArgs& a, cudaStream_t stream);
+
+struct ScoreArgs {
+  int dtype, rows, V, top_n;
+  const void* logits;
+  int64_t ls;
+  const int32_t* tokens;
+  const float* temperature;
+  float* logprob;
+  int32_t* rank;
+  float *entropy, *lse;
+  int32_t* top_ids;
+  float* top_logprob;
+  Ctl* ctl;
+};
+cudaError_t launch_score(const ScoreArgs& a, cudaStream_t stream);
 
 struct SampleArgs {
   int dtype, rows, V;

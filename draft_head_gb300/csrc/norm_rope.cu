@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "packed.cuh"
+#include "pages.cuh"
 #include "rows.cuh"
 #include "waits.cuh"
 
@@ -101,7 +102,7 @@ struct Raw8<__nv_bfloat16> {
 enum { kPairs = 0, kHalves = 1, kHalvesShared = 2 };
 
 // What a lane does with its eight places of a head.
-template <typename T, int MODE, int kWidth>
+template <typename T, int MODE, int kWidth, int CACHE>
 struct Places {
   const NormRopeArgs& a;
   const int e0, half;
@@ -177,7 +178,13 @@ struct Places {
   // z = rstd (x (w c) + x' (w' s)), x' the partner. (An infinity makes rstd 0 and a NaN makes it a
   // NaN, so that a partner's value times 0 adds nothing to what the head's own values do.)
   __device__ __forceinline__ void turn(Raw8<T>& v, bool on, T* dst) {
-    float2 z[4], y[4];
+    float2 z[4];
+    turned(v, on, z);
+    v.set(z);
+    if (on) v.store(dst);
+  }
+  __device__ __forceinline__ void turned(Raw8<T>& v, bool on, float2 (&z)[4]) {
+    float2 y[4];
     if (!on) v.zero();
     v.get(z);
     float2 sq = mul2(z[0], z[0]);
@@ -186,7 +193,7 @@ struct Places {
     float ss = sq.x + sq.y;
 #pragma unroll
     for (int o = kWidth / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float rstd = rsqrtf(ss * inv_d + a.eps);
+    const float rstd = CACHE == kWhole || a.norm ? rsqrtf(ss * inv_d + a.eps) : 1.0f;
     if (MODE == kPairs) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = make_float2(z[e].y, z[e].x);
@@ -206,11 +213,59 @@ struct Places {
       for (int e = 0; e < 4; ++e)
         y[e] = on ? make_float2(x[partner_of(e0 + 2 * e)], x[partner_of(e0 + 2 * e + 1)]) : make_float2(0, 0);
     }
+    if (CACHE != kWhole) {  // without the norm, an infinity that does not turn stays one
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e0 + 2 * e >= a.rot) y[e] = make_float2(0, 0);
+    }
     const float2 r2 = make_float2(rstd, rstd);
 #pragma unroll
     for (int e = 0; e < 4; ++e) z[e] = mul2(r2, fma2(z[e], wc[e], mul2(y[e], ws[e])));
-    v.set(z);
-    if (on) v.store(dst);
+  }
+  // A head's vector as codes and their scale (pages.cuh).
+  __device__ __forceinline__ void store_codes(const float2 (&z)[4], bool on, uint8_t* dst, uint8_t* scale) const {
+    uint32_t most = 0;
+    if (on) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) most = max(most, max(__float_as_uint(z[e].x) & 0x7fffffffu, __float_as_uint(z[e].y) & 0x7fffffffu));
+    }
+#pragma unroll
+    for (int o = kWidth / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (!on) return;
+    const int byte = scale_byte(most);
+    const float f = scale_inverse(byte);
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = byte == kScaleNan ? 0u : pack_e4m3(z[e].x * f, z[e].y * f);
+    *(uint2*)dst = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    if (e0 == 0) *scale = (uint8_t)byte;
+  }
+  // A key head, and a value head as it is, into the cache: `slot` is the row's place there (elements, with e0), page and
+  // s where that is.
+  __device__ __forceinline__ void cache_kv(Raw8<T>& xk, const Raw8<T>& xv, bool on, int h, int64_t slot, int page, int s) {
+    const int64_t at = slot + (int64_t)h * a.hs;
+    if (CACHE == kPagedE4m3) {
+      const int64_t to = scale_at(a.pages, a.hkv, page, h, s);
+      float2 z[4];
+      xv.get(z);
+      store_codes(z, on, (uint8_t*)a.v_cache + at, a.pages.v_scale + to);
+      turned(xk, on, z);
+      store_codes(z, on, (uint8_t*)a.k_cache + at, a.pages.k_scale + to);
+    } else {
+      if (on) xv.store((T*)a.v_cache + at);
+      turn(xk, on, (T*)a.k_cache + at);
+    }
+  }
+  // The row's place in the cache: false where its page is not there.
+  __device__ __forceinline__ bool place(int b, int s, int64_t& slot, int& page) const {
+    if (CACHE == kWhole) {
+      page = 0;
+      slot = (int64_t)b * a.rs + (int64_t)s * a.ss + e0;
+      return true;
+    }
+    page = page_of(a.pages, b, s);
+    slot = (int64_t)page * a.pages.page_stride + (int64_t)slot_in_page(a.pages, s) * a.ss + e0;
+    return page >= 0;
   }
 };
 
@@ -223,13 +278,13 @@ __device__ __forceinline__ void read_weights(const NormRopeArgs& a, float* s_w) 
 }
 
 // Few rows: one or two per CTA, or the heads of one over several. (Also rows too long for the other kernel's ring.)
-template <typename T, int MODE, int kWidth>
+template <typename T, int MODE, int kWidth, int CACHE>
 __global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRopeArgs a, int chunk) {
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // q heads in flight, beside one of k and one of v
   extern __shared__ __align__(16) float s_w[];    // [2][D] weights; kHalvesShared: [groups][D] heads
   constexpr int groups = kNrThreads / kWidth;
   const int group = threadIdx.x / kWidth;
-  Places<T, MODE, kWidth> at(a, s_w + 2 * a.D + group * a.D);
+  Places<T, MODE, kWidth, CACHE> at(a, s_w + 2 * a.D + group * a.D);
   const bool live = at.live;
   const int e0 = at.e0, first = blockIdx.y * groups + group, step = groups * gridDim.y;
   // Loops over heads have the same bounds for the whole block: every lane meets every shuffle.
@@ -258,20 +313,19 @@ __global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRope
   __syncthreads();
   while (true) {
     const int pos = !mine ? 0 : a.rows.positions ? a.rows.positions[t] : ctx + i;
-    const bool placed = mine && (a.rot == 0 || (pos >= 0 && pos < a.max_pos));
+    int64_t slot = 0;
+    int page = 0;
+    const bool placed = mine && (a.rot == 0 || (pos >= 0 && pos < a.max_pos)) && at.place(b, ctx + i, slot, page);
     if (mine && !placed && threadIdx.x == 0) dev_error(a.ctl, DEV_ERR_DATA);
     if (placed) {
       float raw[16];
       at.read_angles(pos, raw);
       at.set_angles(raw);
-      const int64_t slot = (int64_t)b * a.rs + (int64_t)(ctx + i) * a.ss + e0;
       at.weigh(s_w + a.D);
       for (int h0 = first_u; h0 < a.hkv; h0 += step) {
         const int h = h0 + group;
         if (h0 > first_u) fetch_kv(h);
-        const bool on = live && h < a.hkv;
-        if (on) xv.store((T*)a.v_cache + slot + (int64_t)h * a.hs);
-        at.turn(xk, on, (T*)a.k_cache + slot + (int64_t)h * a.hs);
+        at.cache_kv(xk, xv, live && h < a.hkv, h, slot, page, ctx + i);
       }
       at.weigh(s_w);
       T* q_out = (T*)a.q_out + (int64_t)t * a.hq * a.D + e0;
@@ -297,14 +351,14 @@ __global__ void __launch_bounds__(kNrThreads, 5) norm_rope_kernel(const NormRope
 
 // Many rows: a CTA takes a run of rows, which bulk copies bring to a ring of `stages` rows in shared memory while
 // earlier ones are worked on; a row's angles are read one row ahead.
-template <typename T, int MODE, int kWidth>
+template <typename T, int MODE, int kWidth, int CACHE>
 __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(const NormRopeArgs a, int chunk, int stages, uint64_t timeout_ns) {
   constexpr int kBatch = 4;
   extern __shared__ __align__(16) float s_w[];  // [2][D] weights; kHalvesShared: [groups][D] heads; rows
   __shared__ __align__(8) uint64_t full[kMostStages];
   constexpr int groups = kNrThreads / kWidth;
   const int group = threadIdx.x / kWidth;
-  Places<T, MODE, kWidth> at(a, s_w + 2 * a.D + group * a.D);
+  Places<T, MODE, kWidth, CACHE> at(a, s_w + 2 * a.D + group * a.D);
   const bool live = at.live;
   const int e0 = at.e0;
   T* ring = (T*)(s_w + (2 + (MODE == kHalvesShared ? groups : 0)) * a.D);
@@ -326,10 +380,14 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
   report_requests(a.rows, a.ctl);
   int b, i, ctx, rows;
   bool mine, placed;
+  int64_t slot = 0;  // the row's place in the cache
+  int page = 0, s = 0;
   float raw[16];
   auto look = [&](int t) {  // the row's place and angles
     const int pos = !mine ? 0 : a.rows.positions ? __ldg(a.rows.positions + t) : ctx + i;
     placed = mine && (a.rot == 0 || (pos >= 0 && pos < a.max_pos));
+    s = ctx + i;
+    if (placed) placed = at.place(b, s, slot, page);
     if (mine && !placed && threadIdx.x == 0) dev_error(a.ctl, DEV_ERR_DATA);
     if (placed) at.read_angles(pos, raw);
   };
@@ -341,8 +399,9 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
   bool ok = true;
   int t = t0;
   for (; t < t_end; ++t) {
-    const int64_t slot = (int64_t)b * a.rs + (int64_t)(ctx + i) * a.ss + e0;
     const bool on_row = placed;
+    const int64_t row_slot = slot;
+    const int row_page = page, row_s = s;
     if (on_row) at.set_angles(raw);
     if (t + 1 < t_end) {
       if (mine && i + 1 < rows)
@@ -363,9 +422,8 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
         if (on) {
           xk.load(x + nq + h * a.D);
           xv.load(x + nq + nk + h * a.D);
-          xv.store((T*)a.v_cache + slot + (int64_t)h * a.hs);
         }
-        at.turn(xk, on, (T*)a.k_cache + slot + (int64_t)h * a.hs);
+        at.cache_kv(xk, xv, on, h, row_slot, row_page, row_s);
       }
       at.weigh(s_w);
       T* q_out = (T*)a.q_out + (int64_t)t * nq + e0;
@@ -399,8 +457,8 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
     }
 }
 
-template <typename T, int MODE>
-cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
+template <typename T, int MODE, int CACHE>
+cudaError_t launch_on(const NormRopeArgs& a, cudaStream_t stream) {
   // Lanes per head: 8 (a head of up to 64), 16 or 32.
   const int width = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, groups = kNrThreads / width;
   const int rounds = ((a.hq > a.hkv ? a.hq : a.hkv) + groups - 1) / groups;
@@ -423,31 +481,45 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
       return cudaGetLastError();
     };
     static FuncOnce once8, once16, once32;
-    if (width == 8) return run(norm_rope_run_kernel<T, MODE, 8>, once8);
-    if (width == 16) return run(norm_rope_run_kernel<T, MODE, 16>, once16);
-    return run(norm_rope_run_kernel<T, MODE, 32>, once32);
+    if (width == 8) return run(norm_rope_run_kernel<T, MODE, 8, CACHE>, once8);
+    if (width == 16) return run(norm_rope_run_kernel<T, MODE, 16, CACHE>, once16);
+    return run(norm_rope_run_kernel<T, MODE, 32, CACHE>, once32);
   }
   const dim3 grid((unsigned)((a.rows.tokens + chunk - 1) / chunk),
                   (int64_t)a.rows.tokens * rounds <= 2 * num_sms() ? (unsigned)rounds : 1u);
   if (width == 8)
-    norm_rope_kernel<T, MODE, 8><<<grid, kNrThreads, smem, stream>>>(a, chunk);
+    norm_rope_kernel<T, MODE, 8, CACHE><<<grid, kNrThreads, smem, stream>>>(a, chunk);
   else if (width == 16)
-    norm_rope_kernel<T, MODE, 16><<<grid, kNrThreads, smem, stream>>>(a, chunk);
+    norm_rope_kernel<T, MODE, 16, CACHE><<<grid, kNrThreads, smem, stream>>>(a, chunk);
   else
-    norm_rope_kernel<T, MODE, 32><<<grid, kNrThreads, smem, stream>>>(a, chunk);
+    norm_rope_kernel<T, MODE, 32, CACHE><<<grid, kNrThreads, smem, stream>>>(a, chunk);
   return cudaGetLastError();
 }
 
+template <typename T, int MODE>
+cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
+  return launch_on<T, MODE, kWhole>(a, stream);
+}
 template <typename T>
 cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
   if (a.interleaved) return launch<T, kPairs>(a, stream);
   return a.rot % 16 == 0 ? launch<T, kHalves>(a, stream) : launch<T, kHalvesShared>(a, stream);
+}
+template <typename T, int CACHE>
+cudaError_t launch_paged(const NormRopeArgs& a, cudaStream_t stream) {
+  if (a.interleaved) return launch_on<T, kPairs, CACHE>(a, stream);
+  return a.rot % 16 == 0 ? launch_on<T, kHalves, CACHE>(a, stream) : launch_on<T, kHalvesShared, CACHE>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
   return a.dtype == DOMINO_BF16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
+}
+
+cudaError_t launch_paged_append(const NormRopeArgs& a, cudaStream_t stream) {
+  if (a.e4m3) return launch_paged<__nv_bfloat16, kPagedE4m3>(a, stream);
+  return a.dtype == DOMINO_BF16 ? launch_paged<__nv_bfloat16, kPaged>(a, stream) : launch_paged<float, kPaged>(a, stream);
 }
 
 }  // namespace domino

@@ -1,11 +1,13 @@
 """The target's side of a cycle: one attention layer's cache with the calls that
-fill and read it for a drafted block (BlockAttention), and the draw from the
-target's logits (Sampler). Buffer ownership and argument marshalling only; every
+fill and read it for a drafted block, in one piece per request (BlockAttention) or
+in pages (PagedAttention), the draw from the target's logits (Sampler) and what they
+say of given tokens (TokenScorer). Buffer ownership and argument marshalling only; every
 computation runs in libdomino's kernels.
 """
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -21,6 +23,14 @@ def _need(t, dtype, count: int, device: int, what: str):
                          f"on {t.device}")
 
 
+def _run(call, ordinal: int, *args) -> int:
+    """A call of the library on its arrays' device, on torch's current stream there."""
+    if torch.cuda.current_device() == ordinal:
+        return call(*args, B._stream(None))
+    with torch.cuda.device(ordinal):
+        return call(*args, B._stream(None))
+
+
 def rope_table(positions: int, rot_dim: int, base: float = 1e6, device="cuda") -> torch.Tensor:
     """The rotation table domino_qk_norm_rope reads, [positions, rot_dim] fp32: the cosines of pos * base^(-2j / rot_dim)
     for j < rot_dim / 2, then the sines (angles in 64 bits)."""
@@ -29,24 +39,16 @@ def rope_table(positions: int, rot_dim: int, base: float = 1e6, device="cuda") -
     return torch.cat([a.cos(), a.sin()], dim=1).float().contiguous()
 
 
-class BlockAttention:
-    """One attention layer of the target (or of the draft backbone) over its cache.
+class _Attention:
+    """What the layers share: buffers, the checks of a call's arrays, and the calls. `lib`: the library's functions that append and
+    attend, by name; `norm`: arguments of the first one in front of the weights."""
 
-    k_cache, v_cache: [batch, n_kv_heads, capacity, head_dim], bfloat16 or float32, the same strides (any order of the
-    first three axes in memory), on one device with every other array of a call. max_tokens / max_q / max_ctx bound the packed rows of a call, a request's rows and its
-    past. scale defaults to head_dim ** -0.5; window 0 is the whole past. rope: a rotation table [max_pos, rot_dim]
-    (rope_table), float32; q_weight, k_weight: the norms' weights [head_dim], of the cache's type. Rows are packed request after request; q_start
-    [batch + 1] int32 says where each begins (None: every request has max_q rows), ctx_len [batch] int32 how many slots
-    are in use, positions [tokens] int32 where each row is (None: behind the past)."""
-
-    def __init__(self, k_cache, v_cache, n_q_heads: int, max_tokens: int, max_q: int, max_ctx: int, window: int = 0,
-                 sinks: int = 0, scale=None, rope=None, q_weight=None, k_weight=None, eps: float = 1e-6,
-                 interleaved: bool = False):
-        self.cache = B.kv_cache(k_cache, v_cache)
-        self.k_cache, self.v_cache = k_cache, v_cache
+    def _set_up(self, cache, device, dtype, lib, n_q_heads, max_tokens, max_q, max_ctx, window, sinks, scale, rope, q_weight, k_weight,
+                eps, interleaved, norm=()):
+        self.cache = cache
         self.hq, self.hkv, self.dim = n_q_heads, self.cache.n_kv_heads, self.cache.head_dim
-        self.dev, self.dtype = k_cache.device, k_cache.dtype
-        self.ordinal = k_cache.get_device()
+        self.dev, self.dtype = device, dtype
+        self.ordinal = device.index if device.type == "cuda" else -1
         self.max_tokens, self.max_q, self.max_ctx = max_tokens, max_q, max_ctx
         self.window, self.sinks = window, sinks
         self.scale = float(self.dim ** -0.5 if scale is None else scale)
@@ -59,17 +61,19 @@ class BlockAttention:
             _need(rope, torch.float32, 0, self.ordinal, "rope")
         self.rope, self.q_weight, self.k_weight = rope, q_weight, k_weight
         self.eps, self.interleaved = float(eps), int(interleaved)
+        self._append, self._attend = lib
         self.rows = B.block(max_tokens, max_q, max_ctx, None)
-        self.ws = B.workspace(B.domino_block_attention_workspace_bytes(self.cache, self.rows, n_q_heads), self.dev)
+        self.ws = B.workspace(getattr(B, self._attend + "_workspace_bytes")(self.cache, self.rows, n_q_heads), self.dev)
         self.q = torch.empty(max_tokens, n_q_heads, self.dim, dtype=self.dtype, device=self.dev)
         self.out = torch.empty_like(self.q)
         self.lse = torch.empty(max_tokens, n_q_heads, dtype=torch.float32, device=self.dev)
         # Arguments that stay the same from call to call, marshalled once.
         self._refs = (ctypes.byref(self.cache), ctypes.byref(self.rows))
         self._ws = (self.ws.data_ptr(), self.ws.numel())
-        self._norm = (B._ptr(q_weight), B._ptr(k_weight), self.eps, B._ptr(rope), 0 if rope is None else rope.shape[0],
+        self._norm = (*norm, B._ptr(q_weight), B._ptr(k_weight), self.eps, B._ptr(rope), 0 if rope is None else rope.shape[0],
                       0 if rope is None else rope.shape[1], self.interleaved, self.q.data_ptr(), *self._ws)
         self._out = (self.out.data_ptr(), self.lse.data_ptr())
+        self._calls = (getattr(B.lib, self._append), getattr(B.lib, self._attend))
 
     def _set_rows(self, tokens: int, ctx_len, q_start, positions):
         if tokens > self.max_tokens:
@@ -98,10 +102,10 @@ class BlockAttention:
         self._set_rows(tokens, ctx_len, q_start, positions)
         p, stride, size = qkv.data_ptr(), qkv.stride(0), qkv.element_size()
         k = p + self.hq * self.dim * size
-        st = B.lib.domino_qk_norm_rope(*self._refs, self.hq, p, stride, k, stride, k + self.hkv * self.dim * size, stride,
-                                       *self._norm, B._stream(None))
+        st = _run(self._calls[0], self.ordinal, *self._refs, self.hq, p, stride, k, stride, k + self.hkv * self.dim * size, stride,
+                  *self._norm)
         if st:
-            raise B.DominoError(st, "domino_qk_norm_rope")
+            raise B.DominoError(st, self._append)
         return self.q if tokens == self.max_tokens else self.q[:tokens]
 
     def attend(self, q, ctx_len, q_start=None, positions=None, mask="causal", want_lse: bool = False):
@@ -122,13 +126,117 @@ class BlockAttention:
             if mask.dim() == 0 or mask.shape[-1] != n:
                 raise ValueError(f"mask: [{batch}, {n}, {n}], not {tuple(mask.shape)}")
             _need(mask, torch.uint8, batch * n * n, self.ordinal, "mask")
-        st = B.lib.domino_block_attention(*self._refs, self.hq, q.data_ptr(), self.scale, mode, mask_ptr, self.window,
-                                          self.sinks, self._out[0], self._out[1] if want_lse else None, *self._ws,
-                                          B._stream(None))
+        st = _run(self._calls[1], self.ordinal, *self._refs, self.hq, q.data_ptr(), self.scale, mode, mask_ptr, self.window,
+                  self.sinks, self._out[0], self._out[1] if want_lse else None, *self._ws)
         if st:
-            raise B.DominoError(st, "domino_block_attention")
+            raise B.DominoError(st, self._attend)
         out, lse = (self.out, self.lse) if tokens == self.max_tokens else (self.out[:tokens], self.lse[:tokens])
         return (out, lse) if want_lse else out
+
+    def last_status(self) -> int:
+        return B.domino_last_status(self.ws)
+
+
+class BlockAttention(_Attention):
+    """One attention layer of the target (or of the draft backbone) over its cache.
+
+    k_cache, v_cache: [batch, n_kv_heads, capacity, head_dim], bfloat16 or float32, the same strides (any order of the
+    first three axes in memory), on one device with every other array of a call. max_tokens / max_q / max_ctx bound the packed rows of a call, a request's rows and its
+    past. scale defaults to head_dim ** -0.5; window 0 is the whole past. rope: a rotation table [max_pos, rot_dim]
+    (rope_table), float32; q_weight, k_weight: the norms' weights [head_dim], of the cache's type. Rows are packed request after request; q_start
+    [batch + 1] int32 says where each begins (None: every request has max_q rows), ctx_len [batch] int32 how many slots
+    are in use, positions [tokens] int32 where each row is (None: behind the past)."""
+
+    def __init__(self, k_cache, v_cache, n_q_heads: int, max_tokens: int, max_q: int, max_ctx: int, window: int = 0,
+                 sinks: int = 0, scale=None, rope=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False):
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self._set_up(B.kv_cache(k_cache, v_cache), k_cache.device, k_cache.dtype, ("domino_qk_norm_rope", "domino_block_attention"),
+                     n_q_heads, max_tokens, max_q, max_ctx, window, sinks, scale, rope, q_weight, k_weight, eps, interleaved)
+
+
+class PagedAttention(_Attention):
+    """The same over a cache in pages.
+
+    k_pages, v_pages: [n_pages, n_kv_heads, page_size, head_dim], bfloat16, float32 or float8_e4m3fn, the same strides (any order
+    of the first three axes in memory); page_size a power of two from 16 to 4096. float8_e4m3fn pages have k_scale and v_scale,
+    [n_pages, n_kv_heads, page_size] uint8 (or float8_e8m0fnu), a power of two for each head's vector of a slot; their queries, new
+    keys and values and outputs are bfloat16. page_table [batch, max_pages] int32: where slots [page_size j, page_size (j + 1)) of a
+    request are, in place from call to call; entries that no slot of a call needs are not read. norm=False: keys and queries are
+    rotated without a norm. The rest is as for BlockAttention."""
+
+    def __init__(self, k_pages, v_pages, page_table, n_q_heads: int, max_tokens: int, max_q: int, max_ctx: int, k_scale=None,
+                 v_scale=None, window: int = 0, sinks: int = 0, scale=None, rope=None, norm: bool = True, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, interleaved: bool = False):
+        cache = B.paged_cache(k_pages, v_pages, page_table, k_scale, v_scale)
+        self.k_pages, self.v_pages, self.page_table, self.k_scale, self.v_scale = k_pages, v_pages, page_table, k_scale, v_scale
+        if not B.domino_paged_attention_workspace_bytes(cache, B.block(max_tokens, max_q, max_ctx, None), n_q_heads):
+            raise ValueError(f"pages of {k_pages.shape[2]} slots, {n_q_heads} over {k_pages.shape[1]} heads of {k_pages.shape[3]}, "
+                             f"{max_tokens} rows of at most {max_q} behind {max_ctx}: not supported")
+        if not norm and (q_weight is not None or k_weight is not None):
+            raise ValueError("q_weight, k_weight: weights of a norm")
+        dtype = torch.bfloat16 if cache.dtype == B.E4M3 else k_pages.dtype
+        self._set_up(cache, k_pages.device, dtype, ("domino_paged_append", "domino_paged_attention"), n_q_heads, max_tokens, max_q,
+                     max_ctx, window, sinks, scale, rope, q_weight, k_weight, eps, interleaved, (int(norm),))
+
+    def read(self, k_out, v_out, count, first=None):
+        """Slots first[b] .. first[b] + count[b] - 1 of every request (first None: 0) into slots 0 .. count[b] - 1 of a cache in
+        one piece: k_out, v_out [batch, n_kv_heads, capacity, head_dim] of the queries' type. count, first [batch] int32."""
+        out, batch, ordinal = B.kv_cache(k_out, v_out), self.cache.batch, self.ordinal
+        if (k_out.dtype != self.dtype or (out.batch, out.n_kv_heads, out.head_dim) != (batch, self.hkv, self.dim) or
+                k_out.get_device() != ordinal):
+            raise ValueError(f"k_out, v_out: [{batch}, {self.hkv}, capacity, {self.dim}] of {self.dtype} on {self.dev}")
+        _need(count, torch.int32, batch, ordinal, "count")
+        if first is not None:
+            _need(first, torch.int32, batch, ordinal, "first")
+        st = _run(B.lib.domino_paged_read, ordinal, self._refs[0], B._ptr(first), count.data_ptr(), out.capacity, ctypes.byref(out),
+                  *self._ws)
+        if st:
+            raise B.DominoError(st, "domino_paged_read")
+
+
+class Scores(NamedTuple):
+    """What TokenScorer.score gives: [rows] each, top_ids and top_logprob [rows, top_n]."""
+    logprob: torch.Tensor
+    rank: torch.Tensor
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_ids: torch.Tensor
+    top_logprob: torch.Tensor
+
+
+class TokenScorer:
+    """What logits [rows, V] (bfloat16 or float32) say of given tokens: their log-probability and rank, the rows' entropy and
+    log-sum-exp and the top_n (at most 32) most likely tokens. Owns the result buffers for `rows` rows."""
+
+    def __init__(self, rows: int, V: int, dtype=torch.float32, top_n: int = 0, device="cuda"):
+        if not 0 <= top_n <= 32:
+            raise ValueError(f"top_n {top_n}: 0 to 32")
+        self.rows, self.V, self.dtype, self.top_n = rows, V, dtype, top_n
+        self.ws = B.workspace(256, device)
+        f, i = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
+        self.out = Scores(torch.empty(rows, **f), torch.empty(rows, **i), torch.empty(rows, **f), torch.empty(rows, **f),
+                          torch.empty(rows, top_n, **i), torch.empty(rows, top_n, **f))
+        self.dev, self.ordinal = self.ws.device, self.ws.get_device()
+        self._dt = {torch.bfloat16: B.BF16, torch.float32: B.F32}[dtype]
+        self._args = (*(t.data_ptr() or None for t in self.out), self.ws.data_ptr(), self.ws.numel())
+
+    def score(self, logits, tokens=None, temperature=None) -> Scores:
+        """tokens [rows] int32 (-1, or None for all rows: no token, logprob 0 and rank 0), temperature [rows] fp32 (None: 1). The
+        results are buffers of this object."""
+        n, ordinal = logits.shape[0], self.ordinal
+        if (n > self.rows or logits.dtype != self.dtype or logits.dim() != 2 or logits.shape[1] != self.V or logits.stride(1) != 1 or
+                logits.get_device() != ordinal):
+            raise ValueError(f"logits: [up to {self.rows}, {self.V}] of {self.dtype} on {self.dev}")
+        if tokens is not None:
+            _need(tokens, torch.int32, n, ordinal, "tokens")
+        if temperature is not None:
+            _need(temperature, torch.float32, n, ordinal, "temperature")
+        st = _run(B.lib.domino_token_logprobs, ordinal, self._dt, logits.data_ptr(), logits.stride(0), n, self.V, B._ptr(tokens),
+                  B._ptr(temperature), self.top_n, *self._args)
+        if st:
+            raise B.DominoError(st, "domino_token_logprobs")
+        return self.out if n == self.rows else Scores(*(t[:n] for t in self.out))
 
     def last_status(self) -> int:
         return B.domino_last_status(self.ws)

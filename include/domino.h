@@ -64,7 +64,8 @@ typedef enum {
                                   check failed; the access was skipped */
 } domino_status;
 
-typedef enum { DOMINO_F32 = 0, DOMINO_BF16 = 1 } domino_dtype;
+/* DOMINO_E4M3: pages of a cache only. */
+typedef enum { DOMINO_F32 = 0, DOMINO_BF16 = 1, DOMINO_E4M3 = 2 } domino_dtype;
 
 /*
  * The Domino head plus the frozen target LM head and token embedding.
@@ -533,6 +534,99 @@ domino_status domino_sample(int dtype, const void* logits, int64_t logits_stride
                             const float* temperature, const int32_t* top_k, const float* top_p,
                             const float* min_p, const float* gumbel, int64_t gumbel_stride, int32_t* tokens,
                             float* logprob, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * What the logits [rows, V] say of given tokens. With z = logit / T, T the row's temperature, and tokens ordered by
+ * (logit descending, id ascending):
+ *   lse[r] = log sum_v exp(z_v), p_v = exp(z_v - lse[r]);
+ *   logprob[r] = log p of tokens[r], rank[r] = the number of tokens before it in the order; 0 and 0 where tokens[r] is -1
+ *   (no token is given);
+ *   entropy[r] = -sum_v p_v log p_v (0 log 0 = 0);
+ *   top_ids[r, j], top_logprob[r, j] = the j-th token of the order and its log p; tokens of logit -inf are not listed: -1 and
+ *   -inf in their places.
+ * A NaN logit counts as -inf; +inf logits share the whole probability. A row with no logit above -inf has lse and logprob -inf and
+ * entropy 0. Sums are fp32.
+ *   logits       device, dtype (DOMINO_F32 or DOMINO_BF16), row r at r * logits_stride elements
+ *   tokens       [rows] device int32, or NULL: none is given
+ *   temperature  [rows] device fp32, or NULL: 1
+ *   logprob, entropy, lse [rows] device fp32 out, rank [rows] device int32 out: each may be NULL
+ *   top_n        0 to 32; top_ids [rows, top_n] device int32 out, top_logprob [rows, top_n] device fp32 out, each may be NULL
+ * A temperature below 1e-30 or not finite records DOMINO_ERR_DEVICE_DATA and gives the row NaN in place of every fp32 result; a
+ * token below -1 or from V on records it too and gives logprob NaN, rank -1. ws: any workspace of at least 256 bytes.
+ */
+domino_status domino_token_logprobs(int dtype, const void* logits, int64_t logits_stride, int rows, int V,
+                                    const int32_t* tokens, const float* temperature, int top_n, float* logprob,
+                                    int32_t* rank, float* entropy, float* lse, int32_t* top_ids, float* top_logprob,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The same for a cache in pages: a pool of pages that requests share out among
+ * them by a table, in the layer's type or quantised.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Keys and values of one attention layer in pages of page_size slots (a power of two from 16 to 4096). Slot s of request b
+ * lies in page p = page_table[b * table_stride + s / page_size] at place s % page_size; element x of kv head h there is
+ * k[p * page_stride + h * head_stride + (s % page_size) * slot_stride + x], and the same for v (strides in elements, whole units
+ * of 16 bytes, not negative; pointers 16-byte aligned). head_dim is at most 256, a multiple of 8, or of 16 for DOMINO_E4M3.
+ *   dtype      DOMINO_F32, DOMINO_BF16: the vectors as they are; DOMINO_E4M3: each head's vector of a slot as head_dim e4m3 codes
+ *              and one scale, a power of two; its queries, new keys and values and outputs are DOMINO_BF16
+ *   k_scale, v_scale  [n_pages, n_kv_heads, page_size] device uint8 (DOMINO_E4M3 only): E stands for 2^(E - 127), 255 for NaN
+ *   page_table [batch, max_pages] device int32, rows table_stride apart. Entries that no slot of a call needs are not read, and
+ *              requests may share pages that no call writes.
+ * Quantising x: with e the smallest exponent in [-100, 120] for which no |x_i| is above 448 * 2^e, the codes are x_i / 2^e rounded
+ * to nearest even and E = e + 127; an x with an infinity or a NaN gets E = 255 and codes 0, and reads back as NaN. The e4m3 codes
+ * 0x7f and 0xff, which quantising never gives, read as 480 and -480. Values below 2^-110 of any vector may become 0.
+ * A page outside [0, n_pages) that a call needs records DOMINO_ERR_DEVICE_DATA, and nothing is read or written for it.
+ */
+typedef struct {
+  int32_t dtype;
+  int32_t batch, n_kv_heads, head_dim;
+  int32_t n_pages, page_size, max_pages;
+  void* k;
+  void* v;
+  int64_t page_stride, head_stride, slot_stride;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  const int32_t* page_table;
+  int64_t table_stride;
+} domino_paged_cache;
+
+/*
+ * domino_qk_norm_rope for a cache in pages: new queries and keys normed and rotated, keys and values written to the slots
+ * ctx_len[b] + i, quantised (from fp32, in one rounding) where the cache is. Arguments as there, and
+ *   norm   0: no norm, y = x (q_weight and k_weight are then NULL)
+ * Rows whose page is missing are left unwritten, their queries too. Slots of one call have to be different places.
+ */
+domino_status domino_paged_append(const domino_paged_cache* cache, const domino_block* block, int n_q_heads,
+                                  const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, int norm, const void* q_weight,
+                                  const void* k_weight, float eps, const float* rope, int max_pos, int rot_dim,
+                                  int interleaved, void* q_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Reads slots first[b] .. first[b] + count[b] - 1 of every request back into a cache in one piece: slot first[b] + j goes to slot j
+ * of request b of `out`, whose batch, n_kv_heads and head_dim are the pages' and whose dtype is theirs (DOMINO_BF16 for
+ * DOMINO_E4M3). Other slots of `out` stay as they are.
+ *   first  [batch] device int32, or NULL: 0
+ *   count  [batch] device int32, each in [0, max_count]; max_count is at most out's capacity
+ * A range outside its bounds records DOMINO_ERR_DEVICE_DATA and leaves that request's slots as they are, a missing page its own.
+ * ws: any workspace of at least 256 bytes.
+ */
+domino_status domino_paged_read(const domino_paged_cache* cache, const int32_t* first, const int32_t* count, int max_count,
+                                const domino_kv_cache* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * domino_block_attention over a cache in pages; q and out are of its type (DOMINO_BF16 for DOMINO_E4M3). Keys and values count as
+ * what their codes and scales stand for. The rows of a request with a missing page among the slots that are looked at get an
+ * unspecified result.
+ */
+size_t domino_paged_attention_workspace_bytes(const domino_paged_cache* cache, const domino_block* block, int n_q_heads);
+domino_status domino_paged_attention(const domino_paged_cache* cache, const domino_block* block, int n_q_heads,
+                                     const void* q, float scale, int mask_mode, const uint8_t* mask, int window,
+                                     int sinks, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Synchronise `stream`, return the sticky device status recorded in `ws` by
