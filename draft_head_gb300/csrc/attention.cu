@@ -337,7 +337,7 @@ size_t attn_ws_bytes(const AttnArgs& a) {
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
-  if (a.cache == kWhole && attn_rows_applies(a)) return launch_attention_rows(a, stream);
+  if (attn_rows_applies(a)) return launch_attention_rows(a, stream);
   if (a.cache == kWhole && attn_tc_applies(a)) return launch_attention_tc(a, stream);
   SimtP p;
   p.a = a;

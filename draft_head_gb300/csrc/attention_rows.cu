@@ -26,6 +26,7 @@
 
 #include "attention.cuh"
 #include "packed.cuh"
+#include "pages.cuh"
 
 namespace domino {
 
@@ -41,7 +42,10 @@ constexpr int kManyTiles = 96, kLeastMany = 64, kWaves = 4;
 constexpr int kMostPieces = 64;  // of a row tile: their join takes a round trip for every eight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 32.0f;
+constexpr float kLazyBf16 = 32.0f;
+// Codes: weights in fp16, kAtMost at the maximum and kAtMost 2^kLazyCodes at most.
+constexpr float kLazyCodes = 4.0f, kAtMost = 2048.0f;  // 2^11
+constexpr int kCodesCtas = 3;
 
 struct RowsP {
   AttnArgs a;
@@ -55,6 +59,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <int CACHE>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (CACHE == kPagedE4m3)
+    mma16816_f16(d, a0, a1, a2, a3, b0, b1);
+  else
+    mma16816(d, a0, a1, a2, a3, b0, b1);
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -65,6 +81,28 @@ __device__ __forceinline__ uint4 ldg16(const __nv_bfloat16* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
   return x;
 }
+__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+  uint2 x;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+  return x;
+}
+// Eight elements of a slot as they lie in the cache, and as the operand's pairs.
+template <int CACHE>
+struct Piece {
+  uint4 x;
+  __device__ __forceinline__ void load(const void* base, int64_t at) { x = ldg16((const __nv_bfloat16*)base + at); }
+  __device__ __forceinline__ void zero() { x = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint4 pairs() const { return x; }
+};
+template <>
+struct Piece<kPagedE4m3> {
+  uint2 x;
+  __device__ __forceinline__ void load(const void* base, int64_t at) { x = ldg8((const uint8_t*)base + at); }
+  __device__ __forceinline__ void zero() { x = make_uint2(0, 0); }
+  __device__ __forceinline__ uint4 pairs() const {
+    return make_uint4(codes_f16(x.x & 0xffffu), codes_f16(x.x >> 16), codes_f16(x.y & 0xffffu), codes_f16(x.y >> 16));
+  }
+};
 __device__ __forceinline__ uint32_t part(const uint4& x, int t) { return t == 0 ? x.x : t == 1 ? x.y : t == 2 ? x.z : x.w; }
 __device__ __forceinline__ bool bad16(uint32_t x) {  // a bf16 pair with an infinity or a NaN in it
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
@@ -76,9 +114,11 @@ __device__ __forceinline__ uint32_t clear16(uint32_t x) {
 }
 
 // NT: groups of 8 rows; KS: 32-element pieces of a head; JJ: 64-element pieces.
-template <int NT, int KS, int JJ>
-__global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constant__ RowsP p) {
+template <int NT, int KS, int JJ, int CACHE>
+__global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesCtas : 2) attn_rows_kernel(const __grid_constant__ RowsP p) {
   constexpr int kRows = 8 * NT, DP = 64 * JJ;
+  constexpr bool kCodes = CACHE == kPagedE4m3;
+  constexpr float kLazy = kCodes ? kLazyCodes : kLazyBf16;
   __shared__ __align__(16) float s_o[kWarps][kRows][DP + 4];
   __shared__ float2 s_ml[kWarps][kRows];
   __shared__ int s_low[kRows], s_i[kRows], s_last;
@@ -108,6 +148,31 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
       q[g][j][0] = x.x; q[g][j][1] = x.y; q[g][j][2] = x.z; q[g][j][3] = x.w;
     }
   }
+  float qc[NT][2];  // scale log2(e), and the power of two that a row's queries were divided by
+#pragma unroll
+  for (int g = 0; g < NT; ++g) {
+    int e = 0;
+    if (kCodes) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) most = max(most, max((q[g][j][x] << 16) & 0x7fff0000u, q[g][j][x] & 0x7fff0000u));
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      e = query_exponent(most);
+      const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) q[g][j][x] = query_f16(q[g][j][x], f);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int of = kCodes ? __shfl_sync(0xffffffffu, e, (2 * c + x) * 4) : 0;
+      qc[g][x] = kCodes ? p.c * __uint_as_float((uint32_t)(of + 127) << 23) : p.c;
+    }
+  }
   __syncthreads();
   int low_min = 0x7fffffff, low_max = 0;
   for (int r = 0; r < kRows; ++r) {
@@ -123,25 +188,48 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
   const int all_low = a.mode == DOMINO_MASK_CAUSAL ? low_max : min(low_max, ctx);
   const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.rows.max_q * a.rows.max_q : nullptr;
 
-  const __nv_bfloat16* kb = (const __nv_bfloat16*)a.k + (int64_t)b * a.rs + (int64_t)h * a.hs;
-  const __nv_bfloat16* vb = (const __nv_bfloat16*)a.v + (int64_t)b * a.rs + (int64_t)h * a.hs;
   const int end = ctx + rows_n;
-  uint4 kx[2][KS], vx[4][JJ];
-  auto fetch = [&](int k) {
+  Piece<CACHE> kx[2][KS], vx[4][JJ];
+  uint32_t scale_next = 0;  // codes: the byte of slot lane % 16, of the keys (lanes 0 to 15) or the values
+  bool tile_there = true;
+  int64_t tile_at = 0;      // elements from the caches' begin to the tile's first slot
+  // Pages are as large as tiles at least, so a tile lies in one: its number is read one tile ahead of the tile.
+  auto page_at = [&](int k) { return CACHE == kWhole ? 0 : page_of(a.pages, b, kt.slot(k, kBN)); };
+  auto fetch = [&](int k, int page) {
     const int s0 = kt.slot(k, kBN);
+    if (CACHE == kWhole)
+      tile_at = (int64_t)b * a.rs + (int64_t)h * a.hs + (int64_t)s0 * a.ss;
+    else
+      tile_at = (int64_t)page * a.pages.page_stride + (int64_t)h * a.hs + (int64_t)slot_in_page(a.pages, s0) * a.ss;
+    tile_there = CACHE == kWhole || page >= 0;
+    if (!tile_there && lane == 0) dev_error(a.ctl, DEV_ERR_DATA);
+    const int there = tile_there ? end - s0 : 0;  // slots of the tile
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int s = s0 + n + 8 * x;
+      const int s = n + 8 * x;
 #pragma unroll
-      for (int j = 0; j < KS; ++j)
-        kx[x][j] = s < end && 32 * j + 8 * c < a.D ? ldg16(kb + (int64_t)s * a.ss + 32 * j + 8 * c) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < KS; ++j) {
+        if (s < there && 32 * j + 8 * c < a.D)
+          kx[x][j].load(a.k, tile_at + (int64_t)s * a.ss + 32 * j + 8 * c);
+        else
+          kx[x][j].zero();
+      }
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int s = s0 + 2 * c + (x & 1) + 8 * (x >> 1);
+      const int s = 2 * c + (x & 1) + 8 * (x >> 1);
 #pragma unroll
-      for (int j = 0; j < JJ; ++j)
-        vx[x][j] = s < end && 64 * j + 8 * n < a.D ? ldg16(vb + (int64_t)s * a.ss + 64 * j + 8 * n) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < JJ; ++j) {
+        if (s < there && 64 * j + 8 * n < a.D)
+          vx[x][j].load(a.v, tile_at + (int64_t)s * a.ss + 64 * j + 8 * n);
+        else
+          vx[x][j].zero();
+      }
+    }
+    if (kCodes) {
+      scale_next = 127;
+      if ((lane & 15) < there)
+        scale_next = __ldg((lane < 16 ? a.pages.k_scale : a.pages.v_scale) + scale_at(a.pages, a.hkv, page, h, s0 + (lane & 15)));
     }
   };
 
@@ -155,53 +243,96 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
     m[g][0] = m[g][1] = -INFINITY;
     l[g][0] = l[g][1] = 0.0f;
   }
-  if (k_begin + warp < k_end) fetch(k_begin + warp);
+  int page = 0;
+  if (k_begin + warp < k_end) fetch(k_begin + warp, page_at(k_begin + warp));
+  if (k_begin + warp + kWarps < k_end) page = page_at(k_begin + warp + kWarps);
 #pragma unroll 1
   for (int k = k_begin + warp; k < k_end; k += kWarps) {
     const int s0 = kt.slot(k, kBN);
-    uint4 kc[2][KS], vc[4][JJ];
+    const int64_t here = tile_at;
+    Piece<CACHE> kr[2][KS], vr[4][JJ];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int j = 0; j < KS; ++j) kc[x][j] = kx[x][j];
+      for (int j = 0; j < KS; ++j) kr[x][j] = kx[x][j];
 #pragma unroll
     for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int j = 0; j < JJ; ++j) vc[x][j] = vx[x][j];
-    if (k + kWarps < k_end) fetch(k + kWarps);
+      for (int j = 0; j < JJ; ++j) vr[x][j] = vx[x][j];
+    // Codes: the scales of slots n and n + 8 (e / 2 of the scores below), the values' also as exponents.
+    float ks[2], vs[2], ve[2];
+    if (kCodes) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        ks[x] = scale_f32((int)__shfl_sync(0xffffffffu, scale_next, n + 8 * x));
+        const int v = (int)__shfl_sync(0xffffffffu, scale_next, 16 + n + 8 * x);
+        ve[x] = (float)(v - 127);
+        vs[x] = scale_f32(v) * kAtMost;
+        if (v == kScaleNan) ve[x] = 0.0f;
+      }
+    }
+    const bool gone = CACHE != kWhole && !tile_there;  // no such page: nothing was read
+    if (k + kWarps < k_end) {
+      fetch(k + kWarps, page);
+      if (k + 2 * kWarps < k_end) page = page_at(k + 2 * kWarps);
+    }
     const bool whole = s0 + kBN <= all_hi && (s0 >= all_low || s0 + kBN <= a.sinks);
     bool mend = false;
-    if (!whole) {
-      // A weight of 0 does not stop an infinity or a NaN in the product: they are cleared here
-      // and added below to the rows that see them.
+    if constexpr (kCodes) {
+      if (!whole) {  // a value that is no number has that in its scale, and so in its weight; slots without one may hold anything
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int j = 0; j < JJ; ++j) {
-          mend |= bad16(vc[x][j].x) | bad16(vc[x][j].y) | bad16(vc[x][j].z) | bad16(vc[x][j].w);
-          vc[x][j] = make_uint4(clear16(vc[x][j].x), clear16(vc[x][j].y), clear16(vc[x][j].z), clear16(vc[x][j].w));
-        }
-      mend = __any_sync(0xffffffffu, mend);
+          for (int j = 0; j < JJ; ++j)
+            vr[x][j].x = make_uint2(codes_that_are_numbers(vr[x][j].x.x), codes_that_are_numbers(vr[x][j].x.y));
+      }
+    } else {
+      if (!whole) {
+        // A weight of 0 does not stop an infinity or a NaN in the product: they are cleared here
+        // and added below to the rows that see them.
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int j = 0; j < JJ; ++j) {
+            uint4& v = vr[x][j].x;
+            mend |= bad16(v.x) | bad16(v.y) | bad16(v.z) | bad16(v.w);
+            v = make_uint4(clear16(v.x), clear16(v.y), clear16(v.z), clear16(v.w));
+          }
+        mend = __any_sync(0xffffffffu, mend) && !gone;
+      }
     }
+    float s[NT][4];  // slots n, n, n + 8, n + 8 of rows 2c, 2c + 1, 2c, 2c + 1
+#pragma unroll
+    for (int g = 0; g < NT; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[g][e] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+      const uint4 k0 = kr[0][j].pairs(), k1 = kr[1][j].pairs();
+#pragma unroll
+      for (int g = 0; g < NT; ++g) {
+        mma<CACHE>(s[g], k0.x, k1.x, k0.y, k1.y, q[g][j][0], q[g][j][1]);
+        mma<CACHE>(s[g], k0.z, k1.z, k0.w, k1.w, q[g][j][2], q[g][j][3]);
+      }
+    }
+    uint32_t pw[NT][2];
 #pragma unroll
     for (int g = 0; g < NT; ++g) {
-      float s[4] = {0, 0, 0, 0};  // slots n, n, n + 8, n + 8 of rows 2c, 2c + 1, 2c, 2c + 1
-#pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        mma16816(s, kc[0][j].x, kc[1][j].x, kc[0][j].y, kc[1][j].y, q[g][j][0], q[g][j][1]);
-        mma16816(s, kc[0][j].z, kc[1][j].z, kc[0][j].w, kc[1][j].w, q[g][j][2], q[g][j][3]);
-      }
+      bool hidden[4] = {};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[e] *= p.c;
+        s[g][e] *= qc[g][e & 1];
+        if (kCodes) s[g][e] *= ks[e >> 1];
         if (!whole) {
           const int r = g * 8 + 2 * c + (e & 1), slot = s0 + n + 8 * (e >> 1);
-          if (!(slot < end && sees(a.mode, a.sinks, s_low[r], ctx, rows_n, s_i[r],
-                                   mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, slot)))
-            s[e] = -INFINITY;
+          hidden[e] = !(slot < end && sees(a.mode, a.sinks, s_low[r], ctx, rows_n, s_i[r],
+                                           mask ? mask + (int64_t)s_i[r] * a.rows.max_q : nullptr, slot));
+          if (hidden[e]) s[g][e] = -INFINITY;
         }
       }
-      const float top[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+      // Codes: the maximum is that of the weights with their values' scales, which is what fp16 has to hold.
+      const float top[2] = {kCodes ? fmaxf(s[g][0] + ve[0], s[g][2] + ve[1]) : fmaxf(s[g][0], s[g][2]),
+                            kCodes ? fmaxf(s[g][1] + ve[0], s[g][3] + ve[1]) : fmaxf(s[g][1], s[g][3])};
       if (__any_sync(0xffffffffu, top[0] > m[g][0] + kLazy || top[1] > m[g][1] + kLazy)) {
         float f[2];
 #pragma unroll
@@ -221,20 +352,28 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[e] = ex2(s[e] - (m[g][e & 1] == -INFINITY ? 0.0f : m[g][e & 1]));
-        l[g][e & 1] += s[e];
+        s[g][e] = ex2(s[g][e] - (m[g][e & 1] == -INFINITY ? 0.0f : m[g][e & 1]));
+        l[g][e & 1] += s[g][e];
+        if (kCodes) s[g][e] = hidden[e] ? 0.0f : s[g][e] * vs[e >> 1];
       }
-      const uint32_t b0 = transpose8(pack_bf16(s[0], s[1])), b1 = transpose8(pack_bf16(s[2], s[3]));
+      pw[g][0] = transpose8(kCodes ? pack_f16(s[g][0], s[g][1]) : pack_bf16(s[g][0], s[g][1]));
+      pw[g][1] = transpose8(kCodes ? pack_f16(s[g][2], s[g][3]) : pack_bf16(s[g][2], s[g][3]));
+    }
 #pragma unroll
-      for (int j = 0; j < JJ; ++j) {
+    for (int j = 0; j < JJ; ++j) {
+      const uint4 v4[4] = {vr[0][j].pairs(), vr[1][j].pairs(), vr[2][j].pairs(), vr[3][j].pairs()};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t v0 = part(vc[0][j], t), v1 = part(vc[1][j], t), v2 = part(vc[2][j], t), v3 = part(vc[3][j], t);
-          mma16816(o[g][4 * j + t], __byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x5410),
-                   __byte_perm(v2, v3, 0x7632), b0, b1);
-        }
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t v0 = part(v4[0], t), v1 = part(v4[1], t), v2 = part(v4[2], t), v3 = part(v4[3], t);
+#pragma unroll
+        for (int g = 0; g < NT; ++g)
+          mma<CACHE>(o[g][4 * j + t], __byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x5410),
+                     __byte_perm(v2, v3, 0x7632), pw[g][0], pw[g][1]);
       }
-      if (mend) {
+    }
+    if (!kCodes && mend) {
+#pragma unroll
+      for (int g = 0; g < NT; ++g)
         for (int x = 0; x < kBN && s0 + x < end; ++x)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -244,11 +383,10 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
 #pragma unroll
             for (int d = 0; d < 8 * JJ; ++d) {
               const int col = 64 * (d >> 3) + 8 * n + (d & 7);
-              const float v = col < a.D ? __bfloat162float(vb[(int64_t)(s0 + x) * a.ss + col]) : 0.0f;
+              const float v = col < a.D ? __bfloat162float(((const __nv_bfloat16*)a.v)[here + (int64_t)x * a.ss + col]) : 0.0f;
               if (sees_it && !isfinite(v)) o[g][(d >> 3) * 4 + ((d & 7) >> 1)][(d & 1) * 2 + e] += v;
             }
           }
-      }
     }
   }
 
@@ -273,7 +411,7 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(const __grid_constan
   auto finish = [&](int r, int e, float4 x, float mm, float ll) {
     const int i = r / G;
     const int64_t row = (int64_t)(q0 + i) * a.hq + h * G + (r - i * G);
-    const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN);
+    const float inv = (ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN)) * (kCodes ? 1.0f / kAtMost : 1.0f);
     *(uint2*)((__nv_bfloat16*)a.out + row * a.D + e) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
     if (e == 0 && a.lse) a.lse[row] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
   };
@@ -364,7 +502,7 @@ int64_t resident() { return 2 * (int64_t)num_sms(); }
 int64_t want_ctas() { return kWaves * resident(); }
 static_assert(2 * kWaves <= kCountersPerSm, "a counter for every tile that is cut");
 
-template <int NT, int KS, int JJ>
+template <int NT, int KS, int JJ, int CACHE>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   RowsP p;
   p.a = a;
@@ -375,7 +513,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   p.splits = splits_for(row_tiles, many ? want_ctas() : resident(), std::min<int64_t>(key_tiles / p.least, kMostPieces));
   p.part = partials_at(a.scratch, want_ctas(), 16);
   const dim3 grid((unsigned)p.splits, (unsigned)a.hkv, (unsigned)a.rows.batch);
-  attn_rows_kernel<NT, KS, JJ><<<grid, kThr, 0, stream>>>(p);
+  attn_rows_kernel<NT, KS, JJ, CACHE><<<grid, kThr, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -393,10 +531,15 @@ bool attn_rows_applies(const AttnArgs& a) {
 }
 size_t attn_rows_ws_bytes(const AttnArgs& a) { return partial_bytes(want_ctas(), 16, a.D); }
 
-cudaError_t launch_attention_rows(const AttnArgs& a, cudaStream_t stream) {
+template <int CACHE>
+static cudaError_t launch_on(const AttnArgs& a, cudaStream_t stream) {
   const bool many = a.rows.max_q * (a.hq / a.hkv) > 8;
-  if (a.D > 64) return many ? launch<2, 4, 2>(a, stream) : launch<1, 4, 2>(a, stream);
-  return many ? launch<2, 2, 1>(a, stream) : launch<1, 2, 1>(a, stream);
+  if (a.D > 64) return many ? launch<2, 4, 2, CACHE>(a, stream) : launch<1, 4, 2, CACHE>(a, stream);
+  return many ? launch<2, 2, 1, CACHE>(a, stream) : launch<1, 2, 1, CACHE>(a, stream);
+}
+cudaError_t launch_attention_rows(const AttnArgs& a, cudaStream_t stream) {
+  return a.cache == kWhole ? launch_on<kWhole>(a, stream) : a.cache == kPaged ? launch_on<kPaged>(a, stream)
+                                                                             : launch_on<kPagedE4m3>(a, stream);
 }
 
 }  // namespace domino

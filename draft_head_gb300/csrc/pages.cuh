@@ -6,6 +6,8 @@
 // and lose nothing.
 #pragma once
 
+#include <math.h>
+
 #include "common.cuh"
 
 namespace domino {
@@ -45,7 +47,7 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
 }
 
 // Four codes (low byte first) in fp32, without their scale. The fields of a code at fp32's places are its value times 2^-120,
-// subnormal codes included. (The two codes that e4m3 gives to NaN are never written; they read as 480 and -480.)
+// subnormal codes included. (The two codes that e4m3 gives to NaN are never written; here they are 480 and -480.)
 __device__ __forceinline__ float4 codes_f32(uint32_t x) {
   auto one = [](uint32_t b) { return __uint_as_float(((b & 0x80u) << 24) | ((b & 0x7fu) << 20)) * 1.329227995784916e36f; };
   return make_float4(one(x), one(x >> 8), one(x >> 16), one(x >> 24));
@@ -53,6 +55,34 @@ __device__ __forceinline__ float4 codes_f32(uint32_t x) {
 // 2^e of a scale's byte, or NaN.
 __device__ __forceinline__ float scale_f32(int byte) {
   return byte == kScaleNan ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)byte << 23);
+}
+
+// Four codes, those of e4m3's NaN (which are never written, but may lie in slots that were not) as 448.
+__device__ __forceinline__ uint32_t codes_that_are_numbers(uint32_t x) {
+  return x & ~((((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7);
+}
+// Two codes (low byte first) as an fp16 pair, without their scale: every code is a normal fp16 number or 0.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
+  uint32_t r;
+  asm("{\n .reg .b16 c;\n cvt.u16.u32 c, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}\n" : "=r"(r) : "r"(x));
+  return r;
+}
+// A row of queries in fp16, for products with codes: divided by a power of two that brings its largest magnitude, of these bits,
+// to [16, 32), where fp16 holds bf16's 8 bits of every element above 2^-21 of the largest, and smaller ones to within 2^-29 of it.
+__device__ __forceinline__ int query_exponent(uint32_t most) {
+  return most >= 0x7f800000u || most < 0x00800000u ? 0 : min(max((int)(most >> 23) - 127 - 4, -126), 126);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// A bf16 pair times f in fp16. A finite element of a row with an infinity or a NaN stays finite.
+__device__ __forceinline__ uint32_t query_f16(uint32_t x, float f) {
+  float lo = __uint_as_float(x << 16) * f, hi = __uint_as_float(x & 0xffff0000u) * f;
+  if (fabsf(lo) > 65504.0f && fabsf(lo) < INFINITY) lo = copysignf(65504.0f, lo);
+  if (fabsf(hi) > 65504.0f && fabsf(hi) < INFINITY) hi = copysignf(65504.0f, hi);
+  return pack_f16(lo, hi);
 }
 
 // A scale as the bf16 pairs by which codes at bf16's places, 2^-120 of their values, are multiplied: 2^(e + 120). From e = 8 on

@@ -578,7 +578,7 @@ domino_status domino_token_logprobs(int dtype, const void* logits, int64_t logit
  *              requests may share pages that no call writes.
  * Quantising x: with e the smallest exponent in [-100, 120] for which no |x_i| is above 448 * 2^e, the codes are x_i / 2^e rounded
  * to nearest even and E = e + 127; an x with an infinity or a NaN gets E = 255 and codes 0, and reads back as NaN. The e4m3 codes
- * 0x7f and 0xff, which quantising never gives, read as 480 and -480. Values below 2^-110 of any vector may become 0.
+ * 0x7f and 0xff, which quantising never gives, read back as 480 and -480; rows that see a slot with one may get NaN. Values below 2^-110 of any vector may become 0.
  * A page outside [0, n_pages) that a call needs records DOMINO_ERR_DEVICE_DATA, and nothing is read or written for it.
  */
 typedef struct {
