@@ -409,8 +409,8 @@ def paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> domino_paged_ca
             if scale is not None:
                 raise ValueError(f"{what}: only float8_e4m3fn pages have scales")
         elif (scale is None or scale.dtype not in (torch.uint8, torch.float8_e8m0fnu) or scale.shape != k.shape[:3] or
-              not scale.is_contiguous() or scale.device != k.device):
-            raise ValueError(f"{what}: {list(k.shape[:3])} of uint8 or float8_e8m0fnu on {k.device}, contiguous")
+              not scale.is_contiguous() or scale.device != k.device or scale.data_ptr() % 16):
+            raise ValueError(f"{what}: {list(k.shape[:3])} of uint8 or float8_e8m0fnu on {k.device}, contiguous, 16-byte aligned")
     if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or page_table.shape[1] == 0 or
             page_table.device != k.device):
         raise ValueError(f"page_table: [batch, max_pages] of int32 on {k.device}, its rows contiguous")

@@ -141,8 +141,10 @@ __global__ void __launch_bounds__(kThr) attn_simt_kernel(const __grid_constant__
         *(float4*)(sk + r * ldq + e) = in ? load4(kb + (int64_t)(s0 + r) * a.ss + e) : make_float4(0, 0, 0, 0);
         *(float4*)(sv + r * D + e) = in ? load4(vb + (int64_t)(s0 + r) * a.ss + e) : make_float4(0, 0, 0, 0);
       } else {
-        const int page = in ? page_of(a.pages, b, s0 + r) : -1;
-        if (in && page < 0 && e == 0) dev_error(a.ctl, DEV_ERR_DATA);
+        // Pages before the window may be gone.
+        const bool needed = in && (s0 + r < a.sinks || s0 + r >= first_slot(a.mode, low, ctx, ctx + n));
+        const int page = needed ? page_of(a.pages, b, s0 + r) : -1;
+        if (needed && page < 0 && e == 0) dev_error(a.ctl, DEV_ERR_DATA);
         *(float4*)(sk + r * ldq + e) = slot4<T, CACHE>(a, a.k, a.pages.k_scale, page, h, s0 + r, e);
         *(float4*)(sv + r * D + e) = slot4<T, CACHE>(a, a.v, a.pages.v_scale, page, h, s0 + r, e);
       }
@@ -338,7 +340,7 @@ size_t attn_ws_bytes(const AttnArgs& a) {
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
   if (attn_rows_applies(a)) return launch_attention_rows(a, stream);
-  if (a.cache == kWhole && attn_tc_applies(a)) return launch_attention_tc(a, stream);
+  if (attn_tc_applies(a)) return launch_attention_tc(a, stream);
   SimtP p;
   p.a = a;
   p.row_tiles = simt_row_tiles(a);

@@ -30,11 +30,16 @@ __device__ __forceinline__ int window_low(int p, int window) {
   return low < 0 ? 0 : (low > 0x7fffffff ? 0x7fffffff : (int)low);
 }
 
+// The slots that a tile looks at are [0, sinks) and [first_slot, end), `low` the smallest window_low of its rows.
+// Outside the causal mode the window does not reach into the block.
+__device__ __forceinline__ int first_slot(int mode, int low, int ctx, int end) {
+  return mode == DOMINO_MASK_CAUSAL ? min(low, end) : min(low, ctx);
+}
+
 // low: the smallest window_low of the tile's rows; i_last: its last row.
 __device__ __forceinline__ KeyTiles key_tiles(int mode, int sinks, int low, int ctx, int n, int i_last, int BN) {
   const int end = mode == DOMINO_MASK_CAUSAL ? ctx + i_last + 1 : ctx + n;
-  // Outside the causal mode the window does not reach into the block.
-  const int start = mode == DOMINO_MASK_CAUSAL ? min(low, end) : min(low, ctx);
+  const int start = first_slot(mode, low, ctx, end);
   KeyTiles k;
   // A window that begins past the row itself (positions ahead of the slots) leaves all tiles to the sinks.
   k.main_begin = start < end ? start / BN : (end + BN - 1) / BN;

@@ -46,10 +46,12 @@
 #include <cuda.h>
 #include <math.h>
 #include <string.h>
+#include <algorithm>
 #include <mutex>
 
 #include "attention.cuh"
 #include "packed.cuh"
+#include "pages.cuh"
 #include "waits.cuh"
 
 namespace domino {
@@ -70,6 +72,7 @@ struct TcAttnP {
   AttnArgs a;
   int row_tiles;  // per request, of 128 NQ packed rows
   int slots;      // ring buffers
+  int staged;     // codes: buffers in which they arrive
   uint64_t timeout_ns;
   float c;        // scale log2(e)
   unsigned int* arrived;  // per CTA: pieces in, of the row tile that begins in it and goes on
@@ -231,6 +234,28 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
 __device__ __forceinline__ bool bad16(uint32_t x) {  // a bf16 pair with an infinity or a NaN in it
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
+__device__ __forceinline__ uint32_t clear16(uint32_t x) {
+  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+  return x;
+}
+
+// The pages of the 128 slots from s0 on (one, where they are that large): -1 for one that is not there, which is reported, and -2
+// for those of whose slots the row tile looks at none.
+constexpr int kLeastPage = 16;
+__device__ __forceinline__ void tile_pages(const AttnArgs& a, const Unit& w, int b, int s0, int (&pages)[kBN / kLeastPage]) {
+  const int shift = min(a.pages.shift, 7), end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_last + 1 : w.ctx + w.n;
+  const int from = first_slot(a.mode, w.low_min, w.ctx, end);
+#pragma unroll
+  for (int i = 0; i < kBN / kLeastPage; ++i) {
+    const int s = s0 + (i << shift);
+    const bool needed = i << shift < kBN && s < end && (s < a.sinks || s + (1 << shift) > from);
+    pages[i] = needed ? page_of(a.pages, b, s) : -2;
+  }
+#pragma unroll
+  for (int i = 0; i < kBN / kLeastPage; ++i)
+    if (pages[i] == -1) dev_error(a.ctl, DEV_ERR_DATA);
+}
 
 // Visibility of the 128 slots from s0 for one row, as bits.
 __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int i, int low, const uint8_t* mask_row, int s0,
@@ -257,9 +282,9 @@ __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int 
 // Adds the non-finite values that the row sees in the piece's partly seen tiles to columns [e0, e1) of its
 // result in memory (bf16 `out`, or the piece's sums `sums`): the tiles had them cleared, because the product
 // with V would have spread them to the rows that do not see them.
+template <int CACHE>
 __device__ __noinline__ void add_non_finite(const AttnArgs& a, const Unit& w, int b, int h, int k0, int k1, int i, int low,
                                             const uint8_t* mask_row, int e0, int e1, __nv_bfloat16* out, float4* sums) {
-  const uint16_t* v = (const uint16_t*)a.v + (int64_t)b * a.rs + (int64_t)h * a.hs;
   for (int k = k0; k < k1; ++k) {
     const int s0 = w.kt.slot(k, kBN);
     if (all_seen(a, w, s0)) continue;
@@ -268,9 +293,20 @@ __device__ __noinline__ void add_non_finite(const AttnArgs& a, const Unit& w, in
     for (int j = 0; j < kBN; ++j) {
       const uint32_t word = j < 32 ? bits[0] : j < 64 ? bits[1] : j < 96 ? bits[2] : bits[3];
       if (!((word >> (j & 31)) & 1u)) continue;
-      const uint16_t* row = v + (int64_t)(s0 + j) * a.ss;
+      const int page = CACHE == kWhole ? 0 : page_of(a.pages, b, s0 + j);
+      if (page < 0) continue;
+      const int64_t row = CACHE == kWhole
+                              ? (int64_t)b * a.rs + (int64_t)h * a.hs + (int64_t)(s0 + j) * a.ss
+                              : (int64_t)page * a.pages.page_stride + (int64_t)h * a.hs + (int64_t)slot_in_page(a.pages, s0 + j) * a.ss;
+      Scale2 scale = {0, 0};
+      if (CACHE == kPagedE4m3) scale = scale_bf16(a.pages.v_scale[scale_at(a.pages, a.hkv, page, h, s0 + j)]);
       for (int e = e0; e < e1 && e < a.D; ++e) {
-        const uint32_t x = row[e];
+        uint32_t x;
+        if (CACHE == kPagedE4m3) {
+          x = codes8_bf16(make_uint2(((const uint8_t*)a.v)[row + e], 0), scale).x & 0xffffu;
+        } else {
+          x = ((const uint16_t*)a.v)[row + e];
+        }
         if ((x & 0x7f80u) != 0x7f80u) continue;
         if (out)
           out[e] = __float2bfloat16(__bfloat162float(out[e]) + __uint_as_float(x << 16));
@@ -281,9 +317,11 @@ __device__ __noinline__ void add_non_finite(const AttnArgs& a, const Unit& w, in
   }
 }
 
-template <int NQ, int KB>
+template <int NQ, int KB, int CACHE>
 struct Cfg {
   static constexpr int DP = 64 * KB;
+  static constexpr bool kCodes = CACHE == kPagedE4m3;
+  static constexpr uint32_t kStaged = (uint32_t)kBN * DP;  // bytes of a tile of codes
   static constexpr int BMT = 128 * NQ;
   // List places of a row tile beside its key tiles: its start and epilogue take about 11,000 cycles, a key
   // tile 2,000 (NQ = 1) or 3,200. Two more than that for prompts measured best (2: 497 us, 6: 465, 8: 450,
@@ -296,18 +334,25 @@ struct Cfg {
 constexpr int kThreads = 384;
 constexpr uint32_t kOCol = 256;  // TMEM: S of group g at 128 g, O of group g at kOCol + DP g
 
-template <int NQ, int KB>
+template <int NQ, int KB, int CACHE>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnP p) {
-  using C = Cfg<NQ, KB>;
+  using C = Cfg<NQ, KB, CACHE>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* ring = sQ + NQ * C::kQBytes;
   const int slots = p.slots;
   uint8_t* stage = ring + (size_t)slots * C::kTile;  // NQ = 2: 4 KB per softmax warp
-  uint64_t* full = (uint64_t*)(stage + C::kStage);
-  uint64_t* empty = full + slots;
-  uint64_t* v_clean = empty + slots;
-  uint64_t* s_ready = v_clean + slots;  // [2]: per group
+  // The buffers that copies fill, `full` once they have: the ring's own, or codes on their way to it.
+  const int in_slots = C::kCodes ? p.staged : slots;
+  uint8_t* in = C::kCodes ? stage + C::kStage : ring;
+  uint8_t* in_scale = in + (C::kCodes ? (size_t)in_slots * C::kStaged : 0);  // codes: their slots' scales, kBN bytes a buffer
+  uint64_t* full = C::kCodes ? (uint64_t*)(in_scale + (size_t)in_slots * kBN) : (uint64_t*)(stage + C::kStage);
+  uint64_t* empty = full + in_slots;
+  // The ring's: keys ready, values ready, buffers read.
+  uint64_t* v_clean = empty + in_slots;
+  uint64_t* k_ready = C::kCodes ? v_clean + slots : full;
+  uint64_t* freed = C::kCodes ? k_ready + slots : empty;
+  uint64_t* s_ready = (C::kCodes ? freed : v_clean) + slots;  // [2]: per group
   uint64_t* p_ready = s_ready + 2;      // [4]: per group and half
   uint64_t* o_done = p_ready + 4;       // [2]: per group, once per row tile
   uint64_t* q_ready = o_done + 2;
@@ -329,10 +374,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   Ctl* ctl = a.ctl;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < slots; ++s) {
+    for (int s = 0; s < in_slots; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], C::kCodes ? 2 : 1);
+    }
+    for (int s = 0; s < slots; ++s) {
       mbar_init(&v_clean[s], 2);
+      if (C::kCodes) {
+        mbar_init(&k_ready[s], 2);
+        mbar_init(&freed[s], 1);
+      }
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_ready[s], 1);
@@ -440,25 +491,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int b = walk.u / p.row_tiles;
         int k0, k1;
         walk.part(w.cnt, k0, k1);
+        int pages[kBN / kLeastPage], ahead[kBN / kLeastPage];
+        if (CACHE != kWhole && k0 < k1) tile_pages(a, w, b, w.kt.slot(k0, kBN), pages);
         for (int k = k0; k < k1 && ok; ++k) {
           const int s0 = w.kt.slot(k, kBN);
+          if (CACHE != kWhole && k + 1 < k1) tile_pages(a, w, b, w.kt.slot(k + 1, kBN), ahead);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             if (!mbar_wait(&empty[slot], phase ^ 1u, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
-            mbar_expect_tx(&full[slot], C::kTile);
+            if (CACHE == kWhole) {
+              mbar_expect_tx(&full[slot], C::kTile);
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-              tma_load_4d(ring + (size_t)slot * C::kTile + kb * (kBN * 128), kv ? &p.tmV : &p.tmK, kb * 64, s0, walk.h, b,
-                          &full[slot], pol, once);
+              for (int kb = 0; kb < KB; ++kb)
+                tma_load_4d(ring + (size_t)slot * C::kTile + kb * (kBN * 128), kv ? &p.tmV : &p.tmK, kb * 64, s0, walk.h, b,
+                            &full[slot], pol, once);
+            } else {
+              // A box for each page, of zeros for one that is not there.
+              const int shift = min(a.pages.shift, 7), rows = 1 << shift, at = slot_in_page(a.pages, s0);
+              if (C::kCodes) {
+                uint32_t scales = 0;
+#pragma unroll
+                for (int i = 0; i < kBN / kLeastPage; ++i) scales += pages[i] >= 0 ? (uint32_t)rows : 0u;
+                mbar_expect_tx(&full[slot], C::kStaged + scales);
+              } else {
+                mbar_expect_tx(&full[slot], C::kTile);
+              }
+#pragma unroll
+              for (int i = 0; i < kBN / kLeastPage; ++i) {
+                if (i << shift >= kBN) break;
+                if (C::kCodes) {
+                  tma_load_4d(in + (size_t)slot * C::kStaged + (size_t)(i << shift) * C::DP, kv ? &p.tmV : &p.tmK, 0, at, walk.h,
+                              pages[i], &full[slot], pol, once);
+                  if (pages[i] >= 0)
+                    bulk_copy_g2s(in_scale + slot * kBN + (i << shift),
+                                  (kv ? a.pages.v_scale : a.pages.k_scale) + scale_at(a.pages, hkv, pages[i], walk.h, s0),
+                                  (uint32_t)rows, &full[slot]);
+                } else {
+#pragma unroll
+                  for (int kb = 0; kb < KB; ++kb)
+                    tma_load_4d(ring + (size_t)slot * C::kTile + kb * (kBN * 128) + (size_t)(i << shift) * 128,
+                                kv ? &p.tmV : &p.tmK, kb * 64, at, walk.h, pages[i], &full[slot], pol, once);
+                }
+              }
+            }
             ++issued;
-            if (++slot == slots) { slot = 0; phase ^= 1u; }
+            if (++slot == in_slots) { slot = 0; phase ^= 1u; }
+          }
+          if (CACHE != kWhole) {
+#pragma unroll
+            for (int i = 0; i < kBN / kLeastPage; ++i) pages[i] = ahead[i];
           }
         }
         walk.next(w.cnt, hkv);
       }
       // The last copies land before the block ends, also where those who wait for them have given up.
-      for (long j = issued - 1; j >= 0 && j >= issued - slots; --j)
-        mbar_land(&full[j % slots], (uint32_t)((j / slots) & 1), ctl);
+      for (long j = issued - 1; j >= 0 && j >= issued - in_slots; --j)
+        mbar_land(&full[j % in_slots], (uint32_t)((j / in_slots) & 1), ctl);
     } else if (warp == 1) {
       const uint32_t id_s = idesc_bf16_f32(128, kBN);
       const uint32_t id_o = idesc_bf16_f32(128, C::DP) | (1u << 16);  // B is MN-major
@@ -527,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // NQ = 2: tile t + 1 of both groups after tile t; NQ = 1: tile t + 2 after tile t.
         constexpr int kAhead = NQ == 2 ? 1 : 2;
         for (int t = 0; t < kAhead && t < n && ok; ++t) {
-          wait(&full[ks], kph);
+          wait(&k_ready[ks], kph);
           if (!ok) break;
           if (NQ == 2) {
             scores(0, 0);
@@ -536,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             scores(0, t);
           }
           if (t + 1 == n) release(q_free);
-          release(&empty[ks]);
+          release(&freed[ks]);
           step(ks, kph);
         }
         for (int t = 0; t < n && ok; ++t) {
@@ -546,23 +634,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               values(g, t == 0, t + 1 == n);
-              if (more && g == 0) wait(&full[ks], kph);
+              if (more && g == 0) wait(&k_ready[ks], kph);
               if (!ok) break;
               if (more) scores(g, g);
             }
           } else {
             const int g = t & 1;
             values(g, t < 2, t + 2 >= n);
-            if (more) wait(&full[ks], kph);
+            if (more) wait(&k_ready[ks], kph);
             if (!ok) break;
             if (more) scores(0, g);
           }
           if (!ok) break;
-          release(&empty[vs]);
+          release(&freed[vs]);
           step(vs, vph);
           if (more) {
             if (t + kAhead + 1 == n) release(q_free);
-            release(&empty[ks]);
+            release(&freed[ks]);
             step(ks, kph);
           }
         }
@@ -575,6 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int t64 = threadIdx.x - 64;
     int slot = 1;
     uint32_t phase = 0, item = 0, boxes = 0;
+    int from = 0, to = 0;  // codes: the buffer they are in, and the one that they go to
+    uint32_t from_phase = 0, to_phase = 0;
     bool ok = true;
     Unit w;
     int cur = -1;
@@ -620,6 +710,66 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
+      }
+      if constexpr (C::kCodes) {
+        // Keys and values from codes to bf16, exactly: 16 codes of a slot at a time, swizzled as the MMA reads them.
+        constexpr int kPer = C::DP / 16, kRows = 64 / kPer;  // pieces of a slot, slots at a time (whole swizzle atoms)
+        const int piece = t64 % kPer, r0 = t64 / kPer;
+        // A piece is two units of 16 bytes; neighbours of the other half of the head begin with the second one, so that eight
+        // threads reach all banks.
+        const int odd = KB == 2 ? piece >> 2 : 0;
+        for (int k = k0; k < k1 && ok; ++k) {
+          const bool clean = !all_seen(a, w, w.kt.slot(k, kBN));
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = warp_wait(&full[from], from_phase, s_abort, ctl, p.timeout_ns) &&
+                 warp_wait(&freed[to], to_phase ^ 1u, s_abort, ctl, p.timeout_ns);
+            if (!ok) break;
+            const uint8_t* src = in + (size_t)from * C::kStaged + piece * 16;
+            const uint8_t* scale = in_scale + from * kBN;
+            uint8_t* dst = ring + (size_t)to * C::kTile + (piece >> 2) * (kBN * 128);
+            bool bad = false;
+#pragma unroll 4
+            for (int r = r0; r < kBN; r += kRows) {
+              const uint4 x = *(const uint4*)(src + r * C::DP);
+              const int byte = scale[r];
+              uint32_t f = (uint32_t)min(byte + 120, 254) * 0x00800080u;
+              if (byte == kScaleNan) f = 0x7fff7fffu;
+              uint2 y[4] = {codes_bf16(x.x, f), codes_bf16(x.y, f), codes_bf16(x.z, f), codes_bf16(x.w, f)};
+              if (byte > 134 && byte != kScaleNan) {  // the second factor
+                f = scale_bf16(byte).second;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = make_uint2(mul_bf16x2(y[i].x, f), mul_bf16x2(y[i].y, f));
+              }
+              if (kv && clean) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  bad |= bad16(y[i].x) | bad16(y[i].y);
+                  y[i] = make_uint2(clear16(y[i].x), clear16(y[i].y));
+                }
+              }
+              const uint4 u[2] = {make_uint4(y[0].x, y[0].y, y[1].x, y[1].y), make_uint4(y[2].x, y[2].y, y[3].x, y[3].y)};
+              const int unit = (piece & 3) * 2, sw = r & 7;
+              *(uint4*)(dst + r * 128 + (((unit + odd) ^ sw) << 4)) = odd ? u[1] : u[0];
+              *(uint4*)(dst + r * 128 + (((unit + 1 - odd) ^ sw) << 4)) = odd ? u[0] : u[1];
+            }
+            if (bad) {
+              s_bad[item & (kBadRing - 1)] = 1;
+              s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
+              __threadfence_block();
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&empty[from]);
+              mbar_arrive(kv ? &v_clean[to] : &k_ready[to]);
+            }
+            if (++from == in_slots) { from = 0; from_phase ^= 1u; }
+            if (++to == slots) { to = 0; to_phase ^= 1u; }
+          }
+        }
+        ++item;
+        continue;
       }
       // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
       // or a NaN in the product, so these are cleared here and the row tile is marked.
@@ -882,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         __threadfence_block();
         __syncwarp();  // a row's result may have been stored by other lanes
         if (live)
-          add_non_finite(a, w, b, h, k0, k1, i, low, mask_row, col0, col0 + kCols,
+          add_non_finite<CACHE>(a, w, b, h, k0, k1, i, low, mask_row, col0, col0 + kCols,
                          pieces > 1 ? nullptr : (__nv_bfloat16*)a.out + row * a.D,
                          p.o + (mine_at * NQ + (NQ == 2 ? g : 0)) * (C::DP / 4) * 128 + trow);
       }
@@ -1002,6 +1152,22 @@ bool make_tmap(CUtensorMap* tm, const void* base, const AttnArgs& a) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same for pages, {head_dim, slot, kv head, page}: boxes of 64 x 128 slots, or the page's; codes in boxes of whole heads, not swizzled.
+bool make_pages_tmap(CUtensorMap* tm, const void* base, const AttnArgs& a) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const bool codes = a.cache == kPagedE4m3;
+  const int size = codes ? 1 : 2, page = 1 << a.pages.shift;
+  cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)page, (cuuint64_t)a.hkv, (cuuint64_t)a.pages.n_pages};
+  const int64_t st[3] = {a.ss, a.hs, a.pages.page_stride};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] == 1 ? (cuuint64_t)((a.D * size + 15) / 16 * 16) : (cuuint64_t)(st[i] * size);
+  cuuint32_t box[4] = {(cuuint32_t)(codes && a.D > 64 ? 128 : 64), (cuuint32_t)(page < kBN ? page : kBN), 1, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(tm, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The queries or the output as {head_dim, head, row}, boxes of 64 elements of a group's heads of
 // packed / G rows.
 bool make_row_tmap(CUtensorMap* tm, const void* base, int packed, const AttnArgs& a) {
@@ -1016,12 +1182,14 @@ bool make_row_tmap(CUtensorMap* tm, const void* base, int packed, const AttnArgs
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NQ, int KB>
+template <int NQ, int KB, int CACHE>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
-  using C = Cfg<NQ, KB>;
+  using C = Cfg<NQ, KB, CACHE>;
   TcAttnP p;
   memset(&p, 0, sizeof(p));
-  if (!make_tmap(&p.tmK, a.k, a) || !make_tmap(&p.tmV, a.v, a)) return cudaErrorInvalidValue;
+  if (CACHE == kWhole ? !make_tmap(&p.tmK, a.k, a) || !make_tmap(&p.tmV, a.v, a)
+                      : !make_pages_tmap(&p.tmK, a.k, a) || !make_pages_tmap(&p.tmV, a.v, a))
+    return cudaErrorInvalidValue;
   p.q_boxes = make_row_tmap(&p.tmQ, a.q, 128, a) ? 1 : 0;
   p.o_boxes = NQ == 2 && make_row_tmap(&p.tmO, a.out, 32, a) ? 1 : 0;
   p.a = a;
@@ -1035,7 +1203,14 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   // Even: a buffer is always a key or always a value buffer, so every phase of a value
   // buffer is waited for by those who clear it.
   p.slots = slots > 12 ? 12 : slots & ~1;
-  const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + 3 * 1024;
+  size_t staged = 0;
+  if (C::kCodes) {
+    // Of the room for four buffers or more, codes take what is left beside two (prompts) or four of the MMA's.
+    p.slots = NQ == 2 && KB == 2 ? 2 : 4;
+    p.staged = std::min(8, (int)((budget - NQ * C::kQBytes - C::kStage - p.slots * C::kTile) / (C::kStaged + kBN)));
+    staged = (size_t)p.staged * (C::kStaged + kBN);
+  }
+  const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + staged + 3 * 1024;
   const int grid = num_sms();
   static_assert(NQ <= kCountersPerSm, "a counter for every tile that is cut");
   if ((int64_t)a.rows.batch * p.row_tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
@@ -1045,9 +1220,9 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   p.ml = (float2*)w;
   p.o = (float4*)(w + (size_t)2 * grid * C::BMT * 8);
   static FuncOnce once;
-  cudaError_t e = once.set((const void*)attn_tc_kernel<NQ, KB>, 227 * 1024, false);
+  cudaError_t e = once.set((const void*)attn_tc_kernel<NQ, KB, CACHE>, 227 * 1024, false);
   if (e != cudaSuccess) return e;
-  attn_tc_kernel<NQ, KB><<<grid, kThreads, smem, stream>>>(p);
+  attn_tc_kernel<NQ, KB, CACHE><<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -1062,17 +1237,23 @@ size_t attn_tc_ws_bytes(const AttnArgs& a) {
 // one entry with a stride of 0 (requests that share a cache), strides below 2^40 bytes.
 bool attn_tc_applies(const AttnArgs& a) {
   if (a.dtype != DOMINO_BF16 || a.D > 128) return false;
-  const int64_t st[3] = {a.ss, a.hs, a.rs};
-  const int n[3] = {a.rows.capacity, a.hkv, a.rows.batch};
+  const bool whole = a.cache == kWhole;
+  const int64_t st[3] = {a.ss, a.hs, whole ? a.rs : a.pages.page_stride};
+  const int n[3] = {whole ? a.rows.capacity : 1 << a.pages.shift, a.hkv, whole ? a.rows.batch : a.pages.n_pages};
   for (int i = 0; i < 3; ++i)
     if (n[i] > 1 && (st[i] == 0 || st[i] * 2 >= ((int64_t)1 << 40))) return false;
   return true;
 }
 
-cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t stream) {
+template <int CACHE>
+static cudaError_t launch_on(const AttnArgs& a, cudaStream_t stream) {
   const bool wide = a.D > 64;
-  if ((int64_t)a.rows.max_q * (a.hq / a.hkv) > 128) return wide ? launch_tc<2, 2>(a, stream) : launch_tc<2, 1>(a, stream);
-  return wide ? launch_tc<1, 2>(a, stream) : launch_tc<1, 1>(a, stream);
+  if ((int64_t)a.rows.max_q * (a.hq / a.hkv) > 128) return wide ? launch_tc<2, 2, CACHE>(a, stream) : launch_tc<2, 1, CACHE>(a, stream);
+  return wide ? launch_tc<1, 2, CACHE>(a, stream) : launch_tc<1, 1, CACHE>(a, stream);
+}
+cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t stream) {
+  return a.cache == kWhole ? launch_on<kWhole>(a, stream) : a.cache == kPaged ? launch_on<kPaged>(a, stream)
+                                                                             : launch_on<kPagedE4m3>(a, stream);
 }
 
 }  // namespace domino

@@ -573,9 +573,10 @@ domino_status domino_token_logprobs(int dtype, const void* logits, int64_t logit
  * of 16 bytes, not negative; pointers 16-byte aligned). head_dim is at most 256, a multiple of 8, or of 16 for DOMINO_E4M3.
  *   dtype      DOMINO_F32, DOMINO_BF16: the vectors as they are; DOMINO_E4M3: each head's vector of a slot as head_dim e4m3 codes
  *              and one scale, a power of two; its queries, new keys and values and outputs are DOMINO_BF16
- *   k_scale, v_scale  [n_pages, n_kv_heads, page_size] device uint8 (DOMINO_E4M3 only): E stands for 2^(E - 127), 255 for NaN
- *   page_table [batch, max_pages] device int32, rows table_stride apart. Entries that no slot of a call needs are not read, and
- *              requests may share pages that no call writes.
+ *   k_scale, v_scale  [n_pages, n_kv_heads, page_size] device uint8 (DOMINO_E4M3 only), 16-byte aligned: E stands for
+ *              2^(E - 127), 255 for NaN
+ *   page_table [batch, max_pages] device int32, rows table_stride apart. Entries that no slot of a call needs (behind the
+ *              last one, before the window) may be anything, and requests may share pages that no call writes.
  * Quantising x: with e the smallest exponent in [-100, 120] for which no |x_i| is above 448 * 2^e, the codes are x_i / 2^e rounded
  * to nearest even and E = e + 127; an x with an infinity or a NaN gets E = 255 and codes 0, and reads back as NaN. The e4m3 codes
  * 0x7f and 0xff, which quantising never gives, read back as 480 and -480; rows that see a slot with one may get NaN. Values below 2^-110 of any vector may become 0.

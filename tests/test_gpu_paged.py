@@ -526,6 +526,29 @@ def test_missing_pages_are_reported(kind, n, bad):
     assert torch.equal(out[n:], want)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,mode,sinks", [(1, "causal", 0), (1, "causal", 5), (4, "causal", 20), (16, "full", 0), (17, "tree", 3), (200, "causal", 0),
+                                          (200, "causal", 40)])
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 64), (256, 32)])
+def test_pages_before_the_window_may_be_gone(kind, n, mode, sinks, D, page):
+    """Their table entries are no pages any more, and nothing is reported."""
+    window, ctx = 70, [500, 90, 1000]
+    spec = ([n] * 3, ctx, 8, 2, D, mode, window, sinks, False, page)
+    lost = []
+
+    def prepare(pages, q):
+        for r, c in enumerate(ctx):
+            for j in range(pages.table.shape[1]):
+                if (j + 1) * page <= c - window + 1 and j * page >= sinks:
+                    pages.table[r, j] = -1 if j % 2 else 2 ** 31 - 1
+                    lost.append(j)
+
+    q, pages, p, seen, st, out, lse = run(kind, spec, 71 + n, prepare=prepare)
+    assert lost
+    pages.table.clamp_(min=0, max=pages.k.shape[0] - 1)
+    check(spec, q, pages, p, seen, st, out, lse)
+
+
 @pytest.mark.parametrize("kind", [E4M3, BF])
 def test_offsets_pass_32_bits(kind):
     """A pool of more than 2^31 elements, its last pages in use."""
