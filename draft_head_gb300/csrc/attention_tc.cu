@@ -73,6 +73,9 @@ struct TcAttnP {
   int row_tiles;  // per request, of 128 NQ packed rows
   int slots;      // ring buffers
   int staged;     // codes: buffers in which they arrive
+  int folded;     // pages: tmK and tmV are of whole heads (make_pages_tmap)
+  int64_t page_step, head_step;  // pages: their places along the last axis of tmK and tmV, and the first place behind it
+  int no_page;
   uint64_t timeout_ns;
   float c;        // scale log2(e)
   unsigned int* arrived;  // per CTA: pieces in, of the row tile that begins in it and goes on
@@ -224,12 +227,37 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int
                "r"(y), "r"(z), "r"(smem_u32(src))
                : "memory");
 }
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int x, int y, int z, int u, int v, uint64_t* bar,
+                                            uint64_t policy, bool hint) {
+  if (hint)
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+        "l"((uint64_t)tmap), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"((uint64_t)tmap), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(smem_u32(bar))
+        : "memory");
+}
+// How a key or value tile's atoms (8 slots of 64 elements, 1024 bytes) lie: from one to that of the next 8 slots, and to
+// that of the next 64 elements.
+struct Atoms {
+  uint32_t slots, elements;
+};
 // Shared-memory descriptor of an MN-major operand with 128-byte swizzle: rows of 64
 // elements of N, 8 rows (of K) per 1024-byte atom; the next 8 rows follow at the
-// stride offset, the next 64 elements of N at the leading offset (a whole 128-row block).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBN * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+// stride offset, the next 64 elements of N at the leading offset.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, Atoms at) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(at.elements >> 4) << 16) | ((uint64_t)(at.slots >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// The same of a K-major one, whose leading offset is unused.
+__device__ __forceinline__ uint64_t sdesc_k_atoms(uint32_t saddr, Atoms at) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(at.slots >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
 }
 __device__ __forceinline__ bool bad16(uint32_t x) {  // a bf16 pair with an infinity or a NaN in it
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
@@ -240,21 +268,15 @@ __device__ __forceinline__ uint32_t clear16(uint32_t x) {
   return x;
 }
 
-// The pages of the 128 slots from s0 on (one, where they are that large): -1 for one that is not there, which is reported, and -2
-// for those of whose slots the row tile looks at none.
+// The i-th page of the 128 slots from s0 on (one page, where they are that large) in lane i: -1 for one that is not there, -2 for
+// those of whose slots the row tile looks at none.
 constexpr int kLeastPage = 16;
-__device__ __forceinline__ void tile_pages(const AttnArgs& a, const Unit& w, int b, int s0, int (&pages)[kBN / kLeastPage]) {
-  const int shift = min(a.pages.shift, 7), end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_last + 1 : w.ctx + w.n;
-  const int from = first_slot(a.mode, w.low_min, w.ctx, end);
-#pragma unroll
-  for (int i = 0; i < kBN / kLeastPage; ++i) {
-    const int s = s0 + (i << shift);
-    const bool needed = i << shift < kBN && s < end && (s < a.sinks || s + (1 << shift) > from);
-    pages[i] = needed ? page_of(a.pages, b, s) : -2;
-  }
-#pragma unroll
-  for (int i = 0; i < kBN / kLeastPage; ++i)
-    if (pages[i] == -1) dev_error(a.ctl, DEV_ERR_DATA);
+__device__ __forceinline__ int tile_page(const AttnArgs& a, const Unit& w, int b, int s0) {
+  const int i = threadIdx.x & 31, shift = min(a.pages.shift, 7);
+  const int end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_last + 1 : w.ctx + w.n;
+  const int s = s0 + (i << shift);
+  const bool needed = i << shift < kBN && s < end && (s < a.sinks || s + (1 << shift) > first_slot(a.mode, w.low_min, w.ctx, end));
+  return needed ? page_of(a.pages, b, s) : -2;
 }
 
 // Visibility of the 128 slots from s0 for one row, as bits.
@@ -345,8 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   // The buffers that copies fill, `full` once they have: the ring's own, or codes on their way to it.
   const int in_slots = C::kCodes ? p.staged : slots;
   uint8_t* in = C::kCodes ? stage + C::kStage : ring;
-  uint8_t* in_scale = in + (C::kCodes ? (size_t)in_slots * C::kStaged : 0);  // codes: their slots' scales, kBN bytes a buffer
-  uint64_t* full = C::kCodes ? (uint64_t*)(in_scale + (size_t)in_slots * kBN) : (uint64_t*)(stage + C::kStage);
+  uint64_t* full = (uint64_t*)(stage + C::kStage + (C::kCodes ? (size_t)in_slots * C::kStaged : 0));
   uint64_t* empty = full + in_slots;
   // The ring's: keys ready, values ready, buffers read.
   uint64_t* v_clean = empty + in_slots;
@@ -476,7 +497,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   // (128 x 88 + 256 x 208 = 64512 = 384 x 168).
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0 && lane == 0) {
+    if (CACHE != kWhole && warp == 0) {
+      // Pages: the whole warp walks the list and one elected lane issues (from a branch on the lane number a copy takes about
+      // 280 cycles: 64 blocks over pages of 16 slots 415 us). Lane i has the number of a tile's i-th page, read a tile ahead.
+      const uint64_t pol = l2_policy_evict_first();
+      const bool once = p.row_tiles == 1, leader = elect_one();
+      const int shift = min(a.pages.shift, 7);
+      int slot = 0;
+      uint32_t phase = 0;
+      long issued = 0;
+      bool ok = true;
+      Unit w;
+      int cur = -1;
+      while (walk.len > 0 && walk.u < units && ok) {
+        if (walk.u != cur) w = load_unit<C::BMT>(a, p.row_tiles, cur = walk.u, false);
+        if (w.cnt == 0) { ++walk.u; continue; }
+        const int b = walk.u / p.row_tiles;
+        int k0, k1;
+        walk.part(w.cnt, k0, k1);
+        int page = k0 < k1 ? tile_page(a, w, b, w.kt.slot(k0, kBN)) : -2;
+        for (int k = k0; k < k1 && ok; ++k) {
+          const int at = slot_in_page(a.pages, w.kt.slot(k, kBN));
+          if (page == -1) dev_error(ctl, DEV_ERR_DATA);
+          const int place = page < 0 ? p.no_page : (int)(page * p.page_step + walk.h * p.head_step);
+          page = k + 1 < k1 ? tile_page(a, w, b, w.kt.slot(k + 1, kBN)) : -2;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = ok && warp_wait(&empty[slot], phase ^ 1u, s_abort, ctl, p.timeout_ns);
+            if (!ok) break;
+            const void* tm = kv ? &p.tmV : &p.tmK;
+            if (leader) mbar_expect_tx(&full[slot], C::kCodes ? C::kStaged : C::kTile);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kBN / kLeastPage; ++i) {
+              if (i << shift >= kBN) break;
+              const int to = __shfl_sync(0xffffffffu, place, i);
+              if (leader) {
+                if (C::kCodes) {
+                  tma_load_3d(in + (size_t)slot * C::kStaged + (size_t)(i << shift) * C::DP, tm, 0, at, to, &full[slot]);
+                } else if (KB == 2 && p.folded) {
+                  tma_load_5d(ring + (size_t)slot * C::kTile + (size_t)(i << shift) * 256, tm, 0, 0, 0, at / 8, to, &full[slot], pol, once);
+                } else {
+#pragma unroll
+                  for (int kb = 0; kb < KB; ++kb)
+                    tma_load_3d(ring + (size_t)slot * C::kTile + kb * (kBN * 128) + (size_t)(i << shift) * 128, tm, kb * 64, at, to,
+                                &full[slot]);
+                }
+              }
+              __syncwarp();
+            }
+            ++issued;
+            if (++slot == in_slots) { slot = 0; phase ^= 1u; }
+          }
+        }
+        walk.next(w.cnt, hkv);
+      }
+      // The last copies land before the block ends, as below.
+      for (long j = issued - 1; j >= 0 && j >= issued - in_slots; --j)
+        mbar_land(&full[j % in_slots], (uint32_t)((j / in_slots) & 1), ctl);
+    } else if (warp == 0 && lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
       const bool once = p.row_tiles == 1;  // no other row tile reads this cache again
       int slot = 0;
@@ -491,62 +570,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int b = walk.u / p.row_tiles;
         int k0, k1;
         walk.part(w.cnt, k0, k1);
-        int pages[kBN / kLeastPage], ahead[kBN / kLeastPage];
-        if (CACHE != kWhole && k0 < k1) tile_pages(a, w, b, w.kt.slot(k0, kBN), pages);
         for (int k = k0; k < k1 && ok; ++k) {
           const int s0 = w.kt.slot(k, kBN);
-          if (CACHE != kWhole && k + 1 < k1) tile_pages(a, w, b, w.kt.slot(k + 1, kBN), ahead);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             if (!mbar_wait(&empty[slot], phase ^ 1u, s_abort, ctl, p.timeout_ns)) { ok = false; break; }
-            if (CACHE == kWhole) {
-              mbar_expect_tx(&full[slot], C::kTile);
+            mbar_expect_tx(&full[slot], C::kTile);
 #pragma unroll
-              for (int kb = 0; kb < KB; ++kb)
-                tma_load_4d(ring + (size_t)slot * C::kTile + kb * (kBN * 128), kv ? &p.tmV : &p.tmK, kb * 64, s0, walk.h, b,
-                            &full[slot], pol, once);
-            } else {
-              // A box for each page, of zeros for one that is not there.
-              const int shift = min(a.pages.shift, 7), rows = 1 << shift, at = slot_in_page(a.pages, s0);
-              if (C::kCodes) {
-                uint32_t scales = 0;
-#pragma unroll
-                for (int i = 0; i < kBN / kLeastPage; ++i) scales += pages[i] >= 0 ? (uint32_t)rows : 0u;
-                mbar_expect_tx(&full[slot], C::kStaged + scales);
-              } else {
-                mbar_expect_tx(&full[slot], C::kTile);
-              }
-#pragma unroll
-              for (int i = 0; i < kBN / kLeastPage; ++i) {
-                if (i << shift >= kBN) break;
-                if (C::kCodes) {
-                  tma_load_4d(in + (size_t)slot * C::kStaged + (size_t)(i << shift) * C::DP, kv ? &p.tmV : &p.tmK, 0, at, walk.h,
-                              pages[i], &full[slot], pol, once);
-                  if (pages[i] >= 0)
-                    bulk_copy_g2s(in_scale + slot * kBN + (i << shift),
-                                  (kv ? a.pages.v_scale : a.pages.k_scale) + scale_at(a.pages, hkv, pages[i], walk.h, s0),
-                                  (uint32_t)rows, &full[slot]);
-                } else {
-#pragma unroll
-                  for (int kb = 0; kb < KB; ++kb)
-                    tma_load_4d(ring + (size_t)slot * C::kTile + kb * (kBN * 128) + (size_t)(i << shift) * 128,
-                                kv ? &p.tmV : &p.tmK, kb * 64, at, walk.h, pages[i], &full[slot], pol, once);
-                }
-              }
-            }
+            for (int kb = 0; kb < KB; ++kb)
+              tma_load_4d(ring + (size_t)slot * C::kTile + kb * (kBN * 128), kv ? &p.tmV : &p.tmK, kb * 64, s0, walk.h, b,
+                          &full[slot], pol, once);
             ++issued;
-            if (++slot == in_slots) { slot = 0; phase ^= 1u; }
-          }
-          if (CACHE != kWhole) {
-#pragma unroll
-            for (int i = 0; i < kBN / kLeastPage; ++i) pages[i] = ahead[i];
+            if (++slot == slots) { slot = 0; phase ^= 1u; }
           }
         }
         walk.next(w.cnt, hkv);
       }
       // The last copies land before the block ends, also where those who wait for them have given up.
-      for (long j = issued - 1; j >= 0 && j >= issued - in_slots; --j)
-        mbar_land(&full[j % in_slots], (uint32_t)((j / in_slots) & 1), ctl);
+      for (long j = issued - 1; j >= 0 && j >= issued - slots; --j)
+        mbar_land(&full[j % slots], (uint32_t)((j / slots) & 1), ctl);
     } else if (warp == 1) {
       const uint32_t id_s = idesc_bf16_f32(128, kBN);
       const uint32_t id_o = idesc_bf16_f32(128, C::DP) | (1u << 16);  // B is MN-major
@@ -565,16 +607,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (s >= slots) { s -= slots; ph ^= 1u; }
       };
       const uint32_t q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
+      const Atoms atoms = CACHE == kPaged && KB == 2 && p.folded ? Atoms{KB * 1024, 1024} : Atoms{1024, kBN * 128};
       auto scores = [&](int qt, int g) {  // S_g = Q K^T
         const uint64_t ad = sdesc_k_sw128(q_addr + (uint32_t)qt * C::kQBytes);
-        const uint64_t bd = sdesc_k_sw128(ring_addr + (uint32_t)ks * C::kTile);
+        const uint64_t bd = sdesc_k_atoms(ring_addr + (uint32_t)ks * C::kTile, atoms);
         if (leader) {
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               umma_bf16(tmem + (uint32_t)(g * 128), ad + (uint64_t)(kb * (128 * 128 / 16) + 2 * k),
-                        bd + (uint64_t)(kb * (kBN * 128 / 16) + 2 * k), id_s, (kb | k) ? 1u : 0u);
+                        bd + (uint64_t)(kb * (atoms.elements / 16) + 2 * k), id_s, (kb | k) ? 1u : 0u);
           umma_commit(&s_ready[g]);
         }
         __syncwarp();
@@ -584,12 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int half = 0; half < 2; ++half) {
           wait(&p_ready[g * 2 + half], done[g] & 1u);
           if (!ok) return;
-          const uint64_t bd = sdesc_mn_sw128(ring_addr + (uint32_t)vs * C::kTile + (uint32_t)(half * kHalf * 128));
+          const uint64_t bd = sdesc_mn_sw128(ring_addr + (uint32_t)vs * C::kTile + (uint32_t)half * (kHalf / 8) * atoms.slots, atoms);
           if (leader) {
 #pragma unroll
             for (int k = 0; k < kHalf / 16; ++k)
               umma_bf16_ts(tmem + kOCol + (uint32_t)(g * C::DP), tmem + (uint32_t)(g * 128 + half * (kHalf / 2) + 8 * k),
-                           bd + (uint64_t)(k * (16 * 128 / 16)), id_o, (first && half == 0 && k == 0) ? 0u : 1u);
+                           bd + (uint64_t)(k * (2 * atoms.slots / 16)), id_o, (first && half == 0 && k == 0) ? 0u : 1u);
             if (half == 1 && last) umma_commit(&o_done[g]);
           }
           __syncwarp();
@@ -671,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     while (walk.len > 0 && walk.u < units && ok) {
       if (walk.u != cur) w = load_unit<C::BMT>(a, p.row_tiles, cur = walk.u, false);
       if (w.cnt == 0) { ++walk.u; continue; }
-      const int h = walk.h;
+      const int b = walk.u / p.row_tiles, h = walk.h;
       int k0, k1;
       walk.part(w.cnt, k0, k1);
       walk.next(w.cnt, hkv);
@@ -718,45 +761,87 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // A piece is two units of 16 bytes; neighbours of the other half of the head begin with the second one, so that eight
         // threads reach all banks.
         const int odd = KB == 2 ? piece >> 2 : 0;
+        // Scales: a lane has those of slots 4 lane .. 4 lane + 3 of a tile's keys and values, read a tile ahead of it, the
+        // number of their page two tiles ahead. 2^0 where no row looks.
+        const int end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_last + 1 : w.ctx + w.n;
+        const int begin = first_slot(a.mode, w.low_min, w.ctx, end);
+        const int row_lane = r0 >> 2;  // + 2 i: the lane that has row r0 + 8 i, in byte r0 & 3 (kRows 8 or 16)
+        auto page_at = [&](int k) {
+          const int s = w.kt.slot(k, kBN) + 4 * lane;
+          return s < end && (s < a.sinks || s + 4 > begin) ? page_of(a.pages, b, s) : -1;
+        };
+        auto scales_at = [&](int k, int page, uint32_t (&x)[2]) {
+          const int64_t at = page < 0 ? 0 : scale_at(a.pages, hkv, page, h, w.kt.slot(k, kBN) + 4 * lane);
+          x[0] = page < 0 ? 0x7f7f7f7fu : __ldg((const uint32_t*)(a.pages.k_scale + at));
+          x[1] = page < 0 ? 0x7f7f7f7fu : __ldg((const uint32_t*)(a.pages.v_scale + at));
+        };
+        uint32_t scales[2], next[2] = {0, 0};
+        scales_at(k0, page_at(k0), scales);
+        int page = k0 + 1 < k1 ? page_at(k0 + 1) : -1;
         for (int k = k0; k < k1 && ok; ++k) {
           const bool clean = !all_seen(a, w, w.kt.slot(k, kBN));
-#pragma unroll 1
+          if (k + 1 < k1) scales_at(k + 1, page, next);
+          page = k + 2 < k1 ? page_at(k + 2) : -1;
+#pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             ok = warp_wait(&full[from], from_phase, s_abort, ctl, p.timeout_ns) &&
                  warp_wait(&freed[to], to_phase ^ 1u, s_abort, ctl, p.timeout_ns);
             if (!ok) break;
             const uint8_t* src = in + (size_t)from * C::kStaged + piece * 16;
-            const uint8_t* scale = in_scale + from * kBN;
             uint8_t* dst = ring + (size_t)to * C::kTile + (piece >> 2) * (kBN * 128);
-            bool bad = false;
-#pragma unroll 4
-            for (int r = r0; r < kBN; r += kRows) {
-              const uint4 x = *(const uint4*)(src + r * C::DP);
-              const int byte = scale[r];
-              uint32_t f = (uint32_t)min(byte + 120, 254) * 0x00800080u;
-              if (byte == kScaleNan) f = 0x7fff7fffu;
-              uint2 y[4] = {codes_bf16(x.x, f), codes_bf16(x.y, f), codes_bf16(x.z, f), codes_bf16(x.w, f)};
-              if (byte > 134 && byte != kScaleNan) {  // the second factor
-                f = scale_bf16(byte).second;
+            // Scales of more than 2^7 (or NaN) take a second factor.
+            const uint32_t most = __vmaxu4(scales[kv], __vmaxu4(scales[kv] >> 16, scales[kv] >> 8));
+            const bool plain = !__any_sync(0xffffffffu, max(most & 255u, scales[kv] >> 24) > 134u);
+            const int unit = (piece & 3) * 2, sw = r0 & 7;
+            uint8_t* to0 = dst + (((unit + odd) ^ sw) << 4);
+            uint8_t* to1 = dst + (((unit + 1 - odd) ^ sw) << 4);
+            if (plain) {
+              constexpr int kU = 4;
+#pragma unroll 1
+              for (int i0 = 0; i0 < kBN / kRows; i0 += kU) {
+                uint4 x[kU];
+                uint32_t f[kU];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = make_uint2(mul_bf16x2(y[i].x, f), mul_bf16x2(y[i].y, f));
-              }
-              if (kv && clean) {
+                for (int u = 0; u < kU; ++u) x[u] = *(const uint4*)(src + (r0 + (i0 + u) * kRows) * C::DP);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  bad |= bad16(y[i].x) | bad16(y[i].y);
-                  y[i] = make_uint2(clear16(y[i].x), clear16(y[i].y));
+                for (int u = 0; u < kU; ++u) {
+                  const uint32_t word = __shfl_sync(0xffffffffu, scales[kv], row_lane + (i0 + u) * (kRows / 4));
+                  f[u] = (((word >> (8 * (r0 & 3))) & 255u) + 120u) * 0x00800080u;
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                  const uint2 y[4] = {codes_bf16(x[u].x, f[u]), codes_bf16(x[u].y, f[u]), codes_bf16(x[u].z, f[u]),
+                                      codes_bf16(x[u].w, f[u])};
+                  const uint4 y0 = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y), y1 = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
+                  const int at = (r0 + (i0 + u) * kRows) * 128;
+                  *(uint4*)(to0 + at) = odd ? y1 : y0;
+                  *(uint4*)(to1 + at) = odd ? y0 : y1;
                 }
               }
-              const uint4 u[2] = {make_uint4(y[0].x, y[0].y, y[1].x, y[1].y), make_uint4(y[2].x, y[2].y, y[3].x, y[3].y)};
-              const int unit = (piece & 3) * 2, sw = r & 7;
-              *(uint4*)(dst + r * 128 + (((unit + odd) ^ sw) << 4)) = odd ? u[1] : u[0];
-              *(uint4*)(dst + r * 128 + (((unit + 1 - odd) ^ sw) << 4)) = odd ? u[0] : u[1];
-            }
-            if (bad) {
-              s_bad[item & (kBadRing - 1)] = 1;
-              s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
-              __threadfence_block();
+            } else {
+              bool bad = false;
+#pragma unroll 1
+              for (int i = 0; i < kBN / kRows; ++i) {
+                const uint4 x = *(const uint4*)(src + (r0 + i * kRows) * C::DP);
+                const uint32_t word = __shfl_sync(0xffffffffu, scales[kv], row_lane + i * (kRows / 4));
+                const Scale2 scale = scale_bf16((int)((word >> (8 * (r0 & 3))) & 255u));
+                uint4 y[2] = {codes8_bf16(make_uint2(x.x, x.y), scale), codes8_bf16(make_uint2(x.z, x.w), scale)};
+                if (kv && clean) {
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    bad |= bad16(y[e].x) | bad16(y[e].y) | bad16(y[e].z) | bad16(y[e].w);
+                    y[e] = make_uint4(clear16(y[e].x), clear16(y[e].y), clear16(y[e].z), clear16(y[e].w));
+                  }
+                }
+                const int at = (r0 + i * kRows) * 128;
+                *(uint4*)(to0 + at) = odd ? y[1] : y[0];
+                *(uint4*)(to1 + at) = odd ? y[0] : y[1];
+              }
+              if (bad) {
+                s_bad[item & (kBadRing - 1)] = 1;
+                s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
+                __threadfence_block();
+              }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -767,40 +852,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (++from == in_slots) { from = 0; from_phase ^= 1u; }
             if (++to == slots) { to = 0; to_phase ^= 1u; }
           }
+          scales[0] = next[0];
+          scales[1] = next[1];
         }
-        ++item;
-        continue;
-      }
-      // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
-      // or a NaN in the product, so these are cleared here and the row tile is marked.
-      for (int k = k0; k < k1; ++k) {
-        ok = warp_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns);
-        if (!ok) break;
-        if (!all_seen(a, w, w.kt.slot(k, kBN))) {
-          uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
-          bool bad = false;
-#pragma unroll 8
-          for (uint32_t x = t64; x < C::kTile / 16; x += 64) {
-            uint4 y = v[x];
-            if (bad16(y.x) | bad16(y.y) | bad16(y.z) | bad16(y.w)) {
-              bad = true;
-              uint16_t* e = (uint16_t*)&v[x];
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+      } else {
+        // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
+        // or a NaN in the product, so these are cleared here and the row tile is marked.
+        for (int k = k0; k < k1; ++k) {
+          ok = warp_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns);
+          if (!ok) break;
+          if (!all_seen(a, w, w.kt.slot(k, kBN))) {
+            uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
+            bool bad = false;
+  #pragma unroll 8
+            for (uint32_t x = t64; x < C::kTile / 16; x += 64) {
+              uint4 y = v[x];
+              if (bad16(y.x) | bad16(y.y) | bad16(y.z) | bad16(y.w)) {
+                bad = true;
+                uint16_t* e = (uint16_t*)&v[x];
+  #pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+              }
             }
+            if (bad) {
+              s_bad[item & (kBadRing - 1)] = 1;
+              s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
+              __threadfence_block();
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
-          if (bad) {
-            s_bad[item & (kBadRing - 1)] = 1;
-            s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
-            __threadfence_block();
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_clean[slot]);
+          slot += 2;
+          if (slot >= slots) { slot -= slots; phase ^= 1u; }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_clean[slot]);
-        slot += 2;
-        if (slot >= slots) { slot -= slots; phase ^= 1u; }
       }
       ++item;
     }
@@ -1152,19 +1238,41 @@ bool make_tmap(CUtensorMap* tm, const void* base, const AttnArgs& a) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The same for pages, {head_dim, slot, kv head, page}: boxes of 64 x 128 slots, or the page's; codes in boxes of whole heads, not swizzled.
-bool make_pages_tmap(CUtensorMap* tm, const void* base, const AttnArgs& a) {
+// The same for pages. A copy has a cost of its own, so a page's heads are taken whole: pages and kv heads are one axis, in steps of their
+// strides' common divisor, and bf16 heads of 128 are {64 elements, 8 slots, half, groups of 8 slots, place}, which lands as swizzle
+// atoms of the two halves in turn. Codes are {head_dim, slot, place}, not swizzled; other heads {head_dim, slot, place} in
+// boxes of 64.
+int64_t divisor(int64_t x, int64_t y) { return y == 0 ? x : divisor(y, x % y); }
+bool page_places(const AttnArgs& a, int64_t* unit, int64_t* places) {
+  const int64_t ps = a.pages.n_pages > 1 ? a.pages.page_stride : 0, hs = a.hkv > 1 ? a.hs : 0;
+  *unit = std::max<int64_t>(divisor(ps, hs), 16);
+  *places = (a.pages.n_pages - 1) * (ps / *unit) + (a.hkv - 1) * (hs / *unit) + 1;
+  return *places < 0x7fffffff;
+}
+bool make_pages_tmap(TcAttnP& p, CUtensorMap* tm, const void* base, const AttnArgs& a) {
   EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
+  int64_t unit, places;
+  if (!fn || !page_places(a, &unit, &places)) return false;
   const bool codes = a.cache == kPagedE4m3;
-  const int size = codes ? 1 : 2, page = 1 << a.pages.shift;
-  cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)page, (cuuint64_t)a.hkv, (cuuint64_t)a.pages.n_pages};
-  const int64_t st[3] = {a.ss, a.hs, a.pages.page_stride};
-  cuuint64_t strides[3];
-  for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] == 1 ? (cuuint64_t)((a.D * size + 15) / 16 * 16) : (cuuint64_t)(st[i] * size);
-  cuuint32_t box[4] = {(cuuint32_t)(codes && a.D > 64 ? 128 : 64), (cuuint32_t)(page < kBN ? page : kBN), 1, 1}, estr[4] = {1, 1, 1, 1};
-  return fn(tm, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
-            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+  const int size = codes ? 1 : 2, page = 1 << a.pages.shift, box_slots = page < kBN ? page : kBN;
+  p.folded = !codes && a.D == 128;
+  p.no_page = (int)places;
+  p.page_step = a.pages.n_pages > 1 ? a.pages.page_stride / unit : 0;
+  p.head_step = a.hkv > 1 ? a.hs / unit : 0;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const auto type = codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto swizzle = codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (p.folded) {
+    const cuuint64_t dims[5] = {64, 8, 2, (cuuint64_t)(page / 8), (cuuint64_t)places};
+    const cuuint64_t strides[4] = {(cuuint64_t)(a.ss * 2), 128, (cuuint64_t)(a.ss * 16), (cuuint64_t)(unit * 2)};
+    const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)(box_slots / 8), 1};
+    return fn(tm, type, 5, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)page, (cuuint64_t)places};
+  const cuuint64_t strides[2] = {(cuuint64_t)(a.ss * size), (cuuint64_t)(unit * size)};
+  const cuuint32_t box[3] = {(cuuint32_t)(codes && a.D > 64 ? 128 : 64), (cuuint32_t)box_slots, 1};
+  return fn(tm, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1188,7 +1296,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   TcAttnP p;
   memset(&p, 0, sizeof(p));
   if (CACHE == kWhole ? !make_tmap(&p.tmK, a.k, a) || !make_tmap(&p.tmV, a.v, a)
-                      : !make_pages_tmap(&p.tmK, a.k, a) || !make_pages_tmap(&p.tmV, a.v, a))
+                      : !make_pages_tmap(p, &p.tmK, a.k, a) || !make_pages_tmap(p, &p.tmV, a.v, a))
     return cudaErrorInvalidValue;
   p.q_boxes = make_row_tmap(&p.tmQ, a.q, 128, a) ? 1 : 0;
   p.o_boxes = NQ == 2 && make_row_tmap(&p.tmO, a.out, 32, a) ? 1 : 0;
@@ -1207,8 +1315,8 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   if (C::kCodes) {
     // Of the room for four buffers or more, codes take what is left beside two (prompts) or four of the MMA's.
     p.slots = NQ == 2 && KB == 2 ? 2 : 4;
-    p.staged = std::min(8, (int)((budget - NQ * C::kQBytes - C::kStage - p.slots * C::kTile) / (C::kStaged + kBN)));
-    staged = (size_t)p.staged * (C::kStaged + kBN);
+    p.staged = std::min(8, (int)((budget - NQ * C::kQBytes - C::kStage - p.slots * C::kTile) / C::kStaged));
+    staged = (size_t)p.staged * C::kStaged;
   }
   const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + staged + 3 * 1024;
   const int grid = num_sms();
@@ -1242,7 +1350,8 @@ bool attn_tc_applies(const AttnArgs& a) {
   const int n[3] = {whole ? a.rows.capacity : 1 << a.pages.shift, a.hkv, whole ? a.rows.batch : a.pages.n_pages};
   for (int i = 0; i < 3; ++i)
     if (n[i] > 1 && (st[i] == 0 || st[i] * 2 >= ((int64_t)1 << 40))) return false;
-  return true;
+  int64_t unit, places;
+  return whole || page_places(a, &unit, &places);
 }
 
 template <int CACHE>

@@ -20,7 +20,8 @@ constexpr int kScaleNan = 255;                   // a vector that held an infini
 
 // Page of slot s of request b, or -1 for one that is not there.
 __device__ __forceinline__ int page_of(const PagesArgs& p, int b, int s) {
-  const int page = __ldg(p.table + (int64_t)b * p.table_stride + (s >> p.shift));
+  int page;  // read where it is asked for: the compiler would move it to its use, behind other waits
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(page) : "l"(p.table + (int64_t)b * p.table_stride + (s >> p.shift)));
   return (unsigned)page < (unsigned)p.n_pages ? page : -1;
 }
 __device__ __forceinline__ int slot_in_page(const PagesArgs& p, int s) { return s & ((1 << p.shift) - 1); }
