@@ -268,16 +268,19 @@ __device__ __forceinline__ uint32_t clear16(uint32_t x) {
   return x;
 }
 
-// The i-th page of the 128 slots from s0 on (one page, where they are that large) in lane i: -1 for one that is not there, -2 for
-// those of whose slots the row tile looks at none.
+// The page of the `n` slots from s0 + x on, which lie in one, of the key tile at s0: -1 for one that is not there, -2 where the row tile
+// looks at none of them.
 constexpr int kLeastPage = 16;
-__device__ __forceinline__ int tile_page(const AttnArgs& a, const Unit& w, int b, int s0) {
-  const int i = threadIdx.x & 31, shift = min(a.pages.shift, 7);
-  const int end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_last + 1 : w.ctx + w.n;
-  const int s = s0 + (i << shift);
-  const bool needed = i << shift < kBN && s < end && (s < a.sinks || s + (1 << shift) > first_slot(a.mode, w.low_min, w.ctx, end));
+__device__ __forceinline__ int tile_page(const AttnArgs& a, const Unit& w, int b, int s0, int x, int n) {
+  const int end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_last + 1 : w.ctx + w.n, s = s0 + x;
+  const bool needed = x < kBN && s < end && (s < a.sinks || s + n > first_slot(a.mode, w.low_min, w.ctx, end));
   return needed ? page_of(a.pages, b, s) : -2;
 }
+
+// Codes: what goes with a tile to those who turn it into bf16.
+constexpr uint32_t kNotePlain = 1, kNoteValues = 2, kNoteClean = 4, kNoteEnd = 8;  // all scales take one factor; values, some row does not see all; no tile
+constexpr int kNoteItem = 4;                                                     // from this bit on: the row tile's number
+constexpr uint32_t kSecondFactor = 0xffff0000u;  // with a scale's byte: it takes two factors, or is NaN
 
 // Visibility of the 128 slots from s0 for one row, as bits.
 __device__ __forceinline__ void seen_bits(const AttnArgs& a, const Unit& w, int i, int low, const uint8_t* mask_row, int s0,
@@ -344,6 +347,10 @@ struct Cfg {
   static constexpr int DP = 64 * KB;
   static constexpr bool kCodes = CACHE == kPagedE4m3;
   static constexpr uint32_t kStaged = (uint32_t)kBN * DP;  // bytes of a tile of codes
+  static constexpr int kThreads = kCodes ? 512 : 384;
+  // Registers: launched with 65,536 / kThreads a thread; the softmax's 8 warps take kMore, the others keep kLess
+  // (256 x 208 + 128 x 88 = 64,512 = 384 x 168; 256 x 200 + 256 x 56 = 65,536).
+  static constexpr int kMore = kCodes ? 200 : 208, kLess = kCodes ? 56 : 88;
   static constexpr int BMT = 128 * NQ;
   // List places of a row tile beside its key tiles: its start and epilogue take about 11,000 cycles, a key
   // tile 2,000 (NQ = 1) or 3,200. Two more than that for prompts measured best (2: 497 us, 6: 465, 8: 450,
@@ -353,12 +360,12 @@ struct Cfg {
   static constexpr uint32_t kQBytes = (uint32_t)KB * 128 * 128;  // bytes of a query tile
   static constexpr uint32_t kStage = NQ == 2 ? 8 * 4096 : 0;     // output on its way out
 };
-constexpr int kThreads = 384;
 constexpr uint32_t kOCol = 256;  // TMEM: S of group g at 128 g, O of group g at kOCol + DP g
 
 template <int NQ, int KB, int CACHE>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnP p) {
+__global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnP p) {
   using C = Cfg<NQ, KB, CACHE>;
+  constexpr int kThreads = C::kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* ring = sQ + NQ * C::kQBytes;
@@ -367,7 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   // The buffers that copies fill, `full` once they have: the ring's own, or codes on their way to it.
   const int in_slots = C::kCodes ? p.staged : slots;
   uint8_t* in = C::kCodes ? stage + C::kStage : ring;
-  uint64_t* full = (uint64_t*)(stage + C::kStage + (C::kCodes ? (size_t)in_slots * C::kStaged : 0));
+  uint32_t* in_factors = (uint32_t*)(in + (C::kCodes ? (size_t)in_slots * C::kStaged : 0));  // codes: [in_slots][kBN] factors
+  volatile uint32_t* in_notes = in_factors + (C::kCodes ? in_slots * kBN : 0);                // and [8] notes
+  uint64_t* full = C::kCodes ? (uint64_t*)(in_notes + 8) : (uint64_t*)(stage + C::kStage);
   uint64_t* empty = full + in_slots;
   // The ring's: keys ready, values ready, buffers read.
   uint64_t* v_clean = empty + in_slots;
@@ -397,12 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   if (threadIdx.x == 0) {
     for (int s = 0; s < in_slots; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], C::kCodes ? 2 : 1);
+      mbar_init(&empty[s], C::kCodes ? 4 : 1);
     }
     for (int s = 0; s < slots; ++s) {
-      mbar_init(&v_clean[s], 2);
+      mbar_init(&v_clean[s], C::kCodes ? 4 : 2);
       if (C::kCodes) {
-        mbar_init(&k_ready[s], 2);
+        mbar_init(&k_ready[s], 4);
         mbar_init(&freed[s], 1);
       }
     }
@@ -493,18 +502,90 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     walk.k = (int)(in - (int64_t)walk.h * c);
   }
 
-  // Registers: launched with 168 a thread; 4 warps keep 88, 8 warps take 208
-  // (128 x 88 + 256 x 208 = 64512 = 384 x 168).
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (CACHE != kWhole && warp == 0) {
+  if (warp < 4 || warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLess));
+    if (C::kCodes && warp >= 12) {
+      // Keys and values from codes to bf16, exactly: 16 codes of a slot at a time, swizzled as the MMA reads them. What these warps
+      // need to know of a tile comes with it, so that nothing else takes their registers.
+      constexpr int kPer = C::DP / 16, kRows = 128 / kPer;  // pieces of a slot, slots at a time (whole swizzle atoms)
+      const int piece = (threadIdx.x & 127) % kPer, r0 = (threadIdx.x & 127) / kPer;
+      // A piece is two units of 16 bytes; neighbours of the other half of the head begin with the second one, so that eight
+      // threads reach all banks.
+      const int odd = KB == 2 ? piece >> 2 : 0, unit = (piece & 3) * 2, sw = r0 & 7;
+      const uint32_t src0 = (uint32_t)(r0 * C::DP + piece * 16);
+      const uint32_t dst0 = (uint32_t)((piece >> 2) * (kBN * 128) + r0 * 128 + (((unit + odd) ^ sw) << 4));
+      const uint32_t dst1 = (uint32_t)((piece >> 2) * (kBN * 128) + r0 * 128 + (((unit + 1 - odd) ^ sw) << 4));
+      int from = 0, to = 0;  // the buffer that codes are in, and the one that they go to
+      uint32_t from_phase = 0, to_phase = 0;
+      while (warp_wait(&full[from], from_phase, s_abort, ctl, p.timeout_ns)) {
+        const uint32_t note = in_notes[from];
+        if (note & kNoteEnd) break;
+        if (!warp_wait(&freed[to], to_phase ^ 1u, s_abort, ctl, p.timeout_ns)) break;
+        const uint8_t* src = in + (size_t)from * C::kStaged + src0;
+        const uint32_t* factor = in_factors + from * kBN + r0;
+        uint8_t* dst = ring + (size_t)to * C::kTile;
+        if (note & kNotePlain) {
+          constexpr int kU = 4;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kBN / kRows; i0 += kU) {
+            uint4 x[kU];
+            uint32_t f[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              x[u] = *(const uint4*)(src + (i0 + u) * (kRows * C::DP));
+              f[u] = factor[(i0 + u) * kRows];
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              const uint2 y[4] = {codes_bf16(x[u].x, f[u]), codes_bf16(x[u].y, f[u]), codes_bf16(x[u].z, f[u]), codes_bf16(x[u].w, f[u])};
+              const uint4 y0 = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y), y1 = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
+              *(uint4*)(dst + dst0 + (i0 + u) * (kRows * 128)) = odd ? y1 : y0;
+              *(uint4*)(dst + dst1 + (i0 + u) * (kRows * 128)) = odd ? y0 : y1;
+            }
+          }
+        } else {
+          bool bad = false;
+#pragma unroll 1
+          for (int i = 0; i < kBN / kRows; ++i) {
+            const uint4 x = *(const uint4*)(src + i * (kRows * C::DP));
+            const uint32_t f = factor[i * kRows];
+            const Scale2 scale = f >= kSecondFactor ? scale_bf16((int)(f & 255u)) : Scale2{f, 0};
+            uint4 y[2] = {codes8_bf16(make_uint2(x.x, x.y), scale), codes8_bf16(make_uint2(x.z, x.w), scale)};
+            if (note & kNoteClean) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                bad |= bad16(y[e].x) | bad16(y[e].y) | bad16(y[e].z) | bad16(y[e].w);
+                y[e] = make_uint4(clear16(y[e].x), clear16(y[e].y), clear16(y[e].z), clear16(y[e].w));
+              }
+            }
+            *(uint4*)(dst + dst0 + i * (kRows * 128)) = odd ? y[1] : y[0];
+            *(uint4*)(dst + dst1 + i * (kRows * 128)) = odd ? y[0] : y[1];
+          }
+          if (bad) {
+            s_bad[(note >> kNoteItem) & (kBadRing - 1)] = 1;
+            s_bad[kBadRing + ((note >> kNoteItem) & (kBadRing - 1))] = 1;
+            __threadfence_block();
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&empty[from]);
+          mbar_arrive(note & kNoteValues ? &v_clean[to] : &k_ready[to]);
+        }
+        if (++from == in_slots) { from = 0; from_phase ^= 1u; }
+        if (++to == slots) { to = 0; to_phase ^= 1u; }
+      }
+    } else if (CACHE != kWhole && warp == 0) {
       // Pages: the whole warp walks the list and one elected lane issues (from a branch on the lane number a copy takes about
       // 280 cycles: 64 blocks over pages of 16 slots 415 us). Lane i has the number of a tile's i-th page, read a tile ahead.
+      // Codes: the lane has the scales of slots 4 lane .. 4 lane + 3 of the tile's keys and values too, read a tile ahead, the
+      // number of their page two tiles ahead; 2^0 where no row looks.
       const uint64_t pol = l2_policy_evict_first();
       const bool once = p.row_tiles == 1, leader = elect_one();
       const int shift = min(a.pages.shift, 7);
       int slot = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, item = 0;
       long issued = 0;
       bool ok = true;
       Unit w;
@@ -515,17 +596,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int b = walk.u / p.row_tiles;
         int k0, k1;
         walk.part(w.cnt, k0, k1);
-        int page = k0 < k1 ? tile_page(a, w, b, w.kt.slot(k0, kBN)) : -2;
+        int page = k0 < k1 ? tile_page(a, w, b, w.kt.slot(k0, kBN), lane << shift, 1 << shift) : -2;
+        uint32_t scales[2] = {}, scales_next[2] = {};
+        int scale_page = -2;
+        auto scales_at = [&](int k, int in_page, uint32_t (&x)[2]) {
+          const int64_t at = in_page < 0 ? 0 : scale_at(a.pages, hkv, in_page, walk.h, w.kt.slot(k, kBN) + 4 * lane);
+          x[0] = in_page < 0 ? 0x7f7f7f7fu : __ldg((const uint32_t*)(a.pages.k_scale + at));
+          x[1] = in_page < 0 ? 0x7f7f7f7fu : __ldg((const uint32_t*)(a.pages.v_scale + at));
+        };
+        if (C::kCodes && k0 < k1) {
+          scales_at(k0, tile_page(a, w, b, w.kt.slot(k0, kBN), 4 * lane, 4), scales_next);
+          if (k0 + 1 < k1) scale_page = tile_page(a, w, b, w.kt.slot(k0 + 1, kBN), 4 * lane, 4);
+        }
         for (int k = k0; k < k1 && ok; ++k) {
-          const int at = slot_in_page(a.pages, w.kt.slot(k, kBN));
+          const int s0 = w.kt.slot(k, kBN), at = slot_in_page(a.pages, s0);
           if (page == -1) dev_error(ctl, DEV_ERR_DATA);
           const int place = page < 0 ? p.no_page : (int)(page * p.page_step + walk.h * p.head_step);
-          page = k + 1 < k1 ? tile_page(a, w, b, w.kt.slot(k + 1, kBN)) : -2;
+          page = k + 1 < k1 ? tile_page(a, w, b, w.kt.slot(k + 1, kBN), lane << shift, 1 << shift) : -2;
+          if (C::kCodes) {
+            scales[0] = scales_next[0];
+            scales[1] = scales_next[1];
+            if (k + 1 < k1) scales_at(k + 1, scale_page, scales_next);
+            if (k + 2 < k1) scale_page = tile_page(a, w, b, w.kt.slot(k + 2, kBN), 4 * lane, 4);
+          }
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             ok = ok && warp_wait(&empty[slot], phase ^ 1u, s_abort, ctl, p.timeout_ns);
             if (!ok) break;
             const void* tm = kv ? &p.tmV : &p.tmK;
+            if (C::kCodes) {
+              uint32_t f[4], most = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t byte = (scales[kv] >> (8 * i)) & 255u;
+                most = max(most, byte);
+                f[i] = byte > 134u ? kSecondFactor | byte : (byte + 120u) * 0x00800080u;
+              }
+              *(uint4*)(in_factors + slot * kBN + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+              const bool plain = __all_sync(0xffffffffu, most <= 134u);
+              if (lane == 0)
+                in_notes[slot] = (plain ? kNotePlain : 0u) | (kv ? kNoteValues : 0u) | (kv && !all_seen(a, w, s0) ? kNoteClean : 0u) |
+                                 item << kNoteItem;
+              __syncwarp();
+            }
             if (leader) mbar_expect_tx(&full[slot], C::kCodes ? C::kStaged : C::kTile);
             __syncwarp();
 #pragma unroll
@@ -551,9 +664,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
         }
         walk.next(w.cnt, hkv);
+        if (k0 < k1) ++item;
       }
-      // The last copies land before the block ends, as below.
-      for (long j = issued - 1; j >= 0 && j >= issued - in_slots; --j)
+      if (C::kCodes) {  // no more tiles
+        ok = ok && warp_wait(&empty[slot], phase ^ 1u, s_abort, ctl, p.timeout_ns);
+        if (ok && lane == 0) {
+          in_notes[slot] = kNoteEnd;
+          mbar_arrive(&full[slot]);
+        }
+      }
+      // The last copies land before the block ends, as below. (The one that was in the end's buffer has been read.)
+      for (long j = issued - 1; j >= 0 && j >= issued - in_slots + (C::kCodes && ok ? 1 : 0); --j)
         mbar_land(&full[j % in_slots], (uint32_t)((j / in_slots) & 1), ctl);
     } else if (warp == 0 && lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
@@ -706,15 +827,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int t64 = threadIdx.x - 64;
     int slot = 1;
     uint32_t phase = 0, item = 0, boxes = 0;
-    int from = 0, to = 0;  // codes: the buffer they are in, and the one that they go to
-    uint32_t from_phase = 0, to_phase = 0;
     bool ok = true;
     Unit w;
     int cur = -1;
     while (walk.len > 0 && walk.u < units && ok) {
       if (walk.u != cur) w = load_unit<C::BMT>(a, p.row_tiles, cur = walk.u, false);
       if (w.cnt == 0) { ++walk.u; continue; }
-      const int b = walk.u / p.row_tiles, h = walk.h;
+      const int h = walk.h;
       int k0, k1;
       walk.part(w.cnt, k0, k1);
       walk.next(w.cnt, hkv);
@@ -754,146 +873,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
       }
-      if constexpr (C::kCodes) {
-        // Keys and values from codes to bf16, exactly: 16 codes of a slot at a time, swizzled as the MMA reads them.
-        constexpr int kPer = C::DP / 16, kRows = 64 / kPer;  // pieces of a slot, slots at a time (whole swizzle atoms)
-        const int piece = t64 % kPer, r0 = t64 / kPer;
-        // A piece is two units of 16 bytes; neighbours of the other half of the head begin with the second one, so that eight
-        // threads reach all banks.
-        const int odd = KB == 2 ? piece >> 2 : 0;
-        // Scales: a lane has those of slots 4 lane .. 4 lane + 3 of a tile's keys and values, read a tile ahead of it, the
-        // number of their page two tiles ahead. 2^0 where no row looks.
-        const int end = a.mode == DOMINO_MASK_CAUSAL ? w.ctx + w.i_last + 1 : w.ctx + w.n;
-        const int begin = first_slot(a.mode, w.low_min, w.ctx, end);
-        const int row_lane = r0 >> 2;  // + 2 i: the lane that has row r0 + 8 i, in byte r0 & 3 (kRows 8 or 16)
-        auto page_at = [&](int k) {
-          const int s = w.kt.slot(k, kBN) + 4 * lane;
-          return s < end && (s < a.sinks || s + 4 > begin) ? page_of(a.pages, b, s) : -1;
-        };
-        auto scales_at = [&](int k, int page, uint32_t (&x)[2]) {
-          const int64_t at = page < 0 ? 0 : scale_at(a.pages, hkv, page, h, w.kt.slot(k, kBN) + 4 * lane);
-          x[0] = page < 0 ? 0x7f7f7f7fu : __ldg((const uint32_t*)(a.pages.k_scale + at));
-          x[1] = page < 0 ? 0x7f7f7f7fu : __ldg((const uint32_t*)(a.pages.v_scale + at));
-        };
-        uint32_t scales[2], next[2] = {0, 0};
-        scales_at(k0, page_at(k0), scales);
-        int page = k0 + 1 < k1 ? page_at(k0 + 1) : -1;
-        for (int k = k0; k < k1 && ok; ++k) {
-          const bool clean = !all_seen(a, w, w.kt.slot(k, kBN));
-          if (k + 1 < k1) scales_at(k + 1, page, next);
-          page = k + 2 < k1 ? page_at(k + 2) : -1;
+      // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
+      // or a NaN in the product, so these are cleared here and the row tile is marked.
+      for (int k = k0; k < k1 && !C::kCodes; ++k) {  // codes: whoever turns them into bf16 clears them
+        ok = warp_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns);
+        if (!ok) break;
+        if (!all_seen(a, w, w.kt.slot(k, kBN))) {
+          uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
+          bool bad = false;
+#pragma unroll 8
+          for (uint32_t x = t64; x < C::kTile / 16; x += 64) {
+            uint4 y = v[x];
+            if (bad16(y.x) | bad16(y.y) | bad16(y.z) | bad16(y.w)) {
+              bad = true;
+              uint16_t* e = (uint16_t*)&v[x];
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = warp_wait(&full[from], from_phase, s_abort, ctl, p.timeout_ns) &&
-                 warp_wait(&freed[to], to_phase ^ 1u, s_abort, ctl, p.timeout_ns);
-            if (!ok) break;
-            const uint8_t* src = in + (size_t)from * C::kStaged + piece * 16;
-            uint8_t* dst = ring + (size_t)to * C::kTile + (piece >> 2) * (kBN * 128);
-            // Scales of more than 2^7 (or NaN) take a second factor.
-            const uint32_t most = __vmaxu4(scales[kv], __vmaxu4(scales[kv] >> 16, scales[kv] >> 8));
-            const bool plain = !__any_sync(0xffffffffu, max(most & 255u, scales[kv] >> 24) > 134u);
-            const int unit = (piece & 3) * 2, sw = r0 & 7;
-            uint8_t* to0 = dst + (((unit + odd) ^ sw) << 4);
-            uint8_t* to1 = dst + (((unit + 1 - odd) ^ sw) << 4);
-            if (plain) {
-              constexpr int kU = 4;
-#pragma unroll 1
-              for (int i0 = 0; i0 < kBN / kRows; i0 += kU) {
-                uint4 x[kU];
-                uint32_t f[kU];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) x[u] = *(const uint4*)(src + (r0 + (i0 + u) * kRows) * C::DP);
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                  const uint32_t word = __shfl_sync(0xffffffffu, scales[kv], row_lane + (i0 + u) * (kRows / 4));
-                  f[u] = (((word >> (8 * (r0 & 3))) & 255u) + 120u) * 0x00800080u;
-                }
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                  const uint2 y[4] = {codes_bf16(x[u].x, f[u]), codes_bf16(x[u].y, f[u]), codes_bf16(x[u].z, f[u]),
-                                      codes_bf16(x[u].w, f[u])};
-                  const uint4 y0 = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y), y1 = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
-                  const int at = (r0 + (i0 + u) * kRows) * 128;
-                  *(uint4*)(to0 + at) = odd ? y1 : y0;
-                  *(uint4*)(to1 + at) = odd ? y0 : y1;
-                }
-              }
-            } else {
-              bool bad = false;
-#pragma unroll 1
-              for (int i = 0; i < kBN / kRows; ++i) {
-                const uint4 x = *(const uint4*)(src + (r0 + i * kRows) * C::DP);
-                const uint32_t word = __shfl_sync(0xffffffffu, scales[kv], row_lane + i * (kRows / 4));
-                const Scale2 scale = scale_bf16((int)((word >> (8 * (r0 & 3))) & 255u));
-                uint4 y[2] = {codes8_bf16(make_uint2(x.x, x.y), scale), codes8_bf16(make_uint2(x.z, x.w), scale)};
-                if (kv && clean) {
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    bad |= bad16(y[e].x) | bad16(y[e].y) | bad16(y[e].z) | bad16(y[e].w);
-                    y[e] = make_uint4(clear16(y[e].x), clear16(y[e].y), clear16(y[e].z), clear16(y[e].w));
-                  }
-                }
-                const int at = (r0 + i * kRows) * 128;
-                *(uint4*)(to0 + at) = odd ? y[1] : y[0];
-                *(uint4*)(to1 + at) = odd ? y[0] : y[1];
-              }
-              if (bad) {
-                s_bad[item & (kBadRing - 1)] = 1;
-                s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
-                __threadfence_block();
-              }
+              for (int j = 0; j < 8; ++j)
+                if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&empty[from]);
-              mbar_arrive(kv ? &v_clean[to] : &k_ready[to]);
-            }
-            if (++from == in_slots) { from = 0; from_phase ^= 1u; }
-            if (++to == slots) { to = 0; to_phase ^= 1u; }
           }
-          scales[0] = next[0];
-          scales[1] = next[1];
-        }
-      } else {
-        // Values of tiles that not every row sees: a weight of 0 does not stop an infinity
-        // or a NaN in the product, so these are cleared here and the row tile is marked.
-        for (int k = k0; k < k1; ++k) {
-          ok = warp_wait(&full[slot], phase, s_abort, ctl, p.timeout_ns);
-          if (!ok) break;
-          if (!all_seen(a, w, w.kt.slot(k, kBN))) {
-            uint4* v = (uint4*)(ring + (size_t)slot * C::kTile);
-            bool bad = false;
-  #pragma unroll 8
-            for (uint32_t x = t64; x < C::kTile / 16; x += 64) {
-              uint4 y = v[x];
-              if (bad16(y.x) | bad16(y.y) | bad16(y.z) | bad16(y.w)) {
-                bad = true;
-                uint16_t* e = (uint16_t*)&v[x];
-  #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
-              }
-            }
-            if (bad) {
-              s_bad[item & (kBadRing - 1)] = 1;
-              s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
-              __threadfence_block();
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (bad) {
+            s_bad[item & (kBadRing - 1)] = 1;
+            s_bad[kBadRing + (item & (kBadRing - 1))] = 1;
+            __threadfence_block();
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_clean[slot]);
-          slot += 2;
-          if (slot >= slots) { slot -= slots; phase ^= 1u; }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_clean[slot]);
+        slot += 2;
+        if (slot >= slots) { slot -= slots; phase ^= 1u; }
       }
       ++item;
     }
     if (boxes > 0) mbar_land(q_ready, (boxes - 1u) & 1u, ctl);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMore));
     const int g = (warp - 4) >> 2;  // group
     const int quarter = warp & 3;   // TMEM lanes this warp reaches
     const int trow = quarter * 32 + lane, r_in = (NQ == 2 ? g * 128 : 0) + trow;
@@ -950,6 +966,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         ok = warp_wait(&s_ready[g], tiles & 1u, s_abort, ctl, p.timeout_ns);
         if (!ok) break;
         tc_fence_after();
+        if (r_in - lane >= w.rows) {  // no row of the tile is this warp's: its weights may be anything
+          tc_fence_before();
+          __syncwarp();
+          if (lane < 2) mbar_arrive(&p_ready[g * 2 + lane]);
+          continue;
+        }
         uint32_t s[kBN];
 #pragma unroll
         for (int c = 0; c < kBN; c += 32) tmem_ld32_nowait(s_col + c, s + c);
@@ -1315,8 +1337,8 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   if (C::kCodes) {
     // Of the room for four buffers or more, codes take what is left beside two (prompts) or four of the MMA's.
     p.slots = NQ == 2 && KB == 2 ? 2 : 4;
-    p.staged = std::min(8, (int)((budget - NQ * C::kQBytes - C::kStage - p.slots * C::kTile) / C::kStaged));
-    staged = (size_t)p.staged * C::kStaged;
+    p.staged = std::min(8, (int)((budget - NQ * C::kQBytes - C::kStage - p.slots * C::kTile) / (C::kStaged + kBN * 4)));
+    staged = (size_t)p.staged * (C::kStaged + kBN * 4);
   }
   const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + staged + 3 * 1024;
   const int grid = num_sms();
@@ -1330,7 +1352,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   static FuncOnce once;
   cudaError_t e = once.set((const void*)attn_tc_kernel<NQ, KB, CACHE>, 227 * 1024, false);
   if (e != cudaSuccess) return e;
-  attn_tc_kernel<NQ, KB, CACHE><<<grid, kThreads, smem, stream>>>(p);
+  attn_tc_kernel<NQ, KB, CACHE><<<grid, C::kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
