@@ -278,8 +278,8 @@ __device__ __forceinline__ int tile_page(const AttnArgs& a, const Unit& w, int b
 }
 
 // Codes: what goes with a tile to those who turn it into bf16.
-constexpr uint32_t kNotePlain = 1, kNoteValues = 2, kNoteClean = 4, kNoteEnd = 8;  // all scales take one factor; values, some row does not see all; no tile
-constexpr int kNoteItem = 4;                                                     // from this bit on: the row tile's number
+constexpr uint32_t kNotePlain = 1, kNoteClean = 2, kNoteEnd = 4;  // all scales take one factor; values that some row does not see; no tile
+constexpr int kNoteItem = 3;                                      // from this bit on: the row tile's number
 constexpr uint32_t kSecondFactor = 0xffff0000u;  // with a scale's byte: it takes two factors, or is NaN
 
 // Visibility of the 128 slots from s0 for one row, as bits.
@@ -349,8 +349,9 @@ struct Cfg {
   static constexpr uint32_t kStaged = (uint32_t)kBN * DP;  // bytes of a tile of codes
   static constexpr int kThreads = kCodes ? 512 : 384;
   // Registers: launched with 65,536 / kThreads a thread; the softmax's 8 warps take kMore, the others keep kLess
-  // (256 x 208 + 128 x 88 = 64,512 = 384 x 168; 256 x 200 + 256 x 56 = 65,536).
-  static constexpr int kMore = kCodes ? 200 : 208, kLess = kCodes ? 56 : 88;
+  // (256 x 208 + 128 x 88 = 64,512 = 384 x 168; 256 x (200 + 56) = 256 x (192 + 64) = 65,536: chunks 507 us with 200, 482 with
+  // 192, 16 trees 86 and 85, 64 blocks 241 and 246).
+  static constexpr int kMore = kCodes ? (NQ == 2 ? 192 : 200) : 208, kLess = kCodes ? (NQ == 2 ? 64 : 56) : 88;
   static constexpr int BMT = 128 * NQ;
   // List places of a row tile beside its key tiles: its start and epilogue take about 11,000 cycles, a key
   // tile 2,000 (NQ = 1) or 3,200. Two more than that for prompts measured best (2: 497 us, 6: 465, 8: 450,
@@ -380,8 +381,8 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
   uint64_t* empty = full + in_slots;
   // The ring's: keys ready, values ready, buffers read.
   uint64_t* v_clean = empty + in_slots;
-  uint64_t* k_ready = C::kCodes ? v_clean + slots : full;
-  uint64_t* freed = C::kCodes ? k_ready + slots : empty;
+  uint64_t* k_ready = C::kCodes ? v_clean : full;
+  uint64_t* freed = C::kCodes ? v_clean + slots : empty;
   uint64_t* s_ready = (C::kCodes ? freed : v_clean) + slots;  // [2]: per group
   uint64_t* p_ready = s_ready + 2;      // [4]: per group and half
   uint64_t* o_done = p_ready + 4;       // [2]: per group, once per row tile
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
   int64_t* s_prefix = (int64_t*)(drain + 1);
   int64_t* s_scan = s_prefix + 1;       // [kThreads / 32]
   float2* s_ml = (float2*)(s_scan + kThreads / 32);  // [2][128] NQ = 1: the groups' (m, l)
-  int* s_unit = (int*)(s_ml + 256);
+  int* s_unit = (int*)(s_ml + (NQ == 1 || !C::kCodes ? 256 : 0));
   int* s_cnt = s_unit + 1;
   int* s_last = s_cnt + 1;              // [2]
   volatile int* s_bad = s_last + 2;     // [2][kBadRing]
@@ -410,10 +411,7 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
     }
     for (int s = 0; s < slots; ++s) {
       mbar_init(&v_clean[s], C::kCodes ? 4 : 2);
-      if (C::kCodes) {
-        mbar_init(&k_ready[s], 4);
-        mbar_init(&freed[s], 1);
-      }
+      if (C::kCodes) mbar_init(&freed[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_ready[s], 1);
@@ -571,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&empty[from]);
-          mbar_arrive(note & kNoteValues ? &v_clean[to] : &k_ready[to]);
+          mbar_arrive(&v_clean[to]);
         }
         if (++from == in_slots) { from = 0; from_phase ^= 1u; }
         if (++to == slots) { to = 0; to_phase ^= 1u; }
@@ -635,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
               *(uint4*)(in_factors + slot * kBN + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
               const bool plain = __all_sync(0xffffffffu, most <= 134u);
               if (lane == 0)
-                in_notes[slot] = (plain ? kNotePlain : 0u) | (kv ? kNoteValues : 0u) | (kv && !all_seen(a, w, s0) ? kNoteClean : 0u) |
+                in_notes[slot] = (plain ? kNotePlain : 0u) | (kv && !all_seen(a, w, s0) ? kNoteClean : 0u) |
                                  item << kNoteItem;
               __syncwarp();
             }
@@ -1328,19 +1326,23 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   // Masked scores are -inf before they are multiplied and have to stay so with a scale of 0: the smallest normal factor
   // instead, which brings products of up to 2^120 to within 2^-6 of 0.
   p.c = fmaxf(a.scale * kLog2e, 1.17549435e-38f);
-  const uint32_t budget = (227 - 3) * 1024;
+  // Beside the tiles: barriers, notes and (NQ = 1) the groups' maxima and sums.
+  constexpr uint32_t kSmall = NQ == 2 && C::kCodes ? 1024 : 3 * 1024;
+  const uint32_t budget = 227 * 1024 - kSmall;
   int slots = (int)((budget - NQ * C::kQBytes - C::kStage) / C::kTile);
   // Even: a buffer is always a key or always a value buffer, so every phase of a value
   // buffer is waited for by those who clear it.
   p.slots = slots > 12 ? 12 : slots & ~1;
   size_t staged = 0;
   if (C::kCodes) {
-    // Of the room for four buffers or more, codes take what is left beside two (prompts) or four of the MMA's.
-    p.slots = NQ == 2 && KB == 2 ? 2 : 4;
+    // Of the room for four buffers or more, codes take what is left beside three (prompts; with two, the next tile's values wait for
+    // the last product with this one's) or four of the MMA's. Three in turn are keys and values alike, which prompts may: their
+    // products take the buffers in the order in which they are filled.
+    p.slots = NQ == 2 && KB == 2 ? 3 : 4;
     p.staged = std::min(8, (int)((budget - NQ * C::kQBytes - C::kStage - p.slots * C::kTile) / (C::kStaged + kBN * 4)));
     staged = (size_t)p.staged * (C::kStaged + kBN * 4);
   }
-  const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + staged + 3 * 1024;
+  const size_t smem = (size_t)NQ * C::kQBytes + (size_t)p.slots * C::kTile + C::kStage + staged + kSmall;
   const int grid = num_sms();
   static_assert(NQ <= kCountersPerSm, "a counter for every tile that is cut");
   if ((int64_t)a.rows.batch * p.row_tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
