@@ -2,14 +2,15 @@
 // (domino_token_logprobs; the definition is in domino.h).
 //
 // One pass over the row. With m the maximum so far, d = (x - m) / T in log2 units and w = 2^d, a thread keeps S = sum w and
-// E = sum w d; when m rises by r, E' = 2^-r (E - r S) and S' = 2^-r S. Then
+// E = sum w d; when m / T rises by r, E' = 2^-r (E - r S) and S' = 2^-r S. Then
 //   log sum exp = m / T + log S,   entropy = log S - E / S,   log p(t) = (x_t - m) / T - log S,
 // and as m is the true maximum d <= 0, so that both terms of the entropy are >= 0 and nothing cancels.
 //   Rank: the given token's logit is known beforehand; tokens before it in (logit, id) are counted, in the batches of a warp that
 //     have one.
-//   Most likely tokens: a warp holds its best 32 (value, id) keys, one a lane, sorted. A batch of 32 lanes' values is looked at
-//     only if one reaches the bound, the largest that any warp of the block knows: its n-th key, or the n-th largest of its
-//     lanes' maxima, which n tokens reach.
+//   Most likely tokens: the pass leaves every thread's maxima of up to 16 stretches of its tokens in shared memory. The n-th largest of
+//     the threads' maxima is reached by n tokens, so only stretches that reach it (hardly more than n) are read again, and what
+//     reaches it there is sorted. (Collected on the way, in 32 (value, id) keys a warp, they took longer than the rest: 1088
+//     rows 109 us without and 182 with the 8 most likely.)
 // A cluster of CTAs takes a row when there are few; their results meet in the first one's shared memory.
 #include <math.h>
 
@@ -54,12 +55,14 @@ __device__ __forceinline__ float4 dsmem_f4(uint32_t at) {
   return x;
 }
 
-// The sums of part of a row; `m` the maximum of its logits, S and E in units of log2.
+// The sums of part of a row; `m` the maximum of its logits. S and E are in units of log2 from m c as it is rounded, so that d is one
+// multiply-add from the logit and the rounding is nobody's error; where m c is beyond fp32, from m.
 struct Sums {
   float m, S, E;
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m
     if (to == m) return;
-    const float r = (m - to) * c, f = ex2(r);
+    const float at = to * c;
+    const float r = isinf(at) ? (m - to) * c : fmaf(-1.0f, at, m * c), f = ex2(r);
     E = f == 0.0f ? 0.0f : f * fmaf(r, S, E);
     S *= f;
     m = to;
@@ -99,6 +102,16 @@ __device__ __forceinline__ float sorted_down(float x) {
   return x;
 }
 // The 32 largest of two sorted lists, sorted.
+__device__ __forceinline__ float merged(float a, float b) {
+  const int lane = threadIdx.x & 31;
+  float x = fmaxf(a, __shfl_sync(kAll, b, 31 - lane));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const float y = __shfl_xor_sync(kAll, x, d);
+    x = (lane & d) == 0 ? fmaxf(x, y) : fminf(x, y);
+  }
+  return x;
+}
 __device__ __forceinline__ u64 merged(u64 a, u64 b) {
   const int lane = threadIdx.x & 31;
   const u64 r = __shfl_sync(kAll, b, 31 - lane);
@@ -111,56 +124,97 @@ __device__ __forceinline__ u64 merged(u64 a, u64 b) {
   return x;
 }
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // A row's elements in units of 16 aligned bytes: unit u holds elements [u kVec - skew, + kVec).
 template <typename T>
 struct Units {
   static constexpr int kVec = 16 / sizeof(T);
   const T* row;
   int V, skew, units;
+  int whole0, whole1;  // units [whole0, whole1) are the row's alone
   __device__ __forceinline__ Units(const T* r, int n) : row(r), V(n) {
     skew = (int)(((uintptr_t)r & 15) / sizeof(T));
     units = (int)(((int64_t)skew + V + kVec - 1) / kVec);
+    whole0 = skew ? 1 : 0;
+    whole1 = (int)(((int64_t)skew + V) / kVec);
   }
   __device__ __forceinline__ int64_t first(int u) const { return (int64_t)u * kVec - skew; }
-  // Elements that are not the row's are -inf, and not read.
-  __device__ __forceinline__ uint4 load(int u, int end) const {
-    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-    uint4 x = make_uint4(none, none, none, none);
-    if (u >= end) return x;
-    const int64_t i0 = first(u);
-    if (i0 >= 0 && i0 + kVec <= V) {
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(row + i0));
+  // Units u, u + kThr, ... of which those from `end` on are -inf, as are elements that are not the row's; neither is read.
+  template <int kUnits>
+  __device__ __forceinline__ void load(int batch, int end, uint4 (&x)[kUnits]) const {
+    const int u = batch + (int)threadIdx.x;
+    if (batch >= whole0 && batch + kUnits * kThr <= min(whole1, end)) {
+      const uint4* at = (const uint4*)(row - skew) + u;
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[j].x), "=r"(x[j].y), "=r"(x[j].z), "=r"(x[j].w)
+                     : "l"(at + j * kThr));
     } else {
-      uint32_t w[4] = {none, none, none, none};
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        if (i0 + e < 0 || i0 + e >= V) continue;
-        if (sizeof(T) == 2) {
-          const uint32_t y = *(const uint16_t*)(row + i0 + e);
-          w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | y << 16 : (w[e / 2] & 0xffff0000u) | y;
-        } else {
-          w[e & 3] = *(const uint32_t*)(row + i0 + e);
-        }
-      }
-      x = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < kUnits; ++j) x[j] = load_some(u + j * kThr, end);
     }
-    return x;
   }
-  static __device__ __forceinline__ void values(const uint4& x, float* v) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  __device__ __noinline__ uint4 load_some(int u, int end) const {
+    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    if (u >= end) return make_uint4(none, none, none, none);
+    if (u >= whole0 && u < whole1) return __ldg((const uint4*)(row - skew) + u);
+    const int64_t i0 = first(u);
+    uint32_t w[4] = {none, none, none, none};
 #pragma unroll
-    for (int e = 0; e < kVec; ++e)
-      v[e] = sizeof(T) == 4 ? __uint_as_float(w[e & 3]) : __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    for (int e = 0; e < kVec; ++e) {
+      if (i0 + e < 0 || i0 + e >= V) continue;
+      if (sizeof(T) == 2) {
+        const uint32_t y = *(const uint16_t*)(row + i0 + e);
+        w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | y << 16 : (w[e / 2] & 0xffff0000u) | y;
+      } else {
+        w[e & 3] = *(const uint32_t*)(row + i0 + e);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ float value(const uint4& x, int e) {
+    const uint32_t w = sizeof(T) == 4 ? (e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w)
+                                      : (e < 2 ? x.x : e < 4 ? x.y : e < 6 ? x.z : x.w);
+    return sizeof(T) == 4 ? __uint_as_float(w) : __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+  }
+  // The largest of kUnits units; a NaN counts as -inf.
+  template <int kUnits>
+  static __device__ __forceinline__ float largest(const uint4 (&x)[kUnits]) {
+    if (sizeof(T) == 2) {
+      uint32_t m = 0xff80ff80u;
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) m = max_bf16x2(m, max_bf16x2(max_bf16x2(x[j].x, x[j].y), max_bf16x2(x[j].z, x[j].w)));
+      return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j)
+      m = max3(m, max3(__uint_as_float(x[j].x), __uint_as_float(x[j].y), -INFINITY),
+               max3(__uint_as_float(x[j].z), __uint_as_float(x[j].w), -INFINITY));
+    return m;
   }
 };
 
+constexpr int kStretches = 16;
 struct Smem {
+  union {
+    float tops[kStretches][kThr];  // of each stretch of a thread's tokens
+    u64 list[kWarps][32];          // after them
+  };
   u64 buf[kWarps][64];
-  u64 list[kWarps][32];
-  u64 bound;       // keys that are not above it are not among the best
+  float warp_tops[kWarps][32];
+  float reached;
   Sums sums[kWarps];
   int count[kWarps];
-  float4 part;     // the CTA's m, S, E and rank (its bits)
+  int works;
+  uint16_t work[kStretches * kThr];  // stretches to be read again
+  float4 part;                       // the CTA's m, S, E and rank (its bits)
   u64 best[32];
 };
 
@@ -172,7 +226,7 @@ __device__ __forceinline__ float below(float x) {
 template <typename T, int kUnits>
 __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int size) {
   using U = Units<T>;
-  constexpr int kVec = U::kVec, kN = kUnits * kVec;
+  constexpr int kVec = U::kVec;
   __shared__ Smem s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = size > 1 ? (int)cluster_rank() : 0, r = blockIdx.x / size;
@@ -185,133 +239,159 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
   const int token = a.tokens ? a.tokens[r] : -1;
   const bool given = token >= 0 && token < a.V;
   const float xt = given ? fmaxf(to_f<T>(row[token]), -INFINITY) : INFINITY;  // a NaN counts as -inf
-  const float xt_below = below(xt);
   const int n = a.top_n;
   const u64 least = value_id_key(-INFINITY, 0);
-  if (threadIdx.x == 0) s.bound = least;
-  __syncthreads();
+  if (threadIdx.x == 0) s.works = 0;
 
   Sums q = {-INFINITY, 0.0f, 0.0f};
-  int before = 0, held = 0;
-  float lane_top = -INFINITY;
-  u64 best = 0, bound = least;
-  volatile u64* s_bound = &s.bound;
-  u64* buf = s.buf[warp];
+  int before = 0;
+  constexpr int kBatch = kUnits * kThr;  // units
+  const int batches = (u1 - u0 + kBatch - 1) / kBatch, stretch = max(1, (batches + kStretches - 1) / kStretches);  // in batches
+  float here = -INFINITY, thread_top = -INFINITY;  // of the stretch, of all
+  int in_stretch = 0, stretches = 0;
 
-  auto take = [&](int count) {  // the first `count` (32 at most) of the buffer into the list
-    __syncwarp();
-    const u64 x = lane < count ? buf[lane] : 0;
-    best = merged(best, sorted_down(x));
-    const u64 nth = __shfl_sync(kAll, best, n - 1);
-    if (nth > bound) bound = nth;
-    __syncwarp();
-    if (lane < held - count) buf[lane] = buf[count + lane];
-    held -= count;
-    __syncwarp();
-    if (lane == 0) atomicMax(&s.bound, bound);
+  uint4 cur[kUnits], next[kUnits];
+  // One of them by a number that the compiler does not know: the paths that few batches take are loops over units, or
+  // their code, once for every element, would not fit the instruction cache (1088 rows 235 us).
+  auto unit = [&](int j) {
+    uint4 x = cur[0];
+#pragma unroll
+    for (int i = 1; i < kUnits; ++i)
+      if (i == j) x = cur[i];
+    return x;
   };
-
-  uint4 next[kUnits];
-#pragma unroll
-  for (int j = 0; j < kUnits; ++j) next[j] = u.load(u0 + j * kThr + (int)threadIdx.x, u1);
+  u.template load<kUnits>(u0, u1, next);
 #pragma unroll 1
-  for (int ub = u0; ub < u1; ub += kUnits * kThr) {
-    float x[kN];
+  for (int ub = u0; ub < u1; ub += kBatch) {
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) U::values(next[j], x + j * kVec);
-    const int mine = ub + (int)threadIdx.x;  // unit j of this thread: mine + j kThr
-    if (ub + kUnits * kThr < u1) {
-#pragma unroll
-      for (int j = 0; j < kUnits; ++j) next[j] = u.load(mine + (kUnits + j) * kThr, u1);
-    }
-    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int e = 0; e < kN; e += 8)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], x[e + k], x[e + 4 + k]);
-    const float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+    for (int j = 0; j < kUnits; ++j) cur[j] = next[j];
+    if (ub + kBatch < u1) u.template load<kUnits>(ub + kBatch, u1, next);
+    const float top = U::template largest<kUnits>(cur);
 
     if (__any_sync(kAll, top >= xt)) {
-      if (xt == -INFINITY) {
+      const int mine = ub + (int)threadIdx.x;  // unit j of this thread: mine + j kThr
+      const float xt_below = below(xt);
+#pragma unroll 1
+      for (int j = 0; j < kUnits; ++j) {
+        const uint4 x = unit(j);
+        const int64_t id = u.first(mine + j * kThr);
+        if (xt == -INFINITY) {
 #pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          const int64_t id = u.first(mine + (e / kVec) * kThr) + e % kVec;
-          const bool there = mine + (e / kVec) * kThr < u1 && id >= 0 && id < a.V;
-          before += there && (x[e] > xt || id < token) ? 1 : 0;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kUnits; ++j) {
-          const int64_t id = u.first(mine + j * kThr);
+          for (int e = 0; e < kVec; ++e) {
+            const bool there = mine + j * kThr < u1 && id + e >= 0 && id + e < a.V;
+            before += there && (U::value(x, e) > xt || id + e < token) ? 1 : 0;
+          }
+        } else {
           const float over = id + kVec <= token ? xt_below : xt;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) before += x[j * kVec + e] > over ? 1 : 0;
+          for (int e = 0; e < kVec; ++e) before += U::value(x, e) > over ? 1 : 0;
           if (id < token && id + kVec > token) {  // the unit of the token itself: its equals before it
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) before += x[j * kVec + e] == xt && id + e < token ? 1 : 0;
+            for (int e = 0; e < kVec; ++e) before += U::value(x, e) == xt && id + e < token ? 1 : 0;
           }
         }
       }
     }
 
-    if (n > 0) {
-      const u64 known = __shfl_sync(kAll, *s_bound, 0);
-      if (known > bound) bound = known;
-      if (__any_sync(kAll, top >= key_value(bound))) {
-        lane_top = fmaxf(lane_top, top);
-        // n tokens at least reach the n-th largest of the lanes' maxima.
-        const float nth = __shfl_sync(kAll, sorted_down(lane_top), n - 1);
-        const u64 reached = (u64)float_order_key(nth) << 32;  // before every token of that value
-        if (nth > -INFINITY && reached > bound) bound = reached;
-        if (lane == 0) atomicMax(&s.bound, bound);
-#pragma unroll
-        for (int j = 0; j < kUnits; ++j) {
-          const float at_least = key_value(bound);
-          float unit_top = x[j * kVec];
-#pragma unroll
-          for (int e = 1; e < kVec; ++e) unit_top = fmaxf(unit_top, x[j * kVec + e]);
-          if (!__any_sync(kAll, unit_top >= at_least)) continue;
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            const float v = x[j * kVec + e];
-            const unsigned hit = __ballot_sync(kAll, v >= at_least);
-            if (!hit) continue;
-            const u64 key = v >= at_least ? value_id_key(v, (uint32_t)(u.first(mine + j * kThr) + e)) : 0;
-            const unsigned in = __ballot_sync(kAll, key > bound);
-            if (key > bound) buf[held + __popc(in & ((1u << lane) - 1u))] = key;
-            held += __popc(in);
-            if (held >= 32) take(32);
-          }
-        }
-      } else {
-        lane_top = fmaxf(lane_top, top);
-      }
+    here = fmaxf(here, top);
+    if (n > 0 && (++in_stretch == stretch || ub + kBatch >= u1)) {
+      s.tops[stretches++][threadIdx.x] = here;
+      thread_top = fmaxf(thread_top, here);
+      here = -INFINITY;
+      in_stretch = 0;
     }
 
     q.raise(fmaxf(q.m, top), c);
-    if (top == INFINITY) {  // they share everything
+    const float m = q.m == -INFINITY ? 0.0f : q.m, at = m * c;
+    if (isinf(at)) {
+#pragma unroll 1
+      for (int j = 0; j < kUnits; ++j) {
+        const uint4 x = unit(j);
 #pragma unroll
-      for (int e = 0; e < kN; ++e) q.S += x[e] == INFINITY ? 1.0f : 0.0f;
+        for (int e = 0; e < kVec; ++e) {  // infinities share everything
+          const float v = U::value(x, e), d = v == m ? 0.0f : fmaxf((v - m) * c, kLeastD), w = ex2(d);
+          q.S += w;
+          q.E = fmaf(w, d, q.E);
+        }
+      }
     } else {
-      const float m = q.m == -INFINITY ? 0.0f : q.m;
-      const float2 m2 = make_float2(-m, -m), c2 = make_float2(c, c);
+      const float2 c2 = make_float2(c, c), n2 = make_float2(-at, -at);
       float2 S2 = make_float2(q.S, 0.0f), E2 = make_float2(q.E, 0.0f);
 #pragma unroll
-      for (int e = 0; e < kN; e += 2) {
-        float2 d = mul2(add2(make_float2(x[e], x[e + 1]), m2), c2);
-        d.x = fmaxf(d.x, kLeastD);
-        d.y = fmaxf(d.y, kLeastD);
-        const float2 w = make_float2(ex2(d.x), ex2(d.y));
-        S2 = add2(S2, w);
-        E2 = fma2(w, d, E2);
-      }
+      for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) {
+          float2 d = fma2(make_float2(U::value(cur[j], e), U::value(cur[j], e + 1)), c2, n2);
+          d.x = fmaxf(d.x, kLeastD);
+          d.y = fmaxf(d.y, kLeastD);
+          const float2 w = make_float2(ex2(d.x), ex2(d.y));
+          S2 = add2(S2, w);
+          E2 = fma2(w, d, E2);
+        }
       q.S = S2.x + S2.y;
       q.E = E2.x + E2.y;
     }
   }
-  while (held > 0) take(min(held, 32));
 
-  // The warp's, the block's, the cluster's.
+  u64 best = 0;
+  if (n > 0) {
+    // n tokens at least reach the n-th largest of the threads' maxima.
+    float t = sorted_down(thread_top);
+    s.warp_tops[warp][lane] = t;
+    __syncthreads();
+#pragma unroll 1
+    for (int step = kWarps / 2; step > 0; step >>= 1) {
+      if (warp < step) {
+        t = merged(t, s.warp_tops[warp + step][lane]);
+        s.warp_tops[warp][lane] = t;
+      }
+      if (step == 1 && warp == 0 && lane == n - 1) s.reached = t;
+      __syncthreads();
+    }
+    const float reached = s.reached;
+    for (int k = 0; k < stretches; ++k) {
+      const float top = s.tops[k][threadIdx.x];
+      if (top >= reached && top > -INFINITY) s.work[atomicAdd(&s.works, 1)] = (uint16_t)(k * kThr + threadIdx.x);
+    }
+    __syncthreads();
+    // A warp reads a stretch again, an element a lane; what is not below the bound goes to a buffer, which is sorted by 32.
+    u64 bound = max((u64)float_order_key(reached) << 32, least);
+    u64* buf = s.buf[warp];
+    int held = 0;
+    const int works = s.works;
+    for (int i = warp; i < works || held > 0; i += kWarps) {
+      if (i < works) {
+        const int k = s.work[i] / kThr, t = s.work[i] % kThr;
+        for (int b = k * stretch; b < min((k + 1) * stretch, batches); ++b) {
+          const int at = u0 + b * kBatch + (lane / kVec) * kThr + t;
+          const int64_t id = u.first(at) + lane % kVec;
+          u64 key = 0;
+          if (lane < kUnits * kVec && at < u1 && id >= 0 && id < a.V) {
+            const float v = to_f<T>(row[id]);
+            if (v > -INFINITY) key = value_id_key(v, (uint32_t)id);  // and no NaN
+          }
+          const unsigned in = __ballot_sync(kAll, key > bound);
+          if (key > bound) buf[held + __popc(in & ((1u << lane) - 1u))] = key;
+          held += __popc(in);
+          if (held >= 32) {
+            __syncwarp();
+            held -= 32;
+            best = merged(best, sorted_down(buf[held + lane]));
+            bound = max(bound, __shfl_sync(kAll, best, n - 1));
+            __syncwarp();
+          }
+        }
+      } else {
+        __syncwarp();
+        best = merged(best, sorted_down(lane < held ? buf[lane] : 0ull));
+        held = 0;
+      }
+    }
+    __syncthreads();  // the stretches' maxima have been read
+  }
+
+  // The warp's, the block's, the cluster's. Blocks of a cluster by the warps of the first one, whose reads of the others' memory are
+  // then on their way together.
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     Sums o;
@@ -321,47 +401,74 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
     q.join(o, c);
     before += __shfl_xor_sync(kAll, before, d);
   }
-  s.list[warp][lane] = best;
-  if (lane == 0) {
-    s.sums[warp] = q;
-    s.count[warp] = before;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < kWarps; ++w) {
-      q.join(s.sums[w], c);
-      before += s.count[w];
-      if (n > 0) best = merged(best, s.list[w][lane]);
-    }
-    s.best[lane] = best;
-    if (lane == 0) s.part = make_float4(q.m, q.S, q.E, __int_as_float(before));
-  }
-  if (size > 1) {
-    cluster_sync();
-    if (rank == 0 && warp == 0) {
-      for (int k = 1; k < size; ++k) {
-        const float4 p = dsmem_f4(dsmem(&s.part, (uint32_t)k));
-        Sums o = {p.x, p.y, p.z};
-        q.join(o, c);
-        before += __float_as_int(p.w);
-        if (n > 0) best = merged(best, dsmem_u64(dsmem(&s.best[lane], (uint32_t)k)));
+  auto join_warps = [&] {
+#pragma unroll 1
+    for (int step = kWarps / 2; step > 0; step >>= 1) {
+      if (warp < 2 * step) {
+        s.list[warp][lane] = best;
+        if (lane == 0) {
+          s.sums[warp] = q;
+          s.count[warp] = before;
+        }
       }
+      __syncthreads();
+      if (warp < step) {
+        q.join(s.sums[warp + step], c);
+        before += s.count[warp + step];
+        if (n > 0) best = merged(best, s.list[warp + step][lane]);
+      }
+    }
+  };
+  join_warps();
+  if (size > 1) {
+    if (warp == 0) {
+      s.best[lane] = best;
+      if (lane == 0) s.part = make_float4(q.m, q.S, q.E, __int_as_float(before));
+    }
+    cluster_sync();
+    if (rank == 0) {
+      float4 p[kMaxCluster / kWarps];
+      u64 x[kMaxCluster / kWarps];
+#pragma unroll
+      for (int i = 0; i < kMaxCluster / kWarps; ++i) {
+        const int k = warp + i * kWarps;
+        p[i] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        x[i] = 0;
+        if (k < size) {
+          p[i] = dsmem_f4(dsmem(&s.part, (uint32_t)k));
+          x[i] = dsmem_u64(dsmem(&s.best[lane], (uint32_t)k));
+        }
+      }
+      q = Sums{p[0].x, p[0].y, p[0].z};
+      before = __float_as_int(p[0].w);
+      best = x[0];
+#pragma unroll
+      for (int i = 1; i < kMaxCluster / kWarps; ++i) {
+        q.join(Sums{p[i].x, p[i].y, p[i].z}, c);
+        before += __float_as_int(p[i].w);
+        if (n > 0) best = merged(best, x[i]);
+      }
+      __syncthreads();
+      join_warps();
     }
     cluster_sync();  // the others' shared memory has been read
   }
   if (rank != 0 || warp != 0) return;
-  const float log_s = logf(q.S);
+  const float log_s = log2f(q.S), at = q.m * c;
   auto logprob = [&](float x) {
     if (!fine) return __uint_as_float(0x7fffffffu);
-    return (x == q.m ? 0.0f : (x - q.m) / temp) - (q.m == -INFINITY ? INFINITY : log_s);
+    if (q.m == -INFINITY || x == -INFINITY) return -INFINITY;
+    const float d = fmaf(x, c, -at);
+    if (!isfinite(d)) return (x == q.m ? 0.0f : (x - q.m) / temp) - log_s * kLn2;  // beyond fp32 in log2 units
+    return (d - log_s) * kLn2;
   };
   if (lane == 0) {
     const bool none = token == -1;
     if (!fine || (!given && !none)) dev_error(a.ctl, DEV_ERR_DATA);
     if (a.logprob) a.logprob[r] = none && fine ? 0.0f : given ? logprob(xt) : NAN;
     if (a.rank) a.rank[r] = none ? 0 : given ? before : -1;
-    if (a.entropy) a.entropy[r] = !fine ? NAN : q.m == -INFINITY ? 0.0f : log_s - q.E / q.S * kLn2;
-    if (a.lse) a.lse[r] = !fine ? NAN : q.m == -INFINITY ? -INFINITY : q.m / temp + log_s;
+    if (a.entropy) a.entropy[r] = !fine ? NAN : q.m == -INFINITY ? 0.0f : (log_s - q.E / q.S) * kLn2;
+    if (a.lse) a.lse[r] = !fine ? NAN : isinf(at) ? q.m / temp + log_s * kLn2 : (at + log_s) * kLn2;
   }
   if (lane < n) {
     const bool there = best > least;
