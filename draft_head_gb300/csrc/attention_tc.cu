@@ -610,6 +610,9 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
           const int s0 = w.kt.slot(k, kBN), at = slot_in_page(a.pages, s0);
           if (page == -1) dev_error(ctl, DEV_ERR_DATA);
           const int place = page < 0 ? p.no_page : (int)(page * p.page_step + walk.h * p.head_step);
+          int places[kBN / kLeastPage];
+#pragma unroll
+          for (int i = 0; i < kBN / kLeastPage; ++i) places[i] = __shfl_sync(0xffffffffu, place, i);
           page = k + 1 < k1 ? tile_page(a, w, b, w.kt.slot(k + 1, kBN), lane << shift, 1 << shift) : -2;
           if (C::kCodes) {
             scales[0] = scales_next[0];
@@ -637,26 +640,25 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
                                  item << kNoteItem;
               __syncwarp();
             }
-            if (leader) mbar_expect_tx(&full[slot], C::kCodes ? C::kStaged : C::kTile);
-            __syncwarp();
+            if (leader) {
+              mbar_expect_tx(&full[slot], C::kCodes ? C::kStaged : C::kTile);
 #pragma unroll
-            for (int i = 0; i < kBN / kLeastPage; ++i) {
-              if (i << shift >= kBN) break;
-              const int to = __shfl_sync(0xffffffffu, place, i);
-              if (leader) {
+              for (int i = 0; i < kBN / kLeastPage; ++i) {
+                if (i << shift >= kBN) break;
                 if (C::kCodes) {
-                  tma_load_3d(in + (size_t)slot * C::kStaged + (size_t)(i << shift) * C::DP, tm, 0, at, to, &full[slot]);
+                  tma_load_3d(in + (size_t)slot * C::kStaged + (size_t)(i << shift) * C::DP, tm, 0, at, places[i], &full[slot]);
                 } else if (KB == 2 && p.folded) {
-                  tma_load_5d(ring + (size_t)slot * C::kTile + (size_t)(i << shift) * 256, tm, 0, 0, 0, at / 8, to, &full[slot], pol, once);
+                  tma_load_5d(ring + (size_t)slot * C::kTile + (size_t)(i << shift) * 256, tm, 0, 0, 0, at / 8, places[i], &full[slot], pol,
+                              once);
                 } else {
 #pragma unroll
                   for (int kb = 0; kb < KB; ++kb)
-                    tma_load_3d(ring + (size_t)slot * C::kTile + kb * (kBN * 128) + (size_t)(i << shift) * 128, tm, kb * 64, at, to,
+                    tma_load_3d(ring + (size_t)slot * C::kTile + kb * (kBN * 128) + (size_t)(i << shift) * 128, tm, kb * 64, at, places[i],
                                 &full[slot]);
                 }
               }
-              __syncwarp();
             }
+            __syncwarp();
             ++issued;
             if (++slot == in_slots) { slot = 0; phase ^= 1u; }
           }
