@@ -100,7 +100,8 @@ struct Piece<kPagedE4m3> {
   __device__ __forceinline__ void load(const void* base, int64_t at) { x = ldg8((const uint8_t*)base + at); }
   __device__ __forceinline__ void zero() { x = make_uint2(0, 0); }
   __device__ __forceinline__ uint4 pairs() const {
-    return make_uint4(codes_f16(x.x & 0xffffu), codes_f16(x.x >> 16), codes_f16(x.y & 0xffffu), codes_f16(x.y >> 16));
+    const uint2 a = codes_f16(x.x), b = codes_f16(x.y);
+    return make_uint4(a.x, a.y, b.x, b.y);
   }
 };
 __device__ __forceinline__ uint32_t part(const uint4& x, int t) { return t == 0 ? x.x : t == 1 ? x.y : t == 2 ? x.z : x.w; }
@@ -193,6 +194,8 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
   uint32_t scale_next = 0;  // codes: the byte of slot lane % 16, of the keys (lanes 0 to 15) or the values
   bool tile_there = true;
   int64_t tile_at = 0;      // elements from the caches' begin to the tile's first slot
+  // Where in a tile the lane's first piece of keys and of values is.
+  const int64_t k_lane = (int64_t)n * a.ss + 8 * c, v_lane = (int64_t)(2 * c) * a.ss + 8 * n;
   // Pages are as large as tiles at least, so a tile lies in one: its number is read one tile ahead of the tile.
   auto page_at = [&](int k) { return CACHE == kWhole ? 0 : page_of(a.pages, b, kt.slot(k, kBN)); };
   auto fetch = [&](int k, int page) {
@@ -204,26 +207,38 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     tile_there = CACHE == kWhole || page >= 0;
     if (!tile_there && lane == 0) dev_error(a.ctl, DEV_ERR_DATA);
     const int there = tile_there ? end - s0 : 0;  // slots of the tile
+    const int64_t k_at = tile_at + k_lane, v_at = tile_at + v_lane;
+    if (kCodes && there >= kBN && a.D == DP) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int s = n + 8 * x;
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        if (s < there && 32 * j + 8 * c < a.D)
-          kx[x][j].load(a.k, tile_at + (int64_t)s * a.ss + 32 * j + 8 * c);
-        else
-          kx[x][j].zero();
+        for (int j = 0; j < KS; ++j) kx[x][j].load(a.k, k_at + x * (8 * (int64_t)a.ss) + 32 * j);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int j = 0; j < JJ; ++j) vx[x][j].load(a.v, v_at + ((x & 1) + 8 * (x >> 1)) * (int64_t)a.ss + 64 * j);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int s = n + 8 * x;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          if (s < there && 32 * j + 8 * c < a.D)
+            kx[x][j].load(a.k, k_at + x * (8 * (int64_t)a.ss) + 32 * j);
+          else
+            kx[x][j].zero();
+        }
       }
-    }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int s = 2 * c + (x & 1) + 8 * (x >> 1);
+      for (int x = 0; x < 4; ++x) {
+        const int s = 2 * c + (x & 1) + 8 * (x >> 1);
 #pragma unroll
-      for (int j = 0; j < JJ; ++j) {
-        if (s < there && 64 * j + 8 * n < a.D)
-          vx[x][j].load(a.v, tile_at + (int64_t)s * a.ss + 64 * j + 8 * n);
-        else
-          vx[x][j].zero();
+        for (int j = 0; j < JJ; ++j) {
+          if (s < there && 64 * j + 8 * n < a.D)
+            vx[x][j].load(a.v, v_at + ((x & 1) + 8 * (x >> 1)) * (int64_t)a.ss + 64 * j);
+          else
+            vx[x][j].zero();
+        }
       }
     }
     if (kCodes) {
@@ -361,14 +376,22 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     }
 #pragma unroll
     for (int j = 0; j < JJ; ++j) {
-      const uint4 v4[4] = {vr[0][j].pairs(), vr[1][j].pairs(), vr[2][j].pairs(), vr[3][j].pairs()};
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint32_t v0 = part(v4[0], t), v1 = part(v4[1], t), v2 = part(v4[2], t), v3 = part(v4[3], t);
+        // Elements 2 t and 2 t + 1 of slots 2 c and 2 c + 1 (a0, a1), 2 c + 8 and 2 c + 9 (a2, a3); codes are paired as bytes.
+        uint32_t a0, a1, a2, a3;
+        if constexpr (kCodes) {
+          const uint32_t select = t & 1 ? 0x7362 : 0x5140;
+          auto word = [&](int x) { return t < 2 ? vr[x][j].x.x : vr[x][j].x.y; };
+          const uint2 lo = codes_f16(__byte_perm(word(0), word(1), select)), hi = codes_f16(__byte_perm(word(2), word(3), select));
+          a0 = lo.x; a1 = lo.y; a2 = hi.x; a3 = hi.y;
+        } else {
+          const uint32_t v0 = part(vr[0][j].x, t), v1 = part(vr[1][j].x, t), v2 = part(vr[2][j].x, t), v3 = part(vr[3][j].x, t);
+          a0 = __byte_perm(v0, v1, 0x5410); a1 = __byte_perm(v0, v1, 0x7632);
+          a2 = __byte_perm(v2, v3, 0x5410); a3 = __byte_perm(v2, v3, 0x7632);
+        }
 #pragma unroll
-        for (int g = 0; g < NT; ++g)
-          mma<CACHE>(o[g][4 * j + t], __byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x5410),
-                     __byte_perm(v2, v3, 0x7632), pw[g][0], pw[g][1]);
+        for (int g = 0; g < NT; ++g) mma<CACHE>(o[g][4 * j + t], a0, a1, a2, a3, pw[g][0], pw[g][1]);
       }
     }
     if (!kCodes && mend) {

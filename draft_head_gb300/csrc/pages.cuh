@@ -62,10 +62,12 @@ __device__ __forceinline__ float scale_f32(int byte) {
 __device__ __forceinline__ uint32_t codes_that_are_numbers(uint32_t x) {
   return x & ~((((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7);
 }
-// Two codes (low byte first) as an fp16 pair, without their scale: every code is a normal fp16 number or 0.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
-  uint32_t r;
-  asm("{\n .reg .b16 c;\n cvt.u16.u32 c, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}\n" : "=r"(r) : "r"(x));
+// Four codes (low byte first) as two fp16 pairs, without their scale: every code is a normal fp16 number or 0.
+__device__ __forceinline__ uint2 codes_f16(uint32_t x) {
+  uint2 r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(x));
   return r;
 }
 // A row of queries in fp16, for products with codes: divided by a power of two that brings its largest magnitude, of these bits,
