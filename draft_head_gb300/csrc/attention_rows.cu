@@ -45,7 +45,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazyBf16 = 32.0f;
 // Codes: weights in fp16, kAtMost at the maximum and kAtMost 2^kLazyCodes at most.
 constexpr float kLazyCodes = 4.0f, kAtMost = 2048.0f;  // 2^11
-constexpr int kCodesCtas = 3;
+constexpr int kCodesCtas = 3, kDepth = 3;  // of one group of rows, on an SM; tiles of a warp's ring
 
 struct RowsP {
   AttnArgs a;
@@ -81,29 +81,27 @@ __device__ __forceinline__ uint4 ldg16(const __nv_bfloat16* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
   return x;
 }
-__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
-  uint2 x;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
-  return x;
-}
-// Eight elements of a slot as they lie in the cache, and as the operand's pairs.
-template <int CACHE>
+// Eight elements of a slot.
 struct Piece {
   uint4 x;
   __device__ __forceinline__ void load(const void* base, int64_t at) { x = ldg16((const __nv_bfloat16*)base + at); }
   __device__ __forceinline__ void zero() { x = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ uint4 pairs() const { return x; }
 };
-template <>
-struct Piece<kPagedE4m3> {
-  uint2 x;
-  __device__ __forceinline__ void load(const void* base, int64_t at) { x = ldg8((const uint8_t*)base + at); }
-  __device__ __forceinline__ void zero() { x = make_uint2(0, 0); }
-  __device__ __forceinline__ uint4 pairs() const {
-    const uint2 a = codes_f16(x.x), b = codes_f16(x.y);
-    return make_uint4(a.x, a.y, b.x, b.y);
-  }
+// Codes wait in a warp's ring in shared memory: a tile's keys, values and scales, rows padded so that the lanes' 8-byte reads
+// meet every bank once.
+template <int JJ>
+struct Tile {
+  static constexpr int DP = 64 * JJ, kKeyRow = DP + 32, kValueRow = DP + 16;
+  static constexpr int kValues = kBN * kKeyRow, kScales = kValues + kBN * kValueRow, kBytes = kScales + 2 * kBN;
 };
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool there) {  // zeros where it is not
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint2 lds8(const uint8_t* p) { return *(const uint2*)p; }
+__device__ __forceinline__ uint4 pairs8(uint2 x) {
+  const uint2 a = codes_f16(x.x), b = codes_f16(x.y);
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
 __device__ __forceinline__ uint32_t part(const uint4& x, int t) { return t == 0 ? x.x : t == 1 ? x.y : t == 2 ? x.z : x.w; }
 __device__ __forceinline__ bool bad16(uint32_t x) {  // a bf16 pair with an infinity or a NaN in it
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
@@ -120,7 +118,14 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
   constexpr int kRows = 8 * NT, DP = 64 * JJ;
   constexpr bool kCodes = CACHE == kPagedE4m3;
   constexpr float kLazy = kCodes ? kLazyCodes : kLazyBf16;
-  __shared__ __align__(16) float s_o[kWarps][kRows][DP + 4];
+  using Codes = Tile<JJ>;
+  // The warps' sums, and before them the rings of codes.
+  constexpr int kRing = kCodes ? kDepth * Codes::kBytes : 0, kSums = kRows * (DP + 4) * 4;
+  constexpr int kMine = (kRing > kSums ? kRing : kSums);
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  __shared__ __align__(16) uint8_t s_fixed[kCodes ? 16 : kWarps * kMine];
+  uint8_t* s_all = kCodes ? s_dyn : s_fixed;
+  auto s_o = [&](int w, int r, int e) { return (float*)(s_all + w * kMine) + r * (DP + 4) + e; };
   __shared__ float2 s_ml[kWarps][kRows];
   __shared__ int s_low[kRows], s_i[kRows], s_last;
   const AttnArgs& a = p.a;
@@ -190,12 +195,13 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
   const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.rows.max_q * a.rows.max_q : nullptr;
 
   const int end = ctx + rows_n;
-  Piece<CACHE> kx[2][KS], vx[4][JJ];
-  uint32_t scale_next = 0;  // codes: the byte of slot lane % 16, of the keys (lanes 0 to 15) or the values
+  Piece kx[2][KS], vx[4][JJ];
+  int64_t tile_at = 0;  // elements from the caches' begin to the tile's first slot
   bool tile_there = true;
-  int64_t tile_at = 0;      // elements from the caches' begin to the tile's first slot
   // Where in a tile the lane's first piece of keys and of values is.
   const int64_t k_lane = (int64_t)n * a.ss + 8 * c, v_lane = (int64_t)(2 * c) * a.ss + 8 * n;
+  const uint32_t ring = smem_u32(s_all) + (uint32_t)(warp * kMine);
+  int in_ring = 0, out_ring = 0;
   // Pages are as large as tiles at least, so a tile lies in one: its number is read one tile ahead of the tile.
   auto page_at = [&](int k) { return CACHE == kWhole ? 0 : page_of(a.pages, b, kt.slot(k, kBN)); };
   auto fetch = [&](int k, int page) {
@@ -207,44 +213,48 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     tile_there = CACHE == kWhole || page >= 0;
     if (!tile_there && lane == 0) dev_error(a.ctl, DEV_ERR_DATA);
     const int there = tile_there ? end - s0 : 0;  // slots of the tile
-    const int64_t k_at = tile_at + k_lane, v_at = tile_at + v_lane;
-    if (kCodes && there >= kBN && a.D == DP) {
+    if constexpr (kCodes) {
+      const uint32_t to = ring + (uint32_t)(in_ring * Codes::kBytes);
+      constexpr int kPieces = DP / 16, kStep = 32 / kPieces;  // of a row; rows at a time
+      const int piece = lane % kPieces, r0 = lane / kPieces;
+      const uint8_t* kp = (const uint8_t*)a.k + tile_at + (int64_t)r0 * a.ss + piece * 16;
+      const uint8_t* vp = (const uint8_t*)a.v + tile_at + (int64_t)r0 * a.ss + piece * 16;
+      const bool in_head = piece * 16 < a.D;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int j = 0; j < KS; ++j) kx[x][j].load(a.k, k_at + x * (8 * (int64_t)a.ss) + 32 * j);
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int j = 0; j < JJ; ++j) vx[x][j].load(a.v, v_at + ((x & 1) + 8 * (x >> 1)) * (int64_t)a.ss + 64 * j);
-    } else {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int s = n + 8 * x;
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          if (s < there && 32 * j + 8 * c < a.D)
-            kx[x][j].load(a.k, k_at + x * (8 * (int64_t)a.ss) + 32 * j);
-          else
-            kx[x][j].zero();
-        }
+      for (int r = 0; r < kBN; r += kStep) {
+        const bool here = r0 + r < there && in_head;
+        copy16(to + (r0 + r) * Codes::kKeyRow + piece * 16, here ? kp + (int64_t)r * a.ss : (const uint8_t*)a.k, here);
+        copy16(to + Codes::kValues + (r0 + r) * Codes::kValueRow + piece * 16, here ? vp + (int64_t)r * a.ss : (const uint8_t*)a.v, here);
       }
+      if (lane < 2) {
+        const uint8_t* from = lane == 0 ? a.pages.k_scale : a.pages.v_scale;
+        copy16(to + Codes::kScales + lane * kBN, tile_there ? from + scale_at(a.pages, a.hkv, page, h, s0) : from, tile_there);
+      }
+      if (++in_ring == kDepth) in_ring = 0;
+      return;
+    }
+    const int64_t k_at = tile_at + k_lane, v_at = tile_at + v_lane;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int s = 2 * c + (x & 1) + 8 * (x >> 1);
+    for (int x = 0; x < 2; ++x) {
+      const int s = n + 8 * x;
 #pragma unroll
-        for (int j = 0; j < JJ; ++j) {
-          if (s < there && 64 * j + 8 * n < a.D)
-            vx[x][j].load(a.v, v_at + ((x & 1) + 8 * (x >> 1)) * (int64_t)a.ss + 64 * j);
-          else
-            vx[x][j].zero();
-        }
+      for (int j = 0; j < KS; ++j) {
+        if (s < there && 32 * j + 8 * c < a.D)
+          kx[x][j].load(a.k, k_at + x * (8 * (int64_t)a.ss) + 32 * j);
+        else
+          kx[x][j].zero();
       }
     }
-    if (kCodes) {
-      scale_next = 127;
-      if ((lane & 15) < there)
-        scale_next = __ldg((lane < 16 ? a.pages.k_scale : a.pages.v_scale) + scale_at(a.pages, a.hkv, page, h, s0 + (lane & 15)));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int s = 2 * c + (x & 1) + 8 * (x >> 1);
+#pragma unroll
+      for (int j = 0; j < JJ; ++j) {
+        if (s < there && 64 * j + 8 * n < a.D)
+          vx[x][j].load(a.v, v_at + ((x & 1) + 8 * (x >> 1)) * (int64_t)a.ss + 64 * j);
+        else
+          vx[x][j].zero();
+      }
     }
   };
 
@@ -259,47 +269,57 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     l[g][0] = l[g][1] = 0.0f;
   }
   int page = 0;
-  if (k_begin + warp < k_end) fetch(k_begin + warp, page_at(k_begin + warp));
-  if (k_begin + warp + kWarps < k_end) page = page_at(k_begin + warp + kWarps);
+  constexpr int kAhead = kCodes ? kDepth * kWarps : kWarps;  // the tile that is asked for while one is worked on
+#pragma unroll
+  for (int d = 0; d < kAhead; d += kWarps) {
+    const int k = k_begin + warp + d;
+    if (k < k_end) fetch(k, page_at(k));
+    if (kCodes) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  if (!kCodes && k_begin + warp + kAhead < k_end) page = page_at(k_begin + warp + kAhead);
 #pragma unroll 1
   for (int k = k_begin + warp; k < k_end; k += kWarps) {
     const int s0 = kt.slot(k, kBN);
     const int64_t here = tile_at;
-    Piece<CACHE> kr[2][KS], vr[4][JJ];
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int j = 0; j < KS; ++j) kr[x][j] = kx[x][j];
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-      for (int j = 0; j < JJ; ++j) vr[x][j] = vx[x][j];
+    const bool gone = CACHE != kWhole && !tile_there;  // no such page: nothing was read
+    Piece kr[2][KS], vr[4][JJ];
+    const uint8_t* codes = nullptr;
     // Codes: the scales of slots n and n + 8 (e / 2 of the scores below), the values' also as exponents.
     float ks[2], vs[2], ve[2];
-    if (kCodes) {
+    if constexpr (kCodes) {
+      if (k + kAhead < k_end) page = page_at(k + kAhead);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      __syncwarp();
+      codes = s_all + warp * kMine + out_ring * Codes::kBytes;
+      if (++out_ring == kDepth) out_ring = 0;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        ks[x] = scale_f32((int)__shfl_sync(0xffffffffu, scale_next, n + 8 * x));
-        const int v = (int)__shfl_sync(0xffffffffu, scale_next, 16 + n + 8 * x);
-        ve[x] = (float)(v - 127);
+        ks[x] = scale_f32(codes[Codes::kScales + n + 8 * x]);
+        const int v = codes[Codes::kScales + kBN + n + 8 * x];
+        ve[x] = v == kScaleNan ? 0.0f : (float)(v - 127);
         vs[x] = scale_f32(v) * kAtMost;
-        if (v == kScaleNan) ve[x] = 0.0f;
       }
-    }
-    const bool gone = CACHE != kWhole && !tile_there;  // no such page: nothing was read
-    if (k + kWarps < k_end) {
-      fetch(k + kWarps, page);
-      if (k + 2 * kWarps < k_end) page = page_at(k + 2 * kWarps);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int j = 0; j < KS; ++j) kr[x][j] = kx[x][j];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int j = 0; j < JJ; ++j) vr[x][j] = vx[x][j];
+      if (k + kAhead < k_end) {
+        fetch(k + kAhead, page);
+        if (k + 2 * kAhead < k_end) page = page_at(k + 2 * kAhead);
+      }
     }
     const bool whole = s0 + kBN <= all_hi && (s0 >= all_low || s0 + kBN <= a.sinks);
     bool mend = false;
     if constexpr (kCodes) {
       if (!whole) {  // a value that is no number has that in its scale, and so in its weight; slots without one may hold anything
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int j = 0; j < JJ; ++j)
-            vr[x][j].x = make_uint2(codes_that_are_numbers(vr[x][j].x.x), codes_that_are_numbers(vr[x][j].x.y));
+        uint32_t* v = (uint32_t*)(codes + Codes::kValues);
+        for (int x = lane; x < kBN * Codes::kValueRow / 4; x += 32) v[x] = codes_that_are_numbers(v[x]);
+        __syncwarp();
       }
     } else {
       if (!whole) {
@@ -323,7 +343,8 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
       for (int e = 0; e < 4; ++e) s[g][e] = 0.0f;
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
-      const uint4 k0 = kr[0][j].pairs(), k1 = kr[1][j].pairs();
+      const uint8_t* at = codes + n * Codes::kKeyRow + 32 * j + 8 * c;
+      const uint4 k0 = kCodes ? pairs8(lds8(at)) : kr[0][j].x, k1 = kCodes ? pairs8(lds8(at + 8 * Codes::kKeyRow)) : kr[1][j].x;
 #pragma unroll
       for (int g = 0; g < NT; ++g) {
         mma<CACHE>(s[g], k0.x, k1.x, k0.y, k1.y, q[g][j][0], q[g][j][1]);
@@ -376,13 +397,19 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     }
 #pragma unroll
     for (int j = 0; j < JJ; ++j) {
+      uint2 w[4];
+      if constexpr (kCodes) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          w[x] = lds8(codes + Codes::kValues + (2 * c + (x & 1) + 8 * (x >> 1)) * Codes::kValueRow + 64 * j + 8 * n);
+      }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         // Elements 2 t and 2 t + 1 of slots 2 c and 2 c + 1 (a0, a1), 2 c + 8 and 2 c + 9 (a2, a3); codes are paired as bytes.
         uint32_t a0, a1, a2, a3;
         if constexpr (kCodes) {
           const uint32_t select = t & 1 ? 0x7362 : 0x5140;
-          auto word = [&](int x) { return t < 2 ? vr[x][j].x.x : vr[x][j].x.y; };
+          auto word = [&](int x) { return t < 2 ? w[x].x : w[x].y; };
           const uint2 lo = codes_f16(__byte_perm(word(0), word(1), select)), hi = codes_f16(__byte_perm(word(2), word(3), select));
           a0 = lo.x; a1 = lo.y; a2 = hi.x; a3 = hi.y;
         } else {
@@ -393,6 +420,11 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
 #pragma unroll
         for (int g = 0; g < NT; ++g) mma<CACHE>(o[g][4 * j + t], a0, a1, a2, a3, pw[g][0], pw[g][1]);
       }
+    }
+    if (kCodes) {
+      __syncwarp();  // everyone has read the tile
+      if (k + kAhead < k_end) fetch(k + kAhead, page);
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
     if (!kCodes && mend) {
 #pragma unroll
@@ -413,6 +445,10 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     }
   }
 
+  if (kCodes) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  }
   // The warps' results, in shared memory.
 #pragma unroll
   for (int g = 0; g < NT; ++g)
@@ -424,7 +460,7 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
       if (n == 0) s_ml[warp][r] = make_float2(m[g][e], l[g][e]);
 #pragma unroll
       for (int j = 0; j < JJ; ++j) {
-        float* dst = &s_o[warp][r][64 * j + 8 * n];
+        float* dst = s_o(warp, r, 64 * j + 8 * n);
         *(float4*)dst = make_float4(o[g][4 * j][e], o[g][4 * j][2 + e], o[g][4 * j + 1][e], o[g][4 * j + 1][2 + e]);
         *(float4*)(dst + 4) = make_float4(o[g][4 * j + 2][e], o[g][4 * j + 2][2 + e], o[g][4 * j + 3][e], o[g][4 * j + 3][2 + e]);
       }
@@ -448,7 +484,7 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float2 v = s_ml[w][r];
-      const float4 y = *(const float4*)&s_o[w][r][e];
+      const float4 y = *(const float4*)s_o(w, r, e);
       const float f = v.x == -INFINITY || v.x == mm ? 1.0f : ex2(v.x - mm);  // a warp that saw nothing has sums of 0
       ll += v.y * f;
       acc.x += y.x * f; acc.y += y.y * f; acc.z += y.z * f; acc.w += y.w * f;
@@ -536,7 +572,14 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   p.splits = splits_for(row_tiles, many ? want_ctas() : resident(), std::min<int64_t>(key_tiles / p.least, kMostPieces));
   p.part = partials_at(a.scratch, want_ctas(), 16);
   const dim3 grid((unsigned)p.splits, (unsigned)a.hkv, (unsigned)a.rows.batch);
-  attn_rows_kernel<NT, KS, JJ, CACHE><<<grid, kThr, 0, stream>>>(p);
+  size_t smem = 0;
+  if (CACHE == kPagedE4m3) {
+    smem = (size_t)kWarps * std::max(kDepth * Tile<JJ>::kBytes, 8 * NT * (64 * JJ + 4) * 4);
+    static FuncOnce once;
+    const cudaError_t e = once.set((const void*)attn_rows_kernel<NT, KS, JJ, CACHE>, (int)smem, false);
+    if (e != cudaSuccess) return e;
+  }
+  attn_rows_kernel<NT, KS, JJ, CACHE><<<grid, kThr, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
