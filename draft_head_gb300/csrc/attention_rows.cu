@@ -45,7 +45,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazyBf16 = 32.0f;
 // Codes: weights in fp16, kAtMost at the maximum and kAtMost 2^kLazyCodes at most.
 constexpr float kLazyCodes = 4.0f, kAtMost = 2048.0f;  // 2^11
-constexpr int kCodesCtas = 3, kDepth = 3;  // of one group of rows, on an SM; tiles of a warp's ring
+constexpr int kCodesCtas = 3, kDepth = 2;  // of one group of rows, on an SM; tiles of a warp's ring (3 and 2: 128 tokens 229 us, one 11.7; 3 and 3: 231 and 11.8; 4 and 2: 224 and 13.0)
 
 struct RowsP {
   AttnArgs a;
