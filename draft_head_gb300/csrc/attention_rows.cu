@@ -1,6 +1,6 @@
-// Attention of a few rows over the cache (domino_block_attention; the definition
-// is in domino.h): bf16, head_dim <= 128, at most 16 packed rows of a kv head,
-// as when a token is decoded.
+// Attention of a few rows over the cache (domino_block_attention and
+// domino_paged_attention; the definitions are in domino.h): bf16 or codes, head_dim <= 128,
+// at most 16 packed rows of a kv head, as when a token is decoded.
 //
 // Bound by the cache's bytes, or with one request by the time from launch to the last join.
 // So: no shared memory, barriers or tensor memory on the way of the keys and values, and a
@@ -21,6 +21,16 @@
 // One token, 32 heads of 128 over 8 of the cache: over 4000 slots 12.2 us (20 with the tensor core
 // kernel), over 30,000 slots 28.1 us (4.4 TB/s); 64 tokens over up to 4000 slots each 117 us
 // (4.6 TB/s).
+//
+// Pages hold 16 slots at least, so a tile of 16 lies in one: one table entry a tile, read a tile ahead.
+// Codes (e4m3 with a power of two per slot and head) are fp16 to the mma: a conversion instruction makes two of them at once, exactly
+// (in bf16 it takes a permute, a shift, a mask and a product), and no scale is applied to them. A key's scale multiplies its score, a
+// value's its weight, both in fp32: P is rounded to fp16, 2^-12 of a weight where bf16 gives 2^-9, and as the weights carry the scales the
+// running maximum is that of score + scale, which keeps them below 2^15; 2^11 at the maximum, so that weights down to 2^-35 of it count. Queries are
+// brought to fp16's range by a power of two per row. A value that is no number has that in its scale, so a
+// row that does not see it cannot get it: there is nothing to clear. The codes wait in a warp's ring in shared memory (cp.async), which
+// frees the registers of the tiles on their way: one token over 4000 quantised slots 11.7 us, 128 tokens over up to 8000 229 us, 4.8 TB/s of
+// half the bytes (bf16 pages 393 us, 5.6 TB/s).
 #include <math.h>
 #include <algorithm>
 
@@ -590,10 +600,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
 // long caches the tensor core kernel wins, from pasts of about 2500 on: 64 requests of 4 rows in groups of 4, up to 500 /
 // 2000 / 2500 / 3000 / 4000 slots, 31 / 76 / 80 / 96 / 120 us and 47 / 76 / 81 / 92 / 112; 32 requests 18 / 47 / 48 / 55 / 72
 // and 28 / 46 / 50 / 54 / 67. Fewer, which leave SMs idle: 16 requests up to 4000 slots 43.7 and 43.1; one 21 and 21.
+// Codes, which the tensor core kernel has to turn into bf16 first, are this one's up to 16 rows: 64 requests of 4 rows in groups of 4, up to
+// 500 / 2000 / 4000 / 8000 slots, 29 / 70 / 105 / 189 us and 56 / 105 / 162 / 267; 16 requests 15 / 38 / 44 / 62 and 27 / 45 / 64 / 100.
 bool attn_rows_applies(const AttnArgs& a) {
   const int64_t rows = (int64_t)a.rows.max_q * (a.hq / a.hkv);
   if (a.dtype != DOMINO_BF16 || a.D > 128 || rows > 16) return false;
-  return rows <= 8 || a.rows.max_ctx < 2500 || (int64_t)a.hkv * a.rows.batch <= num_sms();
+  return rows <= 8 || a.cache == kPagedE4m3 || a.rows.max_ctx < 2500 || (int64_t)a.hkv * a.rows.batch <= num_sms();
 }
 size_t attn_rows_ws_bytes(const AttnArgs& a) { return partial_bytes(want_ctas(), 16, a.D); }
 

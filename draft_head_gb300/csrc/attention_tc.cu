@@ -1,5 +1,6 @@
 // Attention of a block's rows over the cache on the tensor cores
-// (domino_block_attention; the definition is in domino.h): bf16, head_dim <= 128.
+// (domino_block_attention and domino_paged_attention; the definitions are in domino.h): bf16 or
+// codes, head_dim <= 128.
 //
 // One pass over the keys with the running maximum and sum of the softmax. Per key
 // tile of 128 slots and query tile of 128 packed rows (row and query head of one kv
@@ -43,6 +44,17 @@
 // tensor pipe is busy 43 % of the time in a short call (4096 rows with the window); a softmax group's own path
 // (scores to registers, exponentials, weights back) sets the pace. A polynomial on the FMA pipe for part
 // of the exponentials made it longer (a quarter of them: 450 -> 537 us).
+//
+// Pages: warp 0 reads the table a tile ahead and brings a tile page by page. Codes (e4m3 with a power of two per slot and head)
+// arrive in buffers of their own, and
+//   warps 12-15  turn them into bf16 in the ring: code x scale is exact there (4 significant bits), so all that follows is the
+//                same. A code's fields at bf16's places are 2^-120 of it, and one product with the scale does the rest; 64-bit
+//                shared-memory reads and writes meet every bank once.
+// They share the SM's issue slots and shared memory with the softmax, and set the pace where the cache's bytes would: 64
+// blocks over pages of 64 slots 229 us (bf16 pages 169, of 16 slots 199, 256 181), 16 trees 85 us (66), chunks of 2048 rows for 4 requests
+// 485 us (407), 0.96 PFLOP/s. With the conversion left out, a copy in its place, they take 200, 77 and 463: it is the passes through
+// shared memory, not the arithmetic, that cost. (Products of codes as fp16 with scales relative to a tile's largest: 210, 79 and 502, and
+// small scales beside large ones would lose bits. Keys by two of the warps and values by the other two: 244, 90 and 654.)
 #include <cuda.h>
 #include <math.h>
 #include <string.h>
@@ -1267,7 +1279,8 @@ bool make_tmap(CUtensorMap* tm, const void* base, const AttnArgs& a) {
 int64_t divisor(int64_t x, int64_t y) { return y == 0 ? x : divisor(y, x % y); }
 bool page_places(const AttnArgs& a, int64_t* unit, int64_t* places) {
   const int64_t ps = a.pages.n_pages > 1 ? a.pages.page_stride : 0, hs = a.hkv > 1 ? a.hs : 0;
-  *unit = std::max<int64_t>(divisor(ps, hs), 16);
+  *unit = divisor(ps, hs);
+  if (*unit == 0) *unit = 16;  // one head of one page
   *places = (a.pages.n_pages - 1) * (ps / *unit) + (a.hkv - 1) * (hs / *unit) + 1;
   return *places < 0x7fffffff;
 }

@@ -111,7 +111,7 @@ domino_status check_pages(const domino_paged_cache* c, domino_kv_cache* rows) {
   const int64_t st[3] = {c->page_stride, c->head_stride, c->slot_stride};
   for (int64_t s : st)
     if (e4m3 ? s < 0 || (s & 15) : !stride_ok(s, c->dtype)) return DOMINO_ERR_INVALID_ARG;
-  if (!c->page_table || ((uintptr_t)c->page_table & 3u) || (c->batch > 1 && c->table_stride < c->max_pages)) return DOMINO_ERR_INVALID_ARG;
+  if ((c->batch > 0 && !c->page_table) || ((uintptr_t)c->page_table & 3u) || (c->batch > 1 && c->table_stride < c->max_pages)) return DOMINO_ERR_INVALID_ARG;
   if (e4m3 && (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale))) return DOMINO_ERR_INVALID_ARG;
   if (c->head_dim > 256 || (c->head_dim & (e4m3 ? 15 : 7)) || c->batch > 65535 || c->n_kv_heads > 1024) return DOMINO_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1))) return DOMINO_ERR_UNSUPPORTED;

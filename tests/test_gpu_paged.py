@@ -327,7 +327,33 @@ ATTN = [
     ([3], [50], 4, 4, 16, "causal", 0, 0, False, 32),
     ([200], [900], 8, 1, 128, "full", 0, 0, False, 64),
     ([64, 200], [1000, 1], 16, 2, 64, "causal", 0, 0, False, 16),
+    ([20, 3], [300, 5], 6, 3, 16, "causal", 0, 0, True, 16),
+    ([40, 3], [100, 5], 12, 3, 48, "full", 0, 0, True, 32),
 ]
+
+
+@pytest.mark.parametrize("kind,D", [(BF, 8), (BF, 24), (BF, 72), (BF, 104), (F32, 8), (F32, 72)])
+@pytest.mark.parametrize("slot_major", [False, True])
+@pytest.mark.parametrize("n", [2, 20, 90])
+def test_heads_of_odd_sizes(kind, D, slot_major, n):
+    """Strides that are odd multiples of 16 bytes."""
+    spec = ([n, n], [200, 31], 6, 3, D, "causal", 0, 0, slot_major, 16)
+    check(spec, *run(kind, spec, 900 + D))
+
+
+def test_layers_share_a_pool():
+    """Keys and values of one allocation, several layers' pages in turn: strides beyond what a layer's own pages span."""
+    g = gen(12)
+    pool = randn(g, 40, 3, 2, 2, 32, 64).to(BF)  # page, layer, key or value, head, slot, element
+    table = torch.randperm(40, generator=g, device="cuda").int()[:32].view(2, 16)
+    for at in range(3):
+        k, v = pool[:, at, 0], pool[:, at, 1]
+        for n in (1, 9, 60):
+            q = randn(g, 2 * n, 8, 64).to(BF)
+            out, lse = PagedAttention(k, v, table, 8, 2 * n, n, 400).attend(q, ints([400, 77]), want_lse=True)
+            apart = PagedAttention(k.contiguous(), v.contiguous(), table, 8, 2 * n, n, 400)
+            want, wl = apart.attend(q, ints([400, 77]), want_lse=True)
+            assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
 def run(kind, spec, seed, poison=None, scale=None, qscale=2.0, empty_row=None, prepare=None):
