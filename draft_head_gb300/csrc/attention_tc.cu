@@ -978,7 +978,7 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
         ok = warp_wait(&s_ready[g], tiles & 1u, s_abort, ctl, p.timeout_ns);
         if (!ok) break;
         tc_fence_after();
-        if (r_in - lane >= w.rows) {  // no row of the tile is this warp's: its weights may be anything
+        if (NQ == 1 && r_in - lane >= w.rows) {  // no row of the tile is this warp's: its weights may be anything
           tc_fence_before();
           __syncwarp();
           if (lane < 2) mbar_arrive(&p_ready[g * 2 + lane]);

@@ -385,14 +385,16 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
   report_requests(a.rows, a.ctl);
   int b, i, ctx, rows;
   bool mine, placed;
-  int64_t slot = 0;  // the row's place in the cache
+  int64_t slot = 0;  // the row's place in pages
   int page = 0, s = 0;
   float raw[16];
   auto look = [&](int t) {  // the row's place and angles
     const int pos = !mine ? 0 : a.rows.positions ? __ldg(a.rows.positions + t) : ctx + i;
     placed = mine && (a.rot == 0 || (pos >= 0 && pos < a.max_pos));
-    s = ctx + i;
-    if (placed) placed = at.place(b, s, slot, page);
+    if (CACHE != kWhole) {
+      s = ctx + i;
+      if (placed) placed = at.place(b, s, slot, page);
+    }
     if (mine && !placed && threadIdx.x == 0) dev_error(a.ctl, DEV_ERR_DATA);
     if (placed) at.read_angles(pos, raw);
   };
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(kNrThreads, kRunCtas) norm_rope_run_kernel(con
   int t = t0;
   for (; t < t_end; ++t) {
     const bool on_row = placed;
-    const int64_t row_slot = slot;
+    const int64_t row_slot = CACHE == kWhole ? (int64_t)b * a.rs + (int64_t)(ctx + i) * a.ss + e0 : slot;
     const int row_page = page, row_s = s;
     if (on_row) at.set_angles(raw);
     if (t + 1 < t_end) {

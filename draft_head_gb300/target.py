@@ -23,12 +23,13 @@ def _need(t, dtype, count: int, device: int, what: str):
                          f"on {t.device}")
 
 
-def _run(call, ordinal: int, *args) -> int:
-    """A call of the library on its arrays' device, on torch's current stream there."""
-    if torch.cuda.current_device() == ordinal:
-        return call(*args, B._stream(None))
-    with torch.cuda.device(ordinal):
-        return call(*args, B._stream(None))
+def _stream(ordinal: int):
+    """torch's current stream's handle, or None where the arrays' device is not the current one: the caller goes there and asks
+    again."""
+    at = torch.cuda.current_device()
+    if at != ordinal:
+        return None
+    return B._raw_stream(at) if B._raw_stream is not None else B._stream(None)
 
 
 def rope_table(positions: int, rot_dim: int, base: float = 1e6, device="cuda") -> torch.Tensor:
@@ -100,10 +101,13 @@ class _Attention:
             raise ValueError(f"qkv: [tokens, {width}] of {self.dtype} on {self.dev}")
         tokens = qkv.shape[0]
         self._set_rows(tokens, ctx_len, q_start, positions)
+        stream = _stream(self.ordinal)
+        if stream is None:
+            with torch.cuda.device(self.ordinal):
+                return self.append(qkv, ctx_len, q_start, positions)
         p, stride, size = qkv.data_ptr(), qkv.stride(0), qkv.element_size()
         k = p + self.hq * self.dim * size
-        st = _run(self._calls[0], self.ordinal, *self._refs, self.hq, p, stride, k, stride, k + self.hkv * self.dim * size, stride,
-                  *self._norm)
+        st = self._calls[0](*self._refs, self.hq, p, stride, k, stride, k + self.hkv * self.dim * size, stride, *self._norm, stream)
         if st:
             raise B.DominoError(st, self._append)
         return self.q if tokens == self.max_tokens else self.q[:tokens]
@@ -126,8 +130,12 @@ class _Attention:
             if mask.dim() == 0 or mask.shape[-1] != n:
                 raise ValueError(f"mask: [{batch}, {n}, {n}], not {tuple(mask.shape)}")
             _need(mask, torch.uint8, batch * n * n, self.ordinal, "mask")
-        st = _run(self._calls[1], self.ordinal, *self._refs, self.hq, q.data_ptr(), self.scale, mode, mask_ptr, self.window,
-                  self.sinks, self._out[0], self._out[1] if want_lse else None, *self._ws)
+        stream = _stream(self.ordinal)
+        if stream is None:
+            with torch.cuda.device(self.ordinal):
+                return self.attend(q, ctx_len, q_start, positions, mask, want_lse)
+        st = self._calls[1](*self._refs, self.hq, q.data_ptr(), self.scale, mode, mask_ptr, self.window, self.sinks, self._out[0],
+                            self._out[1] if want_lse else None, *self._ws, stream)
         if st:
             raise B.DominoError(st, self._attend)
         out, lse = (self.out, self.lse) if tokens == self.max_tokens else (self.out[:tokens], self.lse[:tokens])
@@ -189,8 +197,11 @@ class PagedAttention(_Attention):
         _need(count, torch.int32, batch, ordinal, "count")
         if first is not None:
             _need(first, torch.int32, batch, ordinal, "first")
-        st = _run(B.lib.domino_paged_read, ordinal, self._refs[0], B._ptr(first), count.data_ptr(), out.capacity, ctypes.byref(out),
-                  *self._ws)
+        stream = _stream(ordinal)
+        if stream is None:
+            with torch.cuda.device(ordinal):
+                return self.read(k_out, v_out, count, first)
+        st = B.lib.domino_paged_read(self._refs[0], B._ptr(first), count.data_ptr(), out.capacity, ctypes.byref(out), *self._ws, stream)
         if st:
             raise B.DominoError(st, "domino_paged_read")
 
@@ -232,8 +243,12 @@ class TokenScorer:
             _need(tokens, torch.int32, n, ordinal, "tokens")
         if temperature is not None:
             _need(temperature, torch.float32, n, ordinal, "temperature")
-        st = _run(B.lib.domino_token_logprobs, ordinal, self._dt, logits.data_ptr(), logits.stride(0), n, self.V, B._ptr(tokens),
-                  B._ptr(temperature), self.top_n, *self._args)
+        stream = _stream(ordinal)
+        if stream is None:
+            with torch.cuda.device(ordinal):
+                return self.score(logits, tokens, temperature)
+        st = B.lib.domino_token_logprobs(self._dt, logits.data_ptr(), logits.stride(0), n, self.V, B._ptr(tokens), B._ptr(temperature),
+                                         self.top_n, *self._args, stream)
         if st:
             raise B.DominoError(st, "domino_token_logprobs")
         return self.out if n == self.rows else Scores(*(t[:n] for t in self.out))
