@@ -621,7 +621,8 @@ domino_status domino_paged_read(const domino_paged_cache* cache, const int32_t* 
 
 /*
  * domino_block_attention over a cache in pages; q and out are of its type (DOMINO_BF16 for DOMINO_E4M3). Keys and values count as
- * what their codes and scales stand for. The rows of a request with a missing page among the slots that are looked at get an
+ * what their codes and scales stand for (beside quantised values from 2^90 on, the softmax may lose weights below 2^-30 of the
+ * largest). The rows of a request with a missing page among the slots that are looked at get an
  * unspecified result.
  */
 size_t domino_paged_attention_workspace_bytes(const domino_paged_cache* cache, const domino_block* block, int n_q_heads);

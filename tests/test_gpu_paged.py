@@ -245,6 +245,7 @@ READ = [
     (BF, 32, [1, 40], [200, 77], 2, 72, True, 1),
     (F32, 16, [0, 7], [33, 95], 4, 8, False, 0),
     (F32, 128, [0] * 5, [1, 64, 65, 127, 300], 8, 128, False, 9),
+    (E4M3, 32, [3, 0, 31, 64], [0, 0, 5, 0], 2, 64, False, 2),
 ]
 
 

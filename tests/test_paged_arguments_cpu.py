@@ -243,3 +243,18 @@ def test_pages_are_reached_through_the_check_alone():
     assert found == [("pages.cuh", "p.table")]
     check = part(source("pages.cuh"), "int page_of(const PagesArgs& p, int b, int s) {", "}")
     assert "(unsigned)page < (unsigned)p.n_pages ? page : -1" in check
+
+
+def test_waits_over_pages_follow_the_rules():
+    """Whole warps leave a wait with one answer; boxes in flight land on every way out; who converts codes waits on every use of a
+    buffer, in order, and is told when no more come."""
+    text = source("attention_tc.cu")
+    convert = part(text, "if (C::kCodes && warp >= 12) {", "} else if (CACHE != kWhole && warp == 0) {")
+    bring = part(text, "} else if (CACHE != kWhole && warp == 0) {", "} else if (warp == 0 && lane == 0) {")
+    for role in (convert, bring):
+        assert "warp_wait(" in role and not re.search(r"(!|=|&&|\breturn)\s*mbar_wait\(", role)
+    assert "if (note & kNoteEnd) break;" in convert and "++from == in_slots" in convert and "++to == slots" in convert
+    after = bring[bring.index("walk.next("):]
+    assert after.index("kNoteEnd") < after.index("mbar_land(&full[") and "mbar_land(&full[j % in_slots]" in after
+    ring = part(source("attention_rows.cu"), "if (kCodes) {\n    asm volatile(", "}")
+    assert "cp.async.wait_all" in ring  # before the ring's memory becomes the warps' sums
