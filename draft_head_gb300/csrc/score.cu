@@ -14,8 +14,8 @@
 // A cluster of CTAs takes a row when there are few; their results meet in the first one's shared memory.
 //
 // Many rows: bound by instructions, 12.7 a logit with the exponential's unit a third busy. 1088 rows of 151,936 in bf16 with the
-// 8 most likely tokens 95 us, 3.5 TB/s (without them 83), where 1088 blocks are 7.2 rounds of an SM and take 8. Four blocks an SM (three: 98, five:
-// 107; twice as many of 128 threads: 98); a row over two blocks 105. One row: 12.6 us, launch, two batches, three joins and a
+// 8 most likely tokens 94 us, 3.5 TB/s (without them 81), where 1088 blocks are 7.2 rounds of an SM and take 8. Four blocks an SM (three: 98, five:
+// 107; twice as many of 128 threads: 98); a row over two blocks 105. One row: 11.5 us, launch, two batches, three joins and a
 // cluster barrier behind one another.
 #include <math.h>
 
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
     return x;
   };
   u.template load<kUnits>(u0, u1, next);
-#pragma unroll 1
+#pragma unroll 2
   for (int ub = u0; ub < u1; ub += kBatch) {
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) cur[j] = next[j];
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
       __syncthreads();
     }
     const float reached = s.reached;
-    for (int k = 0; k < stretches; ++k) {
+    for (int k = 0; k < stretches && thread_top >= reached; ++k) {
       const float top = s.tops[k][threadIdx.x];
       if (top >= reached && top > -INFINITY) s.work[atomicAdd(&s.works, 1)] = (uint16_t)(k * kThr + threadIdx.x);
     }
@@ -397,14 +397,17 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
 
   // The warp's, the block's, the cluster's. Blocks of a cluster by the warps of the first one, whose reads of the others' memory are
   // then on their way together.
+  {
+    float m = q.m;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    Sums o;
-    o.m = __shfl_xor_sync(kAll, q.m, d);
-    o.S = __shfl_xor_sync(kAll, q.S, d);
-    o.E = __shfl_xor_sync(kAll, q.E, d);
-    q.join(o, c);
-    before += __shfl_xor_sync(kAll, before, d);
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, d));
+    q.raise(m, c);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      q.S += __shfl_xor_sync(kAll, q.S, d);
+      q.E += __shfl_xor_sync(kAll, q.E, d);
+    }
+    before = __reduce_add_sync(kAll, before);
   }
   auto join_warps = [&] {
 #pragma unroll 1
