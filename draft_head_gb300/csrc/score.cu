@@ -54,6 +54,11 @@ __device__ __forceinline__ u64 dsmem_u64(uint32_t at) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
   return x;
 }
+__device__ __forceinline__ int dsmem_s32(uint32_t at) {
+  int x;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
 __device__ __forceinline__ float4 dsmem_f4(uint32_t at) {
   float4 x;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
@@ -62,21 +67,29 @@ __device__ __forceinline__ float4 dsmem_f4(uint32_t at) {
 
 // The sums of part of a row; `m` the maximum of its logits. S and E are in units of log2 from m c as it is rounded, so that d is one
 // multiply-add from the logit and the rounding is nobody's error; where m c is beyond fp32, from m.
+// S is held with what its additions round away, r: where one token has nearly all, the logarithm of S is that of the rest.
 struct Sums {
-  float m, S, E;
+  float m, S, E, r;
+  __device__ __forceinline__ void add(float x) {
+    const float t = S + x, y = t - S;
+    r += (S - (t - y)) + (x - y);
+    S = t;
+  }
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m
     if (to == m) return;
     const float at = to * c;
-    const float r = isinf(at) ? (m - to) * c : fmaf(-1.0f, at, m * c), f = ex2(r);
-    E = f == 0.0f ? 0.0f : f * fmaf(r, S, E);
+    const float d = isinf(at) ? (m - to) * c : fmaf(-1.0f, at, m * c), f = ex2(d);
+    E = f == 0.0f ? 0.0f : f * fmaf(d, S, E);
     S *= f;
+    r *= f;
     m = to;
   }
   __device__ __forceinline__ void join(Sums o, float c) {
     const float to = fmaxf(m, o.m);
     raise(to, c);
     o.raise(to, c);
-    S += o.S;
+    add(o.S);
+    r += o.r;
     E += o.E;
   }
 };
@@ -219,7 +232,8 @@ struct Smem {
   int count[kWarps];
   int works;
   uint16_t work[kStretches * kThr];  // stretches to be read again
-  float4 part;                       // the CTA's m, S, E and rank (its bits)
+  alignas(16) Sums part;             // the CTA's, read as four floats, and
+  int part_count;
   u64 best[32];
 };
 
@@ -248,7 +262,7 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
   const u64 least = value_id_key(-INFINITY, 0);
   if (threadIdx.x == 0) s.works = 0;
 
-  Sums q = {-INFINITY, 0.0f, 0.0f};
+  Sums q = {-INFINITY, 0.0f, 0.0f, 0.0f};
   int before = 0;
   constexpr int kBatch = kUnits * kThr;  // units
   const int batches = (u1 - u0 + kBatch - 1) / kBatch, stretch = max(1, (batches + kStretches - 1) / kStretches);  // in batches
@@ -315,13 +329,13 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {  // infinities share everything
           const float v = U::value(x, e), d = v == m ? 0.0f : fmaxf((v - m) * c, kLeastD), w = ex2(d);
-          q.S += w;
+          q.add(w);
           q.E = fmaf(w, d, q.E);
         }
       }
     } else {
       const float2 c2 = make_float2(c, c), n2 = make_float2(-at, -at);
-      float2 S2 = make_float2(q.S, 0.0f), E2 = make_float2(q.E, 0.0f);
+      float2 S2 = make_float2(0.0f, 0.0f), E2 = make_float2(q.E, 0.0f);
 #pragma unroll
       for (int j = 0; j < kUnits; ++j)
 #pragma unroll
@@ -333,7 +347,8 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
           S2 = add2(S2, w);
           E2 = fma2(w, d, E2);
         }
-      q.S = S2.x + S2.y;
+      q.add(S2.x);
+      q.add(S2.y);
       q.E = E2.x + E2.y;
     }
   }
@@ -404,7 +419,9 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
     q.raise(m, c);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-      q.S += __shfl_xor_sync(kAll, q.S, d);
+      const float S = __shfl_xor_sync(kAll, q.S, d), r = __shfl_xor_sync(kAll, q.r, d);
+      q.add(S);
+      q.r += r;
       q.E += __shfl_xor_sync(kAll, q.E, d);
     }
     before = __reduce_add_sync(kAll, before);
@@ -431,29 +448,35 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
   if (size > 1) {
     if (warp == 0) {
       s.best[lane] = best;
-      if (lane == 0) s.part = make_float4(q.m, q.S, q.E, __int_as_float(before));
+      if (lane == 0) {
+        s.part = q;
+        s.part_count = before;
+      }
     }
     cluster_sync();
     if (rank == 0) {
       float4 p[kMaxCluster / kWarps];
+      int counts[kMaxCluster / kWarps];
       u64 x[kMaxCluster / kWarps];
 #pragma unroll
       for (int i = 0; i < kMaxCluster / kWarps; ++i) {
         const int k = warp + i * kWarps;
         p[i] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
         x[i] = 0;
+        counts[i] = 0;
         if (k < size) {
           p[i] = dsmem_f4(dsmem(&s.part, (uint32_t)k));
+          counts[i] = dsmem_s32(dsmem(&s.part_count, (uint32_t)k));
           x[i] = dsmem_u64(dsmem(&s.best[lane], (uint32_t)k));
         }
       }
-      q = Sums{p[0].x, p[0].y, p[0].z};
-      before = __float_as_int(p[0].w);
+      q = Sums{p[0].x, p[0].y, p[0].z, p[0].w};
+      before = counts[0];
       best = x[0];
 #pragma unroll
       for (int i = 1; i < kMaxCluster / kWarps; ++i) {
-        q.join(Sums{p[i].x, p[i].y, p[i].z}, c);
-        before += __float_as_int(p[i].w);
+        q.join(Sums{p[i].x, p[i].y, p[i].z, p[i].w}, c);
+        before += counts[i];
         if (n > 0) best = merged(best, x[i]);
       }
       __syncthreads();
@@ -462,13 +485,13 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
     cluster_sync();  // the others' shared memory has been read
   }
   if (rank != 0 || warp != 0) return;
-  const float log_s = log2f(q.S), at = q.m * c;
+  // log2 of the sum from m c as it is rounded, and the logarithm from m itself (an infinity: beyond fp32 the sum is from m).
+  const float log_s = log2f(q.S) + (q.r != 0.0f ? q.r / q.S * kLog2e : 0.0f), at = q.m * c;
+  const float log_m = (isinf(at) ? log_s : log_s - fmaf(q.m, c, -at)) * kLn2;
   auto logprob = [&](float x) {
     if (!fine) return __uint_as_float(0x7fffffffu);
     if (q.m == -INFINITY || x == -INFINITY) return -INFINITY;
-    const float d = fmaf(x, c, -at);
-    if (!isfinite(d)) return (x == q.m ? 0.0f : (x - q.m) / temp) - log_s * kLn2;  // beyond fp32 in log2 units
-    return (d - log_s) * kLn2;
+    return (x == q.m ? 0.0f : (x - q.m) / temp) - log_m;
   };
   if (lane == 0) {
     const bool none = token == -1;
