@@ -14,7 +14,7 @@
 // A cluster of CTAs takes a row when there are few; their results meet in the first one's shared memory.
 //
 // Many rows: bound by instructions, 12.7 a logit with the exponential's unit a third busy. 1088 rows of 151,936 in bf16 with the
-// 8 most likely tokens 94 us, 3.5 TB/s (without them 81), where 1088 blocks are 7.2 rounds of an SM and take 8. Four blocks an SM (three: 98, five:
+// 8 most likely tokens 95 us, 3.5 TB/s (without them 83), where 1088 blocks are 7.2 rounds of an SM and take 8. Four blocks an SM (three: 98, five:
 // 107; twice as many of 128 threads: 98); a row over two blocks 105. One row: 11.5 us, launch, two batches, three joins and a
 // cluster barrier behind one another.
 #include <math.h>
