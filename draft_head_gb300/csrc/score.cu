@@ -65,8 +65,13 @@ __device__ __forceinline__ float4 dsmem_f4(uint32_t at) {
   return x;
 }
 
-// The sums of part of a row; `m` the maximum of its logits. S and E are in units of log2 from m c as it is rounded, so that d is one
-// multiply-add from the logit and the rounding is nobody's error; where m c is beyond fp32, from m.
+// Where a maximum's product with c is below this, its weights are in units of log2 from the product as it is rounded: d is one
+// multiply-add from the logit, and the rounding, half a unit at most, is nobody's error. Beyond it (temperatures of 1e-6 and less,
+// logits of 1e8), where the rounding may be more than the exponential holds, they are from the maximum itself: d = (x - m) c.
+constexpr float kRoundedBelow = 16777216.0f;  // 2^24
+__device__ __forceinline__ bool rounded(float at) { return fabsf(at) < kRoundedBelow; }
+
+// The sums of part of a row; `m` the maximum of its logits.
 // S is held with what its additions round away, r: where one token has nearly all, the logarithm of S is that of the rest.
 struct Sums {
   float m, S, E, r;
@@ -77,8 +82,11 @@ struct Sums {
   }
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m
     if (to == m) return;
-    const float at = to * c;
-    const float d = isinf(at) ? (m - to) * c : fmaf(-1.0f, at, m * c), f = ex2(d);
+    // From one point to the other, each rounded or not: products that no addition may take up.
+    const float at = __fmul_rn(to, c), was = __fmul_rn(m, c);
+    float d = __fsub_rn(was, at);
+    if (!rounded(at) || !rounded(was)) d = rounded(at) ? fmaf(m, c, -at) : rounded(was) ? -fmaf(to, c, -was) : (m - to) * c;
+    const float f = ex2(d);
     E = f == 0.0f ? 0.0f : f * fmaf(d, S, E);
     S *= f;
     r *= f;
@@ -321,8 +329,8 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
     }
 
     q.raise(fmaxf(q.m, top), c);
-    const float m = q.m == -INFINITY ? 0.0f : q.m, at = m * c;
-    if (isinf(at)) {
+    const float m = q.m == -INFINITY ? 0.0f : q.m, at = __fmul_rn(m, c);
+    if (!rounded(at)) {
 #pragma unroll 1
       for (int j = 0; j < kUnits; ++j) {
         const uint4 x = unit(j);
@@ -485,9 +493,9 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
     cluster_sync();  // the others' shared memory has been read
   }
   if (rank != 0 || warp != 0) return;
-  // log2 of the sum from m c as it is rounded, and the logarithm from m itself (an infinity: beyond fp32 the sum is from m).
-  const float log_s = log2f(q.S) + (q.r != 0.0f ? q.r / q.S * kLog2e : 0.0f), at = q.m * c;
-  const float log_m = (isinf(at) ? log_s : log_s - fmaf(q.m, c, -at)) * kLn2;
+  // log2 of the sum from m c as it is rounded, or from m, and the logarithm from m itself.
+  const float log_s = log2f(q.S) + (q.r != 0.0f ? q.r / q.S * kLog2e : 0.0f), at = __fmul_rn(q.m, c);
+  const float log_m = (rounded(at) ? log_s - fmaf(q.m, c, -at) : log_s) * kLn2;
   auto logprob = [&](float x) {
     if (!fine) return __uint_as_float(0x7fffffffu);
     if (q.m == -INFINITY || x == -INFINITY) return -INFINITY;
@@ -499,7 +507,7 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
     if (a.logprob) a.logprob[r] = none && fine ? 0.0f : given ? logprob(xt) : NAN;
     if (a.rank) a.rank[r] = none ? 0 : given ? before : -1;
     if (a.entropy) a.entropy[r] = !fine ? NAN : q.m == -INFINITY ? 0.0f : (log_s - q.E / q.S) * kLn2;
-    if (a.lse) a.lse[r] = !fine ? NAN : isinf(at) ? q.m / temp + log_s * kLn2 : (at + log_s) * kLn2;
+    if (a.lse) a.lse[r] = !fine ? NAN : rounded(at) ? (at + log_s) * kLn2 : q.m / temp + log_s * kLn2;
   }
   if (lane < n) {
     const bool there = best > least;
