@@ -25,9 +25,10 @@
 // Pages hold 16 slots at least, so a tile of 16 lies in one: one table entry a tile, read a tile ahead.
 // Codes (e4m3 with a power of two per slot and head) are fp16 to the mma: a conversion instruction makes two of them at once, exactly
 // (in bf16 it takes a permute, a shift, a mask and a product), and no scale is applied to them. A key's scale multiplies its score, a
-// value's its weight, both in fp32: P is rounded to fp16, 2^-12 of a weight where bf16 gives 2^-9, and as the weights carry the scales the
-// running maximum is that of score + scale, which keeps them below 2^15; 2^11 at the maximum, so that weights down to 2^-35 of it count. Queries are
-// brought to fp16's range by a power of two per row. A value that is no number has that in its scale, so a
+// value's its weight, as an addition to the logarithm, in fp32: P is rounded to fp16, 2^-12 of a weight where bf16 gives 2^-9. As the weights
+// carry the scales, the maximum that they are relative to is that of score + scale, 2^11 there and 2^15 at most, so that products down to
+// 2^-35 of the largest count; the softmax's own weights are summed in fp32 relative to the scores' maximum (an exponential more, 229 us both).
+// Queries are brought to fp16's range by a power of two per row. A value that is no number has that in its scale, so a
 // row that does not see it cannot get it: there is nothing to clear. The codes wait in a warp's ring in shared memory (cp.async), which
 // frees the registers of the tiles on their way: one token over 4000 quantised slots 11.7 us, 128 tokens over up to 8000 229 us, 4.8 TB/s of
 // half the bytes (bf16 pages 393 us, 5.6 TB/s).
@@ -53,8 +54,9 @@ constexpr int kMostPieces = 64;  // of a row tile: their join takes a round trip
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazyBf16 = 32.0f;
-// Codes: weights in fp16, kAtMost at the maximum and kAtMost 2^kLazyCodes at most.
-constexpr float kLazyCodes = 4.0f, kAtMost = 2048.0f;  // 2^11
+// Codes: weights with their values' scales in fp16, 2^kAtMost at the maximum and 2^(kAtMost + kLazyCodes) at most.
+constexpr float kLazyCodes = 4.0f, kAtMost = 11.0f;
+constexpr float kRoom = 10.0f;  // a warp's sum of weights is left between 2^-kRoom and twice that: no join passes fp32's range
 constexpr int kCodesCtas = 3, kDepth = 2;  // of one group of rows, on an SM; tiles of a warp's ring (3 and 2: 128 tokens 229 us, one 11.7; 3 and 3: 231 and 11.8; 4 and 2: 224 and 13.0)
 
 struct RowsP {
@@ -268,14 +270,17 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     }
   };
 
-  float o[NT][4 * JJ][4], m[NT][2], l[NT][2];
+  // Codes: o is relative to m, kAtMost below the maximum of score + the value's exponent; l, the sum of the softmax's own
+  // weights, to that of the scores, ms. (From one of them, weights or their sum would leave fp32's range beside values whose
+  // exponents are far apart.) They begin below every score, so that -inf alone has weight 0.
+  float o[NT][4 * JJ][4], m[NT][2], l[NT][2], ms[NT][2];
 #pragma unroll
   for (int g = 0; g < NT; ++g) {
 #pragma unroll
     for (int t = 0; t < 4 * JJ; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[g][t][e] = 0.0f;
-    m[g][0] = m[g][1] = -INFINITY;
+    m[g][0] = m[g][1] = ms[g][0] = ms[g][1] = kCodes ? -3.402823466e+38f : -INFINITY;
     l[g][0] = l[g][1] = 0.0f;
   }
   int page = 0;
@@ -294,8 +299,8 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     const bool gone = CACHE != kWhole && !tile_there;  // no such page: nothing was read
     Piece kr[2][KS], vr[4][JJ];
     const uint8_t* codes = nullptr;
-    // Codes: the scales of slots n and n + 8 (e / 2 of the scores below), the values' also as exponents.
-    float ks[2], vs[2], ve[2];
+    // Codes: the keys' scales of slots n and n + 8 (e / 2 of the scores below), and the values' as exponents.
+    float ks[2], ve[2];
     if constexpr (kCodes) {
       if (k + kAhead < k_end) page = page_at(k + kAhead);
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
@@ -306,8 +311,7 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
       for (int x = 0; x < 2; ++x) {
         ks[x] = scale_f32(codes[Codes::kScales + n + 8 * x]);
         const int v = codes[Codes::kScales + kBN + n + 8 * x];
-        ve[x] = v == kScaleNan ? 0.0f : (float)(v - 127);
-        vs[x] = scale_f32(v) * kAtMost;
+        ve[x] = v == kScaleNan ? scale_f32(v) : (float)(v - 127);
       }
     } else {
 #pragma unroll
@@ -376,31 +380,69 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
           if (hidden[e]) s[g][e] = -INFINITY;
         }
       }
-      // Codes: the maximum is that of the weights with their values' scales, which is what fp16 has to hold.
-      const float top[2] = {kCodes ? fmaxf(s[g][0] + ve[0], s[g][2] + ve[1]) : fmaxf(s[g][0], s[g][2]),
-                            kCodes ? fmaxf(s[g][1] + ve[0], s[g][3] + ve[1]) : fmaxf(s[g][1], s[g][3])};
-      if (__any_sync(0xffffffffu, top[0] > m[g][0] + kLazy || top[1] > m[g][1] + kLazy)) {
-        float f[2];
+      if constexpr (kCodes) {
+        float x[4], y[4];  // the weights' logarithms: of the products', of the softmax's own
+        auto relative = [&] {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = top[e];
+          for (int e = 0; e < 4; ++e) {
+            x[e] = s[g][e] + (ve[e >> 1] - m[g][e & 1]);
+            y[e] = s[g][e] - ms[g][e & 1];
+          }
+        };
+        relative();
+        if (__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > kAtMost + kLazy ||
+                                        fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > kLazy)) {
+          float f[2];
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          const float now = x > m[g][e] + kLazy ? x : m[g][e];
-          f[e] = now == m[g][e] || m[g][e] == -INFINITY ? 1.0f : ex2(m[g][e] - now);
-          m[g][e] = now;
-          l[g][e] *= f[e];
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(s[g][e] + ve[0], s[g][2 + e] + ve[1]), high = fmaxf(s[g][e], s[g][2 + e]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+            }
+            const float now = top - m[g][e] > kAtMost + kLazy ? top - kAtMost : m[g][e];
+            const float now_s = high - ms[g][e] > kLazy ? high : ms[g][e];
+            f[e] = ex2(m[g][e] - now);
+            l[g][e] *= ex2(ms[g][e] - now_s);
+            m[g][e] = now;
+            ms[g][e] = now_s;
+          }
+#pragma unroll
+          for (int t = 0; t < 4 * JJ; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[g][t][e] *= f[e & 1];
+          relative();
         }
 #pragma unroll
-        for (int t = 0; t < 4 * JJ; ++t)
+        for (int e = 0; e < 4; ++e) {
+          l[g][e & 1] += ex2(y[e]);
+          s[g][e] = hidden[e] ? 0.0f : ex2(x[e]);
+        }
+      } else {
+        const float top[2] = {fmaxf(s[g][0], s[g][2]), fmaxf(s[g][1], s[g][3])};
+        if (__any_sync(0xffffffffu, top[0] > m[g][0] + kLazy || top[1] > m[g][1] + kLazy)) {
+          float f[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[g][t][e] *= f[e & 1];
-      }
+          for (int e = 0; e < 2; ++e) {
+            float x = top[e];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[g][e] = ex2(s[g][e] - (m[g][e & 1] == -INFINITY ? 0.0f : m[g][e & 1]));
-        l[g][e & 1] += s[g][e];
-        if (kCodes) s[g][e] = hidden[e] ? 0.0f : s[g][e] * vs[e >> 1];
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            const float now = x > m[g][e] + kLazy ? x : m[g][e];
+            f[e] = now == m[g][e] || m[g][e] == -INFINITY ? 1.0f : ex2(m[g][e] - now);
+            m[g][e] = now;
+            l[g][e] *= f[e];
+          }
+#pragma unroll
+          for (int t = 0; t < 4 * JJ; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[g][t][e] *= f[e & 1];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[g][e] = ex2(s[g][e] - (m[g][e & 1] == -INFINITY ? 0.0f : m[g][e & 1]));
+          l[g][e & 1] += s[g][e];
+        }
       }
       pw[g][0] = transpose8(kCodes ? pack_f16(s[g][0], s[g][1]) : pack_bf16(s[g][0], s[g][1]));
       pw[g][1] = transpose8(kCodes ? pack_f16(s[g][2], s[g][3]) : pack_bf16(s[g][2], s[g][3]));
@@ -467,6 +509,19 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
       const int r = g * 8 + 2 * c + e;
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[g][e] += __shfl_xor_sync(0xffffffffu, l[g][e], d);
+      if (kCodes) {
+        // Both relative to one point, kRoom above the logarithm of l (which is 1 at least where a slot counts at all). The factor
+        // of o may be below fp32's range where the result is not.
+        const float to = ms[g][e] + (kRoom + (float)((int)(__float_as_uint(l[g][e]) >> 23) - 127));
+        const float half = l[g][e] == 0.0f ? 1.0f : ex2(0.5f * (m[g][e] - to));
+        m[g][e] = l[g][e] == 0.0f ? -INFINITY : to;
+        l[g][e] *= ex2(ms[g][e] - to);
+#pragma unroll
+        for (int t = 0; t < 4 * JJ; ++t) {
+          o[g][t][e] = o[g][t][e] * half * half;
+          o[g][t][2 + e] = o[g][t][2 + e] * half * half;
+        }
+      }
       if (n == 0) s_ml[warp][r] = make_float2(m[g][e], l[g][e]);
 #pragma unroll
       for (int j = 0; j < JJ; ++j) {
@@ -480,7 +535,7 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
   auto finish = [&](int r, int e, float4 x, float mm, float ll) {
     const int i = r / G;
     const int64_t row = (int64_t)(q0 + i) * a.hq + h * G + (r - i * G);
-    const float inv = (ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN)) * (kCodes ? 1.0f / kAtMost : 1.0f);
+    const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : NAN);
     *(uint2*)((__nv_bfloat16*)a.out + row * a.D + e) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
     if (e == 0 && a.lse) a.lse[row] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
   };

@@ -621,9 +621,10 @@ domino_status domino_paged_read(const domino_paged_cache* cache, const int32_t* 
 
 /*
  * domino_block_attention over a cache in pages; q and out are of its type (DOMINO_BF16 for DOMINO_E4M3). Keys and values count as
- * what their codes and scales stand for (beside quantised values from 2^90 on, the softmax may lose weights below 2^-30 of the
- * largest). The rows of a request with a missing page among the slots that are looked at get an
- * unspecified result.
+ * what their codes and scales stand for. Over quantised pages, up to 16 packed rows (a request's rows times n_q_heads / n_kv_heads)
+ * have operands in fp16: a query's elements count to within 2^-29 of its largest one, a value times its softmax weight to within
+ * 2^-12 of itself and 2^-35 of the largest such product that its row sees. The rows of a request with a missing page among the
+ * slots that are looked at get an unspecified result.
  */
 size_t domino_paged_attention_workspace_bytes(const domino_paged_cache* cache, const domino_block* block, int n_q_heads);
 domino_status domino_paged_attention(const domino_paged_cache* cache, const domino_block* block, int n_q_heads,
