@@ -4,7 +4,8 @@
 // One pass over the row. With m the maximum so far, d = (x - m) / T in log2 units and w = 2^d, a thread keeps S = sum w and
 // E = sum w d; when m / T rises by r, E' = 2^-r (E - r S) and S' = 2^-r S. Then
 //   log sum exp = m / T + log S,   entropy = log S - E / S,   log p(t) = (x_t - m) / T - log S,
-// and as m is the true maximum d <= 0, so that both terms of the entropy are >= 0 and nothing cancels.
+// where m is the true maximum, so that d <= 0 but for what m's product with log2(e) / T is rounded by (half a unit at most): log S and E / S share
+// that and lose no more to it than its last bits. What they leave of a row that one token has, on the wrong side of 0, is set to 0.
 //   Rank: the given token's logit is known beforehand; tokens before it in (logit, id) are counted, in the batches of a warp that
 //     have one.
 //   Most likely tokens: the pass leaves every thread's maxima of up to 16 stretches of its tokens in shared memory. The n-th largest of
@@ -499,14 +500,14 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
   auto logprob = [&](float x) {
     if (!fine) return __uint_as_float(0x7fffffffu);
     if (q.m == -INFINITY || x == -INFINITY) return -INFINITY;
-    return (x == q.m ? 0.0f : (x - q.m) / temp) - log_m;
+    return fminf((x == q.m ? 0.0f : (x - q.m) / temp) - log_m, 0.0f);
   };
   if (lane == 0) {
     const bool none = token == -1;
     if (!fine || (!given && !none)) dev_error(a.ctl, DEV_ERR_DATA);
     if (a.logprob) a.logprob[r] = none && fine ? 0.0f : given ? logprob(xt) : NAN;
     if (a.rank) a.rank[r] = none ? 0 : given ? before : -1;
-    if (a.entropy) a.entropy[r] = !fine ? NAN : q.m == -INFINITY ? 0.0f : (log_s - q.E / q.S) * kLn2;
+    if (a.entropy) a.entropy[r] = !fine ? NAN : q.m == -INFINITY ? 0.0f : fmaxf((log_s - q.E / q.S) * kLn2, 0.0f);
     if (a.lse) a.lse[r] = !fine ? NAN : rounded(at) ? (at + log_s) * kLn2 : q.m / temp + log_s * kLn2;
   }
   if (lane < n) {

@@ -85,3 +85,15 @@ def test_neighbours_of_large_quotients(value, T, V):
     x = torch.stack([steps(value, 30, 0, V), steps(value, 3, 20, V), steps(value, 40, 40, V).sort().values, steps(value, 40, 40, V).sort(descending=True).values])
     tokens = torch.tensor([0, 7, V - 1, 20], dtype=torch.int32, device="cuda")
     score(x, tokens, torch.full((4,), T, device="cuda"), 8)
+
+
+def test_results_keep_their_signs():
+    """No log-probability above 0 and no entropy below it, where one token has all and its product with log2(e) / T is rounded down."""
+    V = 3001
+    x = torch.randn(400, V, generator=gen(12), device="cuda")
+    x[torch.arange(400), torch.arange(400)] = 7.0 + torch.arange(400, device="cuda") / 64
+    x[7, 100:] = 0.5
+    tokens = torch.arange(400, dtype=torch.int32, device="cuda")
+    for T in (1e-6, 3e-6, 1e-4, 0.01, 1.0):
+        got = score(x, tokens, torch.full((400,), T, device="cuda"), 1)
+        assert bool((got.logprob <= 0).all()) and bool((got.top_logprob <= 0).all()) and bool((got.entropy >= 0).all())
