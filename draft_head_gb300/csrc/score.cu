@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(kThr, 4) score_kernel(const ScoreArgs a, int s
   auto logprob = [&](float x) {
     if (!fine) return __uint_as_float(0x7fffffffu);
     if (q.m == -INFINITY || x == -INFINITY) return -INFINITY;
-    return fminf((x == q.m ? 0.0f : (x - q.m) / temp) - log_m, 0.0f);
+    const float d = x == q.m ? 0.0f : x - q.m;  // beyond fp32 the quotients' difference need not be
+    return fminf((isinf(d) ? x / temp - q.m / temp : d / temp) - log_m, 0.0f);
   };
   if (lane == 0) {
     const bool none = token == -1;

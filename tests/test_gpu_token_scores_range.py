@@ -97,3 +97,18 @@ def test_results_keep_their_signs():
     for T in (1e-6, 3e-6, 1e-4, 0.01, 1.0):
         got = score(x, tokens, torch.full((400,), T, device="cuda"), 1)
         assert bool((got.logprob <= 0).all()) and bool((got.top_logprob <= 0).all()) and bool((got.entropy >= 0).all())
+
+
+@pytest.mark.parametrize("T", [2.0, 4.0, 1e3, 1e37, 3e38])
+def test_distances_beyond_fp32(T):
+    """A logit's distance from the maximum is no fp32 number, over the temperature it is one."""
+    big = torch.finfo(F32).max
+    x = torch.randn(3, 4001, generator=gen(13), device="cuda")
+    x[0, 5], x[0, 9] = big, -big
+    x[1] = torch.linspace(-big / 2, big / 2, 4001, device="cuda") * 2
+    x[2] = -big
+    x[2, 4000] = big
+    tokens = torch.tensor([9, 0, 17], dtype=torch.int32, device="cuda")
+    got = score(x, tokens, torch.full((3,), T, device="cuda"), 32)
+    if T > 2:
+        assert bool(torch.isfinite(got.logprob).all())
