@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThr) paged_read_kernel(const PagedReadArgs a)
 }  // namespace
 
 cudaError_t launch_paged_read(const PagedReadArgs& a, cudaStream_t stream) {
-  const dim3 grid((unsigned)((a.max_count + kSlots - 1) / kSlots), (unsigned)a.hkv, (unsigned)a.batch);
+  const dim3 grid((unsigned)(((int64_t)a.max_count + kSlots - 1) / kSlots), (unsigned)a.hkv, (unsigned)a.batch);
   if (a.e4m3)
     paged_read_kernel<true><<<grid, kThr, 0, stream>>>(a);
   else

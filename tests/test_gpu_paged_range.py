@@ -84,3 +84,18 @@ def test_the_smallest_values(n):
     want = torch.stack([torch.softmax(torch.einsum("hsd,hd->hs", pages.values("k", 0, 300 + n).repeat_interleave(2, 0)[:, :301 + i], q[i].double()) * p.scale, -1)
                         .unsqueeze(1).matmul(pages.values("v", 0, 300 + n).repeat_interleave(2, 0)[:, :301 + i])[:, 0] for i in range(n)])
     assert float((out.double() - want).norm() / want.norm()) < 2.0 ** -7
+
+
+@pytest.mark.parametrize("kind", [E4M3, torch.bfloat16, torch.float32])
+def test_read_into_the_largest_capacity(kind):
+    """2^31 - 1 slots (in one place, a stride of 0): as many as the layer takes."""
+    from tests.test_gpu_paged import layer
+    pages = P.Pages(kind, [40], 2, 16, 64, 4)
+    p = layer(pages, 2, 1, 1, 30)
+    out = [torch.full((1, 2, 1, 64), 7.0, dtype=pages.rows_type, device="cuda").expand(1, 2, 2 ** 31 - 1, 64) for _ in "kv"]
+    p.read(*out, ints([1]), first=ints([37]))
+    assert p.last_status() == 0
+    for which, o in zip("kv", out):
+        assert torch.equal(o[0, :, 0].double(), pages.values(which, 0, 40)[:, 37])
+    p.read(*out, ints([2 ** 31 - 1]))
+    assert p.last_status() == 6
