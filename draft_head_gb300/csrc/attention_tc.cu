@@ -51,8 +51,8 @@
 //                same. A code's fields at bf16's places are 2^-120 of it, and one product with the scale does the rest.
 // They share the SM's issue slots and shared memory with the softmax, and set the pace where the cache's bytes would: 64
 // blocks over pages of 64 slots 229 us (bf16 pages 169, of 16 slots 199, 256 181), 16 trees 85 us (66), chunks of 2048 rows for 4 requests
-// 490 us (395), 0.94 PFLOP/s. With the conversion left out, a copy in its place, they take 200, 77 and 463: it is the passes through
-// shared memory, not the arithmetic, that cost. (Products of codes as fp16 with scales relative to a tile's largest: 210, 79 and 502, and
+// 473 us (394), 0.99 PFLOP/s. With the conversion left out, a copy in its place, they took 200, 77 and 463 (the chunks 490 then): it is the
+// passes through shared memory, not the arithmetic, that cost. (Products of codes as fp16 with scales relative to a tile's largest: 210, 79 and 502, and
 // small scales beside large ones would lose bits. Keys by two of the warps and values by the other two: 244, 90 and 654.)
 #include <cuda.h>
 #include <math.h>
@@ -360,9 +360,9 @@ struct Cfg {
   static constexpr uint32_t kStaged = (uint32_t)kBN * DP;  // bytes of a tile of codes
   static constexpr int kThreads = kCodes ? 512 : 384;
   // Registers: launched with 65,536 / kThreads a thread; the softmax's 8 warps take kMore, the others keep kLess
-  // (256 x 208 + 128 x 88 = 64,512 = 384 x 168; 256 x (200 + 56) = 256 x (192 + 64) = 65,536: chunks 507 us with 200, 482 with
-  // 192, 16 trees 86 and 85, 64 blocks 241 and 246).
-  static constexpr int kMore = kCodes ? (NQ == 2 ? 192 : 200) : 208, kLess = kCodes ? (NQ == 2 ? 64 : 56) : 88;
+  // (256 x 208 + 128 x 88 = 64,512 = 384 x 168; 256 x (200 + 56) = 256 x (192 + 64) = 65,536: over codes chunks take 474 us with
+  // 200 and 489 with 192, 64 blocks 229 and 241, 16 trees 84 and 85).
+  static constexpr int kMore = kCodes ? 200 : 208, kLess = kCodes ? 56 : 88;
   static constexpr int BMT = 128 * NQ;
   // List places of a row tile beside its key tiles: its start and epilogue take about 11,000 cycles, a key
   // tile 2,000 (NQ = 1) or 3,200. Two more than that for prompts measured best (2: 497 us, 6: 465, 8: 450,
