@@ -656,7 +656,9 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
 // 2000 / 2500 / 3000 / 4000 slots, 31 / 76 / 80 / 96 / 120 us and 47 / 76 / 81 / 92 / 112; 32 requests 18 / 47 / 48 / 55 / 72
 // and 28 / 46 / 50 / 54 / 67. Fewer, which leave SMs idle: 16 requests up to 4000 slots 43.7 and 43.1; one 21 and 21.
 // Codes, which the tensor core kernel has to turn into bf16 first, are this one's up to 16 rows: 64 requests of 4 rows in groups of 4, up to
-// 500 / 2000 / 4000 / 8000 slots, 29 / 70 / 105 / 189 us and 56 / 105 / 162 / 267; 16 requests 15 / 38 / 44 / 62 and 27 / 45 / 64 / 100.
+// 500 / 2000 / 8000 slots, 30 / 71 / 193 us and 57 / 106 / 270, and 2 rows in groups of 8, 3 in groups of 5, 8 in groups of 2 or 16 rows of
+// a head of its own within 3 us of either; 16 requests 15 / 39 / 64 and 27 / 45 / 100. (From 9 rows on two CTAs, 8 warps, run on an SM; the bytes
+// of the longest would take 82 us.)
 bool attn_rows_applies(const AttnArgs& a) {
   const int64_t rows = (int64_t)a.rows.max_q * (a.hq / a.hkv);
   if (a.dtype != DOMINO_BF16 || a.D > 128 || rows > 16) return false;

@@ -14,10 +14,11 @@
 //     rows 109 us without and 182 with the 8 most likely.)
 // A cluster of CTAs takes a row when there are few; their results meet in the first one's shared memory.
 //
-// Many rows: bound by instructions, 12.7 a logit with the exponential's unit a third busy. 1088 rows of 151,936 in bf16 with the
-// 8 most likely tokens 95 us, 3.5 TB/s (without them 83), where 1088 blocks are 7.2 rounds of an SM and take 8. Four blocks an SM (three: 98, five:
-// 107; twice as many of 128 threads: 98); a row over two blocks 105. One row: 11.5 us, launch, two batches, three joins and a
-// cluster barrier behind one another.
+// Many rows: 1088 of 151,936 in bf16 with the 8 most likely tokens 97 us, 3.4 TB/s (without them 84), at 12.7 instructions a logit, 71 % of the issue
+// slots and 45 % of memory. The rest is unlike blocks, in 1.8 rounds that take 2: a row whose token is the most likely counts its
+// rank in a batch or two, one whose token lies in the bulk in nearly all (all rows of the first kind 76 us, of the second 125). Four
+// blocks an SM (measured at 95 us; three: 98, five: 107; twice as many of 128 threads: 98); a row over two blocks 105. One row: 13.3 us a call,
+// launch, two batches, three joins and a cluster barrier behind one another.
 #include <math.h>
 
 #include "common.cuh"

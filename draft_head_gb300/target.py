@@ -233,8 +233,9 @@ class TokenScorer:
         self._args = (*(t.data_ptr() or None for t in self.out), self.ws.data_ptr(), self.ws.numel())
 
     def score(self, logits, tokens=None, temperature=None) -> Scores:
-        """tokens [rows] int32 (-1, or None for all rows: no token, logprob 0 and rank 0), temperature [rows] fp32 (None: 1). The
-        results are buffers of this object."""
+        """tokens [rows] int32 (-1, or None for all rows: no token, logprob 0 and rank 0), temperature [rows] fp32 (None: 1), each
+        1e-30 or more. (Sampler's 0, a greedy row, is no distribution: such a row gets NaN and last_status reports it; give it the
+        temperature that its log-probabilities are wanted at.) The results are buffers of this object."""
         n, ordinal = logits.shape[0], self.ordinal
         if (n > self.rows or logits.dtype != self.dtype or logits.dim() != 2 or logits.shape[1] != self.V or logits.stride(1) != 1 or
                 logits.get_device() != ordinal):

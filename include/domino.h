@@ -487,7 +487,9 @@ typedef enum {
  * or infinity reaches the rows that see it, as the formula says. A score of -inf
  * has weight 0; a row whose seen scores are all -inf is like one that sees none.
  * Scores, softmax and sums are fp32; in bf16 the softmax weights are rounded to
- * bf16 for the product with v. scale is finite and not negative.
+ * bf16 for the product with v. They are relative to a maximum that may be 2^32
+ * below the largest: sums over bf16 values from about 2^90 on may pass fp32's
+ * range where the result would not. scale is finite and not negative.
  * Workspace: domino_block_attention_workspace_bytes(cache, block, n_q_heads)
  * (0 if the arguments are invalid; block's device pointers are not read),
  * zeroed before its first use; each call leaves it ready for the next, of any
@@ -551,7 +553,7 @@ domino_status domino_sample(int dtype, const void* logits, int64_t logits_stride
  *   temperature  [rows] device fp32, or NULL: 1
  *   logprob, entropy, lse [rows] device fp32 out, rank [rows] device int32 out: each may be NULL
  *   top_n        0 to 32; top_ids [rows, top_n] device int32 out, top_logprob [rows, top_n] device fp32 out, each may be NULL
- * A temperature below 1e-30 or not finite records DOMINO_ERR_DEVICE_DATA and gives the row NaN in place of every fp32 result; a
+ * A temperature below 1e-30 (a greedy row's 0 is no distribution) or not finite records DOMINO_ERR_DEVICE_DATA and gives the row NaN in place of every fp32 result; a
  * token below -1 or from V on records it too and gives logprob NaN, rank -1. ws: any workspace of at least 256 bytes.
  */
 domino_status domino_token_logprobs(int dtype, const void* logits, int64_t logits_stride, int rows, int V,
@@ -578,7 +580,8 @@ domino_status domino_token_logprobs(int dtype, const void* logits, int64_t logit
  *   page_table [batch, max_pages] device int32, rows table_stride apart. Entries that no slot of a call needs (behind the
  *              last one, before the window) may be anything, and requests may share pages that no call writes.
  * Quantising x: with e the smallest exponent in [-100, 120] for which no |x_i| is above 448 * 2^e, the codes are x_i / 2^e rounded
- * to nearest even and E = e + 127; an x with an infinity or a NaN gets E = 255 and codes 0, and reads back as NaN. The e4m3 codes
+ * to nearest even and E = e + 127; an x with an infinity or a NaN gets E = 255 and codes 0, and reads back as NaN. Elements from 248 * 2^120
+ * (3.2965e38) on become 2^128, an infinity in bf16. The e4m3 codes
  * 0x7f and 0xff, which quantising never gives, read back as 480 and -480; rows that see a slot with one may get NaN. Values below 2^-110 of any vector may become 0.
  * A page outside [0, n_pages) that a call needs records DOMINO_ERR_DEVICE_DATA, and nothing is read or written for it.
  */
