@@ -270,9 +270,10 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     }
   };
 
-  // Codes: o is relative to m, kAtMost below the maximum of score + the value's exponent; l, the sum of the softmax's own
-  // weights, to that of the scores, ms. (From one of them, weights or their sum would leave fp32's range beside values whose
-  // exponents are far apart.) They begin below every score, so that -inf alone has weight 0.
+  // Codes: l, the sum of the softmax's own weights, is relative to the maximum of the scores, ms, and o to m above it: kAtMost below
+  // the maximum of score + the value's exponent. (From one of them, weights or their sum would leave fp32's range beside values
+  // whose exponents are far apart; and added to scores that are large themselves, m would be lost in them.) ms begins below every
+  // score, so that -inf alone has weight 0.
   float o[NT][4 * JJ][4], m[NT][2], l[NT][2], ms[NT][2];
 #pragma unroll
   for (int g = 0; g < NT; ++g) {
@@ -280,7 +281,8 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
     for (int t = 0; t < 4 * JJ; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[g][t][e] = 0.0f;
-    m[g][0] = m[g][1] = ms[g][0] = ms[g][1] = kCodes ? -3.402823466e+38f : -INFINITY;
+    m[g][0] = m[g][1] = kCodes ? 0.0f : -INFINITY;
+    ms[g][0] = ms[g][1] = -3.402823466e+38f;
     l[g][0] = l[g][1] = 0.0f;
   }
   int page = 0;
@@ -371,8 +373,9 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
       bool hidden[4] = {};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[g][e] *= qc[g][e & 1];
-        if (kCodes) s[g][e] *= ks[e >> 1];
+        // Codes: the factors first, as large queries may have small keys; and a product that no subtraction takes up, or large
+        // scores would be their rounding away from their own maximum.
+        s[g][e] = kCodes ? __fmul_rn(s[g][e], qc[g][e & 1] * ks[e >> 1]) : s[g][e] * qc[g][e & 1];
         if (!whole) {
           const int r = g * 8 + 2 * c + (e & 1), slot = s0 + n + 8 * (e >> 1);
           hidden[e] = !(slot < end && sees(a.mode, a.sinks, s_low[r], ctx, rows_n, s_i[r],
@@ -385,8 +388,8 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
         auto relative = [&] {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[e] = s[g][e] + (ve[e >> 1] - m[g][e & 1]);
             y[e] = s[g][e] - ms[g][e & 1];
+            x[e] = y[e] + (ve[e >> 1] - m[g][e & 1]);
           }
         };
         relative();
@@ -395,16 +398,16 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(s[g][e] + ve[0], s[g][2 + e] + ve[1]), high = fmaxf(s[g][e], s[g][2 + e]);
+            float high = fmaxf(s[g][e], s[g][2 + e]);
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
-            }
-            const float now = top - m[g][e] > kAtMost + kLazy ? top - kAtMost : m[g][e];
-            const float now_s = high - ms[g][e] > kLazy ? high : ms[g][e];
-            f[e] = ex2(m[g][e] - now);
-            l[g][e] *= ex2(ms[g][e] - now_s);
+            for (int d = 4; d < 32; d <<= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+            const float now_s = high - ms[g][e] > kLazy ? high : ms[g][e], by = ms[g][e] - now_s;
+            float top = fmaxf(s[g][e] - now_s + ve[0], s[g][2 + e] - now_s + ve[1]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float same = m[g][e] + by, now = top - same > kAtMost + kLazy ? top - kAtMost : same;
+            f[e] = ex2(same - now);
+            l[g][e] *= ex2(by);
             m[g][e] = now;
             ms[g][e] = now_s;
           }
@@ -512,10 +515,10 @@ __global__ void __launch_bounds__(kThr, CACHE == kPagedE4m3 && NT == 1 ? kCodesC
       if (kCodes) {
         // Both relative to one point, kRoom above the logarithm of l (which is 1 at least where a slot counts at all). The factor
         // of o may be below fp32's range where the result is not.
-        const float to = ms[g][e] + (kRoom + (float)((int)(__float_as_uint(l[g][e]) >> 23) - 127));
-        const float half = l[g][e] == 0.0f ? 1.0f : ex2(0.5f * (m[g][e] - to));
+        const float to = ms[g][e] + (kRoom + (float)((int)(__float_as_uint(l[g][e]) >> 23) - 127)), by = ms[g][e] - to;
+        const float half = l[g][e] == 0.0f ? 1.0f : ex2(0.5f * (m[g][e] + by));
         m[g][e] = l[g][e] == 0.0f ? -INFINITY : to;
-        l[g][e] *= ex2(ms[g][e] - to);
+        l[g][e] *= ex2(by);
 #pragma unroll
         for (int t = 0; t < 4 * JJ; ++t) {
           o[g][t][e] = o[g][t][e] * half * half;

@@ -17,7 +17,7 @@
 // Many rows: 1088 of 151,936 in bf16 with the 8 most likely tokens 97 us, 3.4 TB/s (without them 84), at 12.7 instructions a logit, 71 % of the issue
 // slots and 45 % of memory. The rest is unlike blocks, in 1.8 rounds that take 2: a row whose token is the most likely counts its
 // rank in a batch or two, one whose token lies in the bulk in nearly all (all rows of the first kind 76 us, of the second 125). Four
-// blocks an SM (measured at 95 us; three: 98, five: 107; twice as many of 128 threads: 98); a row over two blocks 105. One row: 13.3 us a call,
+// blocks an SM (measured at 95 us; three: 98, five: 107; twice as many of 128 threads: 98); a row over two blocks 105. One row: 12.3 us a call,
 // launch, two batches, three joins and a cluster barrier behind one another.
 #include <math.h>
 

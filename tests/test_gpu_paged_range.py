@@ -99,3 +99,18 @@ def test_read_into_the_largest_capacity(kind):
         assert torch.equal(o[0, :, 0].double(), pages.values(which, 0, 40)[:, 37])
     p.read(*out, ints([2 ** 31 - 1]))
     assert p.last_status() == 6
+
+
+@pytest.mark.parametrize("n", [1, 4, 8, 16, 200])
+@pytest.mark.parametrize("query,byte", [(95, 27), (112, 27), (116, 27), (118, 27), (-110, 235), (-118, 244)])
+def test_queries_and_keys_of_unlike_sizes(n, query, byte):
+    """Large queries over small keys and the other way round: their product is a number."""
+    spec = ([n], [300], 4, 2, 64, "causal", 0, 0, False, 16)
+
+    def prepare(pages, q):
+        pages.k_scale.fill_(byte)
+        q.mul_(2.0 ** query)
+
+    q, pages, p, seen, st, out, lse = run(E4M3, spec, 81, prepare=prepare)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    check(spec, q, pages, p, seen, st, out, lse)
