@@ -71,9 +71,10 @@ __device__ __forceinline__ uint2 codes_f16(uint32_t x) {
   return r;
 }
 // A row of queries in fp16, for products with codes: divided by a power of two that brings its largest magnitude, of these bits,
-// to [16, 32), where fp16 holds bf16's 8 bits of every element above 2^-21 of the largest, and smaller ones to within 2^-29 of it.
+// to [16, 32), where fp16 holds bf16's 8 bits of every element above 2^-21 of the largest, and smaller ones to within 2^-29 of it. (Below
+// 2^-122 it is 2^-126: fp16 then holds all that bf16 has there.)
 __device__ __forceinline__ int query_exponent(uint32_t most) {
-  return most >= 0x7f800000u || most < 0x00800000u ? 0 : min(max((int)(most >> 23) - 127 - 4, -126), 126);
+  return most >= 0x7f800000u ? 0 : min(max((int)(most >> 23) - 127 - 4, -126), 126);
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;

@@ -114,3 +114,17 @@ def test_queries_and_keys_of_unlike_sizes(n, query, byte):
     q, pages, p, seen, st, out, lse = run(E4M3, spec, 81, prepare=prepare)
     assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
     check(spec, q, pages, p, seen, st, out, lse)
+
+
+@pytest.mark.parametrize("n", [1, 4, 8, 16, 200])
+def test_queries_below_the_normal_numbers(n):
+    """Rows whose largest element is subnormal (below 2^-126), over keys next to bf16's largest."""
+    spec = ([n], [300], 4, 2, 64, "causal", 0, 0, False, 16)
+
+    def prepare(pages, q):
+        pages.k_scale.fill_(246)
+        q.mul_(2.0 ** -100).mul_(2.0 ** -30)
+        assert 0 < float(q.abs().max()) < 2.0 ** -126
+
+    q, pages, p, seen, st, out, lse = run(E4M3, spec, 82, prepare=prepare)
+    check(spec, q, pages, p, seen, st, out, lse)
