@@ -74,6 +74,10 @@ constexpr int kHalf = 64;  // and of the halves in which the weights are handed 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 32.0f;  // growth of the maximum (log2) that forces a rescale of O
+// A weight's logarithm is one multiply-add, score x c - m, with m the maximum's product with c as it is rounded, half a unit of its last
+// place off: 32 at most below this. From here on that could be more than the exponential holds, and scores that differ at all
+// differ by 2^6 there: c is replaced by a power of two, whose products are exact.
+constexpr float kExactFrom = 1073741824.0f;  // 2^30
 constexpr int kBadRing = 8;    // items the roles may be apart, at most (the ring holds fewer tiles)
 
 struct TcAttnP {
@@ -89,6 +93,7 @@ struct TcAttnP {
   int no_page;
   uint64_t timeout_ns;
   float c;        // scale log2(e)
+  float c_exact;  // the power of two next above it
   unsigned int* arrived;  // per CTA: pieces in, of the row tile that begins in it and goes on
   float2* ml;             // [2 grid][128 NQ]
   float4* o;              // [2 grid][NQ][DP / 4][128]: four columns of a row, rows next to each other
@@ -970,6 +975,7 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
       const int64_t row = row0 + h * G;
       __nv_bfloat16* out_tile = (__nv_bfloat16*)a.out + ((int64_t)(w.q0 + w.i_first) * a.hq + h * G) * a.D;
       float m = -INFINITY, l = 0.0f;  // m: log2 units
+      float by = p.c, less = 3.402823466e+38f;  // a weight's logarithm is score x by + less; before a score has been seen, above every one
       bool first = true;
       for (int k = NQ == 2 ? k0 : k0 + g; k < k1; k += NQ == 2 ? 1 : 2, ++tiles, first = false) {
         const int s0 = w.kt.slot(k, kBN);
@@ -1003,12 +1009,15 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
           for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
 #pragma unroll
         for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(s[124 + e]));
-        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * p.c;
-        const bool grow = live && mx > m + kLazy;  // from -inf: any finite maximum
+        const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]), over = fmaf(top, by, less);
+        const bool grow = live && over > kLazy;  // at first: any finite maximum
         if (__any_sync(0xffffffffu, grow)) {
-          const float m_new = grow ? mx : m;
-          const float f = m == m_new || m == -INFINITY ? 1.0f : ex2(m - m_new);
+          const float m_new = grow ? top * p.c : m;
+          const bool exact = fabsf(m_new) >= kExactFrom;
+          const float f = !grow || m == -INFINITY ? 1.0f : ex2(exact ? -over : m - m_new);
           m = m_new;
+          by = grow && exact ? p.c_exact : grow ? p.c : by;
+          less = grow ? -(exact ? top * p.c_exact : m_new) : less;
           l *= f;
           if (!first) {
 #pragma unroll 1
@@ -1023,8 +1032,7 @@ __global__ void __launch_bounds__(Cfg<NQ, KB, CACHE>::kThreads, 1) attn_tc_kerne
             tmem_wait_st();
           }
         }
-        const float m_use = m == -INFINITY ? 0.0f : m;
-        const float2 c2 = make_float2(p.c, p.c), n2 = make_float2(-m_use, -m_use);
+        const float2 c2 = make_float2(by, by), n2 = make_float2(less, less);
         float2 sum2[2] = {make_float2(0, 0), make_float2(0, 0)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -1343,6 +1351,8 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   // Masked scores are -inf before they are multiplied and have to stay so with a scale of 0: the smallest normal factor
   // instead, which brings products of up to 2^120 to within 2^-6 of 0.
   p.c = fmaxf(a.scale * kLog2e, 1.17549435e-38f);
+  int c_exponent;
+  p.c_exact = ldexpf(1.0f, frexpf(p.c, &c_exponent) == 0.5f ? c_exponent - 1 : c_exponent);
   // Beside the tiles: barriers, notes and (NQ = 1) the groups' maxima and sums.
   constexpr uint32_t kSmall = NQ == 2 && C::kCodes ? 1024 : 3 * 1024;
   const uint32_t budget = 227 * 1024 - kSmall;
