@@ -50,8 +50,8 @@
 //   warps 12-15  turn them into bf16 in the ring: code x scale is exact there (4 significant bits), so all that follows is the
 //                same. A code's fields at bf16's places are 2^-120 of it, and one product with the scale does the rest.
 // They share the SM's issue slots and shared memory with the softmax, and set the pace where the cache's bytes would: 64
-// blocks over pages of 64 slots 229 us (bf16 pages 169, of 16 slots 199, 256 181), 16 trees 85 us (66), chunks of 2048 rows for 4 requests
-// 473 us (394), 0.99 PFLOP/s. With the conversion left out, a copy in its place, they took 200, 77 and 463 (the chunks 490 then): it is the
+// blocks over pages of 64 slots 229 us (bf16 pages 169, of 16 slots 201, 256 181), 16 trees 85 us (66), chunks of 2048 rows for 4 requests
+// 473 us (400), 0.99 PFLOP/s. With the conversion left out, a copy in its place, they took 200, 77 and 463 (the chunks 490 then): it is the
 // passes through shared memory, not the arithmetic, that cost. (Products of codes as fp16 with scales relative to a tile's largest: 210, 79 and 502, and
 // small scales beside large ones would lose bits. Keys by two of the warps and values by the other two: 244, 90 and 654.)
 #include <cuda.h>
