@@ -76,7 +76,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 32.0f;  // growth of the maximum (log2) that forces a rescale of O
 // A weight's logarithm is one multiply-add, score x c - m, with m the maximum's product with c as it is rounded, half a unit of its last
 // place off: 32 at most below this. From here on that could be more than the exponential holds, and scores that differ at all
-// differ by 2^6 there: c is replaced by a power of two, whose products are exact.
+// differ by 2^6 there: c is replaced by the power of two at or below it, whose products are exact (and by which they differ by 2^5).
 constexpr float kExactFrom = 1073741824.0f;  // 2^30
 constexpr int kBadRing = 8;    // items the roles may be apart, at most (the ring holds fewer tiles)
 
@@ -93,7 +93,7 @@ struct TcAttnP {
   int no_page;
   uint64_t timeout_ns;
   float c;        // scale log2(e)
-  float c_exact;  // the power of two next above it
+  float c_exact;  // the power of two at or below it
   unsigned int* arrived;  // per CTA: pieces in, of the row tile that begins in it and goes on
   float2* ml;             // [2 grid][128 NQ]
   float4* o;              // [2 grid][NQ][DP / 4][128]: four columns of a row, rows next to each other
@@ -1351,8 +1351,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   // Masked scores are -inf before they are multiplied and have to stay so with a scale of 0: the smallest normal factor
   // instead, which brings products of up to 2^120 to within 2^-6 of 0.
   p.c = fmaxf(a.scale * kLog2e, 1.17549435e-38f);
-  int c_exponent;
-  p.c_exact = ldexpf(1.0f, frexpf(p.c, &c_exponent) == 0.5f ? c_exponent - 1 : c_exponent);
+  p.c_exact = ldexpf(1.0f, ilogbf(fminf(p.c, 3.402823466e+38f)));
   // Beside the tiles: barriers, notes and (NQ = 1) the groups' maxima and sums.
   constexpr uint32_t kSmall = NQ == 2 && C::kCodes ? 1024 : 3 * 1024;
   const uint32_t budget = 227 * 1024 - kSmall;

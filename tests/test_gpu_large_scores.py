@@ -33,6 +33,19 @@ def expect(q0, k0, v, scale, seen):
 @pytest.mark.parametrize("sign", [1, -1])
 @pytest.mark.parametrize("D", [64, 128])
 def test_only_ties_count(kind, n, power, sign, D):
+    ties(kind, n, power, sign, D, 0.125)
+
+
+@pytest.mark.parametrize("kind", [E4M3, BF, F32, "whole"])
+@pytest.mark.parametrize("n", [1, 4, 16, 200])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("scale", [0.9, 1.0])
+def test_scores_next_to_the_end_of_the_range(kind, n, sign, scale):
+    """Up to 2^127.7 in powers of two."""
+    ties(kind, n, 124, sign, 64, scale)
+
+
+def ties(kind, n, power, sign, D, scale):
     g = gen(n + power)
     pages = P.Pages(BF if kind == "whole" else kind, [CTX + n], HKV, 32, D, n + power)
     # Keys 1 to 3 at element 0 (all of one sign, so that the maximum is the largest or the smallest product), 0 elsewhere.
@@ -45,18 +58,18 @@ def test_only_ties_count(kind, n, power, sign, D):
     q = torch.zeros(n, HQ, D, device="cuda")
     q[:, :, 0] = q0
     q = q.to(pages.rows_type)
-    p = layer(pages, HQ, n, n, CTX, scale=0.125)
+    p = layer(pages, HQ, n, n, CTX, scale=scale)
     if kind == "whole":
         k, v = (torch.zeros(1, HKV, 640, D, dtype=BF, device="cuda") for _ in "kv")
         p.read(k, v, ints([CTX + n]))
-        p = BlockAttention(k, v, HQ, n, n, CTX, scale=0.125)
+        p = BlockAttention(k, v, HQ, n, n, CTX, scale=scale)
     out, lse = p.attend(q, ints([CTX]), want_lse=True)
     assert p.last_status() == 0
     h = H if kind != F32 else 0.0
     for h_kv in range(HKV):
         v = pages.values("v", 0, CTX + n)[h_kv]
         for i in range(0, n, max(1, n // 10)):
-            want, wl = expect(q0, k0, v, 0.125, CTX + i + 1)
+            want, wl = expect(q0, k0, v, scale, CTX + i + 1)
             tol = 2 * h * v.abs().max() + (CTX + n) * U * v.abs().max()
             for head in range(h_kv * HQ // HKV, (h_kv + 1) * HQ // HKV):
                 assert bool(((out[i, head].double() - want).abs() <= tol).all()), (i, head)
